@@ -8,15 +8,21 @@ if it is missing.
 from ._binding import (  # noqa: F401
     DA_BF16,
     DA_DEVERR_KV_LEN,
+    DA_DEVERR_PAGE,
     DA_DEVERR_POSITION,
     DA_DEVERR_TIMEOUT,
     DA_DEVERR_WORKSPACE,
     DA_F16,
     DecodeAttnError,
     LibraryNotBuilt,
+    alloc_paged_workspace,
     alloc_workspace,
     decode_attn_fwd,
     decode_attn_fwd_static_scratch,
+    decode_attn_paged_fwd,
+    decode_attn_paged_q8_fwd,
+    decode_attn_paged_workspace_size,
+    decode_attn_window_fwd,
     STATIC_SCRATCH_BYTES,
     decode_attn_workspace_size,
     decode_step_fwd,
@@ -25,6 +31,8 @@ from ._binding import (  # noqa: F401
     exported_symbols,
     kernel_for,
     kvcache_append,
+    kvcache_append_paged,
+    kvcache_append_paged_q8,
     library_path,
     load_library,
     plan_splits,

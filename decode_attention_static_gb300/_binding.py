@@ -23,6 +23,7 @@ DA_DEVERR_KV_LEN = 1
 DA_DEVERR_POSITION = 2
 DA_DEVERR_TIMEOUT = 4
 DA_DEVERR_WORKSPACE = 8
+DA_DEVERR_PAGE = 16
 
 _DTYPE_CODE = {torch.float16: DA_F16, torch.bfloat16: DA_BF16}
 
@@ -65,6 +66,12 @@ _SIGNATURES = {
                                 ctypes.c_size_t, _i, _i, _vp, _vp], _i),
     "decode_step_rope_fwd": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _i, _i, _i, _i, _i, ctypes.c_float, _vp, _vp,
                               ctypes.c_size_t, _i, _i, _vp, _vp], _i),
+    "kvcache_append_paged": ([_vp] * 8 + [_i] + [_vp] * 3 + [_i] * 9 + [_vp, _vp], _i),
+    "kvcache_append_paged_q8": ([_vp] * 10 + [_i] + [_vp] * 3 + [_i] * 9 + [_vp, _vp], _i),
+    "decode_attn_paged_workspace_size": ([_i, _i, _i], ctypes.c_size_t),
+    "decode_attn_paged_fwd": ([_vp] * 5 + [_i] * 9 + [ctypes.c_float, _vp, _vp, ctypes.c_size_t, _i, _vp, _vp], _i),
+    "decode_attn_paged_q8_fwd": ([_vp] * 7 + [_i] * 9 + [ctypes.c_float, _vp, _vp, ctypes.c_size_t, _i, _vp, _vp], _i),
+    "decode_attn_window_fwd": ([_vp] * 4 + [_i] * 7 + [ctypes.c_float, _vp, _vp, ctypes.c_size_t, _i, _vp, _vp], _i),
 }
 
 
@@ -487,4 +494,218 @@ def decode_attn_fwd_static_scratch(q: torch.Tensor, k_cache: torch.Tensor, v_cac
         scale = D ** -0.5
     _call("decode_attn_fwd_static_scratch", dev, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(kv_len), B, H, Hkv, D,
           cap, float(scale), _ptr(out), int(max_kv_len_hint), _dtype_code(q), _err_ptr(err_flag, dev), _stream(q))
+    return out
+
+
+def decode_attn_paged_workspace_size(n_head: int, n_kv_head: int, head_dim: int) -> int:
+    """Scratch bytes of one paged or sliding-window attention call on the
+    current device (the same for every batch, length and page size)."""
+    n = load_library().decode_attn_paged_workspace_size(n_head, n_kv_head, head_dim)
+    if n == ctypes.c_size_t(-1).value:
+        raise DecodeAttnError("decode_attn_paged_workspace_size", -2, "invalid sizes or device query failed")
+    return int(n)
+
+
+def alloc_paged_workspace(n_head: int, n_kv_head: int, head_dim: int, device=None) -> torch.Tensor:
+    """A zero-filled device byte buffer of decode_attn_paged_workspace_size() bytes (torch owns it)."""
+    with torch.cuda.device(device):
+        n = decode_attn_paged_workspace_size(n_head, n_kv_head, head_dim)
+    return torch.zeros(max(n, 16), dtype=torch.uint8, device=device or "cuda")
+
+
+def _pool(k_pages, v_pages, dtype, scales):
+    """Shape of a page pool, and checks of its types (and scales)."""
+    _require(k_pages.dim() == 4 and v_pages.shape == k_pages.shape,
+             "k_pages/v_pages must be [num_pages, n_kv_head, page_size, D]")
+    pages, Hkv, size, D = k_pages.shape
+    want = dtype if scales is None else torch.float8_e4m3fn
+    if k_pages.dtype != want or v_pages.dtype != want:
+        raise TypeError(f"pages must be {want}")
+    if scales is not None:
+        for name, t in zip(("k_scale", "v_scale"), scales):
+            _require(t.dtype == torch.float32 and t.shape == (pages, Hkv),
+                     lambda: f"{name} must be float32 [num_pages, n_kv_head]")
+    return pages, Hkv, size, D
+
+
+def _append_paged(fn, k_pages, v_pages, scales, k_new, v_new, page_table, position_ids, token_start, rope_cos,
+                  rope_sin, q, q_out, err_flag):
+    _cuda_contig("k_new", k_new)
+    index = k_new.get_device()
+    code = _code_for(k_new.dtype)
+    pages, Hkv, size, D = _pool(k_pages, v_pages, k_new.dtype, scales)
+    _require(k_new.dim() == 3 and k_new.shape[1] == Hkv and k_new.shape[2] == D and v_new.shape == k_new.shape
+             and v_new.dtype == k_new.dtype, "k_new/v_new must be [tokens, n_kv_head, D] of one type")
+    tokens = k_new.shape[0]
+    _require(page_table.dtype == torch.int32 and page_table.dim() == 2, "page_table must be int32 [B, max_pages]")
+    B, max_pages = page_table.shape
+    _require(position_ids.dtype == torch.int32 and position_ids.numel() == B, "position_ids must be int32 [B]")
+    names = ["v_new", "k_pages", "v_pages", "page_table", "position_ids"]
+    tensors = [v_new, k_pages, v_pages, page_table, position_ids]
+    if scales is not None:
+        names += ["k_scale", "v_scale"]
+        tensors += scales
+    if token_start is not None:
+        _require(token_start.dtype == torch.int32 and token_start.numel() == B + 1, "token_start must be int32 [B + 1]")
+        names.append("token_start")
+        tensors.append(token_start)
+    else:
+        _require(tokens == B, "without token_start there is one token per sequence")
+    rope_rows = n_head = 0
+    cos_ptr = sin_ptr = q_ptr = out_ptr = None
+    _require((rope_cos is None) == (rope_sin is None), "rope_cos and rope_sin come together")
+    if rope_cos is not None:
+        _require(rope_cos.dtype == torch.float32 and rope_sin.dtype == torch.float32 and rope_cos.dim() == 2
+                 and rope_cos.shape == rope_sin.shape and rope_cos.shape[1] == D, "rope tables must be fp32 [rows, D]")
+        rope_rows, cos_ptr, sin_ptr = rope_cos.shape[0], rope_cos.data_ptr(), rope_sin.data_ptr()
+        names += ["rope_cos", "rope_sin"]
+        tensors += [rope_cos, rope_sin]
+    if q is not None:
+        _require(rope_cos is not None, "rotating q needs the rope tables")
+        _require(q.dim() == 3 and q.shape[0] == tokens and q.shape[2] == D and q.dtype == k_new.dtype,
+                 "q must be [tokens, n_head, D] of the type of k_new")
+        if q_out is None:
+            q_out = torch.empty_like(q)
+        _require(q_out.shape == q.shape and q_out.dtype == q.dtype, "q_out must match q")
+        n_head, q_ptr, out_ptr = q.shape[1], q.data_ptr(), q_out.data_ptr()
+        names += ["q", "q_out"]
+        tensors += [q, q_out]
+    else:
+        _require(q_out is None, "q_out comes with q")
+    if err_flag is not None:
+        _require(err_flag.dtype == torch.int32 and err_flag.numel() >= 1, "err_flag must be int32 with one element")
+        names.append("err_flag")
+        tensors.append(err_flag)
+    _same_device_contiguous(index, names, tensors)
+    pool = [k_pages.data_ptr(), v_pages.data_ptr()]
+    if scales is not None:
+        pool += [scales[0].data_ptr(), scales[1].data_ptr()]
+    _call_on(fn, index, *pool, k_new.data_ptr(), v_new.data_ptr(), q_ptr, out_ptr, cos_ptr, sin_ptr, rope_rows,
+             page_table.data_ptr(), position_ids.data_ptr(), None if token_start is None else token_start.data_ptr(),
+             B, tokens, n_head, Hkv, D, pages, size, max_pages, code,
+             None if err_flag is None else err_flag.data_ptr(), _raw_stream(index))
+    return q_out
+
+
+def kvcache_append_paged(k_pages: torch.Tensor, v_pages: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
+                         page_table: torch.Tensor, position_ids: torch.Tensor,
+                         token_start: torch.Tensor | None = None, rope_cos: torch.Tensor | None = None,
+                         rope_sin: torch.Tensor | None = None, q: torch.Tensor | None = None,
+                         q_out: torch.Tensor | None = None,
+                         err_flag: torch.Tensor | None = None) -> torch.Tensor | None:
+    """Append packed new rows to a paged cache, keys (and q) rotated on the way.
+
+    Pools [num_pages, n_kv_head, page_size, D]; page_table int32 [B,
+    max_pages]; k_new/v_new [tokens, n_kv_head, D], sequence b owning tokens
+    [token_start[b], token_start[b + 1]) from position position_ids[b] on
+    (token_start None: one token per sequence). With rope tables the keys are
+    rotated at their positions, and q [tokens, n_head, D] into q_out (may be
+    q), which is returned."""
+    return _append_paged("kvcache_append_paged", k_pages, v_pages, None, k_new, v_new, page_table, position_ids,
+                         token_start, rope_cos, rope_sin, q, q_out, err_flag)
+
+
+def kvcache_append_paged_q8(k_pages: torch.Tensor, v_pages: torch.Tensor, k_scale: torch.Tensor,
+                            v_scale: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
+                            page_table: torch.Tensor, position_ids: torch.Tensor,
+                            token_start: torch.Tensor | None = None, rope_cos: torch.Tensor | None = None,
+                            rope_sin: torch.Tensor | None = None, q: torch.Tensor | None = None,
+                            q_out: torch.Tensor | None = None,
+                            err_flag: torch.Tensor | None = None) -> torch.Tensor | None:
+    """kvcache_append_paged into float8_e4m3fn pools with one power-of-two
+    scale per page and KV head (k_scale/v_scale float32 [num_pages, n_kv_head],
+    updated in place; a page whose scale grows has its earlier rows rounded to
+    the new one)."""
+    return _append_paged("kvcache_append_paged_q8", k_pages, v_pages, [k_scale, v_scale], k_new, v_new, page_table,
+                         position_ids, token_start, rope_cos, rope_sin, q, q_out, err_flag)
+
+
+def _attn_tail(q, out, scale, workspace, err_flag, Hkv, names, tensors):
+    """The checks and arguments that the attention entry points share: out,
+    scale, workspace, error flag; returns (out, index, trailing arguments)."""
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _require(out.shape == q.shape and out.dtype == q.dtype, "out must match q")
+        names.append("out")
+        tensors.append(out)
+    index = q.get_device()
+    D = q.shape[2]
+    if workspace is None:
+        workspace = alloc_paged_workspace(q.shape[1], Hkv, D, q.device)
+    names.append("workspace")
+    tensors.append(workspace)
+    if err_flag is not None:
+        _require(err_flag.dtype == torch.int32 and err_flag.numel() >= 1, "err_flag must be int32 with one element")
+        names.append("err_flag")
+        tensors.append(err_flag)
+    _same_device_contiguous(index, names, tensors)
+    return out, index, (float(D ** -0.5 if scale is None else scale), out.data_ptr(), workspace.data_ptr(),
+                        workspace.numel() * workspace.element_size(), _code_for(q.dtype),
+                        None if err_flag is None else err_flag.data_ptr(), _raw_stream(index))
+
+
+def _attn_paged(fn, q, k_pages, v_pages, scales, page_table, kv_len, window, sinks, out, scale, workspace, err_flag):
+    _cuda_contig("q", q)
+    _require(q.dim() == 3, "q must be [B, n_head, D]")
+    _code_for(q.dtype)
+    B, H, D = q.shape
+    pages, Hkv, size, Dk = _pool(k_pages, v_pages, q.dtype, scales)
+    _require(Dk == D, "head_dim of the pages must match q")
+    _require(page_table.dtype == torch.int32 and page_table.dim() == 2 and page_table.shape[0] == B,
+             "page_table must be int32 [B, max_pages]")
+    _require(kv_len.dtype == torch.int32 and kv_len.numel() == B, "kv_len must be int32 [B]")
+    names, tensors = ["k_pages", "v_pages", "page_table", "kv_len"], [k_pages, v_pages, page_table, kv_len]
+    pool = [k_pages.data_ptr(), v_pages.data_ptr()]
+    if scales is not None:
+        names += ["k_scale", "v_scale"]
+        tensors += scales
+        pool += [scales[0].data_ptr(), scales[1].data_ptr()]
+    out, index, tail = _attn_tail(q, out, scale, workspace, err_flag, Hkv, names, tensors)
+    _call_on(fn, index, q.data_ptr(), *pool, page_table.data_ptr(), kv_len.data_ptr(), B, H, Hkv, D, pages, size,
+             page_table.shape[1], int(window), int(sinks), *tail)
+    return out
+
+
+def decode_attn_paged_fwd(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor,
+                          kv_len: torch.Tensor, window: int = 0, sinks: int = 0, out: torch.Tensor | None = None,
+                          scale: float | None = None, workspace: torch.Tensor | None = None,
+                          err_flag: torch.Tensor | None = None) -> torch.Tensor:
+    """Decode attention of q [B, n_head, D] over the first kv_len[b] rows of a
+    paged cache (or, with window > 0, over the last `window` of them and the
+    first `sinks`); kv_len[b] == 0 gives zeros. A workspace comes from
+    alloc_paged_workspace (reuse it across calls)."""
+    return _attn_paged("decode_attn_paged_fwd", q, k_pages, v_pages, None, page_table, kv_len, window, sinks, out,
+                       scale, workspace, err_flag)
+
+
+def decode_attn_paged_q8_fwd(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, k_scale: torch.Tensor,
+                             v_scale: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tensor, window: int = 0,
+                             sinks: int = 0, out: torch.Tensor | None = None, scale: float | None = None,
+                             workspace: torch.Tensor | None = None,
+                             err_flag: torch.Tensor | None = None) -> torch.Tensor:
+    """decode_attn_paged_fwd over float8_e4m3fn pools with their scales
+    float32 [num_pages, n_kv_head]."""
+    return _attn_paged("decode_attn_paged_q8_fwd", q, k_pages, v_pages, [k_scale, v_scale], page_table, kv_len,
+                       window, sinks, out, scale, workspace, err_flag)
+
+
+def decode_attn_window_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, kv_len: torch.Tensor,
+                           window: int, sinks: int = 0, out: torch.Tensor | None = None, scale: float | None = None,
+                           workspace: torch.Tensor | None = None,
+                           err_flag: torch.Tensor | None = None) -> torch.Tensor:
+    """Decode attention over the last `window` of the first kv_len[b] rows of a
+    static cache and its first `sinks` rows; nothing else is read."""
+    _cuda_contig("q", q)
+    _require(q.dim() == 3, "q must be [B, n_head, D]")
+    _require(k_cache.dim() == 4 and v_cache.shape == k_cache.shape, "caches must be [B, n_kv_head, capacity, D]")
+    B, H, D = q.shape
+    Bk, Hkv, cap, Dk = k_cache.shape
+    _require(Bk == B and Dk == D, "cache batch/head_dim must match q")
+    _require(q.dtype == k_cache.dtype == v_cache.dtype, "dtypes differ")
+    _require(kv_len.dtype == torch.int32 and kv_len.numel() == B, "kv_len must be int32 [B]")
+    out, index, tail = _attn_tail(q, out, scale, workspace, err_flag, Hkv, ["k_cache", "v_cache", "kv_len"],
+                                  [k_cache, v_cache, kv_len])
+    _call_on("decode_attn_window_fwd", index, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), kv_len.data_ptr(),
+             B, H, Hkv, D, cap, int(window), int(sinks), *tail)
     return out

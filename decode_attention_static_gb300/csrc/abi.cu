@@ -8,6 +8,7 @@
 #include <atomic>
 #include <mutex>
 
+#include "cache_params.h"
 #include "decode_attn.h"
 #include "launch.h"
 
@@ -328,6 +329,21 @@ int decode_common(const void* q, const void* k_cache, const void* v_cache, void*
 }
 
 }  // namespace
+
+bool record_timing_before(cudaStream_t stream) {
+  return !t_event_before || record_event(t_event_before, stream) == cudaSuccess;
+}
+
+bool record_timing_after(cudaStream_t stream) {
+  return !t_event_after || record_event(t_event_after, stream) == cudaSuccess;
+}
+
+cudaError_t current_device_sms(int* sms) {
+  int device = 0;
+  const cudaError_t e = current_device(&device);
+  return e != cudaSuccess ? e : device_sms(device, sms);
+}
+
 }  // namespace da
 
 extern "C" {
@@ -337,8 +353,9 @@ const char* da_status_string(int status) {
     case DA_OK: return "ok";
     case DA_ERR_NULL: return "a required pointer is NULL";
     case DA_ERR_SHAPE: return "a size is out of range or inconsistent";
-    case DA_ERR_UNSUPPORTED: return "unsupported head_dim or group size (head_dim in {64,128}, group in {1,2,4,8})";
-    case DA_ERR_WORKSPACE: return "workspace is NULL or smaller than decode_attn_workspace_size()";
+    case DA_ERR_UNSUPPORTED: return "unsupported head_dim, group size or page size (head_dim in {64,128}, group in {1,2,4,8}, page size 16..256, "
+             "a power of two)";
+    case DA_ERR_WORKSPACE: return "workspace is NULL or smaller than the matching *_workspace_size()";
     case DA_ERR_CUDA: return "a CUDA runtime call or kernel launch failed";
     case DA_ERR_ALIGN: return "a pointer is not 16-byte aligned";
     case DA_ERR_DTYPE: return "unknown dtype code";
@@ -346,7 +363,7 @@ const char* da_status_string(int status) {
   }
 }
 
-int da_version(void) { return 100; }
+int da_version(void) { return 200; }
 
 int decode_attn_plan_splits(int B, int n_kv_head, int head_dim, int max_kv_len, int num_sms, int ctas_per_sm,
                             int cluster_max, int* cluster_size) {

@@ -1,0 +1,10 @@
+// Paged and sliding-window attention instances for f16 queries.
+#include "cache_attn.cuh"
+
+namespace da {
+
+cudaError_t launch_cache_attn_f16(const CacheAttnParams& p, int head_dim, bool e4m3, int sms, cudaStream_t stream) {
+  return launch_cache_attn_type<__half>(p, head_dim, e4m3, sms, stream);
+}
+
+}  // namespace da

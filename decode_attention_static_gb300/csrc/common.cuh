@@ -17,6 +17,7 @@ constexpr int32_t kErrKvLen = 1;
 constexpr int32_t kErrPosition = 2;
 constexpr int32_t kErrTimeout = 4;
 constexpr int32_t kErrWorkspace = 8;
+constexpr int32_t kErrPage = 16;
 
 // A pipeline wait gives up after this long and reports kErrTimeout.
 constexpr unsigned long long kWaitLimitNs = 1000ull * 1000ull * 1000ull;  // 1 s

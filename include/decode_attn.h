@@ -62,10 +62,10 @@ typedef enum {
   DA_OK = 0,
   DA_ERR_NULL = -1,        /* a required pointer is NULL */
   DA_ERR_SHAPE = -2,       /* a size is out of range or inconsistent */
-  DA_ERR_UNSUPPORTED = -3, /* valid but not built: head_dim or group size */
+  DA_ERR_UNSUPPORTED = -3, /* valid but not built: head_dim, group size or page size */
   DA_ERR_WORKSPACE = -4,   /* workspace NULL or smaller than required */
   DA_ERR_CUDA = -5,        /* a CUDA runtime call or launch failed */
-  DA_ERR_ALIGN = -6,       /* a pointer is not 16-byte aligned */
+  DA_ERR_ALIGN = -6,       /* a pointer is not 16-byte aligned (int32 and scale arrays: 4-byte) */
   DA_ERR_DTYPE = -7        /* unknown dtype code */
 } da_status;
 
@@ -74,6 +74,7 @@ typedef enum {
 #define DA_DEVERR_POSITION 2u /* some position_ids[b] outside [0, capacity): write skipped */
 #define DA_DEVERR_TIMEOUT 4u  /* a pipeline wait hit its time limit: rows are NaN */
 #define DA_DEVERR_WORKSPACE 8u /* the workspace counters were not zero: rows of the group are NaN */
+#define DA_DEVERR_PAGE 16u /* a page id in use lies outside [0, num_pages): rows are NaN, writes skipped */
 
 /* Human-readable name of a da_status value (static string). */
 DA_API const char* da_status_string(int status);
@@ -361,6 +362,124 @@ DA_API int decode_attn_fwd_static_scratch(const void* q, const void* k_cache, co
                                           int head_dim, int capacity, float scale, void* out,
                                           int max_kv_len_hint, int dtype, int32_t* err_flag,
                                           void* stream);
+
+/* ------------------------------------------------------------------------
+ * Paged caches, 8-bit caches and sliding windows. These entry points are
+ * additions of this library; the pages it follows have no counterpart. They
+ * keep its conventions (device pointers, contiguous row-major, nothing
+ * allocated or synchronised, device facts reported in *err_flag) with these
+ * layouts:
+ *   k_pages, v_pages  [num_pages, n_kv_head, page_size, head_dim], page_size
+ *                     a power of two in [16, 256]; a pool that sequences of
+ *                     any length share
+ *   page_table        int32 [B, max_pages]: rows [i * page_size, (i + 1) *
+ *                     page_size) of sequence b are page page_table[b, i].
+ *                     Entries of pages that a call does not touch are not
+ *                     looked at and may hold anything. Sequences may share
+ *                     pages that are only read; a page that two sequences of
+ *                     one call append to ends up with unspecified rows.
+ * and, for pages in 8 bits (e4m3: sign, four exponent, three mantissa bits, no
+ * infinities),
+ *   k_scale, v_scale  fp32 [num_pages, n_kv_head]: element x of a page and KV
+ *                     head stands for x * scale.
+ * max_pages * page_size stays below 2^31 - 512 (else DA_ERR_SHAPE).
+ */
+
+/*
+ * Append new rows to a paged cache, with the rotary embedding on the way. The
+ * rows are packed: k_new and v_new [tokens, n_kv_head, head_dim]. Sequence b
+ * owns tokens [token_start[b], token_start[b + 1]) (int32 [B + 1], rising),
+ * and its first one has position position_ids[b]; token_start NULL means one
+ * token per sequence (tokens == B, else DA_ERR_SHAPE). Tokens before
+ * token_start[0] and from token_start[B] on (padding) are left alone, and so
+ * are their q_out rows. With tables (rope_cos, rope_sin fp32 [rope_rows,
+ * head_dim], as in decode_step_rope_fwd) the key row at position p becomes
+ * k * cos[p] + rotate_half(k) * sin[p], products and sum rounded to fp32 and
+ * the result once to the storage type; without (both NULL) it is copied. V is
+ * copied. q [tokens, n_head, head_dim] (NULL: none) is rotated the same way
+ * into q_out, which may be q itself; it needs the tables.
+ * A sequence whose positions do not all lie in [0, max_pages * page_size) and
+ * [0, rope_rows) is skipped whole and sets DA_DEVERR_POSITION (its q_out rows
+ * become NaN); rows of a page id outside the pool are skipped and set
+ * DA_DEVERR_PAGE. Only the appended rows of a page are written.
+ */
+DA_API int kvcache_append_paged(void* k_pages, void* v_pages, const void* k_new, const void* v_new, const void* q,
+                    void* q_out, const float* rope_cos, const float* rope_sin, int rope_rows,
+                    const int32_t* page_table, const int32_t* position_ids, const int32_t* token_start, int B,
+                    int tokens, int n_head, int n_kv_head, int head_dim, int num_pages, int page_size, int max_pages,
+                    int dtype, int32_t* err_flag, void* stream);
+
+/*
+ * kvcache_append_paged into pages of e4m3 (dtype is that of k_new, v_new, q
+ * and q_out). For every page and KV head that gets rows, with K and V apart:
+ *   peak  = largest finite |x| among the page's new rows (fp32, the rotated
+ *           key before any rounding)
+ *   scale = the smallest power of two >= peak / 448, at least 2^-100; and at
+ *           least the page's present scale when rows before the first new one
+ *           lie in the page (a page filled from its first row on starts anew)
+ *   x is stored as e4m3(x / scale), nearest even; NaN and infinities as NaN.
+ * Where the scale grows, the page's earlier rows are rounded to the new one
+ * (a power of two: only exponents move, bits are lost below 2^-9 of the new
+ * scale alone). Rows behind the new ones are left as they were. Appending the
+ * same rows at the same positions again changes nothing.
+ */
+DA_API int kvcache_append_paged_q8(void* k_pages, void* v_pages, float* k_scale, float* v_scale, const void* k_new,
+                    const void* v_new, const void* q, void* q_out, const float* rope_cos, const float* rope_sin,
+                    int rope_rows, const int32_t* page_table, const int32_t* position_ids,
+                    const int32_t* token_start, int B, int tokens, int n_head, int n_kv_head, int head_dim,
+                    int num_pages, int page_size, int max_pages, int dtype, int32_t* err_flag, void* stream);
+
+/*
+ * Bytes of scratch that one call of decode_attn_paged_fwd,
+ * decode_attn_paged_q8_fwd or decode_attn_window_fwd needs on the current
+ * device: it depends on the heads alone, not on the batch, the lengths or the
+ * pages. Zero-fill it once before its first use (decode_attn_workspace_init);
+ * every call that completes leaves it ready for the next, whatever its sizes.
+ * Calls that share a workspace must not overlap on the GPU. Returns
+ * (size_t)-1 for invalid sizes or a failed device query.
+ */
+DA_API size_t decode_attn_paged_workspace_size(int n_head, int n_kv_head, int head_dim);
+
+/*
+ * Decode attention over a paged cache. Row j of sequence b is visible when
+ *   j < kv_len[b] and (window == 0 or j >= kv_len[b] - window or j < sinks)
+ * (the last `window` rows, the query's own among them, and the first `sinks`
+ * ones), and out[b, h, :] = softmax_j(scale <q[b, h], K_j>) V_j over those
+ * rows, fp32 arithmetic, rounded once. Rows that are not visible are not
+ * read. kv_len[b] == 0 (an idle slot of a batch) gives a row of zeros;
+ * kv_len[b] < 0 or > max_pages * page_size gives NaN and DA_DEVERR_KV_LEN; a
+ * page id outside the pool gives NaN for the heads that would read it and
+ * DA_DEVERR_PAGE. window >= 0, sinks >= 0, and sinks > 0 needs window > 0
+ * (else DA_ERR_SHAPE). No length bound is needed: the launch does not depend
+ * on the lengths, so a captured graph serves any of them.
+ */
+DA_API int decode_attn_paged_fwd(const void* q, const void* k_pages, const void* v_pages, const int32_t* page_table,
+                    const int32_t* kv_len, int B, int n_head, int n_kv_head, int head_dim, int num_pages,
+                    int page_size, int max_pages, int window, int sinks, float scale, void* out, void* workspace,
+                    size_t workspace_bytes, int dtype, int32_t* err_flag, void* stream);
+
+/*
+ * decode_attn_paged_fwd over pages of e4m3 with their scales: K_j and V_j are
+ * the stored values times the scale of their page and KV head (any finite
+ * scale; those of kvcache_append_paged_q8 are powers of two). dtype is that of
+ * q and out.
+ */
+DA_API int decode_attn_paged_q8_fwd(const void* q, const void* k_pages, const void* v_pages, const float* k_scale,
+                    const float* v_scale, const int32_t* page_table, const int32_t* kv_len, int B, int n_head,
+                    int n_kv_head, int head_dim, int num_pages, int page_size, int max_pages, int window, int sinks,
+                    float scale, void* out, void* workspace, size_t workspace_bytes, int dtype, int32_t* err_flag,
+                    void* stream);
+
+/*
+ * Decode attention with a sliding window and sinks over the static caches of
+ * decode_attn_fwd: the visible rows are those of decode_attn_paged_fwd, with
+ * window >= 1 (else DA_ERR_SHAPE), so a step reads at most window + sinks rows
+ * however long the prefix is. kv_len[b] == 0 gives zeros; kv_len[b] < 0 or >
+ * capacity gives NaN and DA_DEVERR_KV_LEN.
+ */
+DA_API int decode_attn_window_fwd(const void* q, const void* k_cache, const void* v_cache, const int32_t* kv_len,
+                    int B, int n_head, int n_kv_head, int head_dim, int capacity, int window, int sinks, float scale,
+                    void* out, void* workspace, size_t workspace_bytes, int dtype, int32_t* err_flag, void* stream);
 
 #ifdef __cplusplus
 }
