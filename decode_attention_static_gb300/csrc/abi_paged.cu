@@ -55,12 +55,10 @@ int run_attention(CacheAttnParams p, int head_dim, bool e4m3, float scale, void*
   int sms = 0;
   if (current_device_sms(&sms) != cudaSuccess) return DA_ERR_CUDA;
   const size_t need = cache_attn_workspace_bytes(sms, p.group, head_dim);
-  if (need > 0) {
-    if (!workspace || workspace_bytes < need) return DA_ERR_WORKSPACE;
-    if (!aligned(workspace, 16)) return DA_ERR_ALIGN;
-    p.counters = static_cast<unsigned int*>(workspace);
-    p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kCounterBytes);
-  }
+  if (!workspace || workspace_bytes < need) return DA_ERR_WORKSPACE;
+  if (!aligned(workspace, 16)) return DA_ERR_ALIGN;
+  p.counters = static_cast<unsigned int*>(workspace);
+  p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kCounterBytes);
   p.qscale = scale * kLog2e;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (!record_timing_before(st)) return DA_ERR_CUDA;
@@ -160,8 +158,7 @@ int append_paged(void* k_pages, void* v_pages, float* k_scale, float* v_scale, b
 }  // namespace
 
 size_t cache_attn_workspace_bytes(int sms, int group, int head_dim) {
-  (void)sms, (void)group, (void)head_dim;
-  return 0;
+  return kCounterBytes + (size_t)cache_attn_ctas(sms) * 2 * cache_attn_slot_floats(group, head_dim) * sizeof(float);
 }
 
 }  // namespace da

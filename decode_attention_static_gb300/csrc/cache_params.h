@@ -54,7 +54,15 @@ struct AppendPagedParams {
   int32_t* err_flag;       // may be null
 };
 
-// Scratch of the attention: arrival counters and partial states.
+// CTAs of an attention launch: two for each SM, at most 512 (cache_attn.cuh).
+inline int cache_attn_ctas(int sms) { return 2 * sms < 512 ? 2 * sms : 512; }
+// Floats of a partial state: acc [group][D], m [group], l [group], in whole
+// 16-byte vectors.
+__host__ __device__ inline int cache_attn_slot_floats(int group, int head_dim) {
+  return group * head_dim + (2 * group + 3) / 4 * 4;
+}
+// Scratch of the attention: a fixed region of arrival counters (the one of
+// the other decode kernels), then two partial states for each CTA.
 size_t cache_attn_workspace_bytes(int sms, int group, int head_dim);
 cudaError_t launch_cache_attn(const CacheAttnParams& p, int dtype, int head_dim, bool e4m3, int sms,
                               cudaStream_t stream);

@@ -29,8 +29,8 @@ def attend(q, k, v, scale):
     by 2^-25 max|q| sum|k|, and the score's two roundings and the base-2
     exponential by 2^-22 |x| + 2^-20. The sum over n rows, 16 to a step and in
     up to 2 x 152 x 8 parts, errs by (n / 16 + 64) 2^-23 of sum p|v| (a partial
-    sum never exceeds it), and weights held in two 11-bit pieces by
-    2^-20 of it."""
+    sum never exceeds it), and weights held in two 8-bit pieces by half a step
+    of the second, 2^-18, of it."""
     H, D = q.shape
     Hkv, n, _ = k.shape
     qg = q.view(Hkv, H // Hkv, D)
@@ -42,7 +42,7 @@ def attend(q, k, v, scale):
     peak = qg.abs().amax(-1, keepdim=True) * k.abs().sum(-1).amax(-1)[:, None, None]
     dx = abs(scale) * ((D + 8) * 2.0 ** -23 * size + 2.0 ** -25 * peak)
     dx = dx + 2.0 ** -22 * x.abs().amax(-1, keepdim=True) + 2.0 ** -20
-    slack = (2.1 * dx + (n / 16 + 64) * 2.0 ** -23 + 2.0 ** -20) * mass
+    slack = (2.1 * dx + (n / 16 + 64) * 2.0 ** -23 + 2.0 ** -18) * mass
     return out, slack.reshape(H, D)
 
 
