@@ -41,9 +41,7 @@
 namespace da {
 
 constexpr int kHeads = 8;        // columns of the matrix instruction
-constexpr int kTileRows = 16;
-constexpr int kMaxCtas = 512;    // parts of one group, at most
-constexpr int kCtasPerSm = 2;
+constexpr int kMaxCtas = 256;    // one for each SM; parts of one group, at most
 constexpr float kLazy = 8.f;     // m is raised when a score passes it by this (log2)
 // fp16 weights are 2^(x' - m + 7): at most 2^15, inside the type's range, and
 // 2^-32 of the largest one is still held. bf16 has fp32's range: no lift.
@@ -51,23 +49,27 @@ constexpr float kLiftF16 = 7.f;
 
 template <bool E4M3, int D>
 struct CacheAttnShape {
-  static constexpr int kWarps = 4;
+  static constexpr int kWarps = 8;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kRowBytes = E4M3 ? D : 2 * D;
-  static constexpr int kTileBytes = kTileRows * kRowBytes;
+  static constexpr int kRows = kRowBytes > 128 ? 16 : 32;  // of a tile, in pieces of 16
+  static constexpr int kTileBytes = kRows * kRowBytes;
   static constexpr int kStageBytes = 2 * kTileBytes;  // K tile, V tile
-  static constexpr int kStages = 24576 / kStageBytes < 8 ? 24576 / kStageBytes : 8;
+  static constexpr int kStages = 24576 / kStageBytes;
   static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
   static constexpr int kMergeFloats = kWarps * kHeads * D;
-  static constexpr int kMergeBytes = (kMergeFloats > kMaxCtas * kHeads ? kMergeFloats : kMaxCtas * kHeads) * 4;
-  static constexpr int kMetaOffset = kRingBytes + kMergeBytes;  // per warp and stage: k scale, v scale, bad page
-  static constexpr int kStatOffset = kMetaOffset + kWarps * kStages * 16;
+  static constexpr int kMergeBytes = kMergeFloats * 4;
+  static constexpr int kMetaOffset = kRingBytes + kMergeBytes;
+  static constexpr int kMetaBytes = 32;  // of a stage: K and V scale of each piece, bad pages
+  static constexpr int kStatOffset = kMetaOffset + kWarps * kStages * kMetaBytes;
   // (m, l) of each warp, factors, group sums; schedule words
   static constexpr int kStatFloats = 2 * kWarps * kHeads + kWarps * kHeads + 2 * kHeads;
   static constexpr int kWordsOffset = kStatOffset + kStatFloats * 4;
-  static constexpr int kSmemBytes = kWordsOffset + (2 * kWarps + 8) * 8;
+  static constexpr int kSmemBytes = kWordsOffset + (kWarps + 4) * 8;
   static_assert(kStages >= 3, "a ring of at least three stages");
-  static_assert(kCtasPerSm * (kSmemBytes + 1024) <= 228 * 1024, "shared memory of an SM");
+  static_assert(kSmemBytes <= 227 * 1024, "shared memory of a CTA");
+  static_assert(kMaxCtas * kHeads * 4 + kThreads * 16 <= kMergeBytes, "the join's factors and sums fit the merge buffer");
+  static_assert(kHeads * (D / 4) <= kThreads && kHeads <= kWarps, "a thread for each output vector, a warp for each head");
 };
 
 // Byte offset of 16-byte chunk c of row r in a tile: chunks are permuted
@@ -95,8 +97,8 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
 __device__ __forceinline__ void copy16_or_zero(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void copy4_or_zero(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -169,49 +171,51 @@ __device__ __forceinline__ uint32_t split_pair(float a, float b, uint32_t* rest)
 }
 
 // Tiles of one sequence: visible rows [0, s0) and [w0, len). Tile i < sink_tiles
-// is rows [16 i, 16 i + 16); the others start at row 16 first_tile.
+// starts at row ROWS i; the others follow from row ROWS first_tile on.
 struct SequenceTiles {
   int len, w0, s0, sink_tiles, first_tile, tiles;
 };
 
-// -1: the length is out of range.
+// Number of tiles (0: no visible row), or -1 for a length out of range.
+template <int ROWS>
 __device__ __forceinline__ int tiles_of(const CacheAttnParams& p, int len, SequenceTiles* s) {
-  if (len < 0 || len > p.max_len) {
-    s->tiles = 0;
-    return -1;
-  }
+  s->tiles = 0;
+  if (len < 0 || len > p.max_len) return -1;
   s->len = len;
   s->w0 = (p.window > 0 && len > p.window) ? len - p.window : 0;
   s->s0 = min(p.sinks, s->w0);
-  s->first_tile = s->w0 / kTileRows;
+  s->first_tile = s->w0 / ROWS;
   // a sink tile that the window reaches into belongs to the window's tiles
-  s->sink_tiles = min((s->s0 + kTileRows - 1) / kTileRows, s->first_tile);
-  s->tiles = len == 0 ? 0 : s->sink_tiles + (len + kTileRows - 1) / kTileRows - s->first_tile;
+  s->sink_tiles = min((s->s0 + ROWS - 1) / ROWS, s->first_tile);
+  if (len > 0) s->tiles = s->sink_tiles + (len + ROWS - 1) / ROWS - s->first_tile;
   return s->tiles;
 }
 
+template <int ROWS>
 __device__ __forceinline__ int tile_row(const SequenceTiles& s, int i) {
-  return (i < s.sink_tiles ? i : i - s.sink_tiles + s.first_tile) * kTileRows;
+  return (i < s.sink_tiles ? i : i - s.sink_tiles + s.first_tile) * ROWS;
 }
 
-// Bit r: row row0 + r is visible.
+// Bit r: row row0 + r is visible (some row of a tile of the list is).
+template <int ROWS>
 __device__ __forceinline__ uint32_t tile_mask(const SequenceTiles& s, int row0) {
-  const int end = min(s.len - row0, kTileRows);                       // >= 1
-  uint32_t mask = 0xffffu >> (kTileRows - end);
+  constexpr uint32_t kFull = 0xffffffffu >> (32 - ROWS);
+  const int end = min(s.len - row0, ROWS);
+  uint32_t mask = kFull >> (ROWS - end);
   if (row0 < s.w0) {
-    const int gap_lo = max(s.s0 - row0, 0), gap_hi = min(s.w0 - row0, kTileRows);
-    if (gap_hi > gap_lo) mask &= ~((0xffffu >> (kTileRows - (gap_hi - gap_lo))) << gap_lo);
+    const int lo = max(s.s0 - row0, 0), hi = min(s.w0 - row0, ROWS);
+    if (hi > lo) mask &= ~((kFull >> (ROWS - (hi - lo))) << lo);
   }
   return mask;
 }
 
 template <typename T, bool E4M3, int D>
-__global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, kCtasPerSm)
-    cache_attn_kernel(const CacheAttnParams p) {
+__global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_attn_kernel(const CacheAttnParams p) {
   using Sh = CacheAttnShape<E4M3, D>;
   constexpr bool kBf16 = !E4M3 && Storage<T>::kBf16;  // type of the matrix operands
   constexpr float kLift = kBf16 ? 0.f : kLiftF16;
-  constexpr int kW = Sh::kWarps, kS = Sh::kStages, kSteps = D / 16;
+  constexpr int kW = Sh::kWarps, kS = Sh::kStages, kSteps = D / 16, kRows = Sh::kRows, kHalves = kRows / 16;
+  constexpr uint32_t kFull = 0xffffffffu >> (32 - kRows);
   extern __shared__ __align__(128) uint8_t smem[];
   float* merge = reinterpret_cast<float*>(smem + Sh::kRingBytes);
   float* sm_m = reinterpret_cast<float*>(smem + Sh::kStatOffset);  // [kW][8]
@@ -223,15 +227,18 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, kCtasPerSm)
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, gr = lane >> 2, tq = lane & 3;
 
   pdl_wait();
+  pdl_trigger();  // the next grid can take the SMs as they fall free; it waits for this one's memory
 
-  // --- the list of tiles, and this CTA's share [lo, hi) of it
-  int64_t total = 0;
+  // --- the list of tiles, and this CTA's share [lo, hi) of it: one pass over
+  // the lengths for its size, and, for more sequences than threads, a second
+  // one for the sequence that holds `lo`
+  int64_t total = 0, mine = 0, own = 0;  // tiles before this thread's sequence (of the last pass), and its own
   for (int base = 0; base < p.B; base += Sh::kThreads) {
     const int b = base + tid;
-    SequenceTiles s;
     int n = 0;
     if (b < p.B) {
-      n = tiles_of(p, p.kv_len[b], &s);
+      SequenceTiles s;
+      n = tiles_of<kRows>(p, p.kv_len[b], &s);
       if (n <= 0 && b % gridDim.x == blockIdx.x) {
         // no visible row: zeros; no valid length: NaN
         const uint32_t fill = n < 0 ? (uint32_t)Storage<T>::kNaN * 0x10001u : 0u;
@@ -241,68 +248,81 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, kCtasPerSm)
       }
       n = max(n, 0);
     }
-    int64_t sum = n;
+    own = (int64_t)n * p.n_kv_head;
+    int64_t sum = own;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) words[warp] = sum;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += v;
+    }
+    if (base) __syncthreads();  // the words of the pass before have been read
+    if (lane == 31) words[warp] = sum;
     __syncthreads();
+    mine = total + sum - own;
 #pragma unroll
-    for (int w = 0; w < kW; ++w) total += words[w];
-    __syncthreads();
+    for (int w = 0; w < kW; ++w) {
+      if (w < warp) mine += words[w];
+      total += words[w];
+    }
   }
-  total *= p.n_kv_head;
   // at least one tile for every warp
   const int64_t ctas = min((int64_t)gridDim.x, (total + kW - 1) / kW);
   if ((int64_t)blockIdx.x >= ctas) return;
   const int64_t lo = blockIdx.x * total / ctas, hi = (blockIdx.x + 1) * total / ctas;
-  {
+  if (p.B > Sh::kThreads) {
     int64_t before = 0;
-    for (int base = 0; base < p.B; base += Sh::kThreads) {
+    for (int base = 0; before <= lo; base += Sh::kThreads) {
       const int b = base + tid;
       SequenceTiles s;
-      const int64_t n = b < p.B ? (int64_t)max(tiles_of(p, p.kv_len[b], &s), 0) * p.n_kv_head : 0;
-      int64_t sum = n;
+      own = b < p.B ? (int64_t)max(tiles_of<kRows>(p, p.kv_len[b], &s), 0) * p.n_kv_head : 0;
+      int64_t sum = own;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int64_t v = __shfl_up_sync(0xffffffffu, sum, o);
         if (lane >= o) sum += v;
       }
+      __syncthreads();
       if (lane == 31) words[warp] = sum;
       __syncthreads();
-      int64_t mine = before + sum - n;
+      mine = before + sum - own;
 #pragma unroll
       for (int w = 0; w < kW; ++w) {
         if (w < warp) mine += words[w];
         before += words[w];
       }
-      if (n > 0 && mine <= lo && lo < mine + n) {
+      if (mine <= lo && lo < mine + own) {
         words[kW] = b;
         words[kW + 1] = mine;
       }
-      __syncthreads();
-      if (before > lo) break;
     }
+  } else if (mine <= lo && lo < mine + own) {
+    words[kW] = tid;
+    words[kW + 1] = mine;
   }
+  __syncthreads();
   int b = (int)words[kW];
   SequenceTiles seq;
-  tiles_of(p, p.kv_len[b], &seq);
-  int g, first_in_group;  // group of list position `lo`, and its place there
+  tiles_of<kRows>(p, p.kv_len[b], &seq);
+  int g, tile;  // group of list position `lo`, and its place there
   {
     const int64_t in = lo - words[kW + 1];
     g = (int)(in / seq.tiles);
-    first_in_group = (int)(in - (int64_t)g * seq.tiles);
+    tile = (int)(in - (int64_t)g * seq.tiles);
   }
 
-  // --- this warp's loads
+  // --- this warp's loads. A tile is kHalves pieces of 16 rows, each inside one
+  // page; with two, either half of the warp looks up and copies its own.
+  constexpr int kChunks = Sh::kRowBytes / 16, kLanes = 32 / kHalves, kCopies = 16 * kChunks / kLanes;
+  const int half = kHalves == 2 ? lane >> 4 : 0, sub = lane % kLanes;
   const uint32_t ring = smem_addr(smem) + warp * kS * Sh::kStageBytes;
-  const uint32_t meta = smem_addr(smem + Sh::kMetaOffset) + warp * kS * 16;
-  constexpr int kChunks = Sh::kRowBytes / 16, kCopies = kTileRows * kChunks / 32;
-  // the tile to load next, its page number on the way
-  SequenceTiles lseq = seq;
-  int lb = b, lg = g, li = first_in_group, lrow = 0, lpage = 0;
-  int64_t lat = lo;  // list position of (lb, lg, li)
+  const uint32_t meta = smem_addr(smem + Sh::kMetaOffset) + warp * kS * Sh::kMetaBytes;
+  SequenceTiles lseq = seq;  // the tile to load next, its page number on the way
+  int lb = b, lg = g, li = tile, lrow = 0, lpage = 0;
+  uint32_t lmask = 0;  // 0: no tile is left
+  int64_t lat = lo;
   auto look_up = [&](int step) {  // moves on by `step` tiles
     lat += step;
+    lmask = 0;
     if (lat >= hi) return;
     li += step;
     while (li >= lseq.tiles) {
@@ -310,47 +330,55 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, kCtasPerSm)
       if (++lg == p.n_kv_head) {
         lg = 0;
         do ++lb;
-        while (tiles_of(p, p.kv_len[lb], &lseq) <= 0);
+        while (tiles_of<kRows>(p, p.kv_len[lb], &lseq) <= 0);
       }
     }
-    lrow = tile_row(lseq, li);
-    lpage = p.table ? p.table[(int64_t)lb * p.max_pages + (lrow >> p.page_shift)] : lb;
-  };
-  auto issue = [&](int stage, int row0, int page, uint32_t mask, int head) {
-    const bool bad = page < 0 || page >= p.num_pages;
-    if (bad) {
-      page = 0;
-      mask = 0;
+    const int row0 = tile_row<kRows>(lseq, li);
+    lmask = tile_mask<kRows>(lseq, row0);
+    lrow = row0 + 16 * half;
+    if (p.table) {
+      // (a piece with no visible row may lie past the table)
+      lpage = (kHalves == 1 || ((lmask >> (16 * half)) & 0xffffu))
+                  ? p.table[(int64_t)lb * p.max_pages + (lrow >> p.page_shift)] : 0;
+    } else {
+      lpage = lb;
     }
+  };
+  auto issue = [&](int stage, int row, int page, uint32_t mask, int head) {
+    const bool bad = page < 0 || page >= p.num_pages;
+    if (bad) page = 0;
     const int64_t block = (int64_t)page * p.n_kv_head + head;
-    const int64_t at = (block * p.page_rows + (row0 & (p.table ? p.page_rows - 1 : -1))) * Sh::kRowBytes;
+    const int64_t at = (block * p.page_rows + (row & (p.table ? p.page_rows - 1 : -1))) * Sh::kRowBytes + sub * 16;
     const uint8_t* ksrc = p.k + at;
     const uint8_t* vsrc = p.v + at;
-    const uint32_t dst = ring + stage * Sh::kStageBytes;
-    if (mask == 0xffffu) {
+    const uint32_t dst = ring + stage * Sh::kStageBytes + half * 16 * Sh::kRowBytes;
+    const uint32_t rows = bad ? 0u : (mask >> (16 * half)) & 0xffffu;
+    if (__all_sync(0xffffffffu, rows == 0xffffu)) {
 #pragma unroll
       for (int j = 0; j < kCopies; ++j) {
-        const int x = lane + 32 * j;
+        const int x = sub + kLanes * j;
         const uint32_t d = dst + chunk_offset<Sh::kRowBytes>(x / kChunks, x % kChunks);
-        copy16(d, ksrc + x * 16);
-        copy16(d + Sh::kTileBytes, vsrc + x * 16);
+        copy16(d, ksrc + kLanes * j * 16);
+        copy16(d + Sh::kTileBytes, vsrc + kLanes * j * 16);
       }
     } else {
       for (int j = 0; j < kCopies; ++j) {
-        const int x = lane + 32 * j, r = x / kChunks;
-        const bool on = (mask >> r) & 1;
+        const int x = sub + kLanes * j, r = x / kChunks;
+        const bool on = (rows >> r) & 1;
         const uint32_t d = dst + chunk_offset<Sh::kRowBytes>(r, x % kChunks);
-        copy16_or_zero(d, on ? ksrc + x * 16 : p.k, on ? 16 : 0);
-        copy16_or_zero(d + Sh::kTileBytes, on ? vsrc + x * 16 : p.v, on ? 16 : 0);
+        copy16_or_zero(d, on ? ksrc + kLanes * j * 16 : p.k, on ? 16 : 0);
+        copy16_or_zero(d + Sh::kTileBytes, on ? vsrc + kLanes * j * 16 : p.v, on ? 16 : 0);
       }
     }
+    const uint32_t m = meta + stage * Sh::kMetaBytes;
     if constexpr (E4M3) {
-      if (lane < 2) copy4(meta + stage * 16 + lane * 4, (lane ? p.v_scale : p.k_scale) + block);
+      // (the scales of a piece without rows are zeros)
+      if (sub < 2) copy4_or_zero(m + half * 8 + sub * 4, (sub ? p.v_scale : p.k_scale) + block, rows ? 4 : 0);
     }
-    if (lane == 2) asm volatile("st.shared.u32 [%0], %1;" ::"r"(meta + stage * 16 + 8), "r"((uint32_t)bad) : "memory");
-    if (bad && lane == 0 && p.err_flag) atomicOr(p.err_flag, kErrPage);
+    if (sub == 2) asm volatile("st.shared.u32 [%0], %1;" ::"r"(m + 16 + half * 4), "r"((uint32_t)bad) : "memory");
+    if (bad && sub == 0 && p.err_flag) atomicOr(p.err_flag, kErrPage);
   };
-  int put = 0;  // stage that the next load goes to
+  int put = kS - 1;  // stage that the next load goes to
   {
     // the first kS - 1 tiles: their page numbers are looked up together
     int rows[kS - 1], pages[kS - 1], heads[kS - 1];
@@ -361,21 +389,19 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, kCtasPerSm)
       rows[j] = lrow;
       pages[j] = lpage;
       heads[j] = lg;
-      masks[j] = lat < hi ? tile_mask(lseq, lrow) : 0;
+      masks[j] = lmask;
     }
 #pragma unroll
     for (int j = 0; j < kS - 1; ++j) {
       if (masks[j]) issue(j, rows[j], pages[j], masks[j], heads[j]);
       copy_commit();
     }
-    put = kS - 1;
     look_up(kW);
   }
 
   // --- group by group
   int64_t at = lo;  // list position of the next tile to compute
   int get = 0;      // stage of this warp's next tile
-  int tile = first_in_group;
   int turn = warp;  // tiles until this warp's next one
   while (at < hi) {
     const int here = (int)min((int64_t)(seq.tiles - tile), hi - at);  // tiles of the group in this share
@@ -437,51 +463,69 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, kCtasPerSm)
     for (int k = 0; k < kSteps; ++k) o[k][0] = o[k][1] = o[k][2] = o[k][3] = 0.f;
 
     for (; turn < here; turn += kW) {
-      const int row0 = tile_row(seq, tile + turn);
-      const uint32_t mask = tile_mask(seq, row0);
+      const uint32_t mask = tile_mask<kRows>(seq, tile_row<kRows>(seq, tile + turn));
       copy_wait<kS - 2>();
       __syncwarp();
       // refill the stage that the tile before this one has left
-      if (lat < hi) {
-        issue(put, lrow, lpage, tile_mask(lseq, lrow), lg);
+      if (lmask) {
+        issue(put, lrow, lpage, lmask, lg);
         look_up(kW);
       }
       copy_commit();
       put = put + 1 == kS ? 0 : put + 1;
-      const uint32_t stage = ring + get * Sh::kStageBytes;
-      float ks = 1.f, vs = 1.f;
-      uint32_t bad;
-      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(bad) : "r"(meta + get * 16 + 8));
-      if constexpr (E4M3) asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(ks), "=f"(vs) : "r"(meta + get * 16));
+      const uint32_t stage = ring + get * Sh::kStageBytes, m = meta + get * Sh::kMetaBytes;
       get = get + 1 == kS ? 0 : get + 1;
+      uint32_t bad[2];
+      float scales[4];  // K and V of either piece
+      asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(bad[0]), "=r"(bad[1]) : "r"(m + 16));
+      if constexpr (E4M3)
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(scales[0]), "=f"(scales[1]), "=f"(scales[2]), "=f"(scales[3])
+                     : "r"(m));
 
-      // scores: rows gr and gr + 8, heads 2 tq and 2 tq + 1
-      float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
+      // scores: rows gr and gr + 8 of each piece, heads 2 tq and 2 tq + 1
+      float x[kHalves][4];
       const int mr = (lane & 7) + ((lane >> 3) & 1) * 8;
-      if constexpr (!E4M3) {
 #pragma unroll
-        for (int k = 0; k < kSteps; ++k) {
-          uint32_t a[4];
-          ldmatrix_x4(stage + chunk_offset<Sh::kRowBytes>(mr, 2 * k + (lane >> 4)), a);
-          mma_16x8x16<kBf16>(k & 1 ? s2 : s, a[0], a[1], a[2], a[3], qb[k][0], qb[k][1]);
+      for (int i = 0; i < kHalves; ++i) {
+        const uint32_t kst = stage + i * 16 * Sh::kRowBytes;
+        float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
+        if constexpr (!E4M3) {
+#pragma unroll
+          for (int k = 0; k < kSteps; ++k) {
+            uint32_t a[4];
+            ldmatrix_x4(kst + chunk_offset<Sh::kRowBytes>(mr, 2 * k + (lane >> 4)), a);
+            mma_16x8x16<kBf16>(k & 1 ? s2 : s, a[0], a[1], a[2], a[3], qb[k][0], qb[k][1]);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < kSteps; k += 2) {
+            uint32_t a[4];
+            ldmatrix_x4(kst + chunk_offset<Sh::kRowBytes>(mr, k + (lane >> 4)), a);
+            mma_16x8x16<false>(s, e4m3_low(a[0]), e4m3_low(a[1]), e4m3_high(a[0]), e4m3_high(a[1]), qb[k][0],
+                               qb[k][1]);
+            mma_16x8x16<false>(s2, e4m3_low(a[2]), e4m3_low(a[3]), e4m3_high(a[2]), e4m3_high(a[3]), qb[k + 1][0],
+                               qb[k + 1][1]);
+          }
         }
-      } else {
+        const float f0 = E4M3 ? scale0 * scales[2 * i] : scale0, f1 = E4M3 ? scale1 * scales[2 * i] : scale1;
+        x[i][0] = (s[0] + s2[0]) * f0;
+        x[i][1] = (s[1] + s2[1]) * f1;
+        x[i][2] = (s[2] + s2[2]) * f0;
+        x[i][3] = (s[3] + s2[3]) * f1;
+      }
+      if (mask != kFull) {
 #pragma unroll
-        for (int k = 0; k < kSteps; k += 2) {
-          uint32_t a[4];
-          ldmatrix_x4(stage + chunk_offset<Sh::kRowBytes>(mr, k + (lane >> 4)), a);
-          mma_16x8x16<false>(s, e4m3_low(a[0]), e4m3_low(a[1]), e4m3_high(a[0]), e4m3_high(a[1]), qb[k][0], qb[k][1]);
-          mma_16x8x16<false>(s2, e4m3_low(a[2]), e4m3_low(a[3]), e4m3_high(a[2]), e4m3_high(a[3]), qb[k + 1][0],
-                             qb[k + 1][1]);
+        for (int i = 0; i < kHalves; ++i) {
+          if (!((mask >> (16 * i + gr)) & 1)) x[i][0] = x[i][1] = -INFINITY;
+          if (!((mask >> (16 * i + gr + 8)) & 1)) x[i][2] = x[i][3] = -INFINITY;
         }
       }
-      const float f0 = E4M3 ? scale0 * ks : scale0, f1 = E4M3 ? scale1 * ks : scale1;
-      float x[4] = {(s[0] + s2[0]) * f0, (s[1] + s2[1]) * f1, (s[2] + s2[2]) * f0, (s[3] + s2[3]) * f1};
-      if (mask != 0xffffu) {
-        if (!((mask >> gr) & 1)) x[0] = x[1] = -INFINITY;
-        if (!((mask >> (gr + 8)) & 1)) x[2] = x[3] = -INFINITY;
+      float a0 = fmaxf(x[0][0], x[0][2]), a1 = fmaxf(x[0][1], x[0][3]);
+      if constexpr (kHalves == 2) {
+        a0 = fmaxf(a0, fmaxf(x[1][0], x[1][2]));
+        a1 = fmaxf(a1, fmaxf(x[1][1], x[1][3]));
       }
-      float a0 = fmaxf(x[0], x[2]), a1 = fmaxf(x[1], x[3]);
       if (__any_sync(0xffffffffu, a0 > m0 + kLazy || a1 > m1 + kLazy)) {
 #pragma unroll
         for (int i = 4; i < 32; i <<= 1) {
@@ -505,50 +549,57 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, kCtasPerSm)
           o[k][3] *= c1;
         }
       }
-      x[0] = fast_exp2(x[0] + lift0);
-      x[1] = fast_exp2(x[1] + lift1);
-      x[2] = fast_exp2(x[2] + lift0);
-      x[3] = fast_exp2(x[3] + lift1);
-      l0 += x[0] + x[2];
-      l1 += x[1] + x[3];
-      if (bad) l0 = l1 = NAN;  // a page outside the pool: these heads become NaN
-      uint32_t r0, r1;
-      uint32_t h0 = split_pair<kBf16>(x[0], x[1], &r0), h1 = split_pair<kBf16>(x[2], x[3], &r1);
-      h0 = transpose8x8(h0);
-      h1 = transpose8x8(h1);
-      r0 = transpose8x8(r0);
-      r1 = transpose8x8(r1);
-      const uint32_t vstage = stage + Sh::kTileBytes;
-      if constexpr (!E4M3) {
-        const int vr = (lane & 7) + ((lane >> 4) & 1) * 8;
+      uint32_t ph[kHalves][2], pl[kHalves][2];  // weights as the right operand, in two pieces
 #pragma unroll
-        for (int k = 0; k < kSteps; ++k) {
-          uint32_t a[4];
-          ldmatrix_x4_trans(vstage + chunk_offset<Sh::kRowBytes>(vr, 2 * k + ((lane >> 3) & 1)), a);
-          mma_16x8x16<kBf16>(o[k], a[0], a[1], a[2], a[3], h0, h1);
-          mma_16x8x16<kBf16>(o[k], a[0], a[1], a[2], a[3], r0, r1);
+      for (int i = 0; i < kHalves; ++i) {
+        x[i][0] = fast_exp2(x[i][0] + lift0);
+        x[i][1] = fast_exp2(x[i][1] + lift1);
+        x[i][2] = fast_exp2(x[i][2] + lift0);
+        x[i][3] = fast_exp2(x[i][3] + lift1);
+        l0 += x[i][0] + x[i][2];
+        l1 += x[i][1] + x[i][3];
+        if (bad[i]) l0 = l1 = NAN;  // a page outside the pool: these heads become NaN
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          ph[i][e] = split_pair<kBf16>(x[i][2 * e], x[i][2 * e + 1], &pl[i][e]);
+          ph[i][e] = transpose8x8(ph[i][e]);
+          pl[i][e] = transpose8x8(pl[i][e]);
         }
-      } else {
-        // A transposed 16-bit unit holds two neighbouring elements of a row:
-        // bytes are paired along the rows, and a lane's output rows are
-        // elements 2 gr and 2 gr + 1. The scale multiplies the tile's sum
-        // (and takes the lift out of it: V may be as large as fp32 holds).
-        vs *= 1.f / (1 << (int)kLift);
+      }
+      const int vr = (lane & 7) + ((lane >> 4) & 1) * 8;
 #pragma unroll
-        for (int k = 0; k < kSteps; k += 2) {
-          uint32_t a[4];
-          ldmatrix_x4_trans(vstage + chunk_offset<Sh::kRowBytes>(mr, k + (lane >> 4)), a);
+      for (int i = 0; i < kHalves; ++i) {
+        const uint32_t vst = stage + Sh::kTileBytes + i * 16 * Sh::kRowBytes;
+        if constexpr (!E4M3) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) a[i] = __byte_perm(a[i], 0, 0x3120);
+          for (int k = 0; k < kSteps; ++k) {
+            uint32_t a[4];
+            ldmatrix_x4_trans(vst + chunk_offset<Sh::kRowBytes>(vr, 2 * k + ((lane >> 3) & 1)), a);
+            mma_16x8x16<kBf16>(o[k], a[0], a[1], a[2], a[3], ph[i][0], ph[i][1]);
+            mma_16x8x16<kBf16>(o[k], a[0], a[1], a[2], a[3], pl[i][0], pl[i][1]);
+          }
+        } else {
+          // A transposed 16-bit unit holds two neighbouring elements of a row:
+          // bytes are paired along the rows, and a lane's output rows are
+          // elements 2 gr and 2 gr + 1. The scale multiplies the piece's sum
+          // (and takes the lift out of it: V may be as large as fp32 holds).
+          const float vs = scales[2 * i + 1] * (1.f / (1 << (int)kLift));
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t v0 = e4m3_low(a[2 * i]), v1 = e4m3_high(a[2 * i]), v2 = e4m3_low(a[2 * i + 1]),
-                           v3 = e4m3_high(a[2 * i + 1]);
-            float t[4] = {0.f, 0.f, 0.f, 0.f};
-            mma_16x8x16<false>(t, v0, v1, v2, v3, h0, h1);
-            mma_16x8x16<false>(t, v0, v1, v2, v3, r0, r1);
+          for (int k = 0; k < kSteps; k += 2) {
+            uint32_t a[4];
+            ldmatrix_x4_trans(vst + chunk_offset<Sh::kRowBytes>(mr, k + (lane >> 4)), a);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[k + i][e] = fmaf(vs, t[e], o[k + i][e]);
+            for (int e = 0; e < 4; ++e) a[e] = __byte_perm(a[e], 0, 0x3120);
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              const uint32_t v0 = e4m3_low(a[2 * n]), v1 = e4m3_high(a[2 * n]), v2 = e4m3_low(a[2 * n + 1]),
+                             v3 = e4m3_high(a[2 * n + 1]);
+              float t[4] = {0.f, 0.f, 0.f, 0.f};
+              mma_16x8x16<false>(t, v0, v1, v2, v3, ph[i][0], ph[i][1]);
+              mma_16x8x16<false>(t, v0, v1, v2, v3, pl[i][0], pl[i][1]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[k + n][e] = fmaf(vs, t[e], o[k + n][e]);
+            }
           }
         }
       }
@@ -604,38 +655,45 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, kCtasPerSm)
     }
     __syncthreads();
     const bool whole = here == seq.tiles;
-    const int items = p.group * (D / 4);
-    // shares that hold the group, this one's partial state and the group's counter
+    const int items = p.group * (D / 4);  // outputs in vectors of 4
+    // shares that hold the group, and this one's partial state
     const int64_t group_start = at - tile;
-    int from = 0, parts = 1;
-    float* slots = p.partials;
     const int slot_floats = cache_attn_slot_floats(p.group, D);
+    int from = 0, parts = 1;
     if (!whole) {
       from = (int)(((group_start + 1) * ctas - 1) / total);
       parts = (int)(((group_start + seq.tiles) * ctas - 1) / total) - from + 1;
     }
-    const bool leads = (int)blockIdx.x == from;
-    float* slot = slots + (int64_t)(2 * blockIdx.x + (leads ? 1 : 0)) * slot_floats;
+    // (a CTA has at most two groups that others share: the one it begins in
+    // the middle of, slot 0, and the one it leaves in the middle of, slot 1)
+    auto slot_of = [&](int part) {
+      return p.partials + (int64_t)(part ? 2 * (from + part) : 2 * from + 1) * slot_floats;
+    };
+    float* slot = slot_of((int)blockIdx.x - from);
     uint8_t* out = p.out + ((int64_t)b * p.n_head + (int64_t)g * p.group) * D * 2;
-    for (int i = tid; i < items; i += Sh::kThreads) {
-      const int h = i / (D / 4), d = (i % (D / 4)) * 4;
+    auto store = [&](int i, const float4& r, float l) {
+      const float inv = 1.f / l;
+      *reinterpret_cast<uint2*>(out + i * 8) =
+          make_uint2((uint32_t)Storage<T>::round(r.x * inv) | ((uint32_t)Storage<T>::round(r.y * inv) << 16),
+                     (uint32_t)Storage<T>::round(r.z * inv) | ((uint32_t)Storage<T>::round(r.w * inv) << 16));
+    };
+    auto add = [](float4& r, float f, const float4& v) {
+      r.x = fmaf(f, v.x, r.x);
+      r.y = fmaf(f, v.y, r.y);
+      r.z = fmaf(f, v.z, r.z);
+      r.w = fmaf(f, v.w, r.w);
+    };
+    if (tid < items) {
+      const int h = tid / (D / 4), d = (tid % (D / 4)) * 4;
       float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < kW; ++w) {
-        const float f = sm_f[w * kHeads + h];
-        const float4 v = *reinterpret_cast<const float4*>(merge + (w * kHeads + h) * D + merge_column<D>(h, d));
-        r.x = fmaf(f, v.x, r.x);
-        r.y = fmaf(f, v.y, r.y);
-        r.z = fmaf(f, v.z, r.z);
-        r.w = fmaf(f, v.w, r.w);
-      }
+      for (int w = 0; w < kW; ++w)
+        add(r, sm_f[w * kHeads + h],
+            *reinterpret_cast<const float4*>(merge + (w * kHeads + h) * D + merge_column<D>(h, d)));
       if (whole) {
-        const float inv = 1.f / sm_gl[h];
-        *reinterpret_cast<uint2*>(out + i * 8) =
-            make_uint2((uint32_t)Storage<T>::round(r.x * inv) | ((uint32_t)Storage<T>::round(r.y * inv) << 16),
-                       (uint32_t)Storage<T>::round(r.z * inv) | ((uint32_t)Storage<T>::round(r.w * inv) << 16));
+        store(tid, r, sm_gl[h]);
       } else {
-        __stcg(reinterpret_cast<float4*>(slot + h * D + d), r);
+        __stcg(reinterpret_cast<float4*>(slot) + tid, r);
       }
     }
     if (!whole) {
@@ -643,10 +701,10 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, kCtasPerSm)
         __stcg(slot + p.group * D + tid, sm_gm[tid]);
         __stcg(slot + p.group * D + p.group + tid, sm_gl[tid]);
       }
-      __threadfence();
       __syncthreads();
       unsigned int* arrived = reinterpret_cast<unsigned int*>(&words[kW + 2]);
       if (tid == 0) {
+        __threadfence();  // (cumulative: the CTA's writes before the barrier)
         *arrived = atomicAdd(p.counters + from, 1u);
         __threadfence();
       }
@@ -656,45 +714,53 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, kCtasPerSm)
         // the counter was not zero before this call
         if (tid == 0 && p.err_flag) atomicOr(p.err_flag, kErrWorkspace);
         const uint32_t nan2 = (uint32_t)Storage<T>::kNaN * 0x10001u;
-        for (int i = tid; i < items; i += Sh::kThreads) *reinterpret_cast<uint2*>(out + i * 8) = make_uint2(nan2, nan2);
+        if (tid < items) *reinterpret_cast<uint2*>(out + tid * 8) = make_uint2(nan2, nan2);
       } else if (order == (unsigned int)parts - 1) {
-        // the last to arrive: join the partial states
-        auto slot_of = [&](int part) {
-          return slots + (int64_t)(part ? 2 * (from + part) : 2 * from + 1) * slot_floats;
-        };
-        float* factor = merge;  // [parts][8]
-        for (int h = warp; h < p.group; h += kW) {
-          float mm = -INFINITY, ll = 0.f;
-          for (int s = lane; s < parts; s += 32) mm = fmaxf(mm, __ldcg(slot_of(s) + p.group * D + h));
+        // the last to arrive joins the partial states: the threads share the
+        // vectors, and with fewer vectors than threads also the parts; the
+        // first eight of a thread are on their way while the warps find the
+        // parts' factors
+        float* factor = merge;                        // [parts][8]
+        float4* sums = reinterpret_cast<float4*>(merge + kMaxCtas * kHeads);  // [kThreads]
+        const int crews = Sh::kThreads / items, crew = tid / items, i = tid - crew * items, h = i / (D / 4);
+        const bool busy = crew < crews;
+        float4 v[8], r = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto fetch = [&](int s0) {
 #pragma unroll
-          for (int i = 16; i; i >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, i));
+          for (int j = 0; j < 8; ++j)
+            if (busy && s0 + j * crews < parts)
+              v[j] = __ldcg(reinterpret_cast<const float4*>(slot_of(s0 + j * crews)) + i);
+        };
+        fetch(crew);
+        if (warp < p.group) {
+          float mm = -INFINITY, ll = 0.f;
+          for (int s = lane; s < parts; s += 32) mm = fmaxf(mm, __ldcg(slot_of(s) + p.group * D + warp));
+#pragma unroll
+          for (int k = 16; k; k >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, k));
           for (int s = lane; s < parts; s += 32) {
-            const float mw = __ldcg(slot_of(s) + p.group * D + h), f = mw == mm ? 1.f : fast_exp2(mw - mm);
-            factor[s * kHeads + h] = f;
-            ll += f * __ldcg(slot_of(s) + p.group * D + p.group + h);
+            const float mw = __ldcg(slot_of(s) + p.group * D + warp), f = mw == mm ? 1.f : fast_exp2(mw - mm);
+            factor[s * kHeads + warp] = f;
+            ll += f * __ldcg(slot_of(s) + p.group * D + p.group + warp);
           }
 #pragma unroll
-          for (int i = 16; i; i >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, i);
-          if (lane == 0) sm_gl[h] = ll;
+          for (int k = 16; k; k >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, k);
+          if (lane == 0) sm_gl[warp] = ll;
         }
         __syncthreads();
-        for (int i = tid; i < items; i += Sh::kThreads) {
-          const int h = i / (D / 4);
-          float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-          for (int s = 0; s < parts; ++s) {
-            const float f = factor[s * kHeads + h];
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(slot_of(s) + i * 4));
-            r.x = fmaf(f, v.x, r.x);
-            r.y = fmaf(f, v.y, r.y);
-            r.z = fmaf(f, v.z, r.z);
-            r.w = fmaf(f, v.w, r.w);
-          }
-          const float inv = 1.f / sm_gl[h];
-          *reinterpret_cast<uint2*>(out + i * 8) =
-              make_uint2((uint32_t)Storage<T>::round(r.x * inv) | ((uint32_t)Storage<T>::round(r.y * inv) << 16),
-                         (uint32_t)Storage<T>::round(r.z * inv) | ((uint32_t)Storage<T>::round(r.w * inv) << 16));
+        for (int s0 = crew; busy && s0 < parts;) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (s0 + j * crews < parts) add(r, factor[(s0 + j * crews) * kHeads + h], v[j]);
+          s0 += 8 * crews;
+          if (s0 < parts) fetch(s0);
         }
+        if (crews > 1) {
+          if (busy) sums[tid] = r;
+          __syncthreads();
+          if (crew == 0)
+            for (int c = 1; c < crews; ++c) add(r, 1.f, sums[c * items + i]);
+        }
+        if (crew == 0) store(i, r, sm_gl[h]);
         if (tid == 0) p.counters[from] = 0;  // ready for the next call
       }
     }
@@ -706,7 +772,7 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, kCtasPerSm)
     if (at < hi && ++g == p.n_kv_head) {
       g = 0;
       do ++b;
-      while (tiles_of(p, p.kv_len[b], &seq) <= 0);
+      while (tiles_of<kRows>(p, p.kv_len[b], &seq) <= 0);
     }
   }
   copy_wait<0>();

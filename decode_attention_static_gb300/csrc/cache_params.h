@@ -54,8 +54,8 @@ struct AppendPagedParams {
   int32_t* err_flag;       // may be null
 };
 
-// CTAs of an attention launch: two for each SM, at most 512 (cache_attn.cuh).
-inline int cache_attn_ctas(int sms) { return 2 * sms < 512 ? 2 * sms : 512; }
+// CTAs of an attention launch: one for each SM, at most 256 (cache_attn.cuh).
+inline int cache_attn_ctas(int sms) { return sms < 256 ? sms : 256; }
 // Floats of a partial state: acc [group][D], m [group], l [group], in whole
 // 16-byte vectors.
 __host__ __device__ inline int cache_attn_slot_floats(int group, int head_dim) {
