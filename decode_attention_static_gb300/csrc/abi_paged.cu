@@ -152,7 +152,9 @@ int append_paged(void* k_pages, void* v_pages, float* k_scale, float* v_scale, b
   p.limit = max_pages * page_size;
   if (rope_cos && rope_rows < p.limit) p.limit = rope_rows;
   p.err_flag = err_flag;
-  return launch_append_paged(p, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
+  int sms = 0;
+  if (current_device_sms(&sms) != cudaSuccess) return DA_ERR_CUDA;
+  return launch_append_paged(p, dtype, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
 }
 
 }  // namespace

@@ -2,8 +2,16 @@
 // embedding of the keys (and of the query) on the way; 16-bit pages, or e4m3
 // pages with one power-of-two scale per page and KV head.
 //
-// Both kernels move each byte once and are bound by HBM for prompts and by
-// launch latency for single tokens.
+// A head of a row is D / 16 lanes ("a unit"), each with a 16-byte vector c of the
+// first half and its partner c + D / 16 of the second: a rotation needs no
+// other lane. Every byte of q, k_new, v_new and the pages moves once (but for
+// the table rows, which come from L1 and L2 after the first head): prompts are
+// bound by HBM, single tokens by the chain of dependent loads (sequence,
+// position, page).
+#include <stdint.h>
+
+#include <algorithm>
+
 #include "cache_params.h"
 #include "common.cuh"
 #include "decode_attn.h"
@@ -46,26 +54,30 @@ __device__ __forceinline__ int sequence_of(const AppendPagedParams& p, int t) {
   return lo;
 }
 
-// One 16-byte vector x of the first half of a head and its partner y in the
-// second half, rotated in fp32: each product and the sum rounded on their
-// own, as in rope_vec8.
-template <typename T>
-__device__ __forceinline__ void rotate_pair(const uint4& x, const uint4& y, const AppendPagedParams& p, int position,
-                                            int c, float (&a)[8], float (&b)[8]) {
-  float xf[8], yf[8], c0[8], s0[8], c1[8], s1[8];
-  Storage<T>::unpack(x, xf);
-  Storage<T>::unpack(y, yf);
-  const int D = p.head_dim;
-  load_f32x8(p.cos, position, D, 8 * c, c0);
-  load_f32x8(p.sin, position, D, 8 * c, s0);
-  load_f32x8(p.cos, position, D, D / 2 + 8 * c, c1);
-  load_f32x8(p.sin, position, D, D / 2 + 8 * c, s1);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    a[e] = __fsub_rn(__fmul_rn(xf[e], c0[e]), __fmul_rn(yf[e], s0[e]));
-    b[e] = __fadd_rn(__fmul_rn(yf[e], c1[e]), __fmul_rn(xf[e], s1[e]));
+// cos and sin of one row at a lane's two vectors.
+struct RopeRow {
+  float c0[8], s0[8], c1[8], s1[8];
+  __device__ __forceinline__ void load(const AppendPagedParams& p, int position, int c) {
+    const int D = p.head_dim;
+    load_f32x8(p.cos, position, D, 8 * c, c0);
+    load_f32x8(p.sin, position, D, 8 * c, s0);
+    load_f32x8(p.cos, position, D, D / 2 + 8 * c, c1);
+    load_f32x8(p.sin, position, D, D / 2 + 8 * c, s1);
   }
-}
+  // The vectors x and y, rotated in fp32: each product and the sum rounded on
+  // their own, as in rope_vec8.
+  template <typename T>
+  __device__ __forceinline__ void rotate(const uint4& x, const uint4& y, float (&a)[8], float (&b)[8]) const {
+    float xf[8], yf[8];
+    Storage<T>::unpack(x, xf);
+    Storage<T>::unpack(y, yf);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      a[e] = __fsub_rn(__fmul_rn(xf[e], c0[e]), __fmul_rn(yf[e], s0[e]));
+      b[e] = __fadd_rn(__fmul_rn(yf[e], c1[e]), __fmul_rn(xf[e], s1[e]));
+    }
+  }
+};
 
 template <typename T>
 __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
@@ -76,76 +88,84 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
                     (uint32_t)r[4] | ((uint32_t)r[5] << 16), (uint32_t)r[6] | ((uint32_t)r[7] << 16));
 }
 
-template <typename T>
-__device__ __forceinline__ uint4 nan8() {
-  const uint32_t n = (uint32_t)Storage<T>::kNaN * 0x10001u;
-  return make_uint4(n, n, n, n);
-}
+// One unit of one token: heads h, h + stride, ... of the order K, V, q (from
+// `first` on; K and V go to 16-bit pages). kAtOnce heads are loaded before the
+// token's place is looked up, and the table row serves all of them.
+constexpr int kAtOnce = 4;
 
-// Rotates query head `h` of packed token t into q_out (the D / 16 lanes of a
-// head each take vector c and its partner).
 template <typename T>
-__device__ __forceinline__ void rotate_query(const AppendPagedParams& p, int t, int h, int c, bool ok, int position) {
-  const int row_vecs = p.head_dim / 8, half = row_vecs / 2;
-  const int64_t at = ((int64_t)t * p.n_head + h) * row_vecs + c;
-  uint4* out = reinterpret_cast<uint4*>(p.q_out) + at;
-  if (!ok) {
-    out[0] = nan8<T>();
-    out[half] = nan8<T>();
-    return;
+__device__ __forceinline__ void move_token(const AppendPagedParams& p, int t, int first, int stride, int c) {
+  const int row_vecs = p.head_dim / 8, half = row_vecs / 2, Hkv = p.n_kv_head;
+  const int heads = 2 * Hkv + (p.q ? p.n_head : 0);
+  RopeRow rope;
+  int b = 0, page = 0, position = 0;
+  bool ok = false, page_ok = false;
+  for (int h0 = first, turn = 0; h0 < heads; h0 += kAtOnce * stride, ++turn) {
+    // (q may be rotated in place: plain loads, not the read-only path)
+    uint4 x[kAtOnce], y[kAtOnce];
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+      const int h = h0 + j * stride;
+      if (h < heads) {
+        const uint4* in = h < Hkv       ? reinterpret_cast<const uint4*>(p.k_new) + ((int64_t)t * Hkv + h) * row_vecs
+                          : h < 2 * Hkv ? reinterpret_cast<const uint4*>(p.v_new) + ((int64_t)t * Hkv + h - Hkv) * row_vecs
+                                        : reinterpret_cast<const uint4*>(p.q) + ((int64_t)t * p.n_head + h - 2 * Hkv) * row_vecs;
+        x[j] = in[c];
+        y[j] = in[c + half];
+      }
+    }
+    if (turn == 0) {
+      b = sequence_of(p, t);
+      if (b < 0) return;
+      int from = 0, count = 0, p0 = 0;
+      ok = sequence_rows(p, b, &from, &count, &p0) && t >= from && t < from + count;
+      position = p0 + (t - from);
+      if (!ok && first == 0 && c == 0 && p.err_flag) atomicOr(p.err_flag, kErrPosition);
+      if (ok) {
+        if (p.cos) rope.load(p, position, c);
+        page = p.table[(int64_t)b * p.max_pages + (position >> p.page_shift)];
+        page_ok = page >= 0 && page < p.num_pages;
+        if (!page_ok && first == 0 && c == 0 && p.err_flag) atomicOr(p.err_flag, kErrPage);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+      const int h = h0 + j * stride;
+      if (h >= heads) break;
+      const bool is_v = h >= Hkv && h < 2 * Hkv;
+      if (ok && p.cos && !is_v) {
+        float a[8], bb[8];
+        rope.rotate<T>(x[j], y[j], a, bb);
+        x[j] = pack8<T>(a);
+        y[j] = pack8<T>(bb);
+      }
+      uint4* out;
+      if (h >= 2 * Hkv) {
+        out = reinterpret_cast<uint4*>(p.q_out) + ((int64_t)t * p.n_head + h - 2 * Hkv) * row_vecs;
+        if (!ok) {
+          const uint32_t n = (uint32_t)Storage<T>::kNaN * 0x10001u;
+          x[j] = y[j] = make_uint4(n, n, n, n);
+        }
+      } else {
+        if (!ok || !page_ok) continue;
+        const int64_t row = ((int64_t)page * Hkv + (is_v ? h - Hkv : h)) * p.page_rows + (position & (p.page_rows - 1));
+        out = reinterpret_cast<uint4*>(is_v ? p.v_pages : p.k_pages) + row * row_vecs;
+      }
+      out[c] = x[j];
+      out[c + half] = y[j];
+    }
   }
-  const uint4* in = reinterpret_cast<const uint4*>(p.q) + at;
-  float a[8], b[8];
-  rotate_pair<T>(in[0], in[half], p, position, c, a, b);
-  out[0] = pack8<T>(a);
-  out[half] = pack8<T>(b);
 }
 
-// 16-bit pages: one group of D / 16 lanes per (token, head), heads in the
-// order K, V, q.
+// 16-bit pages: `stride` units for each token.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) append_paged_kernel(const AppendPagedParams p) {
+__global__ void __launch_bounds__(kThreads) append_paged_kernel(const AppendPagedParams p, int stride) {
   pdl_wait();
   pdl_trigger();
-  const int row_vecs = p.head_dim / 8, half = row_vecs / 2;
-  const int heads = 2 * p.n_kv_head + (p.q ? p.n_head : 0);
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  const int c = (int)(i % half);
-  const int64_t item = i / half;
-  const int t = (int)(item / heads);
-  int h = (int)(item % heads);
-  if (t >= p.tokens) return;
-  const int b = sequence_of(p, t);
-  if (b < 0) return;
-  int first = 0, count = 0, p0 = 0;
-  const bool ok = sequence_rows(p, b, &first, &count, &p0) && t >= first && t < first + count;
-  if (!ok && h == 0 && c == 0 && p.err_flag) atomicOr(p.err_flag, kErrPosition);
-  const int position = p0 + (t - first);
-  if (h >= 2 * p.n_kv_head) {
-    rotate_query<T>(p, t, h - 2 * p.n_kv_head, c, ok, position);
-    return;
-  }
-  if (!ok) return;
-  const int page = p.table[(int64_t)b * p.max_pages + (position >> p.page_shift)];
-  if (page < 0 || page >= p.num_pages) {
-    if (h == 0 && c == 0 && p.err_flag) atomicOr(p.err_flag, kErrPage);
-    return;
-  }
-  const bool is_k = h < p.n_kv_head;
-  if (!is_k) h -= p.n_kv_head;
-  const uint4* in =
-      reinterpret_cast<const uint4*>(is_k ? p.k_new : p.v_new) + ((int64_t)t * p.n_kv_head + h) * row_vecs + c;
-  const int64_t row = ((int64_t)page * p.n_kv_head + h) * p.page_rows + (position & (p.page_rows - 1));
-  uint4* out = reinterpret_cast<uint4*>(is_k ? p.k_pages : p.v_pages) + row * row_vecs + c;
-  uint4 x = in[0], y = in[half];
-  if (is_k && p.cos) {
-    float a[8], bb[8];
-    rotate_pair<T>(x, y, p, position, c, a, bb);
-    x = pack8<T>(a);
-    y = pack8<T>(bb);
-  }
-  out[0] = x;
-  out[half] = y;
+  const int half = p.head_dim / 16;
+  const int64_t unit = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / half;
+  const int64_t t = unit / stride;
+  if (t < p.tokens) move_token<T>(p, (int)t, (int)(unit - t * stride), stride, threadIdx.x % half);
 }
 
 // Exponent of the smallest power of two s with peak <= 448 s (448 = 1.75 *
@@ -154,6 +174,10 @@ __device__ __forceinline__ int scale_exponent(float peak) {
   const uint32_t u = __float_as_uint(peak);
   const int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
   return max(e, kMinScaleExponent);
+}
+
+__device__ __forceinline__ float scale_of(float peak) {
+  return __uint_as_float((uint32_t)(scale_exponent(peak) + 127) << 23);
 }
 
 __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
@@ -183,6 +207,16 @@ __device__ __forceinline__ uint32_t rescale_e4m3x4(uint32_t v, float ratio) {
   return to_e4m3x2(a.x * ratio, a.y * ratio) | (to_e4m3x2(b.x * ratio, b.y * ratio) << 16);
 }
 
+// Rows [0, count) of a page and head to a larger scale, by `threads` threads.
+__device__ __forceinline__ void rescale_rows(uint8_t* rows, int bytes, float ratio, int thread, int threads) {
+  for (int i = thread; i < bytes / 16; i += threads) {
+    uint4* at = reinterpret_cast<uint4*>(rows) + i;
+    const uint4 v = *at;
+    *at = make_uint4(rescale_e4m3x4(v.x, ratio), rescale_e4m3x4(v.y, ratio), rescale_e4m3x4(v.z, ratio),
+                     rescale_e4m3x4(v.w, ratio));
+  }
+}
+
 __device__ __forceinline__ float finite_peak(float peak, const float (&f)[8]) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
@@ -192,31 +226,94 @@ __device__ __forceinline__ float finite_peak(float peak, const float (&f)[8]) {
   return peak;
 }
 
-// e4m3 pages: one CTA per (touched page, KV head, K or V); the CTAs after
-// those rotate the query rows.
+// e4m3 pages, one token for each sequence: one unit for each (sequence, K or V
+// head), and `stride` units for the query heads of each token. A unit finds
+// its row's peak with shuffles; where a scale grows, its whole warp rounds the
+// page's older rows.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) append_paged_q8_kernel(const AppendPagedParams p, int page_tasks) {
-  __shared__ int sh[6];
-  __shared__ float sh_peak[kThreads / 32];
+__global__ void __launch_bounds__(kThreads) append_token_q8_kernel(const AppendPagedParams p, int row_ctas, int stride) {
   pdl_wait();
   pdl_trigger();
-  const int row_vecs = p.head_dim / 8, half = row_vecs / 2;
-  const int units = kThreads / half, unit = threadIdx.x / half, c = threadIdx.x % half;
-  const int64_t page_ctas = (int64_t)page_tasks * 2 * p.n_kv_head;
-  if (blockIdx.x >= page_ctas) {
-    const int64_t item = (blockIdx.x - page_ctas) * units + unit;
-    const int t = (int)(item / p.n_head), h = (int)(item % p.n_head);
-    if (t >= p.tokens) return;
-    const int b = sequence_of(p, t);
-    if (b < 0) return;
-    int first = 0, count = 0, p0 = 0;
-    const bool ok = sequence_rows(p, b, &first, &count, &p0) && t >= first && t < first + count;
-    rotate_query<T>(p, t, h, c, ok, p0 + (t - first));
+  const int row_vecs = p.head_dim / 8, half = row_vecs / 2, Hkv = p.n_kv_head, c = threadIdx.x % half;
+  if ((int)blockIdx.x >= row_ctas) {
+    const int64_t unit = ((int64_t)(blockIdx.x - row_ctas) * kThreads + threadIdx.x) / half;
+    const int64_t t = unit / stride;
+    if (t < p.tokens) move_token<T>(p, (int)t, 2 * Hkv + (int)(unit - t * stride), stride, c);
     return;
   }
-  const int task = (int)(blockIdx.x / (2 * p.n_kv_head));
-  const int g = (int)(blockIdx.x % (2 * p.n_kv_head)) >> 1;
-  const bool is_k = (blockIdx.x & 1) == 0;
+  const int64_t unit = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / half;
+  const int b = (int)min(unit / (2 * Hkv), (int64_t)p.B - 1), hk = (int)(unit % (2 * Hkv));
+  const bool live = unit < (int64_t)p.B * 2 * Hkv, is_k = hk < Hkv;
+  const int g = is_k ? hk : hk - Hkv;
+  const uint4* in = reinterpret_cast<const uint4*>(is_k ? p.k_new : p.v_new) + ((int64_t)b * Hkv + g) * row_vecs + c;
+  const uint4 x = in[0], y = in[half];
+  const int position = p.pos[b];
+  const bool ok = position >= 0 && position < p.limit;
+  int page = ok ? p.table[(int64_t)b * p.max_pages + (position >> p.page_shift)] : 0;
+  const bool page_ok = page >= 0 && page < p.num_pages;
+  if (live && hk == 0 && c == 0 && p.err_flag && !(ok && page_ok)) atomicOr(p.err_flag, ok ? kErrPage : kErrPosition);
+  const bool write = live && ok && page_ok;
+  if (!write) page = 0;
+  float a[8], bb[8];
+  if (write && is_k && p.cos) {
+    RopeRow rope;
+    rope.load(p, position, c);
+    rope.rotate<T>(x, y, a, bb);
+  } else {
+    Storage<T>::unpack(x, a);
+    Storage<T>::unpack(y, bb);
+  }
+  float peak = finite_peak(finite_peak(0.f, a), bb);
+  for (int o = half / 2; o; o >>= 1) peak = fmaxf(peak, __shfl_xor_sync(0xffffffffu, peak, o));
+  const int old_rows = position & (p.page_rows - 1);
+  const int64_t block = (int64_t)page * Hkv + g;
+  float* scale_at = (is_k ? p.k_scale : p.v_scale) + block;
+  const float old_scale = write && old_rows > 0 ? *scale_at : 0.f;
+  const float scale = fmaxf(scale_of(peak), old_scale);
+  uint8_t* rows = (is_k ? p.k_pages : p.v_pages) + block * p.page_rows * p.head_dim;
+  unsigned todo = __ballot_sync(0xffffffffu, write && old_rows > 0 && scale != old_scale && c == 0);
+  while (todo) {
+    const int src = __ffs(todo) - 1;
+    todo &= todo - 1;
+    uint8_t* at = reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(rows), src));
+    const int n = __shfl_sync(0xffffffffu, old_rows, src);
+    const float ratio = __shfl_sync(0xffffffffu, old_scale / scale, src);
+    rescale_rows(at, n * p.head_dim, ratio, threadIdx.x % 32, 32);
+  }
+  if (write) {
+    const float inv = 1.f / scale;
+    uint2* out = reinterpret_cast<uint2*>(rows + (int64_t)old_rows * p.head_dim) + c;
+    out[0] = quantise8(a, inv);
+    out[half] = quantise8(bb, inv);
+    if (c == 0) *scale_at = scale;
+  }
+}
+
+// e4m3 pages, prompts: one CTA for each (touched page, chunk of K heads or of V
+// heads). A unit takes R rows of the page (as many units as the page has
+// rows, and where the CTA has more, they take further heads) and HC heads,
+// which stay in registers between the peaks and the rounding: R * HC <= 8
+// rows of 32 bytes a thread, so that two CTAs an SM have 128 KB on the way.
+// The table rows are read again for the rounding (from L1). The CTAs after
+// those rotate the queries.
+template <typename T, int R>
+__global__ void __launch_bounds__(kThreads, 2)
+    append_prompt_q8_kernel(const AppendPagedParams p, int page_tasks, int chunks, int stride) {
+  constexpr int HC = R == 1 ? 4 : 8 / R;
+  __shared__ int sh[2];
+  __shared__ float sh_peak[kThreads / 32][HC];
+  pdl_wait();
+  pdl_trigger();
+  const int row_vecs = p.head_dim / 8, half = row_vecs / 2, Hkv = p.n_kv_head;
+  const int units = kThreads / half, unit = threadIdx.x / half, c = threadIdx.x % half, warp = threadIdx.x / 32;
+  const int64_t page_ctas = (int64_t)page_tasks * 2 * chunks;
+  if (blockIdx.x >= page_ctas) {
+    const int64_t u = (blockIdx.x - page_ctas) * units + unit, t = u / stride;
+    if (t < p.tokens) move_token<T>(p, (int)t, 2 * Hkv + (int)(u - t * stride), stride, c);
+    return;
+  }
+  const int task = (int)(blockIdx.x / (2 * chunks)), part = (int)(blockIdx.x % (2 * chunks));
+  const bool is_k = part < chunks;
   if (threadIdx.x < 32) {
     // the task's sequence and page: tasks are the touched pages in sequence order
     int b_found = -1, j = 0, before = 0;
@@ -244,7 +341,7 @@ __global__ void __launch_bounds__(kThreads) append_paged_q8_kernel(const AppendP
       sh[1] = j;
     }
   }
-  if (task == 0 && g == 0 && is_k && p.err_flag) {
+  if (blockIdx.x == 0 && p.err_flag) {
     for (int b = threadIdx.x; b < p.B; b += kThreads) {
       int first, count, p0;
       if (!sequence_rows(p, b, &first, &count, &p0)) atomicOr(p.err_flag, kErrPosition);
@@ -255,78 +352,121 @@ __global__ void __launch_bounds__(kThreads) append_paged_q8_kernel(const AppendP
   if (b < 0) return;
   int first = 0, count = 0, p0 = 0;
   sequence_rows(p, b, &first, &count, &p0);
-  const int j = (p0 >> p.page_shift) + sh[1];
-  const int lo = max(p0, j << p.page_shift), hi = min(p0 + count, (j + 1) << p.page_shift);
+  const int j = (p0 >> p.page_shift) + sh[1], row0 = j << p.page_shift;
+  const int lo = max(p0, row0), hi = min(p0 + count, row0 + p.page_rows);
+  // rows of this unit: slot, slot + slots, ...; its heads: g0, ..., g0 + HC - 1
+  const int slots = p.page_rows / R, slot = unit % slots;
+  const int g0 = ((part % chunks) * (units / slots) + unit / slots) * HC;
+  const uint4* in = reinterpret_cast<const uint4*>(is_k ? p.k_new : p.v_new);
+  uint4 x[R][HC], y[R][HC];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int position = row0 + slot + i * slots;
+    const int64_t t = (int64_t)first + position - p0;
+#pragma unroll
+    for (int k = 0; k < HC; ++k) {
+      x[i][k] = y[i][k] = make_uint4(0, 0, 0, 0);
+      if (position >= lo && position < hi && g0 + k < Hkv) {
+        const uint4* src = in + (t * Hkv + g0 + k) * row_vecs + c;
+        x[i][k] = src[0];
+        y[i][k] = src[half];
+      }
+    }
+  }
   const int page = p.table[(int64_t)b * p.max_pages + j];
   if (page < 0 || page >= p.num_pages) {
-    if (g == 0 && is_k && threadIdx.x == 0 && p.err_flag) atomicOr(p.err_flag, kErrPage);
+    if (part == 0 && threadIdx.x == 0 && p.err_flag) atomicOr(p.err_flag, kErrPage);
     return;
   }
-  const uint4* in = reinterpret_cast<const uint4*>(is_k ? p.k_new : p.v_new);
   const bool rotate = is_k && p.cos;
-  float a[8], bb[8], peak = 0.f;
-  auto load = [&](int position) {
-    const uint4* src = in + ((int64_t)(first + position - p0) * p.n_kv_head + g) * row_vecs + c;
-    const uint4 x = src[0], y = src[half];
+  float peak[HC];
+#pragma unroll
+  for (int k = 0; k < HC; ++k) peak[k] = 0.f;
+  RopeRow rope;
+  float a[8], bb[8];
+  auto values = [&](int i, int k) {
     if (rotate) {
-      rotate_pair<T>(x, y, p, position, c, a, bb);
+      rope.rotate<T>(x[i][k], y[i][k], a, bb);
     } else {
-      Storage<T>::unpack(x, a);
-      Storage<T>::unpack(y, bb);
+      Storage<T>::unpack(x[i][k], a);
+      Storage<T>::unpack(y[i][k], bb);
     }
   };
-  for (int position = lo + unit; position < hi; position += units) {
-    load(position);
-    peak = finite_peak(finite_peak(peak, a), bb);
-  }
 #pragma unroll
-  for (int o = 16; o; o >>= 1) peak = fmaxf(peak, __shfl_xor_sync(0xffffffffu, peak, o));
-  if (threadIdx.x % 32 == 0) sh_peak[threadIdx.x / 32] = peak;
-  const int old_rows = lo & (p.page_rows - 1);
-  float* scale_at = (is_k ? p.k_scale : p.v_scale) + (int64_t)page * p.n_kv_head + g;
-  const float old_scale = old_rows > 0 ? *scale_at : 0.f;
-  __syncthreads();
+  for (int i = 0; i < R; ++i) {
+    const int position = row0 + slot + i * slots;
+    if (position < lo || position >= hi) continue;
+    if (rotate) rope.load(p, position, c);
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) peak = fmaxf(peak, sh_peak[w]);
-  const float scale = fmaxf(__uint_as_float((uint32_t)(scale_exponent(peak) + 127) << 23), old_scale);
-  uint8_t* rows = (is_k ? p.k_pages : p.v_pages) + ((int64_t)page * p.n_kv_head + g) * p.page_rows * p.head_dim;
-  if (old_rows > 0 && scale != old_scale) {
-    const float ratio = old_scale / scale;
-    for (int i = threadIdx.x; i < old_rows * p.head_dim / 16; i += kThreads) {
-      uint4* at = reinterpret_cast<uint4*>(rows) + i;
-      const uint4 v = *at;
-      *at = make_uint4(rescale_e4m3x4(v.x, ratio), rescale_e4m3x4(v.y, ratio), rescale_e4m3x4(v.z, ratio),
-                       rescale_e4m3x4(v.w, ratio));
+    for (int k = 0; k < HC; ++k) {
+      values(i, k);
+      peak[k] = finite_peak(finite_peak(peak[k], a), bb);
     }
   }
-  const float inv = 1.f / scale;
-  for (int position = lo + unit; position < hi; position += units) {
-    load(position);
-    uint2* out = reinterpret_cast<uint2*>(rows + (int64_t)(position & (p.page_rows - 1)) * p.head_dim) + c;
-    out[0] = quantise8(a, inv);
-    out[half] = quantise8(bb, inv);
+#pragma unroll
+  for (int k = 0; k < HC; ++k) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) peak[k] = fmaxf(peak[k], __shfl_xor_sync(0xffffffffu, peak[k], o));
+    if (threadIdx.x % 32 == 0) sh_peak[warp][k] = peak[k];
   }
-  if (threadIdx.x == 0) *scale_at = scale;
+  const int old_rows = lo - row0;
+  const int64_t block = (int64_t)page * Hkv + g0;
+  float* scale_at = (is_k ? p.k_scale : p.v_scale) + block;
+  float scale[HC], old_scale[HC];
+#pragma unroll
+  for (int k = 0; k < HC; ++k) old_scale[k] = old_rows > 0 && g0 + k < Hkv ? scale_at[k] : 0.f;
+  __syncthreads();
+  const int team = slots * half, team_warps = team / 32, warp0 = warp / team_warps * team_warps;  // (whole warps)
+#pragma unroll
+  for (int k = 0; k < HC; ++k) {
+    float m = 0.f;
+    for (int w = 0; w < team_warps; ++w) m = fmaxf(m, sh_peak[warp0 + w][k]);
+    scale[k] = fmaxf(scale_of(m), old_scale[k]);
+  }
+  uint8_t* pages = (is_k ? p.k_pages : p.v_pages);
+  const int64_t page_bytes = (int64_t)p.page_rows * p.head_dim;
+  if (old_rows > 0) {
+#pragma unroll
+    for (int k = 0; k < HC; ++k)
+      if (g0 + k < Hkv && scale[k] != old_scale[k])
+        rescale_rows(pages + (block + k) * page_bytes, old_rows * p.head_dim, old_scale[k] / scale[k],
+                     threadIdx.x % team, team);
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int position = row0 + slot + i * slots;
+    if (position < lo || position >= hi) continue;
+    if (rotate) rope.load(p, position, c);
+#pragma unroll
+    for (int k = 0; k < HC; ++k) {
+      if (g0 + k >= Hkv) break;
+      values(i, k);
+      const float inv = 1.f / scale[k];
+      uint2* out = reinterpret_cast<uint2*>(pages + (block + k) * page_bytes + (int64_t)(position - row0) * p.head_dim) + c;
+      out[0] = quantise8(a, inv);
+      out[half] = quantise8(bb, inv);
+    }
+  }
+  if (unit % slots == 0 && c == 0) {
+#pragma unroll
+    for (int k = 0; k < HC; ++k)
+      if (g0 + k < Hkv) scale_at[k] = scale[k];
+  }
+}
+
+// Units for each token: one for each head while that fills less than about two
+// waves of the SMs (latency), else kAtOnce heads a unit (the table row is read
+// once for them).
+int units_per_token(int64_t tokens, int heads, int half, int sms) {
+  return tokens * heads * half <= (int64_t)sms * 4096 ? heads : (heads + kAtOnce - 1) / kAtOnce;
 }
 
 }  // namespace
 
-cudaError_t launch_append_paged(const AppendPagedParams& p, int dtype, cudaStream_t stream) {
-  const int half = p.head_dim / 16;
-  int64_t ctas, page_tasks = 0;
-  if (p.k_scale) {
-    // every sequence touches at most one page more than its rows fill
-    page_tasks = p.start ? (int64_t)p.tokens / p.page_rows + 2 * (int64_t)p.B : p.B;
-    if (page_tasks > p.tokens) page_tasks = p.tokens;
-    const int64_t query_items = p.q ? (int64_t)p.tokens * p.n_head : 0;
-    ctas = page_tasks * 2 * p.n_kv_head + (query_items * half + kThreads - 1) / kThreads;
-  } else {
-    const int64_t items = (int64_t)p.tokens * (2 * p.n_kv_head + (p.q ? p.n_head : 0));
-    ctas = (items * half + kThreads - 1) / kThreads;
-  }
-  if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
+cudaError_t launch_append_paged(const AppendPagedParams& p, int dtype, int sms, cudaStream_t stream) {
+  const bool f16 = dtype == DA_F16;
+  const int half = p.head_dim / 16, units = kThreads / half, query_heads = p.q ? p.n_head : 0;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr;
@@ -334,11 +474,45 @@ cudaError_t launch_append_paged(const AppendPagedParams& p, int dtype, cudaStrea
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  if (p.k_scale)
-    return dtype == DA_F16 ? cudaLaunchKernelEx(&cfg, append_paged_q8_kernel<__half>, p, (int)page_tasks)
-                           : cudaLaunchKernelEx(&cfg, append_paged_q8_kernel<__nv_bfloat16>, p, (int)page_tasks);
-  return dtype == DA_F16 ? cudaLaunchKernelEx(&cfg, append_paged_kernel<__half>, p)
-                         : cudaLaunchKernelEx(&cfg, append_paged_kernel<__nv_bfloat16>, p);
+  auto grid = [&](int64_t ctas) {
+    cfg.gridDim = dim3((unsigned)ctas);
+    return ctas <= INT32_MAX;
+  };
+  auto ctas_of = [&](int64_t n) { return (n + units - 1) / units; };
+  if (!p.k_scale) {
+    const int heads = 2 * p.n_kv_head + query_heads, stride = units_per_token(p.tokens, heads, half, sms);
+    if (!grid(ctas_of((int64_t)p.tokens * stride))) return cudaErrorInvalidConfiguration;
+    return f16 ? cudaLaunchKernelEx(&cfg, append_paged_kernel<__half>, p, stride)
+               : cudaLaunchKernelEx(&cfg, append_paged_kernel<__nv_bfloat16>, p, stride);
+  }
+  const int stride = query_heads ? units_per_token(p.tokens, query_heads, half, sms) : 1;
+  const int64_t query_ctas = query_heads ? ctas_of((int64_t)p.tokens * stride) : 0;
+  if (!p.start) {
+    const int64_t rows = ctas_of((int64_t)p.B * 2 * p.n_kv_head);
+    if (!grid(rows + query_ctas)) return cudaErrorInvalidConfiguration;
+    return f16 ? cudaLaunchKernelEx(&cfg, append_token_q8_kernel<__half>, p, (int)rows, stride)
+               : cudaLaunchKernelEx(&cfg, append_token_q8_kernel<__nv_bfloat16>, p, (int)rows, stride);
+  }
+  // n rows touch at most (n - 2) / page + 2 pages
+  const int64_t tasks = std::min<int64_t>((int64_t)p.tokens / p.page_rows + 2 * (int64_t)p.B, p.tokens);
+  const int R = std::max(1, p.page_rows / units), hc = R == 1 ? 4 : 8 / R;
+  const int heads_at_once = units / (p.page_rows / R) * hc;
+  const int chunks = (p.n_kv_head + heads_at_once - 1) / heads_at_once;
+  if (tasks * 2 * chunks > INT32_MAX || !grid(tasks * 2 * chunks + query_ctas)) return cudaErrorInvalidConfiguration;
+  switch (R) {
+    case 1:
+      return f16 ? cudaLaunchKernelEx(&cfg, append_prompt_q8_kernel<__half, 1>, p, (int)tasks, chunks, stride)
+                 : cudaLaunchKernelEx(&cfg, append_prompt_q8_kernel<__nv_bfloat16, 1>, p, (int)tasks, chunks, stride);
+    case 2:
+      return f16 ? cudaLaunchKernelEx(&cfg, append_prompt_q8_kernel<__half, 2>, p, (int)tasks, chunks, stride)
+                 : cudaLaunchKernelEx(&cfg, append_prompt_q8_kernel<__nv_bfloat16, 2>, p, (int)tasks, chunks, stride);
+    case 4:
+      return f16 ? cudaLaunchKernelEx(&cfg, append_prompt_q8_kernel<__half, 4>, p, (int)tasks, chunks, stride)
+                 : cudaLaunchKernelEx(&cfg, append_prompt_q8_kernel<__nv_bfloat16, 4>, p, (int)tasks, chunks, stride);
+    default:
+      return f16 ? cudaLaunchKernelEx(&cfg, append_prompt_q8_kernel<__half, 8>, p, (int)tasks, chunks, stride)
+                 : cudaLaunchKernelEx(&cfg, append_prompt_q8_kernel<__nv_bfloat16, 8>, p, (int)tasks, chunks, stride);
+  }
 }
 
 }  // namespace da

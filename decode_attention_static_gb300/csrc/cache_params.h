@@ -68,7 +68,7 @@ cudaError_t launch_cache_attn(const CacheAttnParams& p, int dtype, int head_dim,
                               cudaStream_t stream);
 cudaError_t launch_cache_attn_f16(const CacheAttnParams& p, int head_dim, bool e4m3, int sms, cudaStream_t stream);
 cudaError_t launch_cache_attn_bf16(const CacheAttnParams& p, int head_dim, bool e4m3, int sms, cudaStream_t stream);
-cudaError_t launch_append_paged(const AppendPagedParams& p, int dtype, cudaStream_t stream);
+cudaError_t launch_append_paged(const AppendPagedParams& p, int dtype, int sms, cudaStream_t stream);
 
 // abi.cu: this host thread's profiling events around a kernel, and the SM
 // count of the current device.
