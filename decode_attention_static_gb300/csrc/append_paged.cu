@@ -11,6 +11,8 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <atomic>
+#include <type_traits>
 
 #include "cache_params.h"
 #include "common.cuh"
@@ -81,11 +83,18 @@ struct RopeRow {
 
 template <typename T>
 __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  uint16_t r[8];
+  uint32_t r[4];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) r[e] = Storage<T>::round(f[e]);
-  return make_uint4((uint32_t)r[0] | ((uint32_t)r[1] << 16), (uint32_t)r[2] | ((uint32_t)r[3] << 16),
-                    (uint32_t)r[4] | ((uint32_t)r[5] << 16), (uint32_t)r[6] | ((uint32_t)r[7] << 16));
+  for (int e = 0; e < 4; ++e) {
+    if constexpr (Storage<T>::kBf16) {
+      const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
+      r[e] = *reinterpret_cast<const uint32_t*>(&v);
+    } else {
+      const __half2 v = __floats2half2_rn(f[2 * e], f[2 * e + 1]);
+      r[e] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+  }
+  return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
 // One unit of one token: heads h, h + stride, ... of the order K, V, q (from
@@ -159,7 +168,7 @@ __device__ __forceinline__ void move_token(const AppendPagedParams& p, int t, in
 
 // 16-bit pages: `stride` units for each token.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) append_paged_kernel(const AppendPagedParams p, int stride) {
+__global__ void __launch_bounds__(kThreads, 2) append_paged_kernel(const AppendPagedParams p, int stride) {
   pdl_wait();
   pdl_trigger();
   const int half = p.head_dim / 16;
@@ -192,12 +201,17 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t v) {
   return __half22float2(*reinterpret_cast<__half2*>(&h));
 }
 
-// 8 values over a scale; non-finite ones become the type's NaN (e4m3 has no
-// infinities).
+// 8 values over a scale. NaN becomes the type's NaN by the conversion;
+// infinities, which would be clamped to 448, only with INFINITIES (e4m3 has
+// none).
+template <bool INFINITIES>
 __device__ __forceinline__ uint2 quantise8(const float (&f)[8], float inv) {
   float x[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] = fabsf(f[e]) < INFINITY ? f[e] * inv : NAN;
+  for (int e = 0; e < 8; ++e) {
+    x[e] = f[e] * inv;
+    if (INFINITIES && fabsf(f[e]) == INFINITY) x[e] = NAN;
+  }
   return make_uint2(to_e4m3x2(x[0], x[1]) | (to_e4m3x2(x[2], x[3]) << 16),
                     to_e4m3x2(x[4], x[5]) | (to_e4m3x2(x[6], x[7]) << 16));
 }
@@ -217,6 +231,31 @@ __device__ __forceinline__ void rescale_rows(uint8_t* rows, int bytes, float rat
   }
 }
 
+// Largest |f| so far; NaN does not count, infinity does.
+__device__ __forceinline__ float peak_of(float peak, const float (&f)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) peak = fmaxf(peak, fabsf(f[e]));
+  return peak;
+}
+
+// The same of 8 packed values.
+template <typename T>
+__device__ __forceinline__ float peak_packed(float peak, const uint4& v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  if constexpr (Storage<T>::kBf16) {
+    __nv_bfloat162 m = __float2bfloat162_rn(0.f);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m = __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[e])));
+    return fmaxf(peak, fmaxf(__low2float(m), __high2float(m)));
+  } else {
+    __half2 m = __float2half2_rn(0.f);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m = __hmax2(m, __habs2(*reinterpret_cast<const __half2*>(&w[e])));
+    return fmaxf(peak, fmaxf(__low2float(m), __high2float(m)));
+  }
+}
+
+// The same of the finite values alone: for heads whose peak is infinity.
 __device__ __forceinline__ float finite_peak(float peak, const float (&f)[8]) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
@@ -263,8 +302,13 @@ __global__ void __launch_bounds__(kThreads) append_token_q8_kernel(const AppendP
     Storage<T>::unpack(x, a);
     Storage<T>::unpack(y, bb);
   }
-  float peak = finite_peak(finite_peak(0.f, a), bb);
+  float peak = peak_of(peak_of(0.f, a), bb);
   for (int o = half / 2; o; o >>= 1) peak = fmaxf(peak, __shfl_xor_sync(0xffffffffu, peak, o));
+  const bool infinities = peak == INFINITY;
+  if (__any_sync(0xffffffffu, infinities)) {
+    peak = finite_peak(finite_peak(0.f, a), bb);
+    for (int o = half / 2; o; o >>= 1) peak = fmaxf(peak, __shfl_xor_sync(0xffffffffu, peak, o));
+  }
   const int old_rows = position & (p.page_rows - 1);
   const int64_t block = (int64_t)page * Hkv + g;
   float* scale_at = (is_k ? p.k_scale : p.v_scale) + block;
@@ -283,37 +327,46 @@ __global__ void __launch_bounds__(kThreads) append_token_q8_kernel(const AppendP
   if (write) {
     const float inv = 1.f / scale;
     uint2* out = reinterpret_cast<uint2*>(rows + (int64_t)old_rows * p.head_dim) + c;
-    out[0] = quantise8(a, inv);
-    out[half] = quantise8(bb, inv);
+    if (infinities) {
+      out[0] = quantise8<true>(a, inv);
+      out[half] = quantise8<true>(bb, inv);
+    } else {
+      out[0] = quantise8<false>(a, inv);
+      out[half] = quantise8<false>(bb, inv);
+    }
     if (c == 0) *scale_at = scale;
   }
 }
 
-// e4m3 pages, prompts: one CTA for each (touched page, chunk of K heads or of V
-// heads). A unit takes R rows of the page (as many units as the page has
-// rows, and where the CTA has more, they take further heads) and HC heads,
-// which stay in registers between the peaks and the rounding: R * HC <= 8
-// rows of 32 bytes a thread, so that two CTAs an SM have 128 KB on the way.
-// The table rows are read again for the rounding (from L1). The CTAs after
-// those rotate the queries.
+// e4m3 pages, prompts: one CTA for each (touched page, K or V, range of chunks
+// of heads). A unit takes R rows of the page (as many units as the page has
+// rows; where the CTA has more, they take further heads) and HC heads of a
+// chunk. A thread's rows of the next chunk are on their way into its own
+// places in shared memory while it finds the peaks of this one and rounds it:
+// nothing is waited for but the peaks, once a chunk.
+__host__ __device__ constexpr int prompt_heads(int R) { return R >= 4 ? 1 : 4 / R; }
+__host__ __device__ constexpr int prompt_smem(int R) { return 2 * kThreads * R * prompt_heads(R) * 32; }
+
 template <typename T, int R>
-__global__ void __launch_bounds__(kThreads, 2)
-    append_prompt_q8_kernel(const AppendPagedParams p, int page_tasks, int chunks, int stride) {
-  constexpr int HC = R == 1 ? 4 : 8 / R;
+__global__ void __launch_bounds__(kThreads, R == 8 ? 1 : 2)
+    append_prompt_q8_kernel(const AppendPagedParams p, int page_tasks, int ranges, int range_chunks, int stride) {
+  constexpr int HC = prompt_heads(R), kWarps = kThreads / 32;
+  extern __shared__ __align__(16) uint4 staged[];  // [2][R * HC][2][kThreads]
   __shared__ int sh[2];
-  __shared__ float sh_peak[kThreads / 32][HC];
+  __shared__ uint32_t sh_peak[2][HC][kWarps];
   pdl_wait();
   pdl_trigger();
   const int row_vecs = p.head_dim / 8, half = row_vecs / 2, Hkv = p.n_kv_head;
-  const int units = kThreads / half, unit = threadIdx.x / half, c = threadIdx.x % half, warp = threadIdx.x / 32;
-  const int64_t page_ctas = (int64_t)page_tasks * 2 * chunks;
+  const int units = kThreads / half, unit = threadIdx.x / half, c = threadIdx.x % half;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int64_t page_ctas = (int64_t)page_tasks * 2 * ranges;
   if (blockIdx.x >= page_ctas) {
     const int64_t u = (blockIdx.x - page_ctas) * units + unit, t = u / stride;
     if (t < p.tokens) move_token<T>(p, (int)t, 2 * Hkv + (int)(u - t * stride), stride, c);
     return;
   }
-  const int task = (int)(blockIdx.x / (2 * chunks)), part = (int)(blockIdx.x % (2 * chunks));
-  const bool is_k = part < chunks;
+  const int task = (int)(blockIdx.x / (2 * ranges)), part = (int)(blockIdx.x % (2 * ranges));
+  const bool is_k = part < ranges;
   if (threadIdx.x < 32) {
     // the task's sequence and page: tasks are the touched pages in sequence order
     int b_found = -1, j = 0, before = 0;
@@ -354,111 +407,174 @@ __global__ void __launch_bounds__(kThreads, 2)
   sequence_rows(p, b, &first, &count, &p0);
   const int j = (p0 >> p.page_shift) + sh[1], row0 = j << p.page_shift;
   const int lo = max(p0, row0), hi = min(p0 + count, row0 + p.page_rows);
-  // rows of this unit: slot, slot + slots, ...; its heads: g0, ..., g0 + HC - 1
-  const int slots = p.page_rows / R, slot = unit % slots;
-  const int g0 = ((part % chunks) * (units / slots) + unit / slots) * HC;
+  // rows of this unit: slot, slot + slots, ...; its heads of chunk n: from
+  // (n * at_once + unit / slots) * HC on
+  const int slots = p.page_rows / R, slot = unit % slots, at_once = units / slots;
+  const int chunk_heads = at_once * HC, chunks = (Hkv + chunk_heads - 1) / chunk_heads;
+  const int begin = (part % ranges) * range_chunks, end = min(begin + range_chunks, chunks);
   const uint4* in = reinterpret_cast<const uint4*>(is_k ? p.k_new : p.v_new);
-  uint4 x[R][HC], y[R][HC];
+  auto place = [&](int stage, int i, int k, int which) {
+    return staged + (((stage * R + i) * HC + k) * 2 + which) * kThreads + threadIdx.x;
+  };
+  auto fetch = [&](int n) {
+    const int g0 = (n * at_once + unit / slots) * HC;
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const int position = row0 + slot + i * slots;
-    const int64_t t = (int64_t)first + position - p0;
+    for (int i = 0; i < R; ++i) {
+      const int position = row0 + slot + i * slots;
+      if (position >= lo && position < hi) {
+        const uint4* src = in + (((int64_t)first + position - p0) * Hkv + g0) * row_vecs + c;
 #pragma unroll
-    for (int k = 0; k < HC; ++k) {
-      x[i][k] = y[i][k] = make_uint4(0, 0, 0, 0);
-      if (position >= lo && position < hi && g0 + k < Hkv) {
-        const uint4* src = in + (t * Hkv + g0 + k) * row_vecs + c;
-        x[i][k] = src[0];
-        y[i][k] = src[half];
+        for (int k = 0; k < HC; ++k) {
+          if (g0 + k < Hkv) {
+            copy16(smem_addr(place(n & 1, i, k, 0)), src + k * row_vecs);
+            copy16(smem_addr(place(n & 1, i, k, 1)), src + k * row_vecs + half);
+          }
+        }
       }
     }
-  }
+    copy_commit();
+  };
+  if (begin < end) fetch(begin);
   const int page = p.table[(int64_t)b * p.max_pages + j];
   if (page < 0 || page >= p.num_pages) {
     if (part == 0 && threadIdx.x == 0 && p.err_flag) atomicOr(p.err_flag, kErrPage);
+    copy_wait<0>();
     return;
   }
   const bool rotate = is_k && p.cos;
-  float peak[HC];
-#pragma unroll
-  for (int k = 0; k < HC; ++k) peak[k] = 0.f;
-  RopeRow rope;
-  float a[8], bb[8];
-  auto values = [&](int i, int k) {
-    if (rotate) {
-      rope.rotate<T>(x[i][k], y[i][k], a, bb);
-    } else {
-      Storage<T>::unpack(x[i][k], a);
-      Storage<T>::unpack(y[i][k], bb);
-    }
-  };
-#pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const int position = row0 + slot + i * slots;
-    if (position < lo || position >= hi) continue;
-    if (rotate) rope.load(p, position, c);
-#pragma unroll
-    for (int k = 0; k < HC; ++k) {
-      values(i, k);
-      peak[k] = finite_peak(finite_peak(peak[k], a), bb);
-    }
-  }
-#pragma unroll
-  for (int k = 0; k < HC; ++k) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) peak[k] = fmaxf(peak[k], __shfl_xor_sync(0xffffffffu, peak[k], o));
-    if (threadIdx.x % 32 == 0) sh_peak[warp][k] = peak[k];
-  }
-  const int old_rows = lo - row0;
-  const int64_t block = (int64_t)page * Hkv + g0;
-  float* scale_at = (is_k ? p.k_scale : p.v_scale) + block;
-  float scale[HC], old_scale[HC];
-#pragma unroll
-  for (int k = 0; k < HC; ++k) old_scale[k] = old_rows > 0 && g0 + k < Hkv ? scale_at[k] : 0.f;
-  __syncthreads();
   const int team = slots * half, team_warps = team / 32, warp0 = warp / team_warps * team_warps;  // (whole warps)
-#pragma unroll
-  for (int k = 0; k < HC; ++k) {
-    float m = 0.f;
-    for (int w = 0; w < team_warps; ++w) m = fmaxf(m, sh_peak[warp0 + w][k]);
-    scale[k] = fmaxf(scale_of(m), old_scale[k]);
-  }
+  const int old_rows = lo - row0;
   uint8_t* pages = (is_k ? p.k_pages : p.v_pages);
   const int64_t page_bytes = (int64_t)p.page_rows * p.head_dim;
-  if (old_rows > 0) {
+  RopeRow rope;
+  float a[8], bb[8];
+  for (int n = begin; n < end; ++n) {
+    const int g0 = (n * at_once + unit / slots) * HC, live = min(HC, Hkv - g0);  // (may be none)
+    if (n + 1 < end) {
+      fetch(n + 1);
+      copy_wait<1>();
+    } else {
+      copy_wait<0>();
+    }
+    auto values = [&](int i, int k) {
+      const uint4 x = *place(n & 1, i, k, 0), y = *place(n & 1, i, k, 1);
+      if (rotate) {
+        rope.rotate<T>(x, y, a, bb);
+      } else {
+        Storage<T>::unpack(x, a);
+        Storage<T>::unpack(y, bb);
+      }
+    };
+    float peak[HC];
+    auto find_peaks = [&](auto finite) {
 #pragma unroll
-    for (int k = 0; k < HC; ++k)
-      if (g0 + k < Hkv && scale[k] != old_scale[k])
-        rescale_rows(pages + (block + k) * page_bytes, old_rows * p.head_dim, old_scale[k] / scale[k],
-                     threadIdx.x % team, team);
-  }
+      for (int k = 0; k < HC; ++k) peak[k] = 0.f;
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const int position = row0 + slot + i * slots;
-    if (position < lo || position >= hi) continue;
-    if (rotate) rope.load(p, position, c);
+      for (int i = 0; i < R; ++i) {
+        const int position = row0 + slot + i * slots;
+        if (position < lo || position >= hi) continue;
+        if (rotate) rope.load(p, position, c);
+#pragma unroll
+        for (int k = 0; k < HC; ++k) {
+          if (k >= live) break;
+          if (!rotate && !decltype(finite)::value) {
+            peak[k] = peak_packed<T>(peak_packed<T>(peak[k], *place(n & 1, i, k, 0)), *place(n & 1, i, k, 1));
+            continue;
+          }
+          values(i, k);
+          peak[k] = decltype(finite)::value ? finite_peak(finite_peak(peak[k], a), bb) : peak_of(peak_of(peak[k], a), bb);
+        }
+      }
+      // (non-negative floats order as their bits do)
+#pragma unroll
+      for (int k = 0; k < HC; ++k) {
+        const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(peak[k]));
+        if (lane == 0) sh_peak[n & 1][k][warp] = m;
+      }
+      __syncthreads();
+      bool infinity = false;
+#pragma unroll
+      for (int k = 0; k < HC; ++k) {
+        const uint32_t v = sh_peak[n & 1][k][lane % kWarps];
+        infinity |= __any_sync(0xffffffffu, v == 0x7f800000u);  // in any team
+        const int w = lane % kWarps - warp0;
+        peak[k] = __uint_as_float(__reduce_max_sync(0xffffffffu, w >= 0 && w < team_warps ? v : 0u));
+      }
+      return infinity;
+    };
+    const int64_t block = (int64_t)page * Hkv + g0;
+    float* scale_at = (is_k ? p.k_scale : p.v_scale) + block;
+    uint8_t* rows = pages + block * page_bytes;
+    float old_scale[HC];
+#pragma unroll
+    for (int k = 0; k < HC; ++k) old_scale[k] = old_rows > 0 && k < live ? scale_at[k] : 0.f;
+    const bool infinities = find_peaks(std::false_type());
+    if (infinities) {
+      __syncthreads();
+      find_peaks(std::true_type());
+    }
+    float scale[HC], inv[HC];
 #pragma unroll
     for (int k = 0; k < HC; ++k) {
-      if (g0 + k >= Hkv) break;
-      values(i, k);
-      const float inv = 1.f / scale[k];
-      uint2* out = reinterpret_cast<uint2*>(pages + (block + k) * page_bytes + (int64_t)(position - row0) * p.head_dim) + c;
-      out[0] = quantise8(a, inv);
-      out[half] = quantise8(bb, inv);
+      scale[k] = fmaxf(scale_of(peak[k]), old_scale[k]);
+      inv[k] = 1.f / scale[k];
+      if (old_rows > 0 && k < live && scale[k] != old_scale[k])
+        rescale_rows(rows + k * page_bytes, old_rows * p.head_dim, old_scale[k] / scale[k],
+                     threadIdx.x % team, team);
     }
-  }
-  if (unit % slots == 0 && c == 0) {
+    auto round_rows = [&](auto some) {
 #pragma unroll
-    for (int k = 0; k < HC; ++k)
-      if (g0 + k < Hkv) scale_at[k] = scale[k];
+      for (int i = 0; i < R; ++i) {
+        const int position = row0 + slot + i * slots;
+        if (position < lo || position >= hi) continue;
+        if (R > 1 && rotate) rope.load(p, position, c);
+#pragma unroll
+        for (int k = 0; k < HC; ++k) {
+          if (k >= live) break;
+          values(i, k);
+          uint2* out = reinterpret_cast<uint2*>(rows + k * page_bytes + (position - row0) * p.head_dim) + c;
+          out[0] = quantise8<decltype(some)::value>(a, inv[k]);
+          out[half] = quantise8<decltype(some)::value>(bb, inv[k]);
+        }
+      }
+    };
+    if (infinities) {
+      round_rows(std::true_type());
+    } else {
+      round_rows(std::false_type());
+    }
+    if (slot == 0 && c == 0) {
+#pragma unroll
+      for (int k = 0; k < HC; ++k)
+        if (k < live) scale_at[k] = scale[k];
+    }
   }
 }
 
+template <typename T, int R>
+cudaError_t launch_prompt_q8(cudaLaunchConfig_t cfg, const AppendPagedParams& p, int tasks, int ranges,
+                             int range_chunks, int stride) {
+  auto* fn = append_prompt_q8_kernel<T, R>;
+  cfg.dynamicSmemBytes = prompt_smem(R);
+  static std::atomic<bool> ready[64];  // per device: the shared-memory opt-in is applied
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
+  if (!ready[device].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, prompt_smem(R));
+    if (e != cudaSuccess) return e;
+    ready[device].store(true, std::memory_order_release);
+  }
+  return cudaLaunchKernelEx(&cfg, fn, p, tasks, ranges, range_chunks, stride);
+}
+
 // Units for each token: one for each head while that fills less than about two
-// waves of the SMs (latency), else kAtOnce heads a unit (the table row is read
-// once for them).
+// waves of the SMs (latency), else kTurns * kAtOnce heads a unit (place and
+// table row are looked up once for them).
+constexpr int kTurns = 3;
 int units_per_token(int64_t tokens, int heads, int half, int sms) {
-  return tokens * heads * half <= (int64_t)sms * 4096 ? heads : (heads + kAtOnce - 1) / kAtOnce;
+  return tokens * heads * half <= (int64_t)sms * 4096 ? heads : (heads + kTurns * kAtOnce - 1) / (kTurns * kAtOnce);
 }
 
 }  // namespace
@@ -495,23 +611,24 @@ cudaError_t launch_append_paged(const AppendPagedParams& p, int dtype, int sms, 
   }
   // n rows touch at most (n - 2) / page + 2 pages
   const int64_t tasks = std::min<int64_t>((int64_t)p.tokens / p.page_rows + 2 * (int64_t)p.B, p.tokens);
-  const int R = std::max(1, p.page_rows / units), hc = R == 1 ? 4 : 8 / R;
-  const int heads_at_once = units / (p.page_rows / R) * hc;
-  const int chunks = (p.n_kv_head + heads_at_once - 1) / heads_at_once;
-  if (tasks * 2 * chunks > INT32_MAX || !grid(tasks * 2 * chunks + query_ctas)) return cudaErrorInvalidConfiguration;
+  const int R = std::max(1, p.page_rows / units);
+  const int chunk_heads = units / (p.page_rows / R) * prompt_heads(R);
+  const int chunks = (p.n_kv_head + chunk_heads - 1) / chunk_heads;
+  // a CTA takes several chunks (it looks its page up once, and copies one chunk
+  // ahead) as far as that leaves about two CTAs an SM
+  const int ranges = (int)std::min<int64_t>(chunks, std::max<int64_t>(1, (2 * sms + 2 * tasks - 1) / (2 * tasks)));
+  const int range_chunks = (chunks + ranges - 1) / ranges;
+  if (tasks * 2 * ranges > INT32_MAX || !grid(tasks * 2 * ranges + query_ctas)) return cudaErrorInvalidConfiguration;
+  auto launch = [&](auto rows) {
+    constexpr int kR = decltype(rows)::value;
+    return f16 ? launch_prompt_q8<__half, kR>(cfg, p, (int)tasks, ranges, range_chunks, stride)
+               : launch_prompt_q8<__nv_bfloat16, kR>(cfg, p, (int)tasks, ranges, range_chunks, stride);
+  };
   switch (R) {
-    case 1:
-      return f16 ? cudaLaunchKernelEx(&cfg, append_prompt_q8_kernel<__half, 1>, p, (int)tasks, chunks, stride)
-                 : cudaLaunchKernelEx(&cfg, append_prompt_q8_kernel<__nv_bfloat16, 1>, p, (int)tasks, chunks, stride);
-    case 2:
-      return f16 ? cudaLaunchKernelEx(&cfg, append_prompt_q8_kernel<__half, 2>, p, (int)tasks, chunks, stride)
-                 : cudaLaunchKernelEx(&cfg, append_prompt_q8_kernel<__nv_bfloat16, 2>, p, (int)tasks, chunks, stride);
-    case 4:
-      return f16 ? cudaLaunchKernelEx(&cfg, append_prompt_q8_kernel<__half, 4>, p, (int)tasks, chunks, stride)
-                 : cudaLaunchKernelEx(&cfg, append_prompt_q8_kernel<__nv_bfloat16, 4>, p, (int)tasks, chunks, stride);
-    default:
-      return f16 ? cudaLaunchKernelEx(&cfg, append_prompt_q8_kernel<__half, 8>, p, (int)tasks, chunks, stride)
-                 : cudaLaunchKernelEx(&cfg, append_prompt_q8_kernel<__nv_bfloat16, 8>, p, (int)tasks, chunks, stride);
+    case 1: return launch(std::integral_constant<int, 1>());
+    case 2: return launch(std::integral_constant<int, 2>());
+    case 4: return launch(std::integral_constant<int, 4>());
+    default: return launch(std::integral_constant<int, 8>());
   }
 }
 
