@@ -238,23 +238,6 @@ __device__ __forceinline__ float peak_of(float peak, const float (&f)[8]) {
   return peak;
 }
 
-// The same of 8 packed values.
-template <typename T>
-__device__ __forceinline__ float peak_packed(float peak, const uint4& v) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  if constexpr (Storage<T>::kBf16) {
-    __nv_bfloat162 m = __float2bfloat162_rn(0.f);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) m = __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[e])));
-    return fmaxf(peak, fmaxf(__low2float(m), __high2float(m)));
-  } else {
-    __half2 m = __float2half2_rn(0.f);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) m = __hmax2(m, __habs2(*reinterpret_cast<const __half2*>(&w[e])));
-    return fmaxf(peak, fmaxf(__low2float(m), __high2float(m)));
-  }
-}
-
 // The same of the finite values alone: for heads whose peak is infinity.
 __device__ __forceinline__ float finite_peak(float peak, const float (&f)[8]) {
 #pragma unroll
@@ -447,7 +430,6 @@ __global__ void __launch_bounds__(kThreads, R == 8 ? 1 : 2)
   uint8_t* pages = (is_k ? p.k_pages : p.v_pages);
   const int64_t page_bytes = (int64_t)p.page_rows * p.head_dim;
   RopeRow rope;
-  float a[8], bb[8];
   for (int n = begin; n < end; ++n) {
     const int g0 = (n * at_once + unit / slots) * HC, live = min(HC, Hkv - g0);  // (may be none)
     if (n + 1 < end) {
@@ -456,34 +438,37 @@ __global__ void __launch_bounds__(kThreads, R == 8 ? 1 : 2)
     } else {
       copy_wait<0>();
     }
-    auto values = [&](int i, int k) {
-      const uint4 x = *place(n & 1, i, k, 0), y = *place(n & 1, i, k, 1);
-      if (rotate) {
-        rope.rotate<T>(x, y, a, bb);
-      } else {
-        Storage<T>::unpack(x, a);
-        Storage<T>::unpack(y, bb);
+    // the rows' values, kept between the peaks and the rounding
+    float va[R][HC][8], vb[R][HC][8], peak[HC];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int position = row0 + slot + i * slots;
+      const bool on = position >= lo && position < hi;
+      if (on && rotate) rope.load(p, position, c);
+#pragma unroll
+      for (int k = 0; k < HC; ++k) {
+        if (!on || k >= live) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) va[i][k][e] = vb[i][k][e] = 0.f;
+          continue;
+        }
+        const uint4 x = *place(n & 1, i, k, 0), y = *place(n & 1, i, k, 1);
+        if (rotate) {
+          rope.rotate<T>(x, y, va[i][k], vb[i][k]);
+        } else {
+          Storage<T>::unpack(x, va[i][k]);
+          Storage<T>::unpack(y, vb[i][k]);
+        }
       }
-    };
-    float peak[HC];
+    }
     auto find_peaks = [&](auto finite) {
 #pragma unroll
-      for (int k = 0; k < HC; ++k) peak[k] = 0.f;
+      for (int k = 0; k < HC; ++k) {
+        peak[k] = 0.f;
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
-        const int position = row0 + slot + i * slots;
-        if (position < lo || position >= hi) continue;
-        if (rotate) rope.load(p, position, c);
-#pragma unroll
-        for (int k = 0; k < HC; ++k) {
-          if (k >= live) break;
-          if (!rotate && !decltype(finite)::value) {
-            peak[k] = peak_packed<T>(peak_packed<T>(peak[k], *place(n & 1, i, k, 0)), *place(n & 1, i, k, 1));
-            continue;
-          }
-          values(i, k);
-          peak[k] = decltype(finite)::value ? finite_peak(finite_peak(peak[k], a), bb) : peak_of(peak_of(peak[k], a), bb);
-        }
+        for (int i = 0; i < R; ++i)
+          peak[k] = decltype(finite)::value ? finite_peak(finite_peak(peak[k], va[i][k]), vb[i][k])
+                                            : peak_of(peak_of(peak[k], va[i][k]), vb[i][k]);
       }
       // (non-negative floats order as their bits do)
 #pragma unroll
@@ -527,14 +512,12 @@ __global__ void __launch_bounds__(kThreads, R == 8 ? 1 : 2)
       for (int i = 0; i < R; ++i) {
         const int position = row0 + slot + i * slots;
         if (position < lo || position >= hi) continue;
-        if (R > 1 && rotate) rope.load(p, position, c);
 #pragma unroll
         for (int k = 0; k < HC; ++k) {
           if (k >= live) break;
-          values(i, k);
           uint2* out = reinterpret_cast<uint2*>(rows + k * page_bytes + (position - row0) * p.head_dim) + c;
-          out[0] = quantise8<decltype(some)::value>(a, inv[k]);
-          out[half] = quantise8<decltype(some)::value>(bb, inv[k]);
+          out[0] = quantise8<decltype(some)::value>(va[i][k], inv[k]);
+          out[half] = quantise8<decltype(some)::value>(vb[i][k], inv[k]);
         }
       }
     };
