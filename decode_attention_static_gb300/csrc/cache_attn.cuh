@@ -42,6 +42,7 @@ namespace da {
 
 constexpr int kHeads = 8;        // columns of the matrix instruction
 constexpr int kMaxCtas = 256;    // one for each SM; parts of one group, at most
+constexpr int kGroupCost = 8;    // what the end of a group costs, in tiles
 constexpr float kLazy = 8.f;     // m is raised when a score passes it by this (log2)
 // fp16 weights are 2^(x' - m + 7): at most 2^15, inside the type's range, and
 // 2^-32 of the largest one is still held. bf16 has fp32's range: no lift.
@@ -62,8 +63,8 @@ struct CacheAttnShape {
   static constexpr int kMetaOffset = kRingBytes + kMergeBytes;
   static constexpr int kMetaBytes = 32;  // of a stage: K and V scale of each piece, bad pages
   static constexpr int kStatOffset = kMetaOffset + kWarps * kStages * kMetaBytes;
-  // (m, l) of each warp, factors, group sums; schedule words
-  static constexpr int kStatFloats = 2 * kWarps * kHeads + kWarps * kHeads + 2 * kHeads;
+  // (m, l) of each warp, l of a group; schedule words
+  static constexpr int kStatFloats = 2 * kWarps * kHeads + kHeads;
   static constexpr int kWordsOffset = kStatOffset + kStatFloats * 4;
   static constexpr int kSmemBytes = kWordsOffset + (kWarps + 4) * 8;
   static_assert(kStages >= 3, "a ring of at least three stages");
@@ -204,35 +205,43 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
   float* merge = reinterpret_cast<float*>(smem + Sh::kRingBytes);
   float* sm_m = reinterpret_cast<float*>(smem + Sh::kStatOffset);  // [kW][8]
   float* sm_l = sm_m + kW * kHeads;
-  float* sm_f = sm_l + kW * kHeads;   // factor of each warp's state
-  float* sm_gm = sm_f + kW * kHeads;  // group's m and l
-  float* sm_gl = sm_gm + kHeads;
+  float* sm_gl = sm_l + kW * kHeads;  // l of a group in parts
   int64_t* words = reinterpret_cast<int64_t*>(smem + Sh::kWordsOffset);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, gr = lane >> 2, tq = lane & 3;
 
   pdl_wait();
   pdl_trigger();  // the next grid can take the SMs as they fall free; it waits for this one's memory
 
-  // --- the list of tiles, and this CTA's share [lo, hi) of it: one pass over
-  // the lengths for its size, and, for more sequences than threads, a second
-  // one for the sequence that holds `lo`
-  int64_t total = 0, mine = 0, own = 0;  // tiles before this thread's sequence (of the last pass), and its own
-  for (int base = 0; base < p.B; base += Sh::kThreads) {
+  // --- the list of places, and this CTA's share [lo, hi) of it: the tiles of
+  // each group, and, with more groups than CTAs, kGroupCost places that stand
+  // for its end (short groups are then balanced by what they cost, and those
+  // places hold cuts that would split a group). One pass over the lengths, and,
+  // for more sequences than threads, a second one for the sequence that holds
+  // `lo`.
+  struct Found {
+    int64_t start;  // first place of the sequence
+    int b, len;
+  };
+  Found* found = reinterpret_cast<Found*>(words + kW);
+  constexpr int kCount = 44;  // tiles and non-empty sequences are summed in one word: tiles + sequences * 2^44
+  int64_t before = 0, mine = 0, own = 0;  // before this pass, before this thread's sequence, and its own
+  int len = 0;
+  auto pass = [&](int base, bool idle_rows) {
     const int b = base + tid;
-    int n = 0;
+    own = 0;
     if (b < p.B) {
       SequenceTiles s;
-      n = tiles_of<kRows>(p, p.kv_len[b], &s);
-      if (n <= 0 && b % gridDim.x == blockIdx.x) {
+      len = p.kv_len[b];
+      const int n = tiles_of<kRows>(p, len, &s);
+      if (n > 0) own = n + (1ll << kCount);
+      if (idle_rows && n <= 0 && b % gridDim.x == blockIdx.x) {
         // no visible row: zeros; no valid length: NaN
         const uint32_t fill = n < 0 ? (uint32_t)Storage<T>::kNaN * 0x10001u : 0u;
         if (n < 0 && p.err_flag) atomicOr(p.err_flag, kErrKvLen);
         uint4* out = reinterpret_cast<uint4*>(p.out) + (int64_t)b * p.n_head * (D / 8);
         for (int i = 0; i < p.n_head * (D / 8); ++i) out[i] = make_uint4(fill, fill, fill, fill);
       }
-      n = max(n, 0);
     }
-    own = (int64_t)n * p.n_kv_head;
     int64_t sum = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -242,56 +251,74 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
     if (base) __syncthreads();  // the words of the pass before have been read
     if (lane == 31) words[warp] = sum;
     __syncthreads();
-    mine = total + sum - own;
+    mine = before + sum - own;
 #pragma unroll
     for (int w = 0; w < kW; ++w) {
       if (w < warp) mine += words[w];
-      total += words[w];
+      before += words[w];
     }
-  }
-  // at least one tile for every warp
-  const int64_t ctas = min((int64_t)gridDim.x, (total + kW - 1) / kW);
+  };
+  for (int base = 0; base < p.B; base += Sh::kThreads) pass(base, true);
+  const int64_t tiles = (before & ((1ll << kCount) - 1)) * p.n_kv_head, groups = (before >> kCount) * p.n_kv_head;
+  // as many CTAs as find a tile for every warp
+  const int64_t ctas = min((int64_t)gridDim.x, (tiles + kW - 1) / kW);
   if ((int64_t)blockIdx.x >= ctas) return;
-  const int64_t lo = blockIdx.x * total / ctas, hi = (blockIdx.x + 1) * total / ctas;
-  if (p.B > Sh::kThreads) {
-    int64_t before = 0;
-    for (int base = 0; before <= lo; base += Sh::kThreads) {
-      const int b = base + tid;
-      SequenceTiles s;
-      own = b < p.B ? (int64_t)max(tiles_of<kRows>(p, p.kv_len[b], &s), 0) * p.n_kv_head : 0;
-      int64_t sum = own;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += v;
-      }
+  const int end_cost = groups > ctas ? kGroupCost : 0;
+  auto places = [&](int64_t word) {
+    return ((word & ((1ll << kCount) - 1)) + (word >> kCount) * end_cost) * p.n_kv_head;
+  };
+  const int64_t total = places(before);
+  // first place of share i, and the share that holds place x (in 32 bits where
+  // they suffice: a 64-bit division is some hundred instructions)
+  const bool small = total * ctas < (1ll << 32);
+  auto share_start = [&](int64_t i) {
+    return small ? (int64_t)((uint32_t)i * (uint32_t)total / (uint32_t)ctas) : i * total / ctas;
+  };
+  auto share_of = [&](int64_t x) {
+    return (int)(small ? ((uint32_t)(x + 1) * (uint32_t)ctas - 1) / (uint32_t)total : ((x + 1) * ctas - 1) / total);
+  };
+  const int64_t lo = share_start(blockIdx.x), hi = share_start(blockIdx.x + 1);
+  auto find = [&](int base) {
+    const int64_t at = places(mine);
+    if (at <= lo && lo < at + places(own)) *found = {at, base + tid, len};
+  };
+  if (p.B <= Sh::kThreads) {
+    find(0);
+  } else {
+    before = 0;
+    for (int base = 0; places(before) <= lo; base += Sh::kThreads) {
       __syncthreads();
-      if (lane == 31) words[warp] = sum;
-      __syncthreads();
-      mine = before + sum - own;
-#pragma unroll
-      for (int w = 0; w < kW; ++w) {
-        if (w < warp) mine += words[w];
-        before += words[w];
-      }
-      if (mine <= lo && lo < mine + own) {
-        words[kW] = b;
-        words[kW + 1] = mine;
-      }
+      pass(base, false);
+      find(base);
     }
-  } else if (mine <= lo && lo < mine + own) {
-    words[kW] = tid;
-    words[kW + 1] = mine;
   }
   __syncthreads();
-  int b = (int)words[kW];
+  int b = found->b;
   SequenceTiles seq;
-  tiles_of<kRows>(p, p.kv_len[b], &seq);
-  int g, tile;  // group of list position `lo`, and its place there
+  tiles_of<kRows>(p, found->len, &seq);
+  int g, tile;       // group of list position `lo`, and its place there
+  int64_t at = lo;   // list position of the next tile to compute
   {
-    const int64_t in = lo - words[kW + 1];
-    g = (int)(in / seq.tiles);
-    tile = (int)(in - (int64_t)g * seq.tiles);
+    const int64_t in = lo - found->start;
+    const int size = seq.tiles + end_cost;
+    g = small ? (int)((uint32_t)in / (uint32_t)size) : (int)(in / size);
+    tile = (int)(in - (int64_t)g * size);
+  }
+  // the next group; false when this share ends before it
+  auto next_group = [&](int64_t& place, int& b, int& g, SequenceTiles& s) {
+    if (place >= hi) return false;
+    if (++g == p.n_kv_head) {
+      g = 0;
+      do ++b;
+      while (tiles_of<kRows>(p, p.kv_len[b], &s) <= 0);
+    }
+    return true;
+  };
+  if (tile >= seq.tiles) {
+    // the share begins in the places of a group's end
+    at += seq.tiles + end_cost - tile;
+    tile = 0;
+    if (!next_group(at, b, g, seq)) return;
   }
 
   // --- this warp's loads. A tile is kHalves pieces of 16 rows, each inside one
@@ -303,20 +330,20 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
   SequenceTiles lseq = seq;  // the tile to load next, its page number on the way
   int lb = b, lg = g, li = tile, lrow = 0, lpage = 0;
   uint32_t lmask = 0;  // 0: no tile is left
-  int64_t lat = lo;
+  int64_t lat = at;
+  bool more = true;
   auto look_up = [&](int step) {  // moves on by `step` tiles
     lat += step;
-    lmask = 0;
-    if (lat >= hi) return;
     li += step;
-    while (li >= lseq.tiles) {
+    lmask = 0;
+    while (more && li >= lseq.tiles) {
       li -= lseq.tiles;
-      if (++lg == p.n_kv_head) {
-        lg = 0;
-        do ++lb;
-        while (tiles_of<kRows>(p, p.kv_len[lb], &lseq) <= 0);
-      }
+      lat += end_cost;
+      int64_t start = lat - li;
+      more = next_group(start, lb, lg, lseq);
     }
+    more = more && lat < hi;
+    if (!more) return;
     const int row0 = tile_row<kRows>(lseq, li);
     lmask = tile_mask<kRows>(lseq, row0);
     lrow = row0 + 16 * half;
@@ -384,10 +411,9 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
   }
 
   // --- group by group
-  int64_t at = lo;  // list position of the next tile to compute
   int get = 0;      // stage of this warp's next tile
   int turn = warp;  // tiles until this warp's next one
-  while (at < hi) {
+  for (;;) {
     const int here = (int)min((int64_t)(seq.tiles - tile), hi - at);  // tiles of the group in this share
     // q as the right operand: columns are heads
     uint32_t qb[kSteps][2];
@@ -624,20 +650,6 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
       }
     }
     __syncthreads();
-    if (tid < kHeads) {
-      float mm = -INFINITY, ll = 0.f;
-#pragma unroll
-      for (int w = 0; w < kW; ++w) mm = fmaxf(mm, sm_m[w * kHeads + tid]);
-#pragma unroll
-      for (int w = 0; w < kW; ++w) {
-        const float mw = sm_m[w * kHeads + tid], f = mw == mm ? 1.f : fast_exp2(mw - mm);
-        sm_f[w * kHeads + tid] = f;
-        ll += f * sm_l[w * kHeads + tid];
-      }
-      sm_gm[tid] = mm;
-      sm_gl[tid] = ll;
-    }
-    __syncthreads();
     const bool whole = here == seq.tiles;
     const int items = p.group * (D / 4);  // outputs in vectors of 4
     // shares that hold the group, and this one's partial state
@@ -645,8 +657,8 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
     const int slot_floats = cache_attn_slot_floats(p.group, D);
     int from = 0, parts = 1;
     if (!whole) {
-      from = (int)(((group_start + 1) * ctas - 1) / total);
-      parts = (int)(((group_start + seq.tiles) * ctas - 1) / total) - from + 1;
+      from = share_of(group_start);
+      parts = share_of(group_start + seq.tiles - 1) - from + 1;
     }
     // (a CTA has at most two groups that others share: the one it begins in
     // the middle of, slot 0, and the one it leaves in the middle of, slot 1)
@@ -669,22 +681,30 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
     };
     if (tid < items) {
       const int h = tid / (D / 4), d = (tid % (D / 4)) * 4;
+      float mw[kW], mm = -INFINITY, ll = 0.f;
+#pragma unroll
+      for (int w = 0; w < kW; ++w) {
+        mw[w] = sm_m[w * kHeads + h];
+        mm = fmaxf(mm, mw[w]);
+      }
       float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < kW; ++w)
-        add(r, sm_f[w * kHeads + h],
-            *reinterpret_cast<const float4*>(merge + (w * kHeads + h) * D + merge_column<D>(h, d)));
+      for (int w = 0; w < kW; ++w) {
+        const float f = mw[w] == mm ? 1.f : fast_exp2(mw[w] - mm);
+        ll = fmaf(f, sm_l[w * kHeads + h], ll);
+        add(r, f, *reinterpret_cast<const float4*>(merge + (w * kHeads + h) * D + merge_column<D>(h, d)));
+      }
       if (whole) {
-        store(tid, r, sm_gl[h]);
+        store(tid, r, ll);
       } else {
         __stcg(reinterpret_cast<float4*>(slot) + tid, r);
+        if (d == 0) {
+          __stcg(slot + p.group * D + h, mm);
+          __stcg(slot + p.group * D + p.group + h, ll);
+        }
       }
     }
     if (!whole) {
-      if (tid < p.group) {
-        __stcg(slot + p.group * D + tid, sm_gm[tid]);
-        __stcg(slot + p.group * D + p.group + tid, sm_gl[tid]);
-      }
       __syncthreads();
       unsigned int* arrived = reinterpret_cast<unsigned int*>(&words[kW + 2]);
       if (tid == 0) {
@@ -717,14 +737,24 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
         };
         fetch(crew);
         if (warp < p.group) {
-          float mm = -INFINITY, ll = 0.f;
-          for (int s = lane; s < parts; s += 32) mm = fmaxf(mm, __ldcg(slot_of(s) + p.group * D + warp));
+          // lane s has part s (the m and l of the first 32 parts are read together)
+          float m_s = -INFINITY, l_s = 0.f;
+          if (lane < parts) {
+            m_s = __ldcg(slot_of(lane) + p.group * D + warp);
+            l_s = __ldcg(slot_of(lane) + p.group * D + p.group + warp);
+          }
+          float mm = m_s, ll = 0.f;
+          for (int s = lane + 32; s < parts; s += 32) mm = fmaxf(mm, __ldcg(slot_of(s) + p.group * D + warp));
 #pragma unroll
           for (int k = 16; k; k >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, k));
           for (int s = lane; s < parts; s += 32) {
-            const float mw = __ldcg(slot_of(s) + p.group * D + warp), f = mw == mm ? 1.f : fast_exp2(mw - mm);
+            if (s >= 32) {
+              m_s = __ldcg(slot_of(s) + p.group * D + warp);
+              l_s = __ldcg(slot_of(s) + p.group * D + p.group + warp);
+            }
+            const float f = m_s == mm ? 1.f : fast_exp2(m_s - mm);
             factor[s * kHeads + warp] = f;
-            ll += f * __ldcg(slot_of(s) + p.group * D + p.group + warp);
+            ll = fmaf(f, l_s, ll);
           }
 #pragma unroll
           for (int k = 16; k; k >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, k);
@@ -751,13 +781,9 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
     __syncthreads();  // the merge buffer is free
 
     // --- the next group
-    at += here;
+    at += here + end_cost;
     tile = 0;
-    if (at < hi && ++g == p.n_kv_head) {
-      g = 0;
-      do ++b;
-      while (tiles_of<kRows>(p, p.kv_len[b], &seq) <= 0);
-    }
+    if (!next_group(at, b, g, seq)) break;
   }
   copy_wait<0>();
 }
