@@ -513,77 +513,124 @@ def alloc_paged_workspace(n_head: int, n_kv_head: int, head_dim: int, device=Non
     return torch.zeros(max(n, 16), dtype=torch.uint8, device=device or "cuda")
 
 
-def _pool(k_pages, v_pages, dtype, scales):
+# The entry points below check their tensors in one expression (a call costs
+# more host time in checks than in the library); only when it fails do the
+# _explain functions look for what is wrong, to say it.
+
+
+def _explain_device(index, named):
+    for name, t in named.items():
+        if t is not None:
+            _on(torch.device("cuda", index), **{name: t})
+            _require(t.get_device() == index, f"{name} must be a contiguous CUDA tensor on cuda:{index}")
+
+
+def _explain_pool(k_pages, v_pages, k_scale, v_scale, dtype, eight):
     """Shape of a page pool, and checks of its types (and scales)."""
     _require(k_pages.dim() == 4 and v_pages.shape == k_pages.shape,
              "k_pages/v_pages must be [num_pages, n_kv_head, page_size, D]")
-    pages, Hkv, size, D = k_pages.shape
-    want = dtype if scales is None else torch.float8_e4m3fn
+    want = torch.float8_e4m3fn if eight else dtype
     if k_pages.dtype != want or v_pages.dtype != want:
         raise TypeError(f"pages must be {want}")
-    if scales is not None:
-        for name, t in zip(("k_scale", "v_scale"), scales):
-            _require(t.dtype == torch.float32 and t.shape == (pages, Hkv),
-                     lambda: f"{name} must be float32 [num_pages, n_kv_head]")
-    return pages, Hkv, size, D
+    if eight:
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            _require(t.dtype == torch.float32 and t.shape == k_pages.shape[:2],
+                     f"{name} must be float32 [num_pages, n_kv_head]")
 
 
-def _append_paged(fn, k_pages, v_pages, scales, k_new, v_new, page_table, position_ids, token_start, rope_cos,
-                  rope_sin, q, q_out, err_flag):
+def _explain_err_flag(err_flag):
+    _require(err_flag is None or (err_flag.dtype == torch.int32 and err_flag.numel() >= 1),
+             "err_flag must be int32 with one element")
+
+
+def _explain_append(k_pages, v_pages, k_scale, v_scale, eight, k_new, v_new, page_table, position_ids, token_start,
+                    rope_cos, rope_sin, q, q_out, err_flag):
     _cuda_contig("k_new", k_new)
-    index = k_new.get_device()
-    code = _code_for(k_new.dtype)
-    pages, Hkv, size, D = _pool(k_pages, v_pages, k_new.dtype, scales)
+    _code_for(k_new.dtype)
+    _explain_pool(k_pages, v_pages, k_scale, v_scale, k_new.dtype, eight)
+    Hkv, D = k_pages.shape[1], k_pages.shape[3]
     _require(k_new.dim() == 3 and k_new.shape[1] == Hkv and k_new.shape[2] == D and v_new.shape == k_new.shape
              and v_new.dtype == k_new.dtype, "k_new/v_new must be [tokens, n_kv_head, D] of one type")
-    tokens = k_new.shape[0]
     _require(page_table.dtype == torch.int32 and page_table.dim() == 2, "page_table must be int32 [B, max_pages]")
-    B, max_pages = page_table.shape
+    B = page_table.shape[0]
     _require(position_ids.dtype == torch.int32 and position_ids.numel() == B, "position_ids must be int32 [B]")
-    names = ["v_new", "k_pages", "v_pages", "page_table", "position_ids"]
-    tensors = [v_new, k_pages, v_pages, page_table, position_ids]
-    if scales is not None:
-        names += ["k_scale", "v_scale"]
-        tensors += scales
     if token_start is not None:
         _require(token_start.dtype == torch.int32 and token_start.numel() == B + 1, "token_start must be int32 [B + 1]")
-        names.append("token_start")
-        tensors.append(token_start)
     else:
-        _require(tokens == B, "without token_start there is one token per sequence")
-    rope_rows = n_head = 0
-    cos_ptr = sin_ptr = q_ptr = out_ptr = None
+        _require(k_new.shape[0] == B, "without token_start there is one token per sequence")
     _require((rope_cos is None) == (rope_sin is None), "rope_cos and rope_sin come together")
     if rope_cos is not None:
         _require(rope_cos.dtype == torch.float32 and rope_sin.dtype == torch.float32 and rope_cos.dim() == 2
                  and rope_cos.shape == rope_sin.shape and rope_cos.shape[1] == D, "rope tables must be fp32 [rows, D]")
-        rope_rows, cos_ptr, sin_ptr = rope_cos.shape[0], rope_cos.data_ptr(), rope_sin.data_ptr()
-        names += ["rope_cos", "rope_sin"]
-        tensors += [rope_cos, rope_sin]
     if q is not None:
         _require(rope_cos is not None, "rotating q needs the rope tables")
-        _require(q.dim() == 3 and q.shape[0] == tokens and q.shape[2] == D and q.dtype == k_new.dtype,
+        _require(q.dim() == 3 and q.shape[0] == k_new.shape[0] and q.shape[2] == D and q.dtype == k_new.dtype,
                  "q must be [tokens, n_head, D] of the type of k_new")
-        if q_out is None:
-            q_out = torch.empty_like(q)
-        _require(q_out.shape == q.shape and q_out.dtype == q.dtype, "q_out must match q")
-        n_head, q_ptr, out_ptr = q.shape[1], q.data_ptr(), q_out.data_ptr()
-        names += ["q", "q_out"]
-        tensors += [q, q_out]
+        _require(q_out is None or (q_out.shape == q.shape and q_out.dtype == q.dtype), "q_out must match q")
     else:
         _require(q_out is None, "q_out comes with q")
-    if err_flag is not None:
-        _require(err_flag.dtype == torch.int32 and err_flag.numel() >= 1, "err_flag must be int32 with one element")
-        names.append("err_flag")
-        tensors.append(err_flag)
-    _same_device_contiguous(index, names, tensors)
-    pool = [k_pages.data_ptr(), v_pages.data_ptr()]
-    if scales is not None:
-        pool += [scales[0].data_ptr(), scales[1].data_ptr()]
-    _call_on(fn, index, *pool, k_new.data_ptr(), v_new.data_ptr(), q_ptr, out_ptr, cos_ptr, sin_ptr, rope_rows,
-             page_table.data_ptr(), position_ids.data_ptr(), None if token_start is None else token_start.data_ptr(),
-             B, tokens, n_head, Hkv, D, pages, size, max_pages, code,
-             None if err_flag is None else err_flag.data_ptr(), _raw_stream(index))
+    _explain_err_flag(err_flag)
+    _explain_device(k_new.get_device(), dict(
+        v_new=v_new, k_pages=k_pages, v_pages=v_pages, k_scale=k_scale, v_scale=v_scale, page_table=page_table,
+        position_ids=position_ids, token_start=token_start, rope_cos=rope_cos, rope_sin=rope_sin, q=q, q_out=q_out,
+        err_flag=err_flag))
+    raise ValueError("inconsistent arguments")
+
+
+def _append_paged(fn, k_pages, v_pages, k_scale, v_scale, eight, k_new, v_new, page_table, position_ids, token_start,
+                  rope_cos, rope_sin, q, q_out, err_flag):
+    dtype, pool, new, table = k_new.dtype, k_pages.shape, k_new.shape, page_table.shape
+    code, store = _DTYPE_CODE.get(dtype), torch.float8_e4m3fn if eight else dtype
+    ix = k_new.get_device()
+    i32, f32 = torch.int32, torch.float32
+    ok = (ix >= 0 and code is not None and len(pool) == 4 and len(new) == 3 and len(table) == 2
+          and new[1] == pool[1] and new[2] == pool[3] and v_new.shape == new and v_pages.shape == pool
+          and v_new.dtype == dtype and k_pages.dtype == store and v_pages.dtype == store and page_table.dtype == i32
+          and position_ids.dtype == i32 and position_ids.numel() == table[0]
+          and v_new.get_device() == ix and k_pages.get_device() == ix and v_pages.get_device() == ix
+          and page_table.get_device() == ix and position_ids.get_device() == ix
+          and k_new.is_contiguous() and v_new.is_contiguous() and k_pages.is_contiguous() and v_pages.is_contiguous()
+          and page_table.is_contiguous() and position_ids.is_contiguous()
+          and (not eight or (k_scale.dtype == f32 and v_scale.dtype == f32 and k_scale.shape == pool[:2]
+                             and v_scale.shape == pool[:2] and k_scale.get_device() == ix
+                             and v_scale.get_device() == ix and k_scale.is_contiguous() and v_scale.is_contiguous()))
+          and (new[0] == table[0] if token_start is None else
+               (token_start.dtype == i32 and token_start.numel() == table[0] + 1 and token_start.get_device() == ix
+                and token_start.is_contiguous()))
+          and (rope_cos is None) == (rope_sin is None) and (q is not None or q_out is None)
+          and (err_flag is None or (err_flag.dtype == i32 and err_flag.numel() >= 1 and err_flag.get_device() == ix
+                                    and err_flag.is_contiguous())))
+    rope_rows = n_head = 0
+    cos_ptr = sin_ptr = q_ptr = out_ptr = None
+    if ok and rope_cos is not None:
+        rope = rope_cos.shape
+        ok = (len(rope) == 2 and rope[1] == new[2] and rope_sin.shape == rope and rope_cos.dtype == f32
+              and rope_sin.dtype == f32 and rope_cos.get_device() == ix and rope_sin.get_device() == ix
+              and rope_cos.is_contiguous() and rope_sin.is_contiguous())
+        if ok:
+            rope_rows, cos_ptr, sin_ptr = rope[0], rope_cos.data_ptr(), rope_sin.data_ptr()
+    if ok and q is not None:
+        qs = q.shape
+        ok = (rope_cos is not None and len(qs) == 3 and qs[0] == new[0] and qs[2] == new[2] and q.dtype == dtype
+              and q.get_device() == ix and q.is_contiguous())
+        if ok:
+            if q_out is None:
+                q_out = torch.empty_like(q)
+            else:
+                ok = (q_out.shape == qs and q_out.dtype == dtype and q_out.get_device() == ix
+                      and q_out.is_contiguous())
+            n_head, q_ptr, out_ptr = qs[1], q.data_ptr(), q_out.data_ptr()
+    if not ok:
+        _explain_append(k_pages, v_pages, k_scale, v_scale, eight, k_new, v_new, page_table, position_ids,
+                        token_start, rope_cos, rope_sin, q, q_out, err_flag)
+    tail = (k_new.data_ptr(), v_new.data_ptr(), q_ptr, out_ptr, cos_ptr, sin_ptr, rope_rows, page_table.data_ptr(),
+            position_ids.data_ptr(), None if token_start is None else token_start.data_ptr(), table[0], new[0],
+            n_head, pool[1], pool[3], pool[0], pool[2], table[1], code,
+            None if err_flag is None else err_flag.data_ptr(), _raw_stream(ix))
+    if eight:
+        _call_on(fn, ix, k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), *tail)
+    else:
+        _call_on(fn, ix, k_pages.data_ptr(), v_pages.data_ptr(), *tail)
     return q_out
 
 
@@ -601,8 +648,8 @@ def kvcache_append_paged(k_pages: torch.Tensor, v_pages: torch.Tensor, k_new: to
     (token_start None: one token per sequence). With rope tables the keys are
     rotated at their positions, and q [tokens, n_head, D] into q_out (may be
     q), which is returned."""
-    return _append_paged("kvcache_append_paged", k_pages, v_pages, None, k_new, v_new, page_table, position_ids,
-                         token_start, rope_cos, rope_sin, q, q_out, err_flag)
+    return _append_paged("kvcache_append_paged", k_pages, v_pages, None, None, False, k_new, v_new, page_table,
+                         position_ids, token_start, rope_cos, rope_sin, q, q_out, err_flag)
 
 
 def kvcache_append_paged_q8(k_pages: torch.Tensor, v_pages: torch.Tensor, k_scale: torch.Tensor,
@@ -616,54 +663,65 @@ def kvcache_append_paged_q8(k_pages: torch.Tensor, v_pages: torch.Tensor, k_scal
     scale per page and KV head (k_scale/v_scale float32 [num_pages, n_kv_head],
     updated in place; a page whose scale grows has its earlier rows rounded to
     the new one)."""
-    return _append_paged("kvcache_append_paged_q8", k_pages, v_pages, [k_scale, v_scale], k_new, v_new, page_table,
-                         position_ids, token_start, rope_cos, rope_sin, q, q_out, err_flag)
+    return _append_paged("kvcache_append_paged_q8", k_pages, v_pages, k_scale, v_scale, True, k_new, v_new,
+                         page_table, position_ids, token_start, rope_cos, rope_sin, q, q_out, err_flag)
 
 
-def _attn_tail(q, out, scale, workspace, err_flag, Hkv, names, tensors):
-    """The checks and arguments that the attention entry points share: out,
-    scale, workspace, error flag; returns (out, index, trailing arguments)."""
-    if out is None:
-        out = torch.empty_like(q)
-    else:
-        _require(out.shape == q.shape and out.dtype == q.dtype, "out must match q")
-        names.append("out")
-        tensors.append(out)
-    index = q.get_device()
-    D = q.shape[2]
-    if workspace is None:
-        workspace = alloc_paged_workspace(q.shape[1], Hkv, D, q.device)
-    names.append("workspace")
-    tensors.append(workspace)
-    if err_flag is not None:
-        _require(err_flag.dtype == torch.int32 and err_flag.numel() >= 1, "err_flag must be int32 with one element")
-        names.append("err_flag")
-        tensors.append(err_flag)
-    _same_device_contiguous(index, names, tensors)
-    return out, index, (float(D ** -0.5 if scale is None else scale), out.data_ptr(), workspace.data_ptr(),
-                        workspace.numel() * workspace.element_size(), _code_for(q.dtype),
-                        None if err_flag is None else err_flag.data_ptr(), _raw_stream(index))
-
-
-def _attn_paged(fn, q, k_pages, v_pages, scales, page_table, kv_len, window, sinks, out, scale, workspace, err_flag):
+def _explain_attn(q, k_pages, v_pages, k_scale, v_scale, eight, page_table, kv_len, out, workspace, err_flag):
     _cuda_contig("q", q)
     _require(q.dim() == 3, "q must be [B, n_head, D]")
     _code_for(q.dtype)
-    B, H, D = q.shape
-    pages, Hkv, size, Dk = _pool(k_pages, v_pages, q.dtype, scales)
-    _require(Dk == D, "head_dim of the pages must match q")
+    B, _, D = q.shape
+    _explain_pool(k_pages, v_pages, k_scale, v_scale, q.dtype, eight)
+    _require(k_pages.shape[3] == D, "head_dim of the pages must match q")
     _require(page_table.dtype == torch.int32 and page_table.dim() == 2 and page_table.shape[0] == B,
              "page_table must be int32 [B, max_pages]")
-    _require(kv_len.dtype == torch.int32 and kv_len.numel() == B, "kv_len must be int32 [B]")
-    names, tensors = ["k_pages", "v_pages", "page_table", "kv_len"], [k_pages, v_pages, page_table, kv_len]
-    pool = [k_pages.data_ptr(), v_pages.data_ptr()]
-    if scales is not None:
-        names += ["k_scale", "v_scale"]
-        tensors += scales
-        pool += [scales[0].data_ptr(), scales[1].data_ptr()]
-    out, index, tail = _attn_tail(q, out, scale, workspace, err_flag, Hkv, names, tensors)
-    _call_on(fn, index, q.data_ptr(), *pool, page_table.data_ptr(), kv_len.data_ptr(), B, H, Hkv, D, pages, size,
-             page_table.shape[1], int(window), int(sinks), *tail)
+    _explain_attn_tail(q, kv_len, out, workspace, err_flag, k_pages=k_pages, v_pages=v_pages, k_scale=k_scale,
+                       v_scale=v_scale, page_table=page_table)
+
+
+def _explain_attn_tail(q, kv_len, out, workspace, err_flag, **others):
+    _require(kv_len.dtype == torch.int32 and kv_len.numel() == q.shape[0], "kv_len must be int32 [B]")
+    _require(out.shape == q.shape and out.dtype == q.dtype, "out must match q")
+    _explain_err_flag(err_flag)
+    _explain_device(q.get_device(), dict(kv_len=kv_len, out=out, workspace=workspace, err_flag=err_flag, **others))
+    raise ValueError("inconsistent arguments")
+
+
+def _attn_paged(fn, q, k_pages, v_pages, k_scale, v_scale, eight, page_table, kv_len, window, sinks, out, scale,
+                workspace, err_flag):
+    dtype, shape, pool, table = q.dtype, q.shape, k_pages.shape, page_table.shape
+    code, store = _DTYPE_CODE.get(dtype), torch.float8_e4m3fn if eight else dtype
+    ix = q.get_device()
+    if out is None:
+        out = torch.empty_like(q)
+    if not (ix >= 0 and code is not None and len(shape) == 3 and len(pool) == 4 and len(table) == 2
+            and pool[3] == shape[2] and table[0] == shape[0] and v_pages.shape == pool and k_pages.dtype == store
+            and v_pages.dtype == store and page_table.dtype == torch.int32 and kv_len.dtype == torch.int32
+            and kv_len.numel() == shape[0] and out.shape == shape and out.dtype == dtype
+            and k_pages.get_device() == ix and v_pages.get_device() == ix and page_table.get_device() == ix
+            and kv_len.get_device() == ix and out.get_device() == ix and q.is_contiguous()
+            and k_pages.is_contiguous() and v_pages.is_contiguous() and page_table.is_contiguous()
+            and kv_len.is_contiguous() and out.is_contiguous()
+            and (workspace is None or (workspace.get_device() == ix and workspace.is_contiguous()))
+            and (not eight or (k_scale.dtype == torch.float32 and v_scale.dtype == torch.float32
+                               and k_scale.shape == pool[:2] and v_scale.shape == pool[:2]
+                               and k_scale.get_device() == ix and v_scale.get_device() == ix
+                               and k_scale.is_contiguous() and v_scale.is_contiguous()))
+            and (err_flag is None or (err_flag.dtype == torch.int32 and err_flag.numel() >= 1
+                                      and err_flag.get_device() == ix and err_flag.is_contiguous()))):
+        _explain_attn(q, k_pages, v_pages, k_scale, v_scale, eight, page_table, kv_len, out, workspace, err_flag)
+    if workspace is None:
+        workspace = alloc_paged_workspace(shape[1], pool[1], shape[2], q.device)
+    tail = (page_table.data_ptr(), kv_len.data_ptr(), shape[0], shape[1], pool[1], shape[2], pool[0], pool[2],
+            table[1], int(window), int(sinks), shape[2] ** -0.5 if scale is None else float(scale), out.data_ptr(),
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), code,
+            None if err_flag is None else err_flag.data_ptr(), _raw_stream(ix))
+    if eight:
+        _call_on(fn, ix, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(),
+                 v_scale.data_ptr(), *tail)
+    else:
+        _call_on(fn, ix, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), *tail)
     return out
 
 
@@ -675,8 +733,8 @@ def decode_attn_paged_fwd(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch
     paged cache (or, with window > 0, over the last `window` of them and the
     first `sinks`); kv_len[b] == 0 gives zeros. A workspace comes from
     alloc_paged_workspace (reuse it across calls)."""
-    return _attn_paged("decode_attn_paged_fwd", q, k_pages, v_pages, None, page_table, kv_len, window, sinks, out,
-                       scale, workspace, err_flag)
+    return _attn_paged("decode_attn_paged_fwd", q, k_pages, v_pages, None, None, False, page_table, kv_len, window,
+                       sinks, out, scale, workspace, err_flag)
 
 
 def decode_attn_paged_q8_fwd(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, k_scale: torch.Tensor,
@@ -686,7 +744,7 @@ def decode_attn_paged_q8_fwd(q: torch.Tensor, k_pages: torch.Tensor, v_pages: to
                              err_flag: torch.Tensor | None = None) -> torch.Tensor:
     """decode_attn_paged_fwd over float8_e4m3fn pools with their scales
     float32 [num_pages, n_kv_head]."""
-    return _attn_paged("decode_attn_paged_q8_fwd", q, k_pages, v_pages, [k_scale, v_scale], page_table, kv_len,
+    return _attn_paged("decode_attn_paged_q8_fwd", q, k_pages, v_pages, k_scale, v_scale, True, page_table, kv_len,
                        window, sinks, out, scale, workspace, err_flag)
 
 
@@ -696,16 +754,32 @@ def decode_attn_window_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torc
                            err_flag: torch.Tensor | None = None) -> torch.Tensor:
     """Decode attention over the last `window` of the first kv_len[b] rows of a
     static cache and its first `sinks` rows; nothing else is read."""
-    _cuda_contig("q", q)
-    _require(q.dim() == 3, "q must be [B, n_head, D]")
-    _require(k_cache.dim() == 4 and v_cache.shape == k_cache.shape, "caches must be [B, n_kv_head, capacity, D]")
-    B, H, D = q.shape
-    Bk, Hkv, cap, Dk = k_cache.shape
-    _require(Bk == B and Dk == D, "cache batch/head_dim must match q")
-    _require(q.dtype == k_cache.dtype == v_cache.dtype, "dtypes differ")
-    _require(kv_len.dtype == torch.int32 and kv_len.numel() == B, "kv_len must be int32 [B]")
-    out, index, tail = _attn_tail(q, out, scale, workspace, err_flag, Hkv, ["k_cache", "v_cache", "kv_len"],
-                                  [k_cache, v_cache, kv_len])
-    _call_on("decode_attn_window_fwd", index, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), kv_len.data_ptr(),
-             B, H, Hkv, D, cap, int(window), int(sinks), *tail)
+    dtype, shape, cache = q.dtype, q.shape, k_cache.shape
+    code, ix = _DTYPE_CODE.get(dtype), q.get_device()
+    if out is None:
+        out = torch.empty_like(q)
+    if not (ix >= 0 and code is not None and len(shape) == 3 and len(cache) == 4 and cache[0] == shape[0]
+            and cache[3] == shape[2] and v_cache.shape == cache and k_cache.dtype == dtype and v_cache.dtype == dtype
+            and kv_len.dtype == torch.int32 and kv_len.numel() == shape[0] and out.shape == shape
+            and out.dtype == dtype and k_cache.get_device() == ix and v_cache.get_device() == ix
+            and kv_len.get_device() == ix and out.get_device() == ix and q.is_contiguous()
+            and k_cache.is_contiguous() and v_cache.is_contiguous() and kv_len.is_contiguous()
+            and out.is_contiguous()
+            and (workspace is None or (workspace.get_device() == ix and workspace.is_contiguous()))
+            and (err_flag is None or (err_flag.dtype == torch.int32 and err_flag.numel() >= 1
+                                      and err_flag.get_device() == ix and err_flag.is_contiguous()))):
+        _cuda_contig("q", q)
+        _code_for(dtype)
+        _require(len(shape) == 3, "q must be [B, n_head, D]")
+        _require(len(cache) == 4 and v_cache.shape == cache, "caches must be [B, n_kv_head, capacity, D]")
+        _require(cache[0] == shape[0] and cache[3] == shape[2], "cache batch/head_dim must match q")
+        _require(k_cache.dtype == dtype and v_cache.dtype == dtype, "dtypes differ")
+        _explain_attn_tail(q, kv_len, out, workspace, err_flag, k_cache=k_cache, v_cache=v_cache)
+    if workspace is None:
+        workspace = alloc_paged_workspace(shape[1], cache[1], shape[2], q.device)
+    _call_on("decode_attn_window_fwd", ix, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), kv_len.data_ptr(),
+             shape[0], shape[1], cache[1], shape[2], cache[2], int(window), int(sinks),
+             shape[2] ** -0.5 if scale is None else float(scale), out.data_ptr(), workspace.data_ptr(),
+             workspace.numel() * workspace.element_size(), code, None if err_flag is None else err_flag.data_ptr(),
+             _raw_stream(ix))
     return out

@@ -150,6 +150,49 @@ def test_binding_rejects_host_tensors(eight):
         da.decode_attn_window_fwd(t["q"], t["k"][:2], t["k"][:2], t["n"], 4)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("eight", [False, True], ids=["16bit", "e4m3"])
+def test_binding_says_what_is_wrong(eight):
+    """Every tensor argument in turn with a wrong type, shape, layout or device
+    raises before the library is called; the same call with good ones runs."""
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    t = {n: x.cuda() for n, x in tensors(eight).items()}
+    f32 = dict(dtype=torch.float32, device="cuda")
+    scales = dict(k_scale=t["s"], v_scale=t["s"].clone()) if eight else {}
+    pool = dict(k_pages=t["k"], v_pages=t["k"].clone())
+    append = dict(**pool, **scales, k_new=t["new"], v_new=t["new"], page_table=t["table"], position_ids=t["n"],
+                  token_start=torch.arange(3, dtype=torch.int32, device="cuda"), rope_cos=torch.zeros(48, 64, **f32),
+                  rope_sin=torch.zeros(48, 64, **f32), q=t["q"], q_out=t["q"].clone(),
+                  err_flag=torch.zeros(1, dtype=torch.int32, device="cuda"))
+    ws = da.alloc_paged_workspace(4, 2, 64)
+    attend = dict(q=t["q"], **pool, **scales, page_table=t["table"], kv_len=t["n"], out=t["q"].clone(), workspace=ws,
+                  err_flag=append["err_flag"])
+    window = dict(q=t["q"], k_cache=t["new"][:, :, None], v_cache=t["new"][:, :, None], kv_len=t["n"], window=4,
+                  out=t["q"].clone(), workspace=ws, err_flag=append["err_flag"])
+    calls = [((da.kvcache_append_paged_q8 if eight else da.kvcache_append_paged), append),
+             ((da.decode_attn_paged_q8_fwd if eight else da.decode_attn_paged_fwd), attend)]
+    if not eight:
+        calls.append((da.decode_attn_window_fwd, window))
+    for fn, good in calls:
+        fn(**good)
+        for name, x in good.items():
+            if not isinstance(x, torch.Tensor):
+                continue
+            wrong = [x.cpu()]
+            if name != "workspace":
+                other = torch.float64 if x.dtype != torch.float64 else torch.float32
+                wrong.append(x.to(other))
+            if name not in ("workspace", "err_flag"):
+                wrong.append(torch.cat([x, x]))
+                if x.dim() > 1:
+                    wrong.append(x.transpose(-1, -2).contiguous().transpose(-1, -2) if x.shape[-2] > 1 else x[..., ::2])
+            for bad in wrong:
+                with pytest.raises((ValueError, TypeError)):
+                    fn(**{**good, name: bad})
+    torch.cuda.synchronize()
+
+
 def test_plain_forms_on_known_values():
     """The tests' own plain form: the e4m3 grid against torch's conversion, and
     scales at powers of two."""
