@@ -43,6 +43,7 @@ namespace da {
 constexpr int kHeads = 8;        // columns of the matrix instruction
 constexpr int kMaxCtas = 256;    // one for each SM; parts of one group, at most
 constexpr int kGroupCost = 8;    // what the end of a group costs, in tiles
+constexpr int kJoinCost = 16;    // and of one in parts
 constexpr float kLazy = 8.f;     // m is raised when a score passes it by this (log2)
 // fp16 weights are 2^(x' - m + 7): at most 2^15, inside the type's range, and
 // 2^-32 of the largest one is still held. bf16 has fp32's range: no lift.
@@ -194,6 +195,9 @@ __device__ __forceinline__ uint32_t tile_mask(const SequenceTiles& s, int row0) 
   return mask;
 }
 
+// (out of line: a 64-bit division is some hundred instructions)
+static __device__ __noinline__ int64_t divide(int64_t a, int64_t b) { return a / b; }
+
 template <typename T, bool E4M3, int D>
 __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_attn_kernel(const CacheAttnParams p) {
   using Sh = CacheAttnShape<E4M3, D>;
@@ -239,6 +243,7 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
         const uint32_t fill = n < 0 ? (uint32_t)Storage<T>::kNaN * 0x10001u : 0u;
         if (n < 0 && p.err_flag) atomicOr(p.err_flag, kErrKvLen);
         uint4* out = reinterpret_cast<uint4*>(p.out) + (int64_t)b * p.n_head * (D / 8);
+#pragma unroll 1
         for (int i = 0; i < p.n_head * (D / 8); ++i) out[i] = make_uint4(fill, fill, fill, fill);
       }
     }
@@ -261,9 +266,11 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
   for (int base = 0; base < p.B; base += Sh::kThreads) pass(base, true);
   const int64_t tiles = (before & ((1ll << kCount) - 1)) * p.n_kv_head, groups = (before >> kCount) * p.n_kv_head;
   // as many CTAs as find a tile for every warp
-  const int64_t ctas = min((int64_t)gridDim.x, (tiles + kW - 1) / kW);
+  const int64_t ctas = min((int64_t)gridDim.x, (tiles + kW - 1) >> 3);
+  static_assert(kW == 8, "the shift above");
   if ((int64_t)blockIdx.x >= ctas) return;
-  const int end_cost = groups > ctas ? kGroupCost : 0;
+  const int end_cost =
+      groups > ctas ? kGroupCost : (int)(tiles >= ctas * kJoinCost * 8 ? kJoinCost : (uint32_t)tiles / (uint32_t)ctas / 8);
   auto places = [&](int64_t word) {
     return ((word & ((1ll << kCount) - 1)) + (word >> kCount) * end_cost) * p.n_kv_head;
   };
@@ -272,10 +279,10 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
   // they suffice: a 64-bit division is some hundred instructions)
   const bool small = total * ctas < (1ll << 32);
   auto share_start = [&](int64_t i) {
-    return small ? (int64_t)((uint32_t)i * (uint32_t)total / (uint32_t)ctas) : i * total / ctas;
+    return small ? (int64_t)((uint32_t)i * (uint32_t)total / (uint32_t)ctas) : divide(i * total, ctas);
   };
   auto share_of = [&](int64_t x) {
-    return (int)(small ? ((uint32_t)(x + 1) * (uint32_t)ctas - 1) / (uint32_t)total : ((x + 1) * ctas - 1) / total);
+    return (int)(small ? ((uint32_t)(x + 1) * (uint32_t)ctas - 1) / (uint32_t)total : divide((x + 1) * ctas - 1, total));
   };
   const int64_t lo = share_start(blockIdx.x), hi = share_start(blockIdx.x + 1);
   auto find = [&](int base) {
@@ -301,7 +308,7 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
   {
     const int64_t in = lo - found->start;
     const int size = seq.tiles + end_cost;
-    g = small ? (int)((uint32_t)in / (uint32_t)size) : (int)(in / size);
+    g = small ? (int)((uint32_t)in / (uint32_t)size) : (int)divide(in, size);
     tile = (int)(in - (int64_t)g * size);
   }
   // the next group; false when this share ends before it
@@ -373,6 +380,7 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
         copy16(d + Sh::kTileBytes, vsrc + kLanes * j * 16);
       }
     } else {
+#pragma unroll 1
       for (int j = 0; j < kCopies; ++j) {
         const int x = sub + kLanes * j, r = x / kChunks;
         const bool on = (rows >> r) & 1;
@@ -389,26 +397,18 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
     if (sub == 2) asm volatile("st.shared.u32 [%0], %1;" ::"r"(m + 16 + half * 4), "r"((uint32_t)bad) : "memory");
     if (bad && sub == 0 && p.err_flag) atomicOr(p.err_flag, kErrPage);
   };
-  int put = kS - 1;  // stage that the next load goes to
-  {
-    // the first kS - 1 tiles: their page numbers are looked up together
-    int rows[kS - 1], pages[kS - 1], heads[kS - 1];
-    uint32_t masks[kS - 1];
-#pragma unroll
-    for (int j = 0; j < kS - 1; ++j) {
-      look_up(j ? kW : warp);
-      rows[j] = lrow;
-      pages[j] = lpage;
-      heads[j] = lg;
-      masks[j] = lmask;
+  int put = 0;  // stage that the next load goes to
+  auto load_next = [&]() {
+    if (lmask) {
+      issue(put, lrow, lpage, lmask, lg);
+      look_up(kW);
     }
-#pragma unroll
-    for (int j = 0; j < kS - 1; ++j) {
-      if (masks[j]) issue(j, rows[j], pages[j], masks[j], heads[j]);
-      copy_commit();
-    }
-    look_up(kW);
-  }
+    copy_commit();
+    put = put + 1 == kS ? 0 : put + 1;
+  };
+  look_up(warp);
+#pragma unroll 1
+  for (int j = 0; j < kS - 1; ++j) load_next();
 
   // --- group by group
   int get = 0;      // stage of this warp's next tile
@@ -477,12 +477,7 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
       copy_wait<kS - 2>();
       __syncwarp();
       // refill the stage that the tile before this one has left
-      if (lmask) {
-        issue(put, lrow, lpage, lmask, lg);
-        look_up(kW);
-      }
-      copy_commit();
-      put = put + 1 == kS ? 0 : put + 1;
+      load_next();
       const uint32_t stage = ring + get * Sh::kStageBytes, m = meta + get * Sh::kMetaBytes;
       get = get + 1 == kS ? 0 : get + 1;
       uint32_t bad[2];
