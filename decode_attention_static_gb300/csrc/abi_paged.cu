@@ -47,6 +47,9 @@ int check_pages(int num_pages, int page_size, int max_pages) {
 
 int run_attention(CacheAttnParams p, int head_dim, bool e4m3, float scale, void* workspace, size_t workspace_bytes,
                   int dtype, void* stream) {
+  // the kernel numbers the 16-row tiles of a CTA's share (at least 1 / 128 of
+  // all) in 32 bits
+  if ((int64_t)p.B * p.n_kv_head * ((int64_t)p.max_len / 16 + 32) >= (1ll << 37)) return DA_ERR_SHAPE;
   if (!p.q || !p.k || !p.v || !p.kv_len || !p.out) return DA_ERR_NULL;
   if (!aligned(p.q, 16) || !aligned(p.k, 16) || !aligned(p.v, 16) || !aligned(p.out, 16)) return DA_ERR_ALIGN;
   if (!aligned(p.kv_len, 4) || !aligned(p.table, 4) || !aligned(p.k_scale, 4) || !aligned(p.v_scale, 4) ||

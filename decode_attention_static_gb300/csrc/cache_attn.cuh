@@ -44,6 +44,9 @@ constexpr int kHeads = 8;        // columns of the matrix instruction
 constexpr int kMaxCtas = 256;    // one for each SM; parts of one group, at most
 constexpr int kGroupCost = 8;    // what the end of a group costs, in tiles
 constexpr int kJoinCost = 16;    // and of one in parts
+// A group in more than kJoinWide parts (at most 256) is joined in two rounds, of
+// kJoinWidth neighbours and of the sums of those.
+constexpr int kJoinWide = 32, kJoinWidth = 16;
 constexpr float kLazy = 8.f;     // m is raised when a score passes it by this (log2)
 // fp16 weights are 2^(x' - m + 7): at most 2^15, inside the type's range, and
 // 2^-32 of the largest one is still held. bf16 has fp32's range: no lift.
@@ -57,20 +60,22 @@ struct CacheAttnShape {
   static constexpr int kRows = kRowBytes > 128 ? 16 : 32;  // of a tile, in pieces of 16
   static constexpr int kTileBytes = kRows * kRowBytes;
   static constexpr int kStageBytes = 2 * kTileBytes;  // K tile, V tile
-  static constexpr int kStages = 24576 / kStageBytes;
+  static constexpr int kStages = 196608 / (kWarps * kStageBytes);
   static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
   static constexpr int kMergeFloats = kWarps * kHeads * D;
   static constexpr int kMergeBytes = kMergeFloats * 4;
   static constexpr int kMetaOffset = kRingBytes + kMergeBytes;
-  static constexpr int kMetaBytes = 32;  // of a stage: K and V scale of each piece, bad pages
+  static constexpr int kMetaBytes = 32;  // of a stage: K and V scale of each piece, bad pages, visible rows
   static constexpr int kStatOffset = kMetaOffset + kWarps * kStages * kMetaBytes;
-  // (m, l) of each warp, l of a group; schedule words
-  static constexpr int kStatFloats = 2 * kWarps * kHeads + kHeads;
+  // (m, l) of each warp, and of joined parts; schedule words
+  static constexpr int kStatFloats = 2 * kWarps * kHeads + 2 * kHeads;
   static constexpr int kWordsOffset = kStatOffset + kStatFloats * 4;
   static constexpr int kSmemBytes = kWordsOffset + (kWarps + 4) * 8;
   static_assert(kStages >= 3, "a ring of at least three stages");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory of a CTA");
-  static_assert(kMaxCtas * kHeads * 4 + kThreads * 16 <= kMergeBytes, "the join's factors and sums fit the merge buffer");
+  static_assert(kJoinWide * kHeads * 4 + kThreads * 16 <= kMergeBytes, "the join's factors and sums fit the merge buffer");
+  static_assert(kMaxCtas <= kJoinWidth * kJoinWidth && kJoinWide <= 32 && 3 * kMaxCtas <= kMaxCounterGroups,
+                "two rounds of parts that a warp holds; a counter for each CTA and round");
   static_assert(kHeads * (D / 4) <= kThreads && kHeads <= kWarps, "a thread for each output vector, a warp for each head");
 };
 
@@ -209,7 +214,8 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
   float* merge = reinterpret_cast<float*>(smem + Sh::kRingBytes);
   float* sm_m = reinterpret_cast<float*>(smem + Sh::kStatOffset);  // [kW][8]
   float* sm_l = sm_m + kW * kHeads;
-  float* sm_gl = sm_l + kW * kHeads;  // l of a group in parts
+  float* sm_gl = sm_l + kW * kHeads;  // l and m of joined parts
+  float* sm_gm = sm_gl + kHeads;
   int64_t* words = reinterpret_cast<int64_t*>(smem + Sh::kWordsOffset);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, gr = lane >> 2, tq = lane & 3;
 
@@ -266,11 +272,13 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
   for (int base = 0; base < p.B; base += Sh::kThreads) pass(base, true);
   const int64_t tiles = (before & ((1ll << kCount) - 1)) * p.n_kv_head, groups = (before >> kCount) * p.n_kv_head;
   // as many CTAs as find a tile for every warp
-  const int64_t ctas = min((int64_t)gridDim.x, (tiles + kW - 1) >> 3);
-  static_assert(kW == 8, "the shift above");
+  const int64_t ctas = min((int64_t)gridDim.x, (tiles + kW - 1) / kW);
   if ((int64_t)blockIdx.x >= ctas) return;
-  const int end_cost =
-      groups > ctas ? kGroupCost : (int)(tiles >= ctas * kJoinCost * 8 ? kJoinCost : (uint32_t)tiles / (uint32_t)ctas / 8);
+  int end_cost = kGroupCost;
+  if (groups <= ctas) {
+    const uint32_t n = (uint32_t)ctas;
+    end_cost = n % (uint32_t)groups == 0 ? 0 : (int)(tiles >= ctas * kJoinCost * 8 ? kJoinCost : (uint32_t)tiles / n / 8);
+  }
   auto places = [&](int64_t word) {
     return ((word & ((1ll << kCount) - 1)) + (word >> kCount) * end_cost) * p.n_kv_head;
   };
@@ -304,7 +312,8 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
   SequenceTiles seq;
   tiles_of<kRows>(p, found->len, &seq);
   int g, tile;       // group of list position `lo`, and its place there
-  int64_t at = lo;   // list position of the next tile to compute
+  const int share = (int)(hi - lo);  // (below 2^31: checked on the host)
+  int at = 0;        // place in the share of the next tile to compute
   {
     const int64_t in = lo - found->start;
     const int size = seq.tiles + end_cost;
@@ -312,8 +321,8 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
     tile = (int)(in - (int64_t)g * size);
   }
   // the next group; false when this share ends before it
-  auto next_group = [&](int64_t& place, int& b, int& g, SequenceTiles& s) {
-    if (place >= hi) return false;
+  auto next_group = [&](int place, int& b, int& g, SequenceTiles& s) {
+    if (place >= share) return false;
     if (++g == p.n_kv_head) {
       g = 0;
       do ++b;
@@ -337,7 +346,7 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
   SequenceTiles lseq = seq;  // the tile to load next, its page number on the way
   int lb = b, lg = g, li = tile, lrow = 0, lpage = 0;
   uint32_t lmask = 0;  // 0: no tile is left
-  int64_t lat = at;
+  int lat = at;
   bool more = true;
   auto look_up = [&](int step) {  // moves on by `step` tiles
     lat += step;
@@ -346,10 +355,9 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
     while (more && li >= lseq.tiles) {
       li -= lseq.tiles;
       lat += end_cost;
-      int64_t start = lat - li;
-      more = next_group(start, lb, lg, lseq);
+      more = next_group(lat - li, lb, lg, lseq);
     }
-    more = more && lat < hi;
+    more = more && lat < share;
     if (!more) return;
     const int row0 = tile_row<kRows>(lseq, li);
     lmask = tile_mask<kRows>(lseq, row0);
@@ -395,6 +403,7 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
       if (sub < 2) copy4_or_zero(m + half * 8 + sub * 4, (sub ? p.v_scale : p.k_scale) + block, rows ? 4 : 0);
     }
     if (sub == 2) asm volatile("st.shared.u32 [%0], %1;" ::"r"(m + 16 + half * 4), "r"((uint32_t)bad) : "memory");
+    if (lane == 3) asm volatile("st.shared.u32 [%0], %1;" ::"r"(m + 24), "r"(mask) : "memory");
     if (bad && sub == 0 && p.err_flag) atomicOr(p.err_flag, kErrPage);
   };
   int put = 0;  // stage that the next load goes to
@@ -414,7 +423,7 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
   int get = 0;      // stage of this warp's next tile
   int turn = warp;  // tiles until this warp's next one
   for (;;) {
-    const int here = (int)min((int64_t)(seq.tiles - tile), hi - at);  // tiles of the group in this share
+    const int here = min(seq.tiles - tile, share - at);  // tiles of the group in this share
     // q as the right operand: columns are heads
     uint32_t qb[kSteps][2];
     float scale0 = p.qscale, scale1 = p.qscale;
@@ -473,16 +482,16 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
     for (int k = 0; k < kSteps; ++k) o[k][0] = o[k][1] = o[k][2] = o[k][3] = 0.f;
 
     for (; turn < here; turn += kW) {
-      const uint32_t mask = tile_mask<kRows>(seq, tile_row<kRows>(seq, tile + turn));
       copy_wait<kS - 2>();
       __syncwarp();
       // refill the stage that the tile before this one has left
       load_next();
       const uint32_t stage = ring + get * Sh::kStageBytes, m = meta + get * Sh::kMetaBytes;
       get = get + 1 == kS ? 0 : get + 1;
-      uint32_t bad[2];
+      uint32_t bad[2], mask;
       float scales[4];  // K and V of either piece
       asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(bad[0]), "=r"(bad[1]) : "r"(m + 16));
+      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(mask) : "r"(m + 24));
       if constexpr (E4M3)
         asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
                      : "=f"(scales[0]), "=f"(scales[1]), "=f"(scales[2]), "=f"(scales[3])
@@ -571,39 +580,53 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
           pl[i][e] = transpose8x8(pl[i][e]);
         }
       }
-      const int vr = (lane & 7) + ((lane >> 4) & 1) * 8;
+      const uint32_t vst = stage + Sh::kTileBytes;
+      if constexpr (!E4M3) {
+        const int vr = (lane & 7) + ((lane >> 4) & 1) * 8;
 #pragma unroll
-      for (int i = 0; i < kHalves; ++i) {
-        const uint32_t vst = stage + Sh::kTileBytes + i * 16 * Sh::kRowBytes;
-        if constexpr (!E4M3) {
+        for (int i = 0; i < kHalves; ++i) {
 #pragma unroll
           for (int k = 0; k < kSteps; ++k) {
             uint32_t a[4];
-            ldmatrix_x4_trans(vst + chunk_offset<Sh::kRowBytes>(vr, 2 * k + ((lane >> 3) & 1)), a);
+            ldmatrix_x4_trans(vst + i * 16 * Sh::kRowBytes + chunk_offset<Sh::kRowBytes>(vr, 2 * k + ((lane >> 3) & 1)),
+                              a);
             mma_16x8x16<kBf16>(o[k], a[0], a[1], a[2], a[3], ph[i][0], ph[i][1]);
             mma_16x8x16<kBf16>(o[k], a[0], a[1], a[2], a[3], pl[i][0], pl[i][1]);
           }
-        } else {
-          // A transposed 16-bit unit holds two neighbouring elements of a row:
-          // bytes are paired along the rows, and a lane's output rows are
-          // elements 2 gr and 2 gr + 1. The scale multiplies the piece's sum
-          // (and takes the lift out of it: V may be as large as fp32 holds).
-          const float vs = scales[2 * i + 1] * (1.f / (1 << (int)kLift));
+        }
+      } else {
+        // A transposed 16-bit unit holds two neighbouring elements of a row:
+        // bytes are paired along the rows, and a lane's output rows are
+        // elements 2 gr and 2 gr + 1. The scale multiplies the sum of the
+        // pieces that share it (and takes the lift out of it: V may be as large
+        // as fp32 holds).
+        const float vs0 = scales[1] * (1.f / (1 << (int)kLift)), vs1 = scales[3] * (1.f / (1 << (int)kLift));
+        const bool apart = vs0 != vs1;
 #pragma unroll
-          for (int k = 0; k < kSteps; k += 2) {
+        for (int k = 0; k < kSteps; k += 2) {
+          float t[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
             uint32_t a[4];
-            ldmatrix_x4_trans(vst + chunk_offset<Sh::kRowBytes>(mr, k + (lane >> 4)), a);
+            ldmatrix_x4_trans(vst + i * 16 * Sh::kRowBytes + chunk_offset<Sh::kRowBytes>(mr, k + (lane >> 4)), a);
 #pragma unroll
             for (int e = 0; e < 4; ++e) a[e] = __byte_perm(a[e], 0, 0x3120);
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
               const uint32_t v0 = e4m3_low(a[2 * n]), v1 = e4m3_high(a[2 * n]), v2 = e4m3_low(a[2 * n + 1]),
                              v3 = e4m3_high(a[2 * n + 1]);
-              float t[4] = {0.f, 0.f, 0.f, 0.f};
-              mma_16x8x16<false>(t, v0, v1, v2, v3, ph[i][0], ph[i][1]);
-              mma_16x8x16<false>(t, v0, v1, v2, v3, pl[i][0], pl[i][1]);
+              mma_16x8x16<false>(t[n], v0, v1, v2, v3, ph[i][0], ph[i][1]);
+              mma_16x8x16<false>(t[n], v0, v1, v2, v3, pl[i][0], pl[i][1]);
+            }
+            if (i == 1 || apart) {
+              const float vs = i ? vs1 : vs0;
 #pragma unroll
-              for (int e = 0; e < 4; ++e) o[k + n][e] = fmaf(vs, t[e], o[k + n][e]);
+              for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  o[k + n][e] = fmaf(vs, t[n][e], o[k + n][e]);
+                  if (i == 0) t[n][e] = 0.f;
+                }
             }
           }
         }
@@ -648,7 +671,7 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
     const bool whole = here == seq.tiles;
     const int items = p.group * (D / 4);  // outputs in vectors of 4
     // shares that hold the group, and this one's partial state
-    const int64_t group_start = at - tile;
+    const int64_t group_start = lo + at - tile;
     const int slot_floats = cache_attn_slot_floats(p.group, D);
     int from = 0, parts = 1;
     if (!whole) {
@@ -700,77 +723,101 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
       }
     }
     if (!whole) {
-      __syncthreads();
+      // Join the parts: the last CTA to arrive at a counter joins the parts that
+      // are counted there. Many parts are joined in two rounds, neighbours
+      // first, into the slot of the first of them.
+      const int part = (int)blockIdx.x - from;
+      int width = parts > kJoinWide ? kJoinWidth : parts;  // parts counted together
+      int head = parts > kJoinWide ? part / kJoinWidth * kJoinWidth : 0, step = 1;  // the first of them, and their distance
       unsigned int* arrived = reinterpret_cast<unsigned int*>(&words[kW + 2]);
-      if (tid == 0) {
-        __threadfence();  // (cumulative: the CTA's writes before the barrier)
-        *arrived = atomicAdd(p.counters + from, 1u);
-        __threadfence();
-      }
-      __syncthreads();
-      const unsigned int order = *arrived;
-      if (order >= (unsigned int)parts) {
-        // the counter was not zero before this call
-        if (tid == 0 && p.err_flag) atomicOr(p.err_flag, kErrWorkspace);
-        const uint32_t nan2 = (uint32_t)Storage<T>::kNaN * 0x10001u;
-        if (tid < items) *reinterpret_cast<uint2*>(out + tid * 8) = make_uint2(nan2, nan2);
-      } else if (order == (unsigned int)parts - 1) {
-        // the last to arrive joins the partial states: the threads share the
-        // vectors, and with fewer vectors than threads also the parts; the
-        // first eight of a thread are on their way while the warps find the
-        // parts' factors
-        float* factor = merge;                        // [parts][8]
-        float4* sums = reinterpret_cast<float4*>(merge + kMaxCtas * kHeads);  // [kThreads]
+      for (;;) {
+        const bool last_round = width == parts || step > 1;
+        const int count = min((parts - head + step - 1) / step, width);
+        // the last round's counter is that of the group's first share; a share
+        // leads the first round of at most one group as its part 0 and of one
+        // as a later part
+        unsigned int* counter = p.counters + (last_round ? from : (head ? 2 : 1) * kMaxCtas + from + head);
+        __syncthreads();
+        if (tid == 0) {
+          __threadfence();  // (cumulative: the CTA's writes before the barrier)
+          *arrived = atomicAdd(counter, 1u);
+          __threadfence();
+        }
+        __syncthreads();
+        const unsigned int order = *arrived;
+        if (order >= (unsigned int)count) {
+          // the counter was not zero before this call
+          if (tid == 0 && p.err_flag) atomicOr(p.err_flag, kErrWorkspace);
+          const uint32_t nan2 = (uint32_t)Storage<T>::kNaN * 0x10001u;
+          if (tid < items) *reinterpret_cast<uint2*>(out + tid * 8) = make_uint2(nan2, nan2);
+          break;
+        }
+        if (order != (unsigned int)count - 1) break;
+        // the threads share the vectors, and with fewer vectors than threads also
+        // the parts; a thread's first eight are on their way while the warps
+        // find the parts' factors
+        float* factor = merge;                        // [count][8]
+        float4* sums = reinterpret_cast<float4*>(merge + kJoinWide * kHeads);  // [kThreads]
         const int crews = Sh::kThreads / items, crew = tid / items, i = tid - crew * items, h = i / (D / 4);
-        const bool busy = crew < crews;
         float4 v[8], r = make_float4(0.f, 0.f, 0.f, 0.f);
         auto fetch = [&](int s0) {
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            if (busy && s0 + j * crews < parts)
-              v[j] = __ldcg(reinterpret_cast<const float4*>(slot_of(s0 + j * crews)) + i);
+            if (s0 + j * crews < count)
+              v[j] = __ldcg(reinterpret_cast<const float4*>(slot_of(head + (s0 + j * crews) * step)) + i);
         };
         fetch(crew);
         if (warp < p.group) {
-          // lane s has part s (the m and l of the first 32 parts are read together)
+          // lane s has part s
           float m_s = -INFINITY, l_s = 0.f;
-          if (lane < parts) {
-            m_s = __ldcg(slot_of(lane) + p.group * D + warp);
-            l_s = __ldcg(slot_of(lane) + p.group * D + p.group + warp);
+          const float* at_s = slot_of(head + lane * step) + p.group * D + warp;
+          if (lane < count) {
+            m_s = __ldcg(at_s);
+            l_s = __ldcg(at_s + p.group);
           }
-          float mm = m_s, ll = 0.f;
-          for (int s = lane + 32; s < parts; s += 32) mm = fmaxf(mm, __ldcg(slot_of(s) + p.group * D + warp));
+          float mm = m_s;
 #pragma unroll
           for (int k = 16; k; k >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, k));
-          for (int s = lane; s < parts; s += 32) {
-            if (s >= 32) {
-              m_s = __ldcg(slot_of(s) + p.group * D + warp);
-              l_s = __ldcg(slot_of(s) + p.group * D + p.group + warp);
-            }
-            const float f = m_s == mm ? 1.f : fast_exp2(m_s - mm);
-            factor[s * kHeads + warp] = f;
-            ll = fmaf(f, l_s, ll);
-          }
+          const float f = m_s == mm ? 1.f : fast_exp2(m_s - mm);
+          if (lane < count) factor[lane * kHeads + warp] = f;
+          float ll = lane < count ? f * l_s : 0.f;
 #pragma unroll
           for (int k = 16; k; k >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, k);
-          if (lane == 0) sm_gl[warp] = ll;
+          if (lane == 0) {
+            sm_gl[warp] = ll;
+            sm_gm[warp] = mm;
+          }
         }
         __syncthreads();
-        for (int s0 = crew; busy && s0 < parts;) {
+        for (int s0 = crew; s0 < count;) {
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            if (s0 + j * crews < parts) add(r, factor[(s0 + j * crews) * kHeads + h], v[j]);
+            if (s0 + j * crews < count) add(r, factor[(s0 + j * crews) * kHeads + h], v[j]);
           s0 += 8 * crews;
-          if (s0 < parts) fetch(s0);
+          if (s0 < count) fetch(s0);
         }
         if (crews > 1) {
-          if (busy) sums[tid] = r;
+          sums[tid] = r;
           __syncthreads();
           if (crew == 0)
             for (int c = 1; c < crews; ++c) add(r, 1.f, sums[c * items + i]);
         }
-        if (crew == 0) store(i, r, sm_gl[h]);
-        if (tid == 0) p.counters[from] = 0;  // ready for the next call
+        if (tid == 0) *counter = 0;  // ready for the next call
+        if (last_round) {
+          if (crew == 0) store(i, r, sm_gl[h]);
+          break;
+        }
+        float* joined = slot_of(head);
+        if (crew == 0) {
+          __stcg(reinterpret_cast<float4*>(joined) + i, r);
+          if (i % (D / 4) == 0) {
+            __stcg(joined + p.group * D + h, sm_gm[h]);
+            __stcg(joined + p.group * D + p.group + h, sm_gl[h]);
+          }
+        }
+        width = (parts + kJoinWidth - 1) / kJoinWidth;
+        head = 0;
+        step = kJoinWidth;
       }
     }
     __syncthreads();  // the merge buffer is free
