@@ -42,11 +42,12 @@ namespace da {
 
 constexpr int kHeads = 8;        // columns of the matrix instruction
 constexpr int kMaxCtas = 256;    // one for each SM; parts of one group, at most
+constexpr int kFewestTiles = 8;  // of a share
 constexpr int kGroupCost = 8;    // what the end of a group costs, in tiles
 constexpr int kJoinCost = 16;    // and of one in parts
 // A group in more than kJoinWide parts (at most 256) is joined in two rounds, of
 // kJoinWidth neighbours and of the sums of those.
-constexpr int kJoinWide = 32, kJoinWidth = 16;
+constexpr int kJoinWide = 64, kJoinWidth = 16;
 constexpr float kLazy = 8.f;     // m is raised when a score passes it by this (log2)
 // fp16 weights are 2^(x' - m + 7): at most 2^15, inside the type's range, and
 // 2^-32 of the largest one is still held. bf16 has fp32's range: no lift.
@@ -54,7 +55,7 @@ constexpr float kLiftF16 = 7.f;
 
 template <bool E4M3, int D>
 struct CacheAttnShape {
-  static constexpr int kWarps = 8;
+  static constexpr int kWarps = E4M3 && D == 64 ? 12 : 8;
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kRowBytes = E4M3 ? D : 2 * D;
   static constexpr int kRows = kRowBytes > 128 ? 16 : 32;  // of a tile, in pieces of 16
@@ -74,7 +75,7 @@ struct CacheAttnShape {
   static_assert(kStages >= 3, "a ring of at least three stages");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory of a CTA");
   static_assert(kJoinWide * kHeads * 4 + kThreads * 16 <= kMergeBytes, "the join's factors and sums fit the merge buffer");
-  static_assert(kMaxCtas <= kJoinWidth * kJoinWidth && kJoinWide <= 32 && 3 * kMaxCtas <= kMaxCounterGroups,
+  static_assert(kMaxCtas <= kJoinWidth * kJoinWidth && kJoinWide <= 64 && 3 * kMaxCtas <= kMaxCounterGroups,
                 "two rounds of parts that a warp holds; a counter for each CTA and round");
   static_assert(kHeads * (D / 4) <= kThreads && kHeads <= kWarps, "a thread for each output vector, a warp for each head");
 };
@@ -271,8 +272,8 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
   };
   for (int base = 0; base < p.B; base += Sh::kThreads) pass(base, true);
   const int64_t tiles = (before & ((1ll << kCount) - 1)) * p.n_kv_head, groups = (before >> kCount) * p.n_kv_head;
-  // as many CTAs as find a tile for every warp
-  const int64_t ctas = min((int64_t)gridDim.x, (tiles + kW - 1) / kW);
+  // as many CTAs as find kFewestTiles
+  const int64_t ctas = min((int64_t)gridDim.x, (tiles + kFewestTiles - 1) / kFewestTiles);
   if ((int64_t)blockIdx.x >= ctas) return;
   int end_cost = kGroupCost;
   if (groups <= ctas) {
@@ -768,19 +769,29 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
         };
         fetch(crew);
         if (warp < p.group) {
-          // lane s has part s
-          float m_s = -INFINITY, l_s = 0.f;
-          const float* at_s = slot_of(head + lane * step) + p.group * D + warp;
-          if (lane < count) {
-            m_s = __ldcg(at_s);
-            l_s = __ldcg(at_s + p.group);
+          // lane s has parts s and s + 32
+          float m_s[2] = {-INFINITY, -INFINITY}, l_s[2] = {0.f, 0.f};
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int s = lane + 32 * k;
+            const float* at_s = slot_of(head + s * step) + p.group * D + warp;
+            if (s < count) {
+              m_s[k] = __ldcg(at_s);
+              l_s[k] = __ldcg(at_s + p.group);
+            }
           }
-          float mm = m_s;
+          float mm = fmaxf(m_s[0], m_s[1]), ll = 0.f;
 #pragma unroll
           for (int k = 16; k; k >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, k));
-          const float f = m_s == mm ? 1.f : fast_exp2(m_s - mm);
-          if (lane < count) factor[lane * kHeads + warp] = f;
-          float ll = lane < count ? f * l_s : 0.f;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int s = lane + 32 * k;
+            if (s < count) {
+              const float f = m_s[k] == mm ? 1.f : fast_exp2(m_s[k] - mm);
+              factor[s * kHeads + warp] = f;
+              ll += f * l_s[k];
+            }
+          }
 #pragma unroll
           for (int k = 16; k; k >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, k);
           if (lane == 0) {
