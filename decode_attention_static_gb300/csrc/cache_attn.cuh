@@ -237,15 +237,18 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
   constexpr int kCount = 44;  // tiles and non-empty sequences are summed in one word: tiles + sequences * 2^44
   int64_t before = 0, mine = 0, own = 0;  // before this pass, before this thread's sequence, and its own
   int len = 0;
+  // (with one warp's worth of sequences every warp does it alone: no barrier)
+  const bool alone = p.B <= 32;
+  const int column = alone ? lane : tid, columns = alone ? 32 : Sh::kThreads;
   auto pass = [&](int base, bool idle_rows) {
-    const int b = base + tid;
+    const int b = base + column;
     own = 0;
     if (b < p.B) {
       SequenceTiles s;
       len = p.kv_len[b];
       const int n = tiles_of<kRows>(p, len, &s);
       if (n > 0) own = n + (1ll << kCount);
-      if (idle_rows && n <= 0 && b % gridDim.x == blockIdx.x) {
+      if (idle_rows && n <= 0 && column == tid && b % gridDim.x == blockIdx.x) {
         // no visible row: zeros; no valid length: NaN
         const uint32_t fill = n < 0 ? (uint32_t)Storage<T>::kNaN * 0x10001u : 0u;
         if (n < 0 && p.err_flag) atomicOr(p.err_flag, kErrKvLen);
@@ -255,22 +258,26 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
       }
     }
     int64_t sum = own;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
+#pragma unroll 1
+    for (int o = 1; o < 32 && o < p.B; o <<= 1) {
       const int64_t v = __shfl_up_sync(0xffffffffu, sum, o);
       if (lane >= o) sum += v;
+    }
+    mine = before + sum - own;
+    if (alone) {
+      before = __shfl_sync(0xffffffffu, sum, p.B - 1);
+      return;
     }
     if (base) __syncthreads();  // the words of the pass before have been read
     if (lane == 31) words[warp] = sum;
     __syncthreads();
-    mine = before + sum - own;
 #pragma unroll
     for (int w = 0; w < kW; ++w) {
       if (w < warp) mine += words[w];
       before += words[w];
     }
   };
-  for (int base = 0; base < p.B; base += Sh::kThreads) pass(base, true);
+  for (int base = 0; base < p.B; base += columns) pass(base, true);
   const int64_t tiles = (before & ((1ll << kCount) - 1)) * p.n_kv_head, groups = (before >> kCount) * p.n_kv_head;
   // as many CTAs as find kFewestTiles
   const int64_t ctas = min((int64_t)gridDim.x, (tiles + kFewestTiles - 1) / kFewestTiles);
@@ -294,29 +301,36 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
     return (int)(small ? ((uint32_t)(x + 1) * (uint32_t)ctas - 1) / (uint32_t)total : divide((x + 1) * ctas - 1, total));
   };
   const int64_t lo = share_start(blockIdx.x), hi = share_start(blockIdx.x + 1);
-  auto find = [&](int base) {
+  Found here_first;  // the sequence that holds `lo`
+  auto holds = [&]() {
     const int64_t at = places(mine);
-    if (at <= lo && lo < at + places(own)) *found = {at, base + tid, len};
+    return at <= lo && lo < at + places(own);
   };
-  if (p.B <= Sh::kThreads) {
-    find(0);
+  if (alone) {
+    const int src = __ffs(__ballot_sync(0xffffffffu, holds())) - 1;
+    here_first = {__shfl_sync(0xffffffffu, places(mine), src), src, __shfl_sync(0xffffffffu, len, src)};
   } else {
-    before = 0;
-    for (int base = 0; places(before) <= lo; base += Sh::kThreads) {
-      __syncthreads();
-      pass(base, false);
-      find(base);
+    if (p.B <= Sh::kThreads) {
+      if (holds()) *found = {places(mine), tid, len};
+    } else {
+      before = 0;
+      for (int base = 0; places(before) <= lo; base += Sh::kThreads) {
+        __syncthreads();
+        pass(base, false);
+        if (holds()) *found = {places(mine), base + tid, len};
+      }
     }
+    __syncthreads();
+    here_first = *found;
   }
-  __syncthreads();
-  int b = found->b;
+  int b = here_first.b;
   SequenceTiles seq;
-  tiles_of<kRows>(p, found->len, &seq);
+  tiles_of<kRows>(p, here_first.len, &seq);
   int g, tile;       // group of list position `lo`, and its place there
   const int share = (int)(hi - lo);  // (below 2^31: checked on the host)
   int at = 0;        // place in the share of the next tile to compute
   {
-    const int64_t in = lo - found->start;
+    const int64_t in = lo - here_first.start;
     const int size = seq.tiles + end_cost;
     g = small ? (int)((uint32_t)in / (uint32_t)size) : (int)divide(in, size);
     tile = (int)(in - (int64_t)g * size);
