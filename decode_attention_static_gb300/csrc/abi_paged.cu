@@ -51,6 +51,7 @@ int run_attention(CacheAttnParams p, int head_dim, bool e4m3, float scale, void*
   // all) in 32 bits
   if ((int64_t)p.B * p.n_kv_head * ((int64_t)p.max_len / 16 + 32) >= (1ll << 37)) return DA_ERR_SHAPE;
   if (!p.q || !p.k || !p.v || !p.kv_len || !p.out) return DA_ERR_NULL;
+  if (p.out == p.q) return DA_ERR_SHAPE;  // CTAs read q while others write out
   if (!aligned(p.q, 16) || !aligned(p.k, 16) || !aligned(p.v, 16) || !aligned(p.out, 16)) return DA_ERR_ALIGN;
   if (!aligned(p.kv_len, 4) || !aligned(p.table, 4) || !aligned(p.k_scale, 4) || !aligned(p.v_scale, 4) ||
       !aligned(p.err_flag, 4))
@@ -123,6 +124,7 @@ int append_paged(void* k_pages, void* v_pages, float* k_scale, float* v_scale, b
   if ((rope_cos != nullptr) != (rope_sin != nullptr)) return DA_ERR_NULL;
   if (q && (!q_out || !rope_cos)) return DA_ERR_NULL;
   if (rope_cos && rope_rows < 1) return DA_ERR_SHAPE;
+  if (k_pages == v_pages || (e4m3 && k_scale == v_scale)) return DA_ERR_SHAPE;  // K and V need arrays of their own
   const void* wide[] = {k_pages, v_pages, k_new, v_new, q, q ? q_out : nullptr, rope_cos, rope_sin};
   for (const void* w : wide)
     if (!aligned(w, 16)) return DA_ERR_ALIGN;

@@ -382,7 +382,9 @@ DA_API int decode_attn_fwd_static_scratch(const void* q, const void* k_cache, co
  * infinities),
  *   k_scale, v_scale  fp32 [num_pages, n_kv_head]: element x of a page and KV
  *                     head stands for x * scale.
- * max_pages * page_size stays below 2^31 - 512 (else DA_ERR_SHAPE).
+ * max_pages * page_size stays below 2^31 - 512, and B * n_kv_head times the
+ * 16-row tiles of that below 2^37 (else DA_ERR_SHAPE). Arrays that a call
+ * writes overlap no other argument, but for q_out, which may be q itself.
  */
 
 /*
@@ -401,7 +403,8 @@ DA_API int decode_attn_fwd_static_scratch(const void* q, const void* k_cache, co
  * A sequence whose positions do not all lie in [0, max_pages * page_size) and
  * [0, rope_rows) is skipped whole and sets DA_DEVERR_POSITION (its q_out rows
  * become NaN); rows of a page id outside the pool are skipped and set
- * DA_DEVERR_PAGE. Only the appended rows of a page are written.
+ * DA_DEVERR_PAGE. Only the appended rows of a page are written. k_pages and
+ * v_pages are two arrays (else DA_ERR_SHAPE).
  */
 DA_API int kvcache_append_paged(void* k_pages, void* v_pages, const void* k_new, const void* v_new, const void* q,
                     void* q_out, const float* rope_cos, const float* rope_sin, int rope_rows,
@@ -446,12 +449,15 @@ DA_API size_t decode_attn_paged_workspace_size(int n_head, int n_kv_head, int he
  * (the last `window` rows, the query's own among them, and the first `sinks`
  * ones), and out[b, h, :] = softmax_j(scale <q[b, h], K_j>) V_j over those
  * rows, fp32 arithmetic, rounded once. Rows that are not visible are not
- * read. kv_len[b] == 0 (an idle slot of a batch) gives a row of zeros;
+ * read; NaN among the visible ones reaches the heads that read it, and an
+ * infinite element of V makes that element of its heads' outputs NaN.
+ * kv_len[b] == 0 (an idle slot of a batch) gives a row of zeros;
  * kv_len[b] < 0 or > max_pages * page_size gives NaN and DA_DEVERR_KV_LEN; a
  * page id outside the pool gives NaN for the heads that would read it and
  * DA_DEVERR_PAGE. window >= 0, sinks >= 0, and sinks > 0 needs window > 0
  * (else DA_ERR_SHAPE). No length bound is needed: the launch does not depend
- * on the lengths, so a captured graph serves any of them.
+ * on the lengths, so a captured graph serves any of them. Equal calls give
+ * equal bits. out must not be q (DA_ERR_SHAPE).
  */
 DA_API int decode_attn_paged_fwd(const void* q, const void* k_pages, const void* v_pages, const int32_t* page_table,
                     const int32_t* kv_len, int B, int n_head, int n_kv_head, int head_dim, int num_pages,

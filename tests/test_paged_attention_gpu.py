@@ -163,11 +163,52 @@ def test_splits_and_batches(lens, H, Hkv, page, eight):
     check(Case(lens, H, Hkv, 128, "bf16", page, eight, seed=len(lens)), f"{len(lens)} sequences")
 
 
+@pytest.mark.parametrize("eight", [False, True], ids=["16bit", "e4m3"])
+@pytest.mark.parametrize("lens,H,Hkv,D", [([70001], 8, 1, 128), ([40000], 2, 2, 64), ([30000, 5, 45000], 1, 1, 128)])
+def test_groups_in_many_parts(lens, H, Hkv, D, eight):
+    """Few heads with long prefixes: a group lies in up to every CTA's share and
+    is joined in two rounds; twice, so that every counter is back at zero."""
+    case = Case(lens, H, Hkv, D, "bf16", 64, eight, seed=len(lens))
+    ws = da.alloc_paged_workspace(H, Hkv, D)
+    first = check(case, f"{lens}", workspace=ws).clone()
+    assert not ws[:4096].any()
+    assert torch.equal(R.bits(case.call(workspace=ws)), R.bits(first))
+
+
+def test_counters_left_over_are_reported():
+    """A workspace that was never zero-filled: groups in parts become NaN and
+    the call says so; zero-filled it serves again."""
+    case = Case([5000, 30], 8, 1, 128, "f16", 16, seed=30).cuda()
+    ws = torch.full((da.decode_attn_paged_workspace_size(8, 1, 128),), 1, dtype=torch.uint8, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = case.call(workspace=ws, err_flag=err)
+    assert int(err.item()) == da.DA_DEVERR_WORKSPACE and out[0].isnan().all()
+    da.workspace_init(ws)
+    check(case, "zero-filled again", workspace=ws)
+    with pytest.raises(da.DecodeAttnError):
+        case.call(workspace=ws[:-16])
+
+
+def test_empty_batch():
+    q = torch.empty(0, 8, 64, dtype=torch.float16, device="cuda")
+    pool = [torch.zeros(2, 2, 16, 64, dtype=torch.float16, device="cuda") for _ in range(2)]
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    table = torch.empty(0, 3, dtype=torch.int32, device="cuda")
+    ws = da.alloc_paged_workspace(8, 2, 64)
+    assert da.decode_attn_paged_fwd(q, *pool, table, none, workspace=ws).shape == q.shape
+    da.kvcache_append_paged(*pool, q[:, :2].contiguous(), q[:, :2].contiguous(), table, none)
+    cache = torch.empty(0, 2, 32, 64, dtype=torch.float16, device="cuda")
+    assert da.decode_attn_window_fwd(q, cache, cache.clone(), none, 4, workspace=ws).shape == q.shape
+
+
 def test_more_sequences_than_one_scan_covers():
     gen = torch.Generator().manual_seed(5)
     lens = torch.randint(0, 40, (1500,), generator=gen).tolist()
     check(Case(lens, 2, 1, 64, "f16", 16, seed=6), "1500 sequences")
     check(Case(lens, 2, 1, 64, "f16", 16, True, window=9, sinks=2, seed=6), "1500 sequences, window")
+    lens = [0] * 300 + [700] + [0] * 400 + [3, 0]
+    check(Case(lens, 4, 4, 64, "f16", 16, seed=7), "mostly idle slots")
+    check(Case(lens, 4, 4, 64, "bf16", 16, True, seed=7), "mostly idle slots")
 
 
 @pytest.mark.parametrize("eight", [False, True], ids=["16bit", "e4m3"])

@@ -20,11 +20,11 @@ def lib():
     return da.load_library()
 
 
-APPEND = dict(k=A, v=A, ks=A, vs=A, k_new=A, v_new=A, q=A, q_out=A, cos=A, sin=A, rope_rows=4096, table=A, pos=A, start=A,
+APPEND = dict(k=A, v=2 * A, ks=A, vs=2 * A, k_new=A, v_new=A, q=A, q_out=A, cos=A, sin=A, rope_rows=4096, table=A, pos=A, start=A,
               B=2, tokens=10, H=32, Hkv=8, D=128, pages=64, size=16, max_pages=8, dtype=1, err=None, stream=None)
-ATTN = dict(q=A, k=A, v=A, ks=A, vs=A, table=A, kv_len=A, B=2, H=32, Hkv=8, D=128, pages=64, size=16, max_pages=8,
+ATTN = dict(q=2 * A, k=A, v=A, ks=A, vs=A, table=A, kv_len=A, B=2, H=32, Hkv=8, D=128, pages=64, size=16, max_pages=8,
             window=0, sinks=0, scale=0.1, out=A, ws=A, ws_bytes=1 << 30, dtype=1, err=None, stream=None)
-WINDOW = dict(q=A, k=A, v=A, kv_len=A, B=2, H=32, Hkv=8, D=128, capacity=1024, window=64, sinks=4, scale=0.1, out=A, ws=A,
+WINDOW = dict(q=2 * A, k=A, v=A, kv_len=A, B=2, H=32, Hkv=8, D=128, capacity=1024, window=64, sinks=4, scale=0.1, out=A, ws=A,
               ws_bytes=1 << 30, dtype=1, err=None, stream=None)
 
 
@@ -92,6 +92,9 @@ def test_append_arguments(lib, fn):
         assert call(lib, fn, **{name: A + 4}) == ALIGN
     for name in ("pos", "start"):
         assert call(lib, fn, **{name: A + 2}) == ALIGN
+    assert call(lib, fn, v=A) == SHAPE                    # K and V in one array
+    if "q8" in fn:
+        assert call(lib, fn, vs=A) == SHAPE
 
 
 @pytest.mark.parametrize("fn", PAGED + ["decode_attn_window_fwd"])
@@ -108,12 +111,15 @@ def test_attention_arguments(lib, fn):
         assert call(lib, fn, **{name: A + 2}) == ALIGN
     assert call(lib, fn, kv_len=A + 1) == ALIGN
     assert call(lib, fn, B=0, q=None, k=None) == 0
+    assert call(lib, fn, out=2 * A) == SHAPE              # the output over the query
     if fn == "decode_attn_window_fwd":
         assert call(lib, fn, window=0) == SHAPE
         assert call(lib, fn, capacity=0) == SHAPE
         assert call(lib, fn, capacity=(1 << 31) - 1) == SHAPE
+        assert call(lib, fn, B=65535, H=64, Hkv=64, capacity=1 << 30) == SHAPE  # more tiles than are numbered
     else:
         assert call(lib, fn, window=0, sinks=1) == SHAPE
+        assert call(lib, fn, B=65535, H=64, Hkv=64, max_pages=1 << 26) == SHAPE
 
 
 def test_workspace_size_rejects_bad_sizes(lib):
