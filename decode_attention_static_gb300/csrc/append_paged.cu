@@ -100,7 +100,7 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
 // One unit of one token: heads h, h + stride, ... of the order K, V, q (from
 // `first` on; K and V go to 16-bit pages). kAtOnce heads are loaded before the
 // token's place is looked up, and the table row serves all of them.
-constexpr int kAtOnce = 4;
+constexpr int kAtOnce = 6;
 
 template <typename T>
 __device__ __forceinline__ void move_token(const AppendPagedParams& p, int t, int first, int stride, int c) {
@@ -555,7 +555,7 @@ cudaError_t launch_prompt_q8(cudaLaunchConfig_t cfg, const AppendPagedParams& p,
 // Units for each token: one for each head while that fills less than about two
 // waves of the SMs (latency), else kTurns * kAtOnce heads a unit (place and
 // table row are looked up once for them).
-constexpr int kTurns = 3;
+constexpr int kTurns = 4;
 int units_per_token(int64_t tokens, int heads, int half, int sms) {
   return tokens * heads * half <= (int64_t)sms * 4096 ? heads : (heads + kTurns * kAtOnce - 1) / (kTurns * kAtOnce);
 }
