@@ -220,42 +220,35 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
   int64_t* words = reinterpret_cast<int64_t*>(smem + Sh::kWordsOffset);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, gr = lane >> 2, tq = lane & 3;
 
-  pdl_wait();
-  pdl_trigger();  // the next grid can take the SMs as they fall free; it waits for this one's memory
-
   // --- the list of places, and this CTA's share [lo, hi) of it: the tiles of
   // each group, and, with more groups than CTAs, kGroupCost places that stand
   // for its end (short groups are then balanced by what they cost, and those
   // places hold cuts that would split a group). One pass over the lengths, and,
   // for more sequences than threads, a second one for the sequence that holds
-  // `lo`.
+  // `lo`. A batch of at most 32 is seen by each warp alone, without a barrier,
+  // and first while the kernel before this one still runs: the lengths of then
+  // say which rows to bring into L2 (a hint; page numbers are checked), and if
+  // they are still those after the wait, the share stands.
   struct Found {
     int64_t start;  // first place of the sequence
     int b, len;
   };
   Found* found = reinterpret_cast<Found*>(words + kW);
   constexpr int kCount = 44;  // tiles and non-empty sequences are summed in one word: tiles + sequences * 2^44
-  int64_t before = 0, mine = 0, own = 0;  // before this pass, before this thread's sequence, and its own
-  int len = 0;
-  // (with one warp's worth of sequences every warp does it alone: no barrier)
+  constexpr int kChunks = Sh::kRowBytes / 16, kLanes = 32 / kHalves, kCopies = 16 * kChunks / kLanes;
+  const int half = kHalves == 2 ? lane >> 4 : 0, sub = lane % kLanes;
   const bool alone = p.B <= 32;
   const int column = alone ? lane : tid, columns = alone ? 32 : Sh::kThreads;
-  auto pass = [&](int base, bool idle_rows) {
+  int64_t before = 0, mine = 0, own = 0;  // before this pass, before this thread's sequence, and its own
+  int len = 0;
+  auto pass = [&](int base) {
     const int b = base + column;
     own = 0;
     if (b < p.B) {
       SequenceTiles s;
-      len = p.kv_len[b];
+      len = __ldcg(p.kv_len + b);  // (L2: read before the wait, it may be read again)
       const int n = tiles_of<kRows>(p, len, &s);
       if (n > 0) own = n + (1ll << kCount);
-      if (idle_rows && n <= 0 && column == tid && b % gridDim.x == blockIdx.x) {
-        // no visible row: zeros; no valid length: NaN
-        const uint32_t fill = n < 0 ? (uint32_t)Storage<T>::kNaN * 0x10001u : 0u;
-        if (n < 0 && p.err_flag) atomicOr(p.err_flag, kErrKvLen);
-        uint4* out = reinterpret_cast<uint4*>(p.out) + (int64_t)b * p.n_head * (D / 8);
-#pragma unroll 1
-        for (int i = 0; i < p.n_head * (D / 8); ++i) out[i] = make_uint4(fill, fill, fill, fill);
-      }
     }
     int64_t sum = own;
 #pragma unroll 1
@@ -277,64 +270,116 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
       before += words[w];
     }
   };
-  for (int base = 0; base < p.B; base += columns) pass(base, true);
-  const int64_t tiles = (before & ((1ll << kCount) - 1)) * p.n_kv_head, groups = (before >> kCount) * p.n_kv_head;
-  // as many CTAs as find kFewestTiles
-  const int64_t ctas = min((int64_t)gridDim.x, (tiles + kFewestTiles - 1) / kFewestTiles);
-  if ((int64_t)blockIdx.x >= ctas) return;
-  int end_cost = kGroupCost;
-  if (groups <= ctas) {
-    const uint32_t n = (uint32_t)ctas;
-    end_cost = n % (uint32_t)groups == 0 ? 0 : (int)(tiles >= ctas * kJoinCost * 8 ? kJoinCost : (uint32_t)tiles / n / 8);
-  }
+  // Sequences without a visible row get zeros, those without a valid length NaN.
+  auto fill_idle = [&](int base) {
+    const int b = base + column;
+    const bool bad = len < 0 || len > p.max_len;
+    unsigned todo = __ballot_sync(0xffffffffu, b < p.B && (bad || len == 0) && b % gridDim.x == blockIdx.x);
+    if (alone && warp) todo = 0;
+    while (todo) {
+      const int src = __ffs(todo) - 1;
+      todo &= todo - 1;
+      const int64_t row = __shfl_sync(0xffffffffu, b, src);
+      const uint32_t fill = __shfl_sync(0xffffffffu, bad ? (uint32_t)Storage<T>::kNaN * 0x10001u : 0u, src);
+      if (fill && lane == 0 && p.err_flag) atomicOr(p.err_flag, kErrKvLen);
+      uint4* out = reinterpret_cast<uint4*>(p.out) + row * p.n_head * (D / 8);
+#pragma unroll 1
+      for (int i = lane; i < p.n_head * (D / 8); i += 32) out[i] = make_uint4(fill, fill, fill, fill);
+    }
+  };
+  int64_t ctas = 0, total = 0, lo = 0, hi = 0;
+  int end_cost = 0;
+  bool small = true;
   auto places = [&](int64_t word) {
     return ((word & ((1ll << kCount) - 1)) + (word >> kCount) * end_cost) * p.n_kv_head;
   };
-  const int64_t total = places(before);
   // first place of share i, and the share that holds place x (in 32 bits where
   // they suffice: a 64-bit division is some hundred instructions)
-  const bool small = total * ctas < (1ll << 32);
   auto share_start = [&](int64_t i) {
     return small ? (int64_t)((uint32_t)i * (uint32_t)total / (uint32_t)ctas) : divide(i * total, ctas);
   };
   auto share_of = [&](int64_t x) {
     return (int)(small ? ((uint32_t)(x + 1) * (uint32_t)ctas - 1) / (uint32_t)total : divide((x + 1) * ctas - 1, total));
   };
-  const int64_t lo = share_start(blockIdx.x), hi = share_start(blockIdx.x + 1);
-  Found here_first;  // the sequence that holds `lo`
-  auto holds = [&]() {
-    const int64_t at = places(mine);
-    return at <= lo && lo < at + places(own);
-  };
-  if (alone) {
-    const int src = __ffs(__ballot_sync(0xffffffffu, holds())) - 1;
-    here_first = {__shfl_sync(0xffffffffu, places(mine), src), src, __shfl_sync(0xffffffffu, len, src)};
-  } else {
-    if (p.B <= Sh::kThreads) {
-      if (holds()) *found = {places(mine), tid, len};
-    } else {
-      before = 0;
-      for (int base = 0; places(before) <= lo; base += Sh::kThreads) {
+  SequenceTiles seq;  // the sequence that holds `lo`
+  int b = 0, g = 0, tile = 0;  // group of list position `lo`, and its place there
+  bool waited = !alone;
+  if (waited) {
+    pdl_wait();
+    pdl_trigger();  // the next grid can take the SMs as they fall free; it waits for this one's memory
+  }
+  for (;;) {
+    before = 0;
+    for (int base = 0; base < p.B; base += columns) {
+      pass(base);
+      if (!alone) fill_idle(base);
+    }
+    const int64_t tiles = (before & ((1ll << kCount) - 1)) * p.n_kv_head, groups = (before >> kCount) * p.n_kv_head;
+    // as many CTAs as find kFewestTiles
+    ctas = min((int64_t)gridDim.x, (tiles + kFewestTiles - 1) / kFewestTiles);
+    if ((int64_t)blockIdx.x < ctas) {
+      end_cost = kGroupCost;
+      if (groups <= ctas) {
+        const uint32_t n = (uint32_t)ctas;
+        end_cost =
+            n % (uint32_t)groups == 0 ? 0 : (int)(tiles >= ctas * kJoinCost * 8 ? kJoinCost : (uint32_t)tiles / n / 8);
+      }
+      total = places(before);
+      small = total * ctas < (1ll << 32);
+      lo = share_start(blockIdx.x);
+      hi = share_start(blockIdx.x + 1);
+      Found first;
+      auto holds = [&]() {
+        const int64_t at = places(mine);
+        return at <= lo && lo < at + places(own);
+      };
+      if (alone) {
+        const int src = __ffs(__ballot_sync(0xffffffffu, holds())) - 1;
+        first = {__shfl_sync(0xffffffffu, places(mine), src), src, __shfl_sync(0xffffffffu, len, src)};
+      } else {
+        if (p.B <= Sh::kThreads) {
+          if (holds()) *found = {places(mine), tid, len};
+        } else {
+          before = 0;
+          for (int base = 0; places(before) <= lo; base += Sh::kThreads) {
+            __syncthreads();
+            pass(base);
+            if (holds()) *found = {places(mine), base + tid, len};
+          }
+        }
         __syncthreads();
-        pass(base, false);
-        if (holds()) *found = {places(mine), base + tid, len};
+        first = *found;
+      }
+      b = first.b;
+      tiles_of<kRows>(p, first.len, &seq);
+      const int64_t in = lo - first.start;
+      const int size = seq.tiles + end_cost;
+      g = small ? (int)((uint32_t)in / (uint32_t)size) : (int)divide(in, size);
+      tile = (int)(in - (int64_t)g * size);
+    }
+    if (waited) break;
+    if ((int64_t)blockIdx.x < ctas) {
+#pragma unroll 1
+      for (int i = tile + warp, j = 0; j < kS - 1 && i < seq.tiles && i - tile < hi - lo; i += kW, ++j) {
+        const int row = tile_row<kRows>(seq, i) + 16 * half;
+        if (row + 16 > seq.len) break;
+        const int page = p.table ? __ldcg(p.table + (int64_t)b * p.max_pages + (row >> p.page_shift)) : b;
+        if (page < 0 || page >= p.num_pages || sub > 1) continue;
+        const int64_t from =
+            ((int64_t)page * p.n_kv_head + g) * p.page_rows + (row & (p.table ? p.page_rows - 1 : -1));
+        prefetch_l2((sub ? p.v : p.k) + from * Sh::kRowBytes, 16 * Sh::kRowBytes);
       }
     }
-    __syncthreads();
-    here_first = *found;
+    pdl_wait();
+    pdl_trigger();
+    waited = true;
+    const int now = lane < p.B ? __ldcg(p.kv_len + lane) : 0;
+    if (__all_sync(0xffffffffu, now == len)) break;
   }
-  int b = here_first.b;
-  SequenceTiles seq;
-  tiles_of<kRows>(p, here_first.len, &seq);
-  int g, tile;       // group of list position `lo`, and its place there
+  if (alone) fill_idle(0);
+  if ((int64_t)blockIdx.x >= ctas) return;
   const int share = (int)(hi - lo);  // (below 2^31: checked on the host)
-  int at = 0;        // place in the share of the next tile to compute
-  {
-    const int64_t in = lo - here_first.start;
-    const int size = seq.tiles + end_cost;
-    g = small ? (int)((uint32_t)in / (uint32_t)size) : (int)divide(in, size);
-    tile = (int)(in - (int64_t)g * size);
-  }
+  int at = 0;                        // place in the share of the next tile to compute
   // the next group; false when this share ends before it
   auto next_group = [&](int place, int& b, int& g, SequenceTiles& s) {
     if (place >= share) return false;
@@ -354,8 +399,6 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
 
   // --- this warp's loads. A tile is kHalves pieces of 16 rows, each inside one
   // page; with two, either half of the warp looks up and copies its own.
-  constexpr int kChunks = Sh::kRowBytes / 16, kLanes = 32 / kHalves, kCopies = 16 * kChunks / kLanes;
-  const int half = kHalves == 2 ? lane >> 4 : 0, sub = lane % kLanes;
   const uint32_t ring = smem_addr(smem) + warp * kS * Sh::kStageBytes;
   const uint32_t meta = smem_addr(smem + Sh::kMetaOffset) + warp * kS * Sh::kMetaBytes;
   SequenceTiles lseq = seq;  // the tile to load next, its page number on the way
