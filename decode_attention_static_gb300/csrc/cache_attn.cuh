@@ -48,6 +48,11 @@ constexpr int kJoinCost = 16;    // and of one in parts
 // A group in more than kJoinWide parts (at most 256) is joined in two rounds, of
 // kJoinWidth neighbours and of the sums of those.
 constexpr int kJoinWide = 64, kJoinWidth = 16;
+// In a batch of more groups than CTAs, none of more rows than this, a warp takes
+// a group by itself: no barrier, nothing to join (us for 256 sequences of up
+// to 128 rows, 8 KV heads, 21.1 instead of 42.7; 64 of 256 rows 15.7 instead
+// of 22.1; with groups of up to 500 rows 20.9 against 18.9).
+constexpr int kShortRows = 256;
 constexpr float kLazy = 8.f;     // m is raised when a score passes it by this (log2)
 // fp16 weights are 2^(x' - m + 7): at most 2^15, inside the type's range, and
 // 2^-32 of the largest one is still held. bf16 has fp32's range: no lift.
@@ -240,7 +245,7 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
   const bool alone = p.B <= 32;
   const int column = alone ? lane : tid, columns = alone ? 32 : Sh::kThreads;
   int64_t before = 0, mine = 0, own = 0;  // before this pass, before this thread's sequence, and its own
-  int len = 0;
+  int len = 0, most = 0;                  // most tiles of a sequence
   auto pass = [&](int base) {
     const int b = base + column;
     own = 0;
@@ -249,6 +254,7 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
       len = __ldcg(p.kv_len + b);  // (L2: read before the wait, it may be read again)
       const int n = tiles_of<kRows>(p, len, &s);
       if (n > 0) own = n + (1ll << kCount);
+      most = max(most, n);
     }
     int64_t sum = own;
 #pragma unroll 1
@@ -303,21 +309,50 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
   };
   SequenceTiles seq;  // the sequence that holds `lo`
   int b = 0, g = 0, tile = 0;  // group of list position `lo`, and its place there
+  bool short_groups = false;
+  // From (b, g) on to the first group with rows, in steps of the list (with
+  // short groups, of the warps); false when there is none.
+  auto settle = [&](int& b, int& g, SequenceTiles& s) {
+#pragma unroll 1
+    while (b < p.B && tiles_of<kRows>(p, __ldcg(p.kv_len + b), &s) <= 0) {
+      if (short_groups) g += kW * gridDim.x;
+      b += short_groups ? g / p.n_kv_head : 1;
+      g = short_groups ? g % p.n_kv_head : 0;
+    }
+    return b < p.B;
+  };
   bool waited = !alone;
   if (waited) {
     pdl_wait();
     pdl_trigger();  // the next grid can take the SMs as they fall free; it waits for this one's memory
   }
   for (;;) {
-    before = 0;
+    before = lo = 0;
+    most = 0;
+    short_groups = false;
     for (int base = 0; base < p.B; base += columns) {
       pass(base);
       if (!alone) fill_idle(base);
     }
     const int64_t tiles = (before & ((1ll << kCount) - 1)) * p.n_kv_head, groups = (before >> kCount) * p.n_kv_head;
+    if (groups > gridDim.x) {
+      // (uniform in the grid: every warp, or every CTA, sees all lengths)
+      const bool few = most <= kShortRows / kRows;
+      short_groups = alone ? __all_sync(0xffffffffu, few) : __syncthreads_and(few);
+      if (short_groups) {
+        ctas = gridDim.x;
+        g = warp * gridDim.x + blockIdx.x;
+        b = g / p.n_kv_head;
+        g -= b * p.n_kv_head;
+        if (!settle(b, g, seq)) ctas = 0;
+        tile = 0;
+        hi = INT32_MAX;
+        end_cost = 0;
+      }
+    }
     // as many CTAs as find kFewestTiles
-    ctas = min((int64_t)gridDim.x, (tiles + kFewestTiles - 1) / kFewestTiles);
-    if ((int64_t)blockIdx.x < ctas) {
+    if (!short_groups) ctas = min((int64_t)gridDim.x, (tiles + kFewestTiles - 1) / kFewestTiles);
+    if (!short_groups && (int64_t)blockIdx.x < ctas) {
       end_cost = kGroupCost;
       if (groups <= ctas) {
         const uint32_t n = (uint32_t)ctas;
@@ -360,7 +395,8 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
     if (waited) break;
     if ((int64_t)blockIdx.x < ctas) {
 #pragma unroll 1
-      for (int i = tile + warp, j = 0; j < kS - 1 && i < seq.tiles && i - tile < hi - lo; i += kW, ++j) {
+      for (int i = tile + (short_groups ? 0 : warp), j = 0; j < kS - 1 && i < seq.tiles && i - tile < hi - lo;
+           i += short_groups ? 1 : kW, ++j) {
         const int row = tile_row<kRows>(seq, i) + 16 * half;
         if (row + 16 > seq.len) break;
         const int page = p.table ? __ldcg(p.table + (int64_t)b * p.max_pages + (row >> p.page_shift)) : b;
@@ -378,17 +414,19 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
   }
   if (alone) fill_idle(0);
   if ((int64_t)blockIdx.x >= ctas) return;
+  const int step = short_groups ? 1 : kW;  // tiles between this warp's
   const int share = (int)(hi - lo);  // (below 2^31: checked on the host)
   int at = 0;                        // place in the share of the next tile to compute
-  // the next group; false when this share ends before it
+  // the next group of this CTA (with short groups, of this warp); false when
+  // the share ends before it
+  const int skip = short_groups ? kW * gridDim.x : 1;
   auto next_group = [&](int place, int& b, int& g, SequenceTiles& s) {
     if (place >= share) return false;
-    if (++g == p.n_kv_head) {
-      g = 0;
-      do ++b;
-      while (tiles_of<kRows>(p, p.kv_len[b], &s) <= 0);
-    }
-    return true;
+    g += skip;
+    if (g < p.n_kv_head) return true;
+    b += short_groups ? g / p.n_kv_head : 1;
+    g = short_groups ? g % p.n_kv_head : 0;
+    return settle(b, g, s);
   };
   if (tile >= seq.tiles) {
     // the share begins in the places of a group's end
@@ -468,18 +506,18 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
   auto load_next = [&]() {
     if (lmask) {
       issue(put, lrow, lpage, lmask, lg);
-      look_up(kW);
+      look_up(step);
     }
     copy_commit();
     put = put + 1 == kS ? 0 : put + 1;
   };
-  look_up(warp);
+  look_up(short_groups ? 0 : warp);
 #pragma unroll 1
   for (int j = 0; j < kS - 1; ++j) load_next();
 
   // --- group by group
   int get = 0;      // stage of this warp's next tile
-  int turn = warp;  // tiles until this warp's next one
+  int turn = short_groups ? 0 : warp;  // tiles until this warp's next one
   for (;;) {
     const int here = min(seq.tiles - tile, share - at);  // tiles of the group in this share
     // q as the right operand: columns are heads
@@ -539,7 +577,7 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
 #pragma unroll
     for (int k = 0; k < kSteps; ++k) o[k][0] = o[k][1] = o[k][2] = o[k][3] = 0.f;
 
-    for (; turn < here; turn += kW) {
+    for (; turn < here; turn += step) {
       copy_wait<kS - 2>();
       __syncwarp();
       // refill the stage that the tile before this one has left
@@ -725,23 +763,6 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
         }
       }
     }
-    __syncthreads();
-    const bool whole = here == seq.tiles;
-    const int items = p.group * (D / 4);  // outputs in vectors of 4
-    // shares that hold the group, and this one's partial state
-    const int64_t group_start = lo + at - tile;
-    const int slot_floats = cache_attn_slot_floats(p.group, D);
-    int from = 0, parts = 1;
-    if (!whole) {
-      from = share_of(group_start);
-      parts = share_of(group_start + seq.tiles - 1) - from + 1;
-    }
-    // (a CTA has at most two groups that others share: the one it begins in
-    // the middle of, slot 0, and the one it leaves in the middle of, slot 1)
-    auto slot_of = [&](int part) {
-      return p.partials + (int64_t)(part ? 2 * (from + part) : 2 * from + 1) * slot_floats;
-    };
-    float* slot = slot_of((int)blockIdx.x - from);
     uint8_t* out = p.out + ((int64_t)b * p.n_head + (int64_t)g * p.group) * D * 2;
     auto store = [&](int i, const float4& r, float l) {
       const float inv = 1.f / l;
@@ -749,146 +770,174 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
           make_uint2((uint32_t)Storage<T>::round(r.x * inv) | ((uint32_t)Storage<T>::round(r.y * inv) << 16),
                      (uint32_t)Storage<T>::round(r.z * inv) | ((uint32_t)Storage<T>::round(r.w * inv) << 16));
     };
-    auto add = [](float4& r, float f, const float4& v) {
-      r.x = fmaf(f, v.x, r.x);
-      r.y = fmaf(f, v.y, r.y);
-      r.z = fmaf(f, v.z, r.z);
-      r.w = fmaf(f, v.w, r.w);
-    };
-    if (tid < items) {
-      const int h = tid / (D / 4), d = (tid % (D / 4)) * 4;
-      float mw[kW], mm = -INFINITY, ll = 0.f;
-#pragma unroll
-      for (int w = 0; w < kW; ++w) {
-        mw[w] = sm_m[w * kHeads + h];
-        mm = fmaxf(mm, mw[w]);
+    const int items = p.group * (D / 4);  // outputs in vectors of 4
+    if (short_groups) {
+      // the group is this warp's alone
+      __syncwarp();
+      for (int i = lane; i < items; i += 32) {
+        const int h = i / (D / 4), d = (i % (D / 4)) * 4;
+        store(i, *reinterpret_cast<const float4*>(merge + (warp * kHeads + h) * D + merge_column<D>(h, d)),
+              sm_l[warp * kHeads + h]);
       }
-      float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kW; ++w) {
-        const float f = mw[w] == mm ? 1.f : fast_exp2(mw[w] - mm);
-        ll = fmaf(f, sm_l[w * kHeads + h], ll);
-        add(r, f, *reinterpret_cast<const float4*>(merge + (w * kHeads + h) * D + merge_column<D>(h, d)));
+      __syncwarp();  // the merge buffer is free
+    } else {
+      __syncthreads();
+      const bool whole = here == seq.tiles;
+      // shares that hold the group, and this one's partial state
+      const int64_t group_start = lo + at - tile;
+      const int slot_floats = cache_attn_slot_floats(p.group, D);
+      int from = 0, parts = 1;
+      if (!whole) {
+        from = share_of(group_start);
+        parts = share_of(group_start + seq.tiles - 1) - from + 1;
       }
-      if (whole) {
-        store(tid, r, ll);
-      } else {
-        __stcg(reinterpret_cast<float4*>(slot) + tid, r);
-        if (d == 0) {
-          __stcg(slot + p.group * D + h, mm);
-          __stcg(slot + p.group * D + p.group + h, ll);
+      // (a CTA has at most two groups that others share: the one it begins in
+      // the middle of, slot 0, and the one it leaves in the middle of, slot 1)
+      auto slot_of = [&](int part) {
+        return p.partials + (int64_t)(part ? 2 * (from + part) : 2 * from + 1) * slot_floats;
+      };
+      float* slot = slot_of((int)blockIdx.x - from);
+      auto add = [](float4& r, float f, const float4& v) {
+        r.x = fmaf(f, v.x, r.x);
+        r.y = fmaf(f, v.y, r.y);
+        r.z = fmaf(f, v.z, r.z);
+        r.w = fmaf(f, v.w, r.w);
+      };
+      if (tid < items) {
+        const int h = tid / (D / 4), d = (tid % (D / 4)) * 4;
+        float mw[kW], mm = -INFINITY, ll = 0.f;
+#pragma unroll
+        for (int w = 0; w < kW; ++w) {
+          mw[w] = sm_m[w * kHeads + h];
+          mm = fmaxf(mm, mw[w]);
         }
-      }
-    }
-    if (!whole) {
-      // Join the parts: the last CTA to arrive at a counter joins the parts that
-      // are counted there. Many parts are joined in two rounds, neighbours
-      // first, into the slot of the first of them.
-      const int part = (int)blockIdx.x - from;
-      int width = parts > kJoinWide ? kJoinWidth : parts;  // parts counted together
-      int head = parts > kJoinWide ? part / kJoinWidth * kJoinWidth : 0, step = 1;  // the first of them, and their distance
-      unsigned int* arrived = reinterpret_cast<unsigned int*>(&words[kW + 2]);
-      for (;;) {
-        const bool last_round = width == parts || step > 1;
-        const int count = min((parts - head + step - 1) / step, width);
-        // the last round's counter is that of the group's first share; a share
-        // leads the first round of at most one group as its part 0 and of one
-        // as a later part
-        unsigned int* counter = p.counters + (last_round ? from : (head ? 2 : 1) * kMaxCtas + from + head);
-        __syncthreads();
-        if (tid == 0) {
-          __threadfence();  // (cumulative: the CTA's writes before the barrier)
-          *arrived = atomicAdd(counter, 1u);
-          __threadfence();
+        float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kW; ++w) {
+          const float f = mw[w] == mm ? 1.f : fast_exp2(mw[w] - mm);
+          ll = fmaf(f, sm_l[w * kHeads + h], ll);
+          add(r, f, *reinterpret_cast<const float4*>(merge + (w * kHeads + h) * D + merge_column<D>(h, d)));
         }
-        __syncthreads();
-        const unsigned int order = *arrived;
-        if (order >= (unsigned int)count) {
-          // the counter was not zero before this call
-          if (tid == 0 && p.err_flag) atomicOr(p.err_flag, kErrWorkspace);
-          const uint32_t nan2 = (uint32_t)Storage<T>::kNaN * 0x10001u;
-          if (tid < items) *reinterpret_cast<uint2*>(out + tid * 8) = make_uint2(nan2, nan2);
-          break;
-        }
-        if (order != (unsigned int)count - 1) break;
-        // the threads share the vectors, and with fewer vectors than threads also
-        // the parts; a thread's first eight are on their way while the warps
-        // find the parts' factors
-        float* factor = merge;                        // [count][8]
-        float4* sums = reinterpret_cast<float4*>(merge + kJoinWide * kHeads);  // [kThreads]
-        const int crews = Sh::kThreads / items, crew = tid / items, i = tid - crew * items, h = i / (D / 4);
-        float4 v[8], r = make_float4(0.f, 0.f, 0.f, 0.f);
-        auto fetch = [&](int s0) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (s0 + j * crews < count)
-              v[j] = __ldcg(reinterpret_cast<const float4*>(slot_of(head + (s0 + j * crews) * step)) + i);
-        };
-        fetch(crew);
-        if (warp < p.group) {
-          // lane s has parts s and s + 32
-          float m_s[2] = {-INFINITY, -INFINITY}, l_s[2] = {0.f, 0.f};
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int s = lane + 32 * k;
-            const float* at_s = slot_of(head + s * step) + p.group * D + warp;
-            if (s < count) {
-              m_s[k] = __ldcg(at_s);
-              l_s[k] = __ldcg(at_s + p.group);
-            }
-          }
-          float mm = fmaxf(m_s[0], m_s[1]), ll = 0.f;
-#pragma unroll
-          for (int k = 16; k; k >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, k));
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int s = lane + 32 * k;
-            if (s < count) {
-              const float f = m_s[k] == mm ? 1.f : fast_exp2(m_s[k] - mm);
-              factor[s * kHeads + warp] = f;
-              ll += f * l_s[k];
-            }
-          }
-#pragma unroll
-          for (int k = 16; k; k >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, k);
-          if (lane == 0) {
-            sm_gl[warp] = ll;
-            sm_gm[warp] = mm;
+        if (whole) {
+          store(tid, r, ll);
+        } else {
+          __stcg(reinterpret_cast<float4*>(slot) + tid, r);
+          if (d == 0) {
+            __stcg(slot + p.group * D + h, mm);
+            __stcg(slot + p.group * D + p.group + h, ll);
           }
         }
-        __syncthreads();
-        for (int s0 = crew; s0 < count;) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (s0 + j * crews < count) add(r, factor[(s0 + j * crews) * kHeads + h], v[j]);
-          s0 += 8 * crews;
-          if (s0 < count) fetch(s0);
-        }
-        if (crews > 1) {
-          sums[tid] = r;
+      }
+      if (!whole) {
+        // Join the parts: the last CTA to arrive at a counter joins the parts that
+        // are counted there. Many parts are joined in two rounds, neighbours
+        // first, into the slot of the first of them.
+        const int part = (int)blockIdx.x - from;
+        int width = parts > kJoinWide ? kJoinWidth : parts;  // parts counted together
+        int head = parts > kJoinWide ? part / kJoinWidth * kJoinWidth : 0, step = 1;  // the first of them, and their distance
+        unsigned int* arrived = reinterpret_cast<unsigned int*>(&words[kW + 2]);
+        for (;;) {
+          const bool last_round = width == parts || step > 1;
+          const int count = min((parts - head + step - 1) / step, width);
+          // the last round's counter is that of the group's first share; a share
+          // leads the first round of at most one group as its part 0 and of one
+          // as a later part
+          unsigned int* counter = p.counters + (last_round ? from : (head ? 2 : 1) * kMaxCtas + from + head);
           __syncthreads();
-          if (crew == 0)
-            for (int c = 1; c < crews; ++c) add(r, 1.f, sums[c * items + i]);
-        }
-        if (tid == 0) *counter = 0;  // ready for the next call
-        if (last_round) {
-          if (crew == 0) store(i, r, sm_gl[h]);
-          break;
-        }
-        float* joined = slot_of(head);
-        if (crew == 0) {
-          __stcg(reinterpret_cast<float4*>(joined) + i, r);
-          if (i % (D / 4) == 0) {
-            __stcg(joined + p.group * D + h, sm_gm[h]);
-            __stcg(joined + p.group * D + p.group + h, sm_gl[h]);
+          if (tid == 0) {
+            __threadfence();  // (cumulative: the CTA's writes before the barrier)
+            *arrived = atomicAdd(counter, 1u);
+            __threadfence();
           }
+          __syncthreads();
+          const unsigned int order = *arrived;
+          if (order >= (unsigned int)count) {
+            // the counter was not zero before this call
+            if (tid == 0 && p.err_flag) atomicOr(p.err_flag, kErrWorkspace);
+            const uint32_t nan2 = (uint32_t)Storage<T>::kNaN * 0x10001u;
+            if (tid < items) *reinterpret_cast<uint2*>(out + tid * 8) = make_uint2(nan2, nan2);
+            break;
+          }
+          if (order != (unsigned int)count - 1) break;
+          // the threads share the vectors, and with fewer vectors than threads also
+          // the parts; a thread's first eight are on their way while the warps
+          // find the parts' factors
+          float* factor = merge;                        // [count][8]
+          float4* sums = reinterpret_cast<float4*>(merge + kJoinWide * kHeads);  // [kThreads]
+          const int crews = Sh::kThreads / items, crew = tid / items, i = tid - crew * items, h = i / (D / 4);
+          float4 v[8], r = make_float4(0.f, 0.f, 0.f, 0.f);
+          auto fetch = [&](int s0) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (s0 + j * crews < count)
+                v[j] = __ldcg(reinterpret_cast<const float4*>(slot_of(head + (s0 + j * crews) * step)) + i);
+          };
+          fetch(crew);
+          if (warp < p.group) {
+            // lane s has parts s and s + 32
+            float m_s[2] = {-INFINITY, -INFINITY}, l_s[2] = {0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int s = lane + 32 * k;
+              const float* at_s = slot_of(head + s * step) + p.group * D + warp;
+              if (s < count) {
+                m_s[k] = __ldcg(at_s);
+                l_s[k] = __ldcg(at_s + p.group);
+              }
+            }
+            float mm = fmaxf(m_s[0], m_s[1]), ll = 0.f;
+#pragma unroll
+            for (int k = 16; k; k >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, k));
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int s = lane + 32 * k;
+              if (s < count) {
+                const float f = m_s[k] == mm ? 1.f : fast_exp2(m_s[k] - mm);
+                factor[s * kHeads + warp] = f;
+                ll += f * l_s[k];
+              }
+            }
+#pragma unroll
+            for (int k = 16; k; k >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, k);
+            if (lane == 0) {
+              sm_gl[warp] = ll;
+              sm_gm[warp] = mm;
+            }
+          }
+          __syncthreads();
+          for (int s0 = crew; s0 < count;) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (s0 + j * crews < count) add(r, factor[(s0 + j * crews) * kHeads + h], v[j]);
+            s0 += 8 * crews;
+            if (s0 < count) fetch(s0);
+          }
+          if (crews > 1) {
+            sums[tid] = r;
+            __syncthreads();
+            if (crew == 0)
+              for (int c = 1; c < crews; ++c) add(r, 1.f, sums[c * items + i]);
+          }
+          if (tid == 0) *counter = 0;  // ready for the next call
+          if (last_round) {
+            if (crew == 0) store(i, r, sm_gl[h]);
+            break;
+          }
+          float* joined = slot_of(head);
+          if (crew == 0) {
+            __stcg(reinterpret_cast<float4*>(joined) + i, r);
+            if (i % (D / 4) == 0) {
+              __stcg(joined + p.group * D + h, sm_gm[h]);
+              __stcg(joined + p.group * D + p.group + h, sm_gl[h]);
+            }
+          }
+          width = (parts + kJoinWidth - 1) / kJoinWidth;
+          head = 0;
+          step = kJoinWidth;
         }
-        width = (parts + kJoinWidth - 1) / kJoinWidth;
-        head = 0;
-        step = kJoinWidth;
       }
+      __syncthreads();  // the merge buffer is free
     }
-    __syncthreads();  // the merge buffer is free
 
     // --- the next group
     at += here + end_cost;

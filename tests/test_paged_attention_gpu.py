@@ -201,6 +201,34 @@ def test_empty_batch():
     assert da.decode_attn_window_fwd(q, cache, cache.clone(), none, 4, workspace=ws).shape == q.shape
 
 
+@pytest.mark.parametrize("eight", [False, True], ids=["16bit", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("longest", [15, 255, 256, 257, 511, 513])
+def test_many_short_groups(longest, D, eight):
+    """More groups than CTAs, around the length up to which one warp takes a
+    whole group; with idle slots, a window, and lengths that make all warps but
+    a few idle."""
+    gen = torch.Generator().manual_seed(longest)
+    for B, H, Hkv, window, sinks in ((70, 8, 4, 0, 0), (20, 16, 16, 9, 3), (200, 2, 1, 0, 0), (31, 40, 5, 0, 0)):
+        lens = torch.randint(0, longest + 1, (B,), generator=gen).tolist()
+        lens[B // 2] = longest
+        check(Case(lens, H, Hkv, D, "bf16", 16, eight, window, sinks, seed=longest), f"{B} up to {longest}")
+
+
+def test_short_groups_of_bad_lengths_and_pages():
+    lens = [30, 17, 100, 5] * 50
+    case = Case(lens, 8, 2, 64, "f16", 16, seed=31).cuda()
+    kv, table = case.kv_len.clone(), case.table.clone()
+    kv[7], kv[60], table[90, 1] = -3, 1 << 20, 1 << 25
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = da.decode_attn_paged_fwd(case.q, case.k, case.v, table, kv, err_flag=err)
+    assert int(err.item()) == da.DA_DEVERR_KV_LEN | da.DA_DEVERR_PAGE
+    bad = torch.tensor([7, 60, 90])
+    assert out[bad.cuda()].isnan().all()
+    good = torch.tensor([b for b in range(200) if b not in (7, 60, 90)])
+    R.assert_rows(out[good.cuda()], case.ref[good], case.slack[good])
+
+
 def test_more_sequences_than_one_scan_covers():
     gen = torch.Generator().manual_seed(5)
     lens = torch.randint(0, 40, (1500,), generator=gen).tolist()
