@@ -513,6 +513,8 @@ def alloc_paged_workspace(n_head: int, n_kv_head: int, head_dim: int, device=Non
     return torch.zeros(max(n, 16), dtype=torch.uint8, device=device or "cuda")
 
 
+_I32, _F32, _E4M3 = torch.int32, torch.float32, torch.float8_e4m3fn
+
 # The entry points below check their tensors in one expression (a call costs
 # more host time in checks than in the library); only when it fails do the
 # _explain functions look for what is wrong, to say it.
@@ -580,32 +582,31 @@ def _explain_append(k_pages, v_pages, k_scale, v_scale, eight, k_new, v_new, pag
 def _append_paged(fn, k_pages, v_pages, k_scale, v_scale, eight, k_new, v_new, page_table, position_ids, token_start,
                   rope_cos, rope_sin, q, q_out, err_flag):
     dtype, pool, new, table = k_new.dtype, k_pages.shape, k_new.shape, page_table.shape
-    code, store = _DTYPE_CODE.get(dtype), torch.float8_e4m3fn if eight else dtype
+    code, store = _DTYPE_CODE.get(dtype), _E4M3 if eight else dtype
     ix = k_new.get_device()
-    i32, f32 = torch.int32, torch.float32
     ok = (ix >= 0 and code is not None and len(pool) == 4 and len(new) == 3 and len(table) == 2
           and new[1] == pool[1] and new[2] == pool[3] and v_new.shape == new and v_pages.shape == pool
-          and v_new.dtype == dtype and k_pages.dtype == store and v_pages.dtype == store and page_table.dtype == i32
-          and position_ids.dtype == i32 and position_ids.numel() == table[0]
+          and v_new.dtype == dtype and k_pages.dtype == store and v_pages.dtype == store and page_table.dtype == _I32
+          and position_ids.dtype == _I32 and position_ids.numel() == table[0]
           and v_new.get_device() == ix and k_pages.get_device() == ix and v_pages.get_device() == ix
           and page_table.get_device() == ix and position_ids.get_device() == ix
           and k_new.is_contiguous() and v_new.is_contiguous() and k_pages.is_contiguous() and v_pages.is_contiguous()
           and page_table.is_contiguous() and position_ids.is_contiguous()
-          and (not eight or (k_scale.dtype == f32 and v_scale.dtype == f32 and k_scale.shape == pool[:2]
-                             and v_scale.shape == pool[:2] and k_scale.get_device() == ix
+          and (not eight or (k_scale.dtype == _F32 and v_scale.dtype == _F32 and k_scale.shape == (pairs := pool[:2])
+                               and v_scale.shape == pairs and k_scale.get_device() == ix
                              and v_scale.get_device() == ix and k_scale.is_contiguous() and v_scale.is_contiguous()))
           and (new[0] == table[0] if token_start is None else
-               (token_start.dtype == i32 and token_start.numel() == table[0] + 1 and token_start.get_device() == ix
+               (token_start.dtype == _I32 and token_start.numel() == table[0] + 1 and token_start.get_device() == ix
                 and token_start.is_contiguous()))
           and (rope_cos is None) == (rope_sin is None) and (q is not None or q_out is None)
-          and (err_flag is None or (err_flag.dtype == i32 and err_flag.numel() >= 1 and err_flag.get_device() == ix
+          and (err_flag is None or (err_flag.dtype == _I32 and err_flag.numel() >= 1 and err_flag.get_device() == ix
                                     and err_flag.is_contiguous())))
     rope_rows = n_head = 0
     cos_ptr = sin_ptr = q_ptr = out_ptr = None
     if ok and rope_cos is not None:
         rope = rope_cos.shape
-        ok = (len(rope) == 2 and rope[1] == new[2] and rope_sin.shape == rope and rope_cos.dtype == f32
-              and rope_sin.dtype == f32 and rope_cos.get_device() == ix and rope_sin.get_device() == ix
+        ok = (len(rope) == 2 and rope[1] == new[2] and rope_sin.shape == rope and rope_cos.dtype == _F32
+              and rope_sin.dtype == _F32 and rope_cos.get_device() == ix and rope_sin.get_device() == ix
               and rope_cos.is_contiguous() and rope_sin.is_contiguous())
         if ok:
             rope_rows, cos_ptr, sin_ptr = rope[0], rope_cos.data_ptr(), rope_sin.data_ptr()
@@ -691,21 +692,22 @@ def _explain_attn_tail(q, kv_len, out, workspace, err_flag, **others):
 def _attn_paged(fn, q, k_pages, v_pages, k_scale, v_scale, eight, page_table, kv_len, window, sinks, out, scale,
                 workspace, err_flag):
     dtype, shape, pool, table = q.dtype, q.shape, k_pages.shape, page_table.shape
-    code, store = _DTYPE_CODE.get(dtype), torch.float8_e4m3fn if eight else dtype
+    code, store = _DTYPE_CODE.get(dtype), _E4M3 if eight else dtype
     ix = q.get_device()
     if out is None:
         out = torch.empty_like(q)
     if not (ix >= 0 and code is not None and len(shape) == 3 and len(pool) == 4 and len(table) == 2
             and pool[3] == shape[2] and table[0] == shape[0] and v_pages.shape == pool and k_pages.dtype == store
-            and v_pages.dtype == store and page_table.dtype == torch.int32 and kv_len.dtype == torch.int32
+            and v_pages.dtype == store and page_table.dtype == _I32 and kv_len.dtype == _I32
             and kv_len.numel() == shape[0] and out.shape == shape and out.dtype == dtype
             and k_pages.get_device() == ix and v_pages.get_device() == ix and page_table.get_device() == ix
             and kv_len.get_device() == ix and out.get_device() == ix and q.is_contiguous()
             and k_pages.is_contiguous() and v_pages.is_contiguous() and page_table.is_contiguous()
             and kv_len.is_contiguous() and out.is_contiguous()
             and (workspace is None or (workspace.get_device() == ix and workspace.is_contiguous()))
-            and (not eight or (k_scale.dtype == torch.float32 and v_scale.dtype == torch.float32
-                               and k_scale.shape == pool[:2] and v_scale.shape == pool[:2]
+            and (not eight or (k_scale.dtype == _F32 and v_scale.dtype == _F32
+                               and k_scale.shape == (pairs := pool[:2])
+                               and v_scale.shape == pairs
                                and k_scale.get_device() == ix and v_scale.get_device() == ix
                                and k_scale.is_contiguous() and v_scale.is_contiguous()))
             and (err_flag is None or (err_flag.dtype == torch.int32 and err_flag.numel() >= 1
