@@ -39,6 +39,7 @@ class DecodeAttnError(RuntimeError):
 
 
 _lib = None
+_fast = None  # the fast path's module; False where there is none
 
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
@@ -92,6 +93,31 @@ def load_library() -> ctypes.CDLL:
             fn.restype = res
         _lib = lib
     return _lib
+
+
+def _load_fast():
+    """The binding's fast path (csrc/fastcall.cpp), bound to the library; False
+    where it has not been built. Its functions return NotImplemented for calls
+    that they leave to the Python path."""
+    global _fast
+    lib = load_library()
+    from .build import fastcall_path
+
+    path = fastcall_path()
+    if not path.exists():
+        _fast = False
+        return _fast
+    import importlib.machinery
+    import importlib.util
+
+    loader = importlib.machinery.ExtensionFileLoader("_fastcall", str(path))
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_fastcall", loader))
+    loader.exec_module(module)
+    module.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
+        "decode_attn_paged_fwd", "decode_attn_paged_q8_fwd", "decode_attn_window_fwd", "kvcache_append_paged",
+        "kvcache_append_paged_q8")))
+    _fast = module
+    return _fast
 
 
 def exported_symbols() -> list[str]:
@@ -649,6 +675,12 @@ def kvcache_append_paged(k_pages: torch.Tensor, v_pages: torch.Tensor, k_new: to
     (token_start None: one token per sequence). With rope tables the keys are
     rotated at their positions, and q [tokens, n_head, D] into q_out (may be
     q), which is returned."""
+    fast = _load_fast() if _fast is None else _fast
+    if fast:
+        r = fast.append(k_pages, v_pages, None, None, k_new, v_new, page_table, position_ids, token_start, rope_cos,
+                        rope_sin, q, q_out, err_flag)
+        if r is not NotImplemented:
+            return r
     return _append_paged("kvcache_append_paged", k_pages, v_pages, None, None, False, k_new, v_new, page_table,
                          position_ids, token_start, rope_cos, rope_sin, q, q_out, err_flag)
 
@@ -664,6 +696,12 @@ def kvcache_append_paged_q8(k_pages: torch.Tensor, v_pages: torch.Tensor, k_scal
     scale per page and KV head (k_scale/v_scale float32 [num_pages, n_kv_head],
     updated in place; a page whose scale grows has its earlier rows rounded to
     the new one)."""
+    fast = _load_fast() if _fast is None else _fast
+    if fast and k_scale is not None:
+        r = fast.append(k_pages, v_pages, k_scale, v_scale, k_new, v_new, page_table, position_ids, token_start,
+                        rope_cos, rope_sin, q, q_out, err_flag)
+        if r is not NotImplemented:
+            return r
     return _append_paged("kvcache_append_paged_q8", k_pages, v_pages, k_scale, v_scale, True, k_new, v_new,
                          page_table, position_ids, token_start, rope_cos, rope_sin, q, q_out, err_flag)
 
@@ -735,6 +773,12 @@ def decode_attn_paged_fwd(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch
     paged cache (or, with window > 0, over the last `window` of them and the
     first `sinks`); kv_len[b] == 0 gives zeros. A workspace comes from
     alloc_paged_workspace (reuse it across calls)."""
+    fast = _load_fast() if _fast is None else _fast
+    if fast:
+        r = fast.attn_paged(q, k_pages, v_pages, None, None, page_table, kv_len, window, sinks, out, scale, workspace,
+                            err_flag)
+        if r is not NotImplemented:
+            return r
     return _attn_paged("decode_attn_paged_fwd", q, k_pages, v_pages, None, None, False, page_table, kv_len, window,
                        sinks, out, scale, workspace, err_flag)
 
@@ -746,6 +790,12 @@ def decode_attn_paged_q8_fwd(q: torch.Tensor, k_pages: torch.Tensor, v_pages: to
                              err_flag: torch.Tensor | None = None) -> torch.Tensor:
     """decode_attn_paged_fwd over float8_e4m3fn pools with their scales
     float32 [num_pages, n_kv_head]."""
+    fast = _load_fast() if _fast is None else _fast
+    if fast and k_scale is not None:
+        r = fast.attn_paged(q, k_pages, v_pages, k_scale, v_scale, page_table, kv_len, window, sinks, out, scale,
+                            workspace, err_flag)
+        if r is not NotImplemented:
+            return r
     return _attn_paged("decode_attn_paged_q8_fwd", q, k_pages, v_pages, k_scale, v_scale, True, page_table, kv_len,
                        window, sinks, out, scale, workspace, err_flag)
 
@@ -756,6 +806,11 @@ def decode_attn_window_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torc
                            err_flag: torch.Tensor | None = None) -> torch.Tensor:
     """Decode attention over the last `window` of the first kv_len[b] rows of a
     static cache and its first `sinks` rows; nothing else is read."""
+    fast = _load_fast() if _fast is None else _fast
+    if fast:
+        r = fast.attn_window(q, k_cache, v_cache, kv_len, window, sinks, out, scale, workspace, err_flag)
+        if r is not NotImplemented:
+            return r
     dtype, shape, cache = q.dtype, q.shape, k_cache.shape
     code, ix = _DTYPE_CODE.get(dtype), q.get_device()
     if out is None:

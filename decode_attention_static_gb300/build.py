@@ -11,6 +11,9 @@ import os
 import pathlib
 import shutil
 import subprocess
+import sys
+import sysconfig
+import warnings
 
 PKG = pathlib.Path(__file__).resolve().parent
 ROOT = PKG.parent
@@ -49,8 +52,53 @@ def _stale(output: pathlib.Path) -> bool:
     return any(d.stat().st_mtime > t for d in deps)
 
 
+def fastcall_path() -> pathlib.Path:
+    """The fast path's module for this Python and torch (it is bound to both)."""
+    import torch
+
+    return PKG / f"_fastcall.{sys.implementation.cache_tag}.torch-{torch.__version__}.so"
+
+
+def build_fastcall(force: bool = False) -> pathlib.Path | None:
+    """Compile the binding's fast path if a source is newer than it; None (and
+    a warning) where that does not work."""
+    import torch
+
+    out = fastcall_path()
+    if not force and not _stale(out):
+        return out
+    root = pathlib.Path(torch.__file__).parent
+    cuda = pathlib.Path(nvcc()).parent.parent
+    tmp = out.with_name(out.name + f".tmp{os.getpid()}")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-I{INCLUDE}",
+           f"-I{root / 'include'}", f"-I{root / 'include/torch/csrc/api/include'}",
+           f"-I{sysconfig.get_paths()['include']}", f"-I{cuda / 'include'}", str(CSRC / "fastcall.cpp"), "-o", str(tmp),
+           f"-L{root / 'lib'}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python",
+           f"-Wl,-rpath,{root / 'lib'}"]
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+    except OSError as e:
+        warnings.warn(f"the binding's fast path was not built: {e}")
+        return None
+    if r.returncode != 0:
+        warnings.warn(f"the binding's fast path was not built:\n{' '.join(cmd)}\n{r.stderr[-2000:]}")
+        return None
+    os.replace(tmp, out)
+    return out
+
+
 def build_library(force: bool = False, verbose_ptxas: bool = False) -> pathlib.Path:
-    """Compile and link the library if any source is newer than it."""
+    """Compile and link the library (and the binding's fast path) if any source
+    is newer than it."""
+    with cf.ThreadPoolExecutor(max_workers=1) as fast:
+        extra = fast.submit(build_fastcall, force)
+        path = _build_library(force, verbose_ptxas)
+        extra.result()
+    return path
+
+
+def _build_library(force: bool, verbose_ptxas: bool) -> pathlib.Path:
     if not force and not _stale(LIBRARY):
         return LIBRARY
     BUILD_DIR.mkdir(exist_ok=True)
@@ -71,6 +119,4 @@ def build_library(force: bool = False, verbose_ptxas: bool = False) -> pathlib.P
 
 
 if __name__ == "__main__":
-    import sys
-
     print(build_library(force=True, verbose_ptxas="-v" in sys.argv))

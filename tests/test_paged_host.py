@@ -199,6 +199,64 @@ def test_binding_says_what_is_wrong(eight):
     torch.cuda.synchronize()
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("eight", [False, True], ids=["16bit", "e4m3"])
+def test_both_paths_of_the_binding(eight, monkeypatch):
+    """The calls made in C++ and those made from Python do the same, on a stream
+    of their own too, and the C++ path is there."""
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from decode_attention_static_gb300 import _binding
+
+    da_build.build_library()
+    assert _binding._load_fast()
+    gen = torch.Generator().manual_seed(0)
+    new, q = torch.randn(5, 2, 64, generator=gen).half().cuda(), torch.randn(5, 4, 64, generator=gen).half().cuda()
+    tab = torch.arange(5, dtype=torch.int32, device="cuda")[:, None].contiguous()
+    pos = torch.tensor([0, 3, 15, 7, 8], dtype=torch.int32, device="cuda")
+    cos, sin = torch.rand(16, 64, generator=gen).cuda(), torch.rand(16, 64, generator=gen).cuda()
+    ws, out = da.alloc_paged_workspace(4, 2, 64), torch.empty_like(q)
+    taken = []
+
+    def run():
+        pool = [torch.full((6, 2, 16, 64), 0.5, device="cuda").to(R.E4M3 if eight else torch.float16) for _ in range(2)]
+        pool += [torch.full((6, 2), 0.25, device="cuda") for _ in range(2)] if eight else []
+        append = da.kvcache_append_paged_q8 if eight else da.kvcache_append_paged
+        attend = da.decode_attn_paged_q8_fwd if eight else da.decode_attn_paged_fwd
+        got = [append(*pool, new, new, tab, pos), append(*pool, new, new, tab, pos, rope_cos=cos, rope_sin=sin, q=q),
+               append(*pool, new, new, tab, pos, rope_cos=cos, rope_sin=sin, q=q, q_out=out)]
+        assert got[0] is None and got[2] is out
+        got = [got[1], out.clone(), *pool]
+        got.append(attend(q, *pool, tab, pos, workspace=ws))
+        got.append(attend(q, *pool, tab, pos, window=3, sinks=1, scale=0.3, workspace=ws, out=out).clone())
+        cache = torch.full((5, 2, 16, 64), 0.5, device="cuda").half()
+        got.append(da.decode_attn_window_fwd(q, cache, new[:, :, None].repeat(1, 1, 16, 1), pos, 4, workspace=ws))
+        return [t.view({1: torch.uint8, 2: torch.int16, 4: torch.int32}[t.element_size()]).cpu() for t in got]
+
+    class Counted:
+        def __init__(self, module):
+            self.module = module
+
+        def __getattr__(self, name):
+            def call(*args):
+                r = getattr(self.module, name)(*args)
+                taken.append(r is not NotImplemented)
+                return r
+            return call
+
+    monkeypatch.setattr(_binding, "_fast", Counted(_binding._fast))
+    fast = run()
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        again = run()
+    assert all(taken) and len(taken) == 12
+    monkeypatch.setattr(_binding, "_fast", False)
+    slow = run()
+    for f, a, s in zip(fast, again, slow):
+        assert torch.equal(f, s) and torch.equal(a, s)
+
+
 def test_plain_forms_on_known_values():
     """The tests' own plain form: the e4m3 grid against torch's conversion, and
     scales at powers of two."""
