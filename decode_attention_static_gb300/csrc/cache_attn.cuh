@@ -221,6 +221,14 @@ __device__ __forceinline__ uint32_t tile_mask(const SequenceTiles& s, int row0) 
   return mask;
 }
 
+// Counts this CTA in and returns how many were before it: its writes ahead of
+// the last barrier are visible to whoever counts later, and theirs to it.
+__device__ __forceinline__ unsigned int arrive(unsigned int* counter) {
+  unsigned int n;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(n) : "l"(counter) : "memory");
+  return n;
+}
+
 // (out of line: a 64-bit division is some hundred instructions)
 static __device__ __noinline__ int64_t divide(int64_t a, int64_t b) { return a / b; }
 
@@ -863,10 +871,8 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
           unsigned int* counter = p.counters + (last_round ? from : (head ? 2 : 1) * kMaxCtas + from + head);
           __syncthreads();
           if (tid == 0) {
-            __threadfence();  // (cumulative: the CTA's writes before the barrier)
-            *arrived = atomicAdd(counter, 1u);
-            __threadfence();
-          }
+            *arrived = arrive(counter);
+        }
           __syncthreads();
           const unsigned int order = *arrived;
           if (order >= (unsigned int)count) {
