@@ -884,15 +884,15 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
           }
           if (order != (unsigned int)count - 1) break;
           // the threads share the vectors, and with fewer vectors than threads also
-          // the parts; a thread's first eight are on their way while the warps
+          // the parts; a thread's first ten are on their way while the warps
           // find the parts' factors
           float* factor = merge;                        // [count][8]
           float4* sums = reinterpret_cast<float4*>(merge + kJoinWide * kHeads);  // [kThreads]
           const int crews = Sh::kThreads / items, crew = tid / items, i = tid - crew * items, h = i / (D / 4);
-          float4 v[8], r = make_float4(0.f, 0.f, 0.f, 0.f);
+          float4 v[10], r = make_float4(0.f, 0.f, 0.f, 0.f);
           auto fetch = [&](int s0) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
+            for (int j = 0; j < 10; ++j)
               if (s0 + j * crews < count)
                 v[j] = __ldcg(reinterpret_cast<const float4*>(slot_of(head + (s0 + j * crews) * step)) + i);
           };
@@ -931,9 +931,9 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
           __syncthreads();
           for (int s0 = crew; s0 < count;) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
+            for (int j = 0; j < 10; ++j)
               if (s0 + j * crews < count) add(r, factor[(s0 + j * crews) * kHeads + h], v[j]);
-            s0 += 8 * crews;
+            s0 += 10 * crews;
             if (s0 < count) fetch(s0);
           }
           if (crews > 1) {
