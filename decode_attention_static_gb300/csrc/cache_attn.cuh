@@ -253,10 +253,11 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
   // for its end (short groups are then balanced by what they cost, and those
   // places hold cuts that would split a group). One pass over the lengths, and,
   // for more sequences than threads, a second one for the sequence that holds
-  // `lo`. A batch of at most 32 is seen by each warp alone, without a barrier,
-  // and first while the kernel before this one still runs: the lengths of then
-  // say which rows to bring into L2 (a hint; page numbers are checked), and if
-  // they are still those after the wait, the share stands.
+  // `lo`. A batch of at most 32 is seen by each warp alone, without a barrier.
+  // Where one pass will do it is made while the kernel before this one still
+  // runs: the lengths of then say which rows to bring into L2 (a hint; page
+  // numbers are checked), and if they are still those after the wait, the share
+  // stands.
   struct Found {
     int64_t start;  // first place of the sequence
     int b, len;
@@ -345,7 +346,8 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
     }
     return b < p.B;
   };
-  bool waited = !alone;
+  const bool one_pass = p.B <= Sh::kThreads;
+  bool waited = !one_pass;
   if (waited) {
     pdl_wait();
     pdl_trigger();  // the next grid can take the SMs as they fall free; it waits for this one's memory
@@ -356,7 +358,7 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
     short_groups = false;
     for (int base = 0; base < p.B; base += columns) {
       pass(base);
-      if (!alone) fill_idle(base);
+      if (!one_pass) fill_idle(base);
     }
     const int64_t tiles = (before & ((1ll << kCount) - 1)) * p.n_kv_head, groups = (before >> kCount) * p.n_kv_head;
     if (groups > gridDim.x) {
@@ -396,7 +398,7 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
         const int src = __ffs(__ballot_sync(0xffffffffu, holds())) - 1;
         first = {__shfl_sync(0xffffffffu, places(mine), src), src, __shfl_sync(0xffffffffu, len, src)};
       } else {
-        if (p.B <= Sh::kThreads) {
+        if (one_pass) {
           if (holds()) *found = {places(mine), tid, len};
         } else {
           before = 0;
@@ -433,10 +435,10 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
     pdl_wait();
     pdl_trigger();
     waited = true;
-    const int now = lane < p.B ? __ldcg(p.kv_len + lane) : 0;
-    if (__all_sync(0xffffffffu, now == len)) break;
+    const bool same = column >= p.B || __ldcg(p.kv_len + column) == len;
+    if (alone ? __all_sync(0xffffffffu, same) : __syncthreads_and(same)) break;
   }
-  if (alone) fill_idle(0);
+  if (one_pass) fill_idle(0);
   if ((int64_t)blockIdx.x >= ctas) return;
   const int step = short_groups ? 1 : kW;  // tiles between this warp's
   const int share = (int)(hi - lo);  // (below 2^31: checked on the host)
