@@ -55,9 +55,14 @@ namespace da {
 
 constexpr int kHeads = 8;        // columns of the matrix instruction
 constexpr int kMaxCtas = 256;    // one for each SM; parts of one group, at most
-constexpr int kFewestTiles = 8;  // of a share
-constexpr int kGroupCost = 8;    // what the end of a group costs, in tiles
-constexpr int kJoinCost = 16;    // and of one in parts
+// The split, in tiles; each was swept on the device. A share of kFewestTiles: with
+// 4, 1 x 1024 of 16/8 heads takes 11.0 us for 6.8. The end of a group costs
+// kGroupCost, that of one in parts kJoinCost: without the latter 8 ragged to 8191
+// take 32.4 us for 29.2. With as many CTAs for every group a share saves kEvenGain,
+// and kAloneGain where there is then nothing to join; its tiles take 7/8 of the
+// time, as fewer SMs share HBM. 16 x 8192 of 16/8 heads: 81.7 us even, 85.3 not;
+// 12 ragged to 2000, e4m3: 13.8 and 15.1; but 5 ragged to 3000: 13.4 and 12.7.
+constexpr int kFewestTiles = 8, kGroupCost = 8, kJoinCost = 16, kEvenGain = 12, kAloneGain = 48;
 // A group in more than kJoinWide parts (at most 256) is joined in two rounds, of
 // kJoinWidth neighbours and of the sums of those.
 constexpr int kJoinWide = 64, kJoinWidth = 16;
@@ -89,7 +94,7 @@ struct CacheAttnShape {
   // (m, l) of each warp, and of joined parts; schedule words
   static constexpr int kStatFloats = 2 * kWarps * kHeads + 2 * kHeads;
   static constexpr int kWordsOffset = kStatOffset + kStatFloats * 4;
-  static constexpr int kSmemBytes = kWordsOffset + (kWarps + 4) * 8;
+  static constexpr int kSmemBytes = kWordsOffset + (kWarps + 4 + (kWarps + 1) / 2) * 8;
   static_assert(kStages >= 3, "a ring of at least three stages");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory of a CTA");
   static_assert(kJoinWide * kHeads * 4 + kThreads * 16 <= kMergeBytes,
@@ -249,9 +254,10 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, gr = lane >> 2, tq = lane & 3;
 
   // --- the list of places, and this CTA's share [lo, hi) of it: the tiles of
-  // each group, and, with more groups than CTAs, kGroupCost places that stand
-  // for its end (short groups are then balanced by what they cost, and those
-  // places hold cuts that would split a group). One pass over the lengths, and,
+  // each group, and some places that stand for its end (short groups are then
+  // balanced by what they cost, and those places hold cuts that would split a
+  // group); or, with groups about equal, as many places for each, so that the
+  // cuts fall between them. One pass over the lengths, and,
   // for more sequences than threads, a second one for the sequence that holds
   // `lo`. A batch of at most 32 is seen by each warp alone, without a barrier.
   // Where one pass will do it is made while the kernel before this one still
@@ -270,16 +276,17 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
   const int column = alone ? lane : tid, columns = alone ? 32 : Sh::kThreads;
   int64_t before = 0, mine = 0, own = 0;  // before this pass, before this thread's sequence, and its own
   int len = 0, most = 0;                  // most tiles of a sequence
+  int* tops = reinterpret_cast<int*>(words + kW + 4);  // [kW]
   auto pass = [&](int base) {
     const int b = base + column;
-    own = 0;
+    int n = 0;
     if (b < p.B) {
       SequenceTiles s;
       len = __ldcg(p.kv_len + b);  // (L2: read before the wait, it may be read again)
-      const int n = tiles_of<kRows>(p, len, &s);
-      if (n > 0) own = n + (1ll << kCount);
-      most = max(most, n);
+      n = max(tiles_of<kRows>(p, len, &s), 0);
     }
+    own = n ? n + (1ll << kCount) : 0;
+    const int top = __reduce_max_sync(0xffffffffu, n);
     int64_t sum = own;
 #pragma unroll 1
     for (int o = 1; o < 32 && o < p.B; o <<= 1) {
@@ -289,15 +296,20 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
     mine = before + sum - own;
     if (alone) {
       before = __shfl_sync(0xffffffffu, sum, p.B - 1);
+      most = top;
       return;
     }
     if (base) __syncthreads();  // the words of the pass before have been read
-    if (lane == 31) words[warp] = sum;
+    if (lane == 31) {
+      words[warp] = sum;
+      tops[warp] = top;
+    }
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kW; ++w) {
       if (w < warp) mine += words[w];
       before += words[w];
+      most = max(most, tops[w]);
     }
   };
   // Sequences without a visible row get zeros, those without a valid length NaN.
@@ -318,11 +330,13 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
     }
   };
   int64_t ctas = 0, total = 0, lo = 0, hi = 0;
-  int end_cost = 0;
+  int end_cost = 0, even = 0;  // places behind a group's tiles; with even groups, places of every group
   bool small = true;
   auto places = [&](int64_t word) {
-    return ((word & ((1ll << kCount) - 1)) + (word >> kCount) * end_cost) * p.n_kv_head;
+    const int64_t n = word >> kCount;
+    return (even ? n * even : (word & ((1ll << kCount) - 1)) + n * end_cost) * p.n_kv_head;
   };
+  auto behind = [&](const SequenceTiles& s) { return even ? even - s.tiles : end_cost; };
   // first place of share i, and the share that holds place x (in 32 bits where
   // they suffice: a 64-bit division is some hundred instructions)
   auto share_start = [&](int64_t i) {
@@ -361,10 +375,9 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
       if (!one_pass) fill_idle(base);
     }
     const int64_t tiles = (before & ((1ll << kCount) - 1)) * p.n_kv_head, groups = (before >> kCount) * p.n_kv_head;
+    even = 0;
     if (groups > gridDim.x) {
-      // (uniform in the grid: every warp, or every CTA, sees all lengths)
-      const bool few = most <= kShortRows / kRows;
-      short_groups = alone ? __all_sync(0xffffffffu, few) : __syncthreads_and(few);
+      short_groups = most <= kShortRows / kRows;
       if (short_groups) {
         ctas = gridDim.x;
         g = warp * gridDim.x + blockIdx.x;
@@ -378,13 +391,22 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
     }
     // as many CTAs as find kFewestTiles
     if (!short_groups) ctas = min((int64_t)gridDim.x, (tiles + kFewestTiles - 1) / kFewestTiles);
-    if (!short_groups && (int64_t)blockIdx.x < ctas) {
+    if (!short_groups) {
       end_cost = kGroupCost;
-      if (groups <= ctas) {
-        const uint32_t n = (uint32_t)ctas;
-        end_cost =
-            n % (uint32_t)groups == 0 ? 0 : (int)(tiles >= ctas * kJoinCost * 8 ? kJoinCost : (uint32_t)tiles / n / 8);
+      if (groups <= ctas && groups > 0) {
+        // as many CTAs for every group, where the largest part then takes no longer
+        // than an even share of all tiles with the ends of groups in it
+        const uint32_t n = (uint32_t)ctas, each = n / (uint32_t)groups;
+        const int64_t part = (most + each - 1) / each;
+        if (part * ctas * 7 <= (tiles + ctas * (each == 1 ? kAloneGain : kEvenGain)) * 8) {
+          ctas = each * groups;
+          even = (int)(part * each);
+        } else {
+          end_cost = tiles >= ctas * kJoinCost * 8 ? kJoinCost : (int)((uint32_t)tiles / n / 8);
+        }
       }
+    }
+    if (!short_groups && (int64_t)blockIdx.x < ctas) {
       total = places(before);
       small = total * ctas < (1ll << 32);
       lo = share_start(blockIdx.x);
@@ -414,7 +436,7 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
       b = first.b;
       tiles_of<kRows>(p, first.len, &seq);
       const int64_t in = lo - first.start;
-      const int size = seq.tiles + end_cost;
+      const int size = seq.tiles + behind(seq);
       g = small ? (int)((uint32_t)in / (uint32_t)size) : (int)divide(in, size);
       tile = (int)(in - (int64_t)g * size);
     }
@@ -456,7 +478,7 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
   };
   if (tile >= seq.tiles) {
     // the share begins in the places of a group's end
-    at += seq.tiles + end_cost - tile;
+    at += seq.tiles + behind(seq) - tile;
     tile = 0;
     if (!next_group(at, b, g, seq)) return;
   }
@@ -476,7 +498,7 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
     lmask = 0;
     while (more && li >= lseq.tiles) {
       li -= lseq.tiles;
-      lat += end_cost;
+      lat += behind(lseq);
       more = next_group(lat - li, lb, lg, lseq);
     }
     more = more && lat < share;
@@ -966,7 +988,7 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
     }
 
     // --- the next group
-    at += here + end_cost;
+    at += here + behind(seq);
     tile = 0;
     if (!next_group(at, b, g, seq)) break;
   }
