@@ -9,9 +9,9 @@
 // bound by HBM, single tokens by the chain of dependent loads (sequence,
 // position, page). Measured (of the measured 6782 GB/s copy): prompts of 8.4k
 // tokens, 8 KV and 32 query heads of 128, fp16, 225 MB in 37.6 us (88%); the
-// same heads, 21k tokens into 8 bits, 482 MB in 87.8 us (81%; its K and V part
-// alone 40 us, bound by the chain of peaks and rounding at two CTAs an SM); 8
-// sequences, one token each, 2.4 us, 64 into 8 bits 2.4 us.
+// same heads, 21k tokens into 8 bits, 482 MB in 86.7 us (82%; the 30% that are K
+// and V take 35 us, bound by the chain of peaks and rounding at two CTAs an SM);
+// 8 sequences, one token each, 2.4 us, 64 into 8 bits 2.4 us.
 #include <stdint.h>
 
 #include <algorithm>
@@ -59,6 +59,14 @@ __device__ __forceinline__ int sequence_of(const AppendPagedParams& p, int t) {
   return lo;
 }
 
+__device__ __forceinline__ void load_f32x4(const float* from, float (&out)[4]) {
+  const uint4 v = ld_global_nc_v4(from);
+  out[0] = __uint_as_float(v.x);
+  out[1] = __uint_as_float(v.y);
+  out[2] = __uint_as_float(v.z);
+  out[3] = __uint_as_float(v.w);
+}
+
 // cos and sin of one row at a lane's two vectors.
 struct RopeRow {
   float c0[8], s0[8], c1[8], s1[8];
@@ -83,6 +91,31 @@ struct RopeRow {
     }
   }
 };
+
+// The same for a row's unpacked vectors of N heads, in place; 4 elements at a
+// time, so that few registers hold the table row.
+template <int N>
+__device__ __forceinline__ void rotate_rows(const AppendPagedParams& p, int position, int c, float (&a)[N][8],
+                                            float (&b)[N][8]) {
+  const int64_t at = (int64_t)position * p.head_dim + 8 * c;
+#pragma unroll
+  for (int q = 0; q < 8; q += 4) {
+    float c0[4], s0[4], c1[4], s1[4];
+    load_f32x4(p.cos + at + q, c0);
+    load_f32x4(p.sin + at + q, s0);
+    load_f32x4(p.cos + at + p.head_dim / 2 + q, c1);
+    load_f32x4(p.sin + at + p.head_dim / 2 + q, s1);
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float x = a[k][q + e], y = b[k][q + e];
+        a[k][q + e] = __fsub_rn(__fmul_rn(x, c0[e]), __fmul_rn(y, s0[e]));
+        b[k][q + e] = __fadd_rn(__fmul_rn(y, c1[e]), __fmul_rn(x, s1[e]));
+      }
+    }
+  }
+}
 
 template <typename T>
 __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
@@ -326,20 +359,26 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// e4m3 pages, prompts: one CTA for each (touched page, K or V, range of chunks
-// of heads). A unit takes R rows of the page (as many units as the page has
-// rows; where the CTA has more, they take further heads) and HC heads of a
-// chunk. A thread's rows of the next chunk are on their way into its own
-// places in shared memory while it finds the peaks of this one and rounds it:
-// nothing is waited for but the peaks, once a chunk.
+// e4m3 pages, prompts. An item is a touched page, K or V of it, and a chunk of
+// heads; the page CTAs take equal runs of the items' list. A unit takes R rows
+// of the page (as many units as the page has rows; where the CTA has more, they
+// take further heads) and HC heads of a chunk. A thread's rows of the next item
+// are on their way into its own places in shared memory while it finds the
+// peaks of this one and rounds it: nothing is waited for but the peaks, once an
+// item. Two CTAs of 64 values a thread fill an SM's registers. (21k tokens of 8
+// KV and 32 query heads, us: pages of 16 / 64 / 128 87.6 / 86.7 / 89.9; one CTA for
+// each page and K or V, with no load ahead of it, 97 / 87 / 93; three CTAs of 32
+// values 92 / 101 / 90; the values rotated twice instead of kept 98 / 97 / 102.)
 __host__ __device__ constexpr int prompt_heads(int R) { return R >= 4 ? 1 : 4 / R; }
 __host__ __device__ constexpr int prompt_smem(int R) { return 2 * kThreads * R * prompt_heads(R) * 32; }
+__host__ __device__ constexpr int prompt_ctas(int R) { return R == 8 ? 1 : 2; }  // on an SM
 
 template <typename T, int R>
-__global__ void __launch_bounds__(kThreads, R == 8 ? 1 : 2)
-    append_prompt_q8_kernel(const AppendPagedParams p, int page_tasks, int ranges, int range_chunks, int stride) {
+__global__ void __launch_bounds__(kThreads, prompt_ctas(R))
+    append_prompt_q8_kernel(const AppendPagedParams p, int page_ctas, int chunks, int stride) {
   constexpr int HC = prompt_heads(R), kWarps = kThreads / 32;
   extern __shared__ __align__(16) uint4 staged[];  // [2][R * HC][2][kThreads]
+  __shared__ int64_t sh_items;
   __shared__ int sh[2];
   __shared__ uint32_t sh_peak[2][HC][kWarps];
   pdl_wait();
@@ -347,124 +386,133 @@ __global__ void __launch_bounds__(kThreads, R == 8 ? 1 : 2)
   const int row_vecs = p.head_dim / 8, half = row_vecs / 2, Hkv = p.n_kv_head;
   const int units = kThreads / half, unit = threadIdx.x / half, c = threadIdx.x % half;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int64_t page_ctas = (int64_t)page_tasks * 2 * ranges;
-  if (blockIdx.x >= page_ctas) {
-    const int64_t u = (blockIdx.x - page_ctas) * units + unit, t = u / stride;
+  if ((int)blockIdx.x >= page_ctas) {
+    const int64_t u = (int64_t)(blockIdx.x - page_ctas) * units + unit, t = u / stride;
     if (t < p.tokens) move_token<T>(p, (int)t, 2 * Hkv + (int)(u - t * stride), stride, c);
     return;
   }
-  const int task = (int)(blockIdx.x / (2 * ranges)), part = (int)(blockIdx.x % (2 * ranges));
-  const bool is_k = part < ranges;
-  if (threadIdx.x < 32) {
-    // the task's sequence and page: tasks are the touched pages in sequence order
-    int b_found = -1, j = 0, before = 0;
-    for (int base = 0; base < p.B && b_found < 0; base += 32) {
-      const int b = base + threadIdx.x;
-      int pages = 0, first, count, p0;
-      if (b < p.B && sequence_rows(p, b, &first, &count, &p0) && count > 0)
-        pages = ((p0 + count - 1) >> p.page_shift) - (p0 >> p.page_shift) + 1;
+  int first = 0, count = 0, p0 = 0;  // new rows of the sequence at hand
+  auto pages_of = [&](int b) {
+    return b < p.B && sequence_rows(p, b, &first, &count, &p0) && count > 0
+               ? ((p0 + count - 1) >> p.page_shift) - (p0 >> p.page_shift) + 1 : 0;
+  };
+  if (warp == 0) {
+    // the touched pages, in sequence order; the sequence and page of the first item
+    int64_t items = 0;
+    for (int b = lane; b < p.B; b += 32) items += pages_of(b);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) items += __shfl_xor_sync(0xffffffffu, items, o);
+    items *= 2 * chunks;
+    const int64_t task = items * blockIdx.x / page_ctas / (2 * chunks);
+    int64_t before = 0;
+    for (int base = 0; base < p.B; base += 32) {
+      const int pages = pages_of(base + lane);
       int sum = pages;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, sum, o);
-        if (threadIdx.x >= o) sum += v;
+        if (lane >= o) sum += v;
       }
-      const unsigned hit = __ballot_sync(0xffffffffu, before + sum > task);
-      if (hit) {
-        const int src = __ffs(hit) - 1;
-        b_found = base + src;
-        j = task - before - (__shfl_sync(0xffffffffu, sum, src) - __shfl_sync(0xffffffffu, pages, src));
+      if (task >= before + sum - pages && task < before + sum) {
+        sh[0] = base + lane;
+        sh[1] = (int)(task - (before + sum - pages));
       }
       before += __shfl_sync(0xffffffffu, sum, 31);
+      if (before > task) break;
     }
-    if (threadIdx.x == 0) {
-      sh[0] = b_found;
-      sh[1] = j;
-    }
+    if (lane == 0) sh_items = items;
   }
   if (blockIdx.x == 0 && p.err_flag) {
     for (int b = threadIdx.x; b < p.B; b += kThreads) {
-      int first, count, p0;
       if (!sequence_rows(p, b, &first, &count, &p0)) atomicOr(p.err_flag, kErrPosition);
     }
   }
   __syncthreads();
-  const int b = sh[0];
-  if (b < 0) return;
-  int first = 0, count = 0, p0 = 0;
-  sequence_rows(p, b, &first, &count, &p0);
-  const int j = (p0 >> p.page_shift) + sh[1], row0 = j << p.page_shift;
-  const int lo = max(p0, row0), hi = min(p0 + count, row0 + p.page_rows);
-  // rows of this unit: slot, slot + slots, ...; its heads of chunk n: from
-  // (n * at_once + unit / slots) * HC on
+  const int64_t begin = sh_items * blockIdx.x / page_ctas;
+  int left = (int)(sh_items * (blockIdx.x + 1) / page_ctas - begin);  // items of this CTA
+  if (left == 0) return;
+  // the next item: chunk `chunk` of V (which) or K of page j of sequence b
+  int b = sh[0], chunk = (int)(begin % chunks), which = (int)(begin / chunks % 2);
+  pages_of(b);
+  int j = (p0 >> p.page_shift) + sh[1];
+  // rows of this unit: slot, slot + slots, ...; its heads of a chunk: from
+  // (chunk * at_once + unit / slots) * HC on
   const int slots = p.page_rows / R, slot = unit % slots, at_once = units / slots;
-  const int chunk_heads = at_once * HC, chunks = (Hkv + chunk_heads - 1) / chunk_heads;
-  const int begin = (part % ranges) * range_chunks, end = min(begin + range_chunks, chunks);
-  const uint4* in = reinterpret_cast<const uint4*>(is_k ? p.k_new : p.v_new);
+  struct Item {
+    int row0, lo, hi, page, which, g0;  // first row of the page, rows [lo, hi) of it, first head of the unit
+  };
   auto place = [&](int stage, int i, int k, int which) {
     return staged + (((stage * R + i) * HC + k) * 2 + which) * kThreads + threadIdx.x;
   };
-  auto fetch = [&](int n) {
-    const int g0 = (n * at_once + unit / slots) * HC;
+  auto fetch = [&](int stage) {
+    Item it;
+    it.row0 = j << p.page_shift;
+    it.lo = max(p0, it.row0);
+    it.hi = min(p0 + count, it.row0 + p.page_rows);
+    it.which = which;
+    it.g0 = (chunk * at_once + unit / slots) * HC;
+    const uint4* in = reinterpret_cast<const uint4*>(which ? p.v_new : p.k_new);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      const int position = row0 + slot + i * slots;
-      if (position >= lo && position < hi) {
-        const uint4* src = in + (((int64_t)first + position - p0) * Hkv + g0) * row_vecs + c;
+      const int position = it.row0 + slot + i * slots;
+      if (position >= it.lo && position < it.hi) {
+        const uint4* src = in + (((int64_t)first + position - p0) * Hkv + it.g0) * row_vecs + c;
 #pragma unroll
         for (int k = 0; k < HC; ++k) {
-          if (g0 + k < Hkv) {
-            copy16(smem_addr(place(n & 1, i, k, 0)), src + k * row_vecs);
-            copy16(smem_addr(place(n & 1, i, k, 1)), src + k * row_vecs + half);
+          if (it.g0 + k < Hkv) {
+            copy16(smem_addr(place(stage, i, k, 0)), src + k * row_vecs);
+            copy16(smem_addr(place(stage, i, k, 1)), src + k * row_vecs + half);
           }
         }
       }
     }
     copy_commit();
+    it.page = p.table[(int64_t)b * p.max_pages + j];
+    return it;
   };
-  if (begin < end) fetch(begin);
-  const int page = p.table[(int64_t)b * p.max_pages + j];
-  if (page < 0 || page >= p.num_pages) {
-    if (part == 0 && threadIdx.x == 0 && p.err_flag) atomicOr(p.err_flag, kErrPage);
-    copy_wait<0>();
-    return;
-  }
-  const bool rotate = is_k && p.cos;
+  auto advance = [&]() {
+    if (++chunk < chunks) return;
+    chunk = 0;
+    which ^= 1;
+    if (which) return;
+    if (++j <= (p0 + count - 1) >> p.page_shift) return;
+    do ++b; while (pages_of(b) == 0 && b < p.B - 1);  // (an item is left, so there is one)
+    j = p0 >> p.page_shift;
+  };
   const int team = slots * half, team_warps = team / 32, warp0 = warp / team_warps * team_warps;  // (whole warps)
-  const int old_rows = lo - row0;
-  uint8_t* pages = (is_k ? p.k_pages : p.v_pages);
   const int64_t page_bytes = (int64_t)p.page_rows * p.head_dim;
-  RopeRow rope;
-  for (int n = begin; n < end; ++n) {
-    const int g0 = (n * at_once + unit / slots) * HC, live = min(HC, Hkv - g0);  // (may be none)
-    if (n + 1 < end) {
-      fetch(n + 1);
+  int turn = 0;  // items rounded: the one before may still be read where the next one's peaks go
+  Item it, ahead = fetch(0);
+  for (int n = 0; n < left; ++n) {
+    it = ahead;
+    if (n + 1 < left) {
+      advance();
+      ahead = fetch((n + 1) & 1);
       copy_wait<1>();
     } else {
       copy_wait<0>();
     }
+    if (it.page < 0 || it.page >= p.num_pages) {
+      if (threadIdx.x == 0 && p.err_flag) atomicOr(p.err_flag, kErrPage);
+      continue;
+    }
+    const int row0 = it.row0, lo = it.lo, hi = it.hi, g0 = it.g0, live = min(HC, Hkv - g0);  // (may be none)
+    const bool is_k = !it.which, rotate = is_k && p.cos;
+    const int old_rows = lo - row0;
     // the rows' values, kept between the peaks and the rounding
     float va[R][HC][8], vb[R][HC][8], peak[HC];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       const int position = row0 + slot + i * slots;
       const bool on = position >= lo && position < hi;
-      if (on && rotate) rope.load(p, position, c);
 #pragma unroll
       for (int k = 0; k < HC; ++k) {
-        if (!on || k >= live) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) va[i][k][e] = vb[i][k][e] = 0.f;
-          continue;
-        }
-        const uint4 x = *place(n & 1, i, k, 0), y = *place(n & 1, i, k, 1);
-        if (rotate) {
-          rope.rotate<T>(x, y, va[i][k], vb[i][k]);
-        } else {
-          Storage<T>::unpack(x, va[i][k]);
-          Storage<T>::unpack(y, vb[i][k]);
-        }
+        const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+        const bool in = on && k < live;
+        Storage<T>::unpack(in ? *place(n & 1, i, k, 0) : none, va[i][k]);
+        Storage<T>::unpack(in ? *place(n & 1, i, k, 1) : none, vb[i][k]);
       }
+      if (on && rotate) rotate_rows<HC>(p, position, c, va[i], vb[i]);
     }
     auto find_peaks = [&](auto finite) {
 #pragma unroll
@@ -479,22 +527,22 @@ __global__ void __launch_bounds__(kThreads, R == 8 ? 1 : 2)
 #pragma unroll
       for (int k = 0; k < HC; ++k) {
         const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(peak[k]));
-        if (lane == 0) sh_peak[n & 1][k][warp] = m;
+        if (lane == 0) sh_peak[turn][k][warp] = m;
       }
       __syncthreads();
       bool infinity = false;
 #pragma unroll
       for (int k = 0; k < HC; ++k) {
-        const uint32_t v = sh_peak[n & 1][k][lane % kWarps];
+        const uint32_t v = sh_peak[turn][k][lane % kWarps];
         infinity |= __any_sync(0xffffffffu, v == 0x7f800000u);  // in any team
         const int w = lane % kWarps - warp0;
         peak[k] = __uint_as_float(__reduce_max_sync(0xffffffffu, w >= 0 && w < team_warps ? v : 0u));
       }
       return infinity;
     };
-    const int64_t block = (int64_t)page * Hkv + g0;
+    const int64_t block = (int64_t)it.page * Hkv + g0;
     float* scale_at = (is_k ? p.k_scale : p.v_scale) + block;
-    uint8_t* rows = pages + block * page_bytes;
+    uint8_t* rows = (is_k ? p.k_pages : p.v_pages) + block * page_bytes;
     float old_scale[HC];
 #pragma unroll
     for (int k = 0; k < HC; ++k) old_scale[k] = old_rows > 0 && k < live ? scale_at[k] : 0.f;
@@ -536,12 +584,13 @@ __global__ void __launch_bounds__(kThreads, R == 8 ? 1 : 2)
       for (int k = 0; k < HC; ++k)
         if (k < live) scale_at[k] = scale[k];
     }
+    turn ^= 1;
   }
 }
 
 template <typename T, int R>
-cudaError_t launch_prompt_q8(cudaLaunchConfig_t cfg, const AppendPagedParams& p, int tasks, int ranges,
-                             int range_chunks, int stride) {
+cudaError_t launch_prompt_q8(cudaLaunchConfig_t cfg, const AppendPagedParams& p, int page_ctas, int chunks,
+                             int stride) {
   auto* fn = append_prompt_q8_kernel<T, R>;
   cfg.dynamicSmemBytes = prompt_smem(R);
   static std::atomic<bool> ready[64];  // per device: the shared-memory opt-in is applied
@@ -554,7 +603,7 @@ cudaError_t launch_prompt_q8(cudaLaunchConfig_t cfg, const AppendPagedParams& p,
     if (e != cudaSuccess) return e;
     ready[device].store(true, std::memory_order_release);
   }
-  return cudaLaunchKernelEx(&cfg, fn, p, tasks, ranges, range_chunks, stride);
+  return cudaLaunchKernelEx(&cfg, fn, p, page_ctas, chunks, stride);
 }
 
 // Units for each token. A unit that takes more heads looks its place and table
@@ -607,15 +656,12 @@ cudaError_t launch_append_paged(const AppendPagedParams& p, int dtype, int sms, 
   const int R = std::max(1, p.page_rows / units);
   const int chunk_heads = units / (p.page_rows / R) * prompt_heads(R);
   const int chunks = (p.n_kv_head + chunk_heads - 1) / chunk_heads;
-  // a CTA takes several chunks (it looks its page up once, and copies one chunk
-  // ahead) as far as that leaves about two CTAs an SM
-  const int ranges = (int)std::min<int64_t>(chunks, std::max<int64_t>(1, (2 * sms + 2 * tasks - 1) / (2 * tasks)));
-  const int range_chunks = (chunks + ranges - 1) / ranges;
-  if (tasks * 2 * ranges > INT32_MAX || !grid(tasks * 2 * ranges + query_ctas)) return cudaErrorInvalidConfiguration;
+  const int64_t page_ctas = std::min(tasks * 2 * chunks, (int64_t)sms * prompt_ctas(R));
+  if (!grid(page_ctas + query_ctas)) return cudaErrorInvalidConfiguration;
   auto launch = [&](auto rows) {
     constexpr int kR = decltype(rows)::value;
-    return f16 ? launch_prompt_q8<__half, kR>(cfg, p, (int)tasks, ranges, range_chunks, stride)
-               : launch_prompt_q8<__nv_bfloat16, kR>(cfg, p, (int)tasks, ranges, range_chunks, stride);
+    return f16 ? launch_prompt_q8<__half, kR>(cfg, p, (int)page_ctas, chunks, stride)
+               : launch_prompt_q8<__nv_bfloat16, kR>(cfg, p, (int)page_ctas, chunks, stride);
   };
   switch (R) {
     case 1: return launch(std::integral_constant<int, 1>());

@@ -896,7 +896,7 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
           __syncthreads();
           if (tid == 0) {
             *arrived = arrive(counter);
-        }
+          }
           __syncthreads();
           const unsigned int order = *arrived;
           if (order >= (unsigned int)count) {

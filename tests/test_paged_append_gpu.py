@@ -180,6 +180,26 @@ def test_bad_pages_are_skipped(eight):
 
 
 @BOTH
+@pytest.mark.parametrize("page,Hkv,D,count", [(16, 24, 128, 150), (64, 9, 128, 300), (16, 17, 64, 200),
+                                              (128, 6, 128, 500)])
+def test_more_pages_and_heads_than_the_device_takes_at_once(page, Hkv, D, count, eight):
+    """Every part of the device goes through several pages, over the ends of
+    sequences, empty and refused ones, and pages outside the pool."""
+    gen = torch.Generator().manual_seed(page + Hkv)
+    counts = torch.randint(count // 2, count, (41,), generator=gen).tolist()
+    positions = torch.randint(0, 3 * page, (41,), generator=gen).tolist()
+    for b in (0, 7, 8, 40):
+        counts[b] = 0
+    inp = Inputs(counts, positions, Hkv, Hkv, D, "bf16", page, eight, with_q=False, seed=Hkv)
+    check(inp, "long runs")
+    inp.table[3, positions[3] // page] = -1
+    inp.table[20, positions[20] // page + 1] = inp.k.shape[0]
+    inp.position[11] = -1
+    inp.position[39] = 1 << 30
+    check(inp, "refused places", flag=da.DA_DEVERR_POSITION | da.DA_DEVERR_PAGE)
+
+
+@BOTH
 def test_rows_of_a_page_past_the_last_sequence(eight):
     """A token range that leaves the packed tokens is refused on the device."""
     inp = Inputs([3, 4], [2, 0], 4, 2, 64, "f16", 16, eight, seed=8)
