@@ -9,7 +9,7 @@
 // bound by HBM, single tokens by the chain of dependent loads (sequence,
 // position, page). Measured (of the measured 6782 GB/s copy): prompts of 8.4k
 // tokens, 8 KV and 32 query heads of 128, fp16, 225 MB in 37.6 us (88%); the
-// same heads, 21k tokens into 8 bits, 482 MB in 86.7 us (82%; the 30% that are K
+// same heads, 21k tokens into 8 bits, 482 MB in 86.4 us (82%; the 30% that are K
 // and V take 35 us, bound by the chain of peaks and rounding at two CTAs an SM);
 // 8 sequences, one token each, 2.4 us, 64 into 8 bits 2.4 us.
 #include <stdint.h>
@@ -245,9 +245,10 @@ template <bool INFINITIES>
 __device__ __forceinline__ uint2 quantise8(const float (&f)[8], float inv) {
   float x[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    x[e] = f[e] * inv;
-    if (INFINITIES && fabsf(f[e]) == INFINITY) x[e] = NAN;
+  for (int e = 0; e < 8; e += 2) {
+    const float2 v = __fmul2_rn(make_float2(f[e], f[e + 1]), make_float2(inv, inv));
+    x[e] = INFINITIES && fabsf(f[e]) == INFINITY ? NAN : v.x;
+    x[e + 1] = INFINITIES && fabsf(f[e + 1]) == INFINITY ? NAN : v.y;
   }
   return make_uint2(to_e4m3x2(x[0], x[1]) | (to_e4m3x2(x[2], x[3]) << 16),
                     to_e4m3x2(x[4], x[5]) | (to_e4m3x2(x[6], x[7]) << 16));
@@ -271,7 +272,8 @@ __device__ __forceinline__ void rescale_rows(uint8_t* rows, int bytes, float rat
 // Largest |f| so far; NaN does not count, infinity does.
 __device__ __forceinline__ float peak_of(float peak, const float (&f)[8]) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) peak = fmaxf(peak, fabsf(f[e]));
+  for (int e = 0; e < 8; e += 2)
+    asm("max.abs.f32 %0, %0, %1, %2;" : "+f"(peak) : "f"(f[e]), "f"(f[e + 1]));
   return peak;
 }
 
@@ -366,7 +368,7 @@ __global__ void __launch_bounds__(kThreads)
 // are on their way into its own places in shared memory while it finds the
 // peaks of this one and rounds it: nothing is waited for but the peaks, once an
 // item. Two CTAs of 64 values a thread fill an SM's registers. (21k tokens of 8
-// KV and 32 query heads, us: pages of 16 / 64 / 128 87.6 / 86.7 / 89.9; one CTA for
+// KV and 32 query heads, us: pages of 16 / 64 / 128 87.2 / 86.4 / 88.3; one CTA for
 // each page and K or V, with no load ahead of it, 97 / 87 / 93; three CTAs of 32
 // values 92 / 101 / 90; the values rotated twice instead of kept 98 / 97 / 102.)
 __host__ __device__ constexpr int prompt_heads(int R) { return R >= 4 ? 1 : 4 / R; }
