@@ -15,8 +15,9 @@
 // order. CTA i of n owns an even share of the list, whatever the lengths, the
 // window or the batch are: every CTA computes the list from kv_len itself, so
 // the launch does not depend on lengths and ragged batches are balanced to a
-// tile. A group that lies in several shares is joined through the workspace by
-// the last CTA to arrive; nothing waits for another CTA.
+// tile (groups of about one length get the same number of CTAs each instead,
+// so that fewer parts are joined). A group that lies in several shares is joined
+// through the workspace by the last CTA to arrive; nothing waits for another CTA.
 //
 // A warp takes every kWarps-th tile of the share, with a ring of its own in
 // shared memory that asynchronous copies keep filled (page numbers are looked
@@ -39,11 +40,14 @@
 //
 // Measured (graph of calls, data from HBM, of the measured 6782 GB/s copy): 32
 // ragged sequences up to 32768 rows, 32 / 8 heads, 2.04 GB in 295 us (102%),
-// in 8 bits 1.02 GB in 153 us (99%); 8 ragged up to 8191, 16 / 8 heads, 159 MB
-// in 29.9 us (78%); one of 1024 rows, 16 / 16 heads, 7.0 us. Short calls are a
-// chain of dependent steps, each about as long as a memory round trip: lengths
-// and share (0.8 us after the wait), page numbers (0.6), rows (0.8), the tile,
-// the join of the warps (0.7), arrival (1.2) and the join of the parts (1.5).
+// in 8 bits 1.02 GB in 153 us (98%); 8 ragged up to 8191, 16 / 8 heads, 159 MB
+// in 29.4 us (80%); 16 ragged with window 1021 and 16 / 8 heads, 68 MB in 12.6
+// us (80%); window 4096 in 8 bits, 16 ragged, 64 / 8 heads, 135 MB in 25.7 us
+// (77%); one of 1024 rows, 16 / 16 heads, 6.7 us. Short calls are a chain of
+// dependent steps, each about as long as a memory round trip: page numbers (0.6
+// us after the wait; lengths, share and L2 prefetch come before it), rows (0.8),
+// the tile, the join of the warps (0.7), arrival (1.0) and the join of the parts
+// (1.5).
 #pragma once
 
 #include <atomic>
@@ -257,9 +261,9 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
   // each group, and some places that stand for its end (short groups are then
   // balanced by what they cost, and those places hold cuts that would split a
   // group); or, with groups about equal, as many places for each, so that the
-  // cuts fall between them. One pass over the lengths, and,
-  // for more sequences than threads, a second one for the sequence that holds
-  // `lo`. A batch of at most 32 is seen by each warp alone, without a barrier.
+  // cuts fall between them. One pass over the lengths, and, for more sequences
+  // than threads, a second one for the sequence that holds `lo`. A batch of at
+  // most 32 is seen by each warp alone, without a barrier.
   // Where one pass will do it is made while the kernel before this one still
   // runs: the lengths of then say which rows to bring into L2 (a hint; page
   // numbers are checked), and if they are still those after the wait, the share
