@@ -41,9 +41,9 @@
 // Measured (graph of calls, data from HBM, of the measured 6782 GB/s copy): 32
 // ragged sequences up to 32768 rows, 32 / 8 heads, 2.04 GB in 295 us (102%),
 // in 8 bits 1.02 GB in 153 us (98%); 8 ragged up to 8191, 16 / 8 heads, 159 MB
-// in 29.4 us (80%); 16 ragged with window 1021 and 16 / 8 heads, 68 MB in 12.6
-// us (80%); window 4096 in 8 bits, 16 ragged, 64 / 8 heads, 135 MB in 25.7 us
-// (77%); one of 1024 rows, 16 / 16 heads, 6.7 us. Short calls are a chain of
+// in 29.3 us (80%); 16 ragged with window 1021 and 16 / 8 heads, 68 MB in 12.5
+// us (80%); window 4096 in 8 bits, 16 ragged, 64 / 8 heads, 135 MB in 25.6 us
+// (78%); one of 1024 rows, 16 / 16 heads, 6.7 us. Short calls are a chain of
 // dependent steps, each about as long as a memory round trip: page numbers (0.6
 // us after the wait; lengths, share and L2 prefetch come before it), rows (0.8),
 // the tile, the join of the warps (0.7), arrival (1.0) and the join of the parts
@@ -88,6 +88,10 @@ struct CacheAttnShape {
   static constexpr int kRows = kRowBytes > 128 ? 16 : 32;  // of a tile, in pieces of 16
   static constexpr int kTileBytes = kRows * kRowBytes;
   static constexpr int kStageBytes = 2 * kTileBytes;  // K tile, V tile
+  // Tiles of a warp that take as long as a join: 1 x 300 of 16/8 heads 4.9 us with
+  // 2 or 3 (no join), 5.9 with 1; 3 ragged to 1000, 16/4 heads of 64, 5.6 with 3, 6.0
+  // with 2; 1 x 700 in e4m3, 32/8 heads, whose tiles take longer, 6.6 with 1, 6.8 with 2.
+  static constexpr int kJoinTurns = E4M3 ? 1 : 3;
   static constexpr int kStages = 196608 / (kWarps * kStageBytes);
   static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
   static constexpr int kMergeFloats = kWarps * kHeads * D;
@@ -397,15 +401,20 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
     if (!short_groups) ctas = min((int64_t)gridDim.x, (tiles + kFewestTiles - 1) / kFewestTiles);
     if (!short_groups) {
       end_cost = kGroupCost;
-      if (groups <= ctas && groups > 0) {
-        // as many CTAs for every group, where the largest part then takes no longer
-        // than an even share of all tiles with the ends of groups in it
-        const uint32_t n = (uint32_t)ctas, each = n / (uint32_t)groups;
-        const int64_t part = (most + each - 1) / each;
-        if (part * ctas * 7 <= (tiles + ctas * (each == 1 ? kAloneGain : kEvenGain)) * 8) {
+      if (groups <= gridDim.x && groups > 0) {
+        // As many CTAs for every group: one where a warp then has at most
+        // kJoinTurns tiles more than with all CTAs, or else as few as leave it no
+        // more tiles. Taken where the largest part then takes no
+        // longer than an even share of all tiles with the ends of groups in it.
+        const uint32_t n = (uint32_t)ctas, fit = gridDim.x / (uint32_t)groups;
+        const uint32_t turns = ((uint32_t)most + kW * fit - 1) / (kW * fit);
+        const uint32_t each = (uint32_t)most <= kW * (turns + Sh::kJoinTurns)
+                                  ? 1 : ((uint32_t)most + kW * turns - 1) / (kW * turns);
+        const int64_t part = ((uint32_t)most + each - 1) / each;
+        if (part * n * 7 <= (tiles + n * (each == 1 ? kAloneGain : kEvenGain)) * 8) {
           ctas = each * groups;
           even = (int)(part * each);
-        } else {
+        } else if (groups <= n) {
           end_cost = tiles >= ctas * kJoinCost * 8 ? kJoinCost : (int)((uint32_t)tiles / n / 8);
         }
       }
