@@ -70,11 +70,13 @@ constexpr int kFewestTiles = 8, kGroupCost = 8, kJoinCost = 16, kEvenGain = 12, 
 // A group in more than kJoinWide parts (at most 256) is joined in two rounds, of
 // kJoinWidth neighbours and of the sums of those.
 constexpr int kJoinWide = 64, kJoinWidth = 16;
-// In a batch of more groups than CTAs, none of more rows than this, a warp takes
-// a group by itself: no barrier, nothing to join (us for 256 sequences of up
-// to 128 rows, 8 KV heads, 21.1 instead of 42.7; 64 of 256 rows 15.7 instead
-// of 22.1; with groups of up to 500 rows 20.9 against 18.9).
-constexpr int kShortRows = 256;
+// In a batch of more groups than CTAs, none of more rows than kShortRows, a warp
+// takes a group by itself: no barrier, nothing to join (us for 256 sequences of
+// up to 128 rows, 8 KV heads, 18.9 instead of 42.7; 64 of 256 rows 15.1 instead of
+// 22.1; with groups of up to 500 rows 20.9 against 18.9). With none of more than
+// kWholeRows a CTA does: 24 of up to 300 rows 7.8 instead of 10.5, 64 of up to 400
+// 17.5 instead of 19.9, but 38 of 500 rows, 16 KV heads, 28.4 against 25.8.
+constexpr int kShortRows = 256, kWholeRows = 400;
 constexpr float kLazy = 8.f;     // m is raised when a score passes it by this (log2)
 // fp16 weights are 2^(x' - m + 7): at most 2^15, inside the type's range, and
 // 2^-32 of the largest one is still held. bf16 has fp32's range: no lift.
@@ -356,20 +358,20 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
   };
   SequenceTiles seq;  // the sequence that holds `lo`
   int b = 0, g = 0, tile = 0;  // group of list position `lo`, and its place there
-  bool short_groups = false;
-  // From (b, g) on to the first group with rows, in steps of the list (with
-  // short groups, of the warps); false when there is none.
+  bool short_groups = false, strided = false;  // a group to a warp; a group to a warp or a CTA
+  const bool one_pass = p.B <= Sh::kThreads;
+  bool waited = !one_pass;
+  // From (b, g) on to the first group with rows, in steps of the list (strided:
+  // of the warps or CTAs); false when there is none.
   auto settle = [&](int& b, int& g, SequenceTiles& s) {
 #pragma unroll 1
-    while (b < p.B && tiles_of<kRows>(p, __ldcg(p.kv_len + b), &s) <= 0) {
-      if (short_groups) g += kW * gridDim.x;
-      b += short_groups ? g / p.n_kv_head : 1;
-      g = short_groups ? g % p.n_kv_head : 0;
+    while (b < p.B && tiles_of<kRows>(p, waited ? p.kv_len[b] : __ldcg(p.kv_len + b), &s) <= 0) {
+      if (strided) g += (short_groups ? kW : 1) * gridDim.x;
+      b += strided ? g / p.n_kv_head : 1;
+      g = strided ? g % p.n_kv_head : 0;
     }
     return b < p.B;
   };
-  const bool one_pass = p.B <= Sh::kThreads;
-  bool waited = !one_pass;
   if (waited) {
     pdl_wait();
     pdl_trigger();  // the next grid can take the SMs as they fall free; it waits for this one's memory
@@ -377,7 +379,7 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
   for (;;) {
     before = lo = 0;
     most = 0;
-    short_groups = false;
+    short_groups = strided = false;
     for (int base = 0; base < p.B; base += columns) {
       pass(base);
       if (!one_pass) fill_idle(base);
@@ -386,9 +388,10 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
     even = 0;
     if (groups > gridDim.x) {
       short_groups = most <= kShortRows / kRows;
-      if (short_groups) {
+      strided = short_groups || most <= kWholeRows / kRows;
+      if (strided) {
         ctas = gridDim.x;
-        g = warp * gridDim.x + blockIdx.x;
+        g = (short_groups ? warp * gridDim.x : 0) + blockIdx.x;
         b = g / p.n_kv_head;
         g -= b * p.n_kv_head;
         if (!settle(b, g, seq)) ctas = 0;
@@ -398,8 +401,8 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
       }
     }
     // as many CTAs as find kFewestTiles
-    if (!short_groups) ctas = min((int64_t)gridDim.x, (tiles + kFewestTiles - 1) / kFewestTiles);
-    if (!short_groups) {
+    if (!strided) {
+      ctas = min((int64_t)gridDim.x, (tiles + kFewestTiles - 1) / kFewestTiles);
       end_cost = kGroupCost;
       if (groups <= gridDim.x && groups > 0) {
         // As many CTAs for every group: one where a warp then has at most
@@ -419,7 +422,7 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
         }
       }
     }
-    if (!short_groups && (int64_t)blockIdx.x < ctas) {
+    if (!strided && (int64_t)blockIdx.x < ctas) {
       total = places(before);
       small = total * ctas < (1ll << 32);
       lo = share_start(blockIdx.x);
@@ -480,13 +483,13 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
   int at = 0;                        // place in the share of the next tile to compute
   // the next group of this CTA (with short groups, of this warp); false when
   // the share ends before it
-  const int skip = short_groups ? kW * gridDim.x : 1;
+  const int skip = strided ? (short_groups ? kW : 1) * gridDim.x : 1;
   auto next_group = [&](int place, int& b, int& g, SequenceTiles& s) {
     if (place >= share) return false;
     g += skip;
     if (g < p.n_kv_head) return true;
-    b += short_groups ? g / p.n_kv_head : 1;
-    g = short_groups ? g % p.n_kv_head : 0;
+    b += strided ? g / p.n_kv_head : 1;
+    g = strided ? g % p.n_kv_head : 0;
     return settle(b, g, s);
   };
   if (tile >= seq.tiles) {
@@ -500,6 +503,12 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
   // page; with two, either half of the warp looks up and copies its own.
   const uint32_t ring = smem_addr(smem) + warp * kS * Sh::kStageBytes;
   const uint32_t meta = smem_addr(smem + Sh::kMetaOffset) + warp * kS * Sh::kMetaBytes;
+  // a group's q, on its way to L1 when the first of its tiles is looked up
+  auto prefetch_q = [&](int b, int g) {
+    const int bytes = p.group * D * 2;
+    if (lane * 128 < bytes)
+      asm volatile("prefetch.global.L1 [%0];" ::"l"(p.q + ((int64_t)b * p.n_head + g * p.group) * D * 2 + lane * 128));
+  };
   SequenceTiles lseq = seq;  // the tile to load next, its page number on the way
   int lb = b, lg = g, li = tile, lrow = 0, lpage = 0;
   uint32_t lmask = 0;  // 0: no tile is left
@@ -513,6 +522,7 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
       li -= lseq.tiles;
       lat += behind(lseq);
       more = next_group(lat - li, lb, lg, lseq);
+      if (more) prefetch_q(lb, lg);
     }
     more = more && lat < share;
     if (!more) return;

@@ -229,6 +229,40 @@ def test_short_groups_of_bad_lengths_and_pages():
     R.assert_rows(out[good.cuda()], case.ref[good], case.slack[good])
 
 
+@pytest.mark.parametrize("eight", [False, True], ids=["16bit", "e4m3"])
+@pytest.mark.parametrize("longest", [300, 385, 400, 401, 416, 417])
+def test_many_groups_of_a_few_hundred_rows(longest, eight):
+    """The same around the length up to which one CTA takes a whole group, for
+    batches that one scan covers and for one that it does not, with lengths and
+    pages that are refused."""
+    gen = torch.Generator().manual_seed(longest)
+    for B, H, Hkv, D, window, sinks in ((45, 8, 4, 128, 0, 0), (12, 16, 16, 64, 350, 3), (500, 4, 1, 64, 0, 0)):
+        lens = torch.randint(0, longest + 1, (B,), generator=gen).tolist()
+        lens[B // 2] = longest
+        check(Case(lens, H, Hkv, D, "f16", 16, eight, window, sinks, seed=longest), f"{B} up to {longest}")
+    lens = [longest, 17, longest // 2, 0] * 40
+    case = Case(lens, 8, 2, 64, "f16", 16, eight, seed=31).cuda()
+    case.kv_len[4], case.kv_len[61] = -3, 1 << 20
+    case.table[90, 1], case.table[120, 0] = 1 << 25, -1
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = case.call(err_flag=err)
+    assert int(err.item()) == da.DA_DEVERR_KV_LEN | da.DA_DEVERR_PAGE
+    bad = torch.tensor([4, 61, 90, 120], device="cuda")
+    assert out[bad].isnan().all()
+    good = torch.tensor([b for b in range(160) if b not in (4, 61, 90, 120)])
+    R.assert_rows(out[good.cuda()], case.ref[good], case.slack[good])
+
+
+@pytest.mark.parametrize("eight", [False, True], ids=["16bit", "e4m3"])
+@pytest.mark.parametrize("H,Hkv,D", [(16, 8, 128), (4, 4, 64), (8, 1, 64), (24, 24, 128), (150, 75, 64)])
+def test_groups_of_about_one_length(H, Hkv, D, eight):
+    """Groups that get the same number of CTAs each: one, several, all; equal
+    lengths, nearly equal ones, and one that is far shorter."""
+    for lens in ([16], [64], [129], [300, 290], [511, 513, 512], [700], [1025, 1000, 1], [2600, 0, 2590]):
+        check(Case(lens, H, Hkv, D, "bf16", 16, eight, seed=len(lens)), f"{lens}")
+        check(Case(lens, H, Hkv, D, "f16", 32, eight, window=250, sinks=5, seed=2), f"{lens}, window")
+
+
 def test_more_sequences_than_one_scan_covers():
     gen = torch.Generator().manual_seed(5)
     lens = torch.randint(0, 40, (1500,), generator=gen).tolist()
