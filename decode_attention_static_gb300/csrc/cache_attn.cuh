@@ -30,7 +30,7 @@
 // costs the same, and scores and weights stay in registers. (For tcgen05 a
 // tile of one query token is too small: its 128-row operand would hold 8
 // pieces of different pages, and its accumulator would have to come back from
-// tensor memory for every softmax; here the tensor pipe is busy 11 to 24% of
+// tensor memory for every softmax; here the tensor pipe is busy 11 to 25% of
 // the time.) Weights
 // are split in two 16-bit pieces, p = hi + lo, each multiplied with V: the sum
 // keeps the 16 (bf16) to 22 (fp16) bits of a weight that one 16-bit number
