@@ -70,13 +70,14 @@ constexpr int kFewestTiles = 8, kGroupCost = 8, kJoinCost = 16, kEvenGain = 12, 
 // A group in more than kJoinWide parts (at most 256) is joined in two rounds, of
 // kJoinWidth neighbours and of the sums of those.
 constexpr int kJoinWide = 64, kJoinWidth = 16;
-// In a batch of more groups than CTAs, none of more rows than kShortRows, a warp
-// takes a group by itself: no barrier, nothing to join (us for 256 sequences of
-// up to 128 rows, 8 KV heads, 18.9 instead of 42.7; 64 of 256 rows 15.1 instead of
-// 22.1; with groups of up to 500 rows 20.9 against 18.9). With none of more than
-// kWholeRows a CTA does: 24 of up to 300 rows 7.8 instead of 10.5, 64 of up to 400
-// 17.5 instead of 19.9, but 38 of 500 rows, 16 KV heads, 28.4 against 25.8.
-constexpr int kShortRows = 256, kWholeRows = 400;
+// With more groups than CTAs, teams of 1, 2 or 4 warps may take whole groups: no
+// barrier of the CTA, nothing to join. The cost of either way is counted in tiles
+// a warp goes through, a group's end as one and an even share's joins as kTeamGain.
+// us in teams / in even shares, 8 KV heads: 256 ragged to 128 rows 19.0 / 42.7, 64 to
+// 400 14.0 / 19.9, 24 to 300 7.6 / 10.5, e4m3 64 to 800 20.6 / 24.9. With 3 for 6 the
+// last three stay in even shares; with 10, e4m3 40 to 2000 of 64 goes in teams and
+// takes 23.0 for 20.8.
+constexpr int kTeamGain = 6;
 constexpr float kLazy = 8.f;     // m is raised when a score passes it by this (log2)
 // fp16 weights are 2^(x' - m + 7): at most 2^15, inside the type's range, and
 // 2^-32 of the largest one is still held. bf16 has fp32's range: no lift.
@@ -264,7 +265,7 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, gr = lane >> 2, tq = lane & 3;
 
   // --- the list of places, and this CTA's share [lo, hi) of it: the tiles of
-  // each group, and some places that stand for its end (short groups are then
+  // each group, and some places that stand for its end (groups are then
   // balanced by what they cost, and those places hold cuts that would split a
   // group); or, with groups about equal, as many places for each, so that the
   // cuts fall between them. One pass over the lengths, and, for more sequences
@@ -358,15 +359,18 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
   };
   SequenceTiles seq;  // the sequence that holds `lo`
   int b = 0, g = 0, tile = 0;  // group of list position `lo`, and its place there
-  bool short_groups = false, strided = false;  // a group to a warp; a group to a warp or a CTA
+  bool strided = false;  // groups are taken whole, by teams of warps
+  int team = kW;         // warps that share a group,
+  int lead = warp;       // and those of them before this one
+  int hop = 1;           // groups from one of a team to its next one
   const bool one_pass = p.B <= Sh::kThreads;
   bool waited = !one_pass;
   // From (b, g) on to the first group with rows, in steps of the list (strided:
-  // of the warps or CTAs); false when there is none.
+  // of the teams); false when there is none. (After the wait only.)
   auto settle = [&](int& b, int& g, SequenceTiles& s) {
 #pragma unroll 1
-    while (b < p.B && tiles_of<kRows>(p, waited ? p.kv_len[b] : __ldcg(p.kv_len + b), &s) <= 0) {
-      if (strided) g += (short_groups ? kW : 1) * gridDim.x;
+    while (b < p.B && tiles_of<kRows>(p, p.kv_len[b], &s) <= 0) {
+      if (strided) g += hop;
       b += strided ? g / p.n_kv_head : 1;
       g = strided ? g % p.n_kv_head : 0;
     }
@@ -379,7 +383,10 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
   for (;;) {
     before = lo = 0;
     most = 0;
-    short_groups = strided = false;
+    strided = false;
+    team = kW;
+    lead = warp;
+    hop = 1;
     for (int base = 0; base < p.B; base += columns) {
       pass(base);
       if (!one_pass) fill_idle(base);
@@ -387,14 +394,28 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
     const int64_t tiles = (before & ((1ll << kCount) - 1)) * p.n_kv_head, groups = (before >> kCount) * p.n_kv_head;
     even = 0;
     if (groups > gridDim.x) {
-      short_groups = most <= kShortRows / kRows;
-      strided = short_groups || most <= kWholeRows / kRows;
+      // whole groups, by teams of 1, 2 or 4 warps, where the longest way through
+      // them is no longer than an even share with its ends and joins (in floats:
+      // an estimate, and a 64-bit division is some hundred instructions)
+      const float each = 1.f / (float)(gridDim.x * kW);
+      float least = (float)tiles * each + (float)groups * each * kW + kTeamGain;
+#pragma unroll
+      for (int t = 1; t <= 4; t *= 2) {
+        const float cost = ceilf(((float)groups - 0.5f) * each * t) * (float)((uint32_t)(most + t - 1) / t + 1);
+        if (cost <= least) {
+          least = cost;
+          strided = true;
+          team = t;
+          lead = warp % t;
+          hop = kW / t * gridDim.x;
+          g = warp / t * gridDim.x + blockIdx.x;
+        }
+      }
       if (strided) {
         ctas = gridDim.x;
-        g = (short_groups ? warp * gridDim.x : 0) + blockIdx.x;
         b = g / p.n_kv_head;
         g -= b * p.n_kv_head;
-        if (!settle(b, g, seq)) ctas = 0;
+        tiles_of<kRows>(p, b < p.B ? __ldcg(p.kv_len + b) : 0, &seq);  // (for the prefetch; settled after the wait)
         tile = 0;
         hi = INT32_MAX;
         end_cost = 0;
@@ -459,8 +480,7 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
     if (waited) break;
     if ((int64_t)blockIdx.x < ctas) {
 #pragma unroll 1
-      for (int i = tile + (short_groups ? 0 : warp), j = 0; j < kS - 1 && i < seq.tiles && i - tile < hi - lo;
-           i += short_groups ? 1 : kW, ++j) {
+      for (int i = tile + lead, j = 0; j < kS - 1 && i < seq.tiles && i - tile < hi - lo; i += team, ++j) {
         const int row = tile_row<kRows>(seq, i) + 16 * half;
         if (row + 16 > seq.len) break;
         const int page = p.table ? __ldcg(p.table + (int64_t)b * p.max_pages + (row >> p.page_shift)) : b;
@@ -478,15 +498,15 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
   }
   if (one_pass) fill_idle(0);
   if ((int64_t)blockIdx.x >= ctas) return;
-  const int step = short_groups ? 1 : kW;  // tiles between this warp's
+  if (strided && !settle(b, g, seq)) return;
+  const int step = team;             // tiles between this warp's
   const int share = (int)(hi - lo);  // (below 2^31: checked on the host)
   int at = 0;                        // place in the share of the next tile to compute
   // the next group of this CTA (with short groups, of this warp); false when
   // the share ends before it
-  const int skip = strided ? (short_groups ? kW : 1) * gridDim.x : 1;
   auto next_group = [&](int place, int& b, int& g, SequenceTiles& s) {
     if (place >= share) return false;
-    g += skip;
+    g += hop;
     if (g < p.n_kv_head) return true;
     b += strided ? g / p.n_kv_head : 1;
     g = strided ? g % p.n_kv_head : 0;
@@ -582,13 +602,13 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
     copy_commit();
     put = put + 1 == kS ? 0 : put + 1;
   };
-  look_up(short_groups ? 0 : warp);
+  look_up(lead);
 #pragma unroll 1
   for (int j = 0; j < kS - 1; ++j) load_next();
 
   // --- group by group
   int get = 0;      // stage of this warp's next tile
-  int turn = short_groups ? 0 : warp;  // tiles until this warp's next one
+  int turn = lead;  // tiles until this warp's next one
   for (;;) {
     const int here = min(seq.tiles - tile, share - at);  // tiles of the group in this share
     // q as the right operand: columns are heads
@@ -841,8 +861,14 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
           make_uint2((uint32_t)Storage<T>::round(r.x * inv) | ((uint32_t)Storage<T>::round(r.y * inv) << 16),
                      (uint32_t)Storage<T>::round(r.z * inv) | ((uint32_t)Storage<T>::round(r.w * inv) << 16));
     };
+    auto add = [](float4& r, float f, const float4& v) {
+      r.x = fmaf(f, v.x, r.x);
+      r.y = fmaf(f, v.y, r.y);
+      r.z = fmaf(f, v.z, r.z);
+      r.w = fmaf(f, v.w, r.w);
+    };
     const int items = p.group * (D / 4);  // outputs in vectors of 4
-    if (short_groups) {
+    if (team == 1) {
       // the group is this warp's alone
       __syncwarp();
       for (int i = lane; i < items; i += 32) {
@@ -851,6 +877,27 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
               sm_l[warp * kHeads + h]);
       }
       __syncwarp();  // the merge buffer is free
+    } else if (strided) {
+      auto team_sync = [&]() {
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + (warp - lead) / 2), "r"(team * 32) : "memory");
+      };
+      team_sync();
+      const int w0 = warp - lead;
+      for (int i = lead * 32 + lane; i < items; i += team * 32) {
+        const int h = i / (D / 4), d = (i % (D / 4)) * 4;
+        float mm = -INFINITY, ll = 0.f;
+#pragma unroll 2
+        for (int w = w0; w < w0 + team; ++w) mm = fmaxf(mm, sm_m[w * kHeads + h]);
+        float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+        for (int w = w0; w < w0 + team; ++w) {
+          const float m = sm_m[w * kHeads + h], f = m == mm ? 1.f : fast_exp2(m - mm);
+          ll = fmaf(f, sm_l[w * kHeads + h], ll);
+          add(r, f, *reinterpret_cast<const float4*>(merge + (w * kHeads + h) * D + merge_column<D>(h, d)));
+        }
+        store(i, r, ll);
+      }
+      team_sync();  // the team's part of the merge buffer is free
     } else {
       __syncthreads();
       const bool whole = here == seq.tiles;
@@ -868,12 +915,6 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
         return p.partials + (int64_t)(part ? 2 * (from + part) : 2 * from + 1) * slot_floats;
       };
       float* slot = slot_of((int)blockIdx.x - from);
-      auto add = [](float4& r, float f, const float4& v) {
-        r.x = fmaf(f, v.x, r.x);
-        r.y = fmaf(f, v.y, r.y);
-        r.z = fmaf(f, v.z, r.z);
-        r.w = fmaf(f, v.w, r.w);
-      };
       if (tid < items) {
         const int h = tid / (D / 4), d = (tid % (D / 4)) * 4;
         float mw[kW], mm = -INFINITY, ll = 0.f;
