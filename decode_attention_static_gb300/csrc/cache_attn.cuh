@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
   const int step = team;             // tiles between this warp's
   const int share = (int)(hi - lo);  // (below 2^31: checked on the host)
   int at = 0;                        // place in the share of the next tile to compute
-  // the next group of this CTA (with short groups, of this warp); false when
+  // the next group of this CTA (strided, of this team); false when
   // the share ends before it
   auto next_group = [&](int place, int& b, int& g, SequenceTiles& s) {
     if (place >= share) return false;
