@@ -105,7 +105,7 @@ struct CacheAttnShape {
   // (m, l) of each warp, and of joined parts; schedule words
   static constexpr int kStatFloats = 2 * kWarps * kHeads + 2 * kHeads;
   static constexpr int kWordsOffset = kStatOffset + kStatFloats * 4;
-  static constexpr int kSmemBytes = kWordsOffset + (kWarps + 4 + (kWarps + 1) / 2) * 8;
+  static constexpr int kSmemBytes = kWordsOffset + (2 * kWarps + 4 + (kWarps + 1) / 2) * 8;
   static_assert(kStages >= 3, "a ring of at least three stages");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory of a CTA");
   static_assert(kJoinWide * kHeads * 4 + kThreads * 16 <= kMergeBytes,
@@ -270,7 +270,8 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
   // group); or, with groups about equal, as many places for each, so that the
   // cuts fall between them. One pass over the lengths, and, for more sequences
   // than threads, a second one for the sequence that holds `lo`. A batch of at
-  // most 32 is seen by each warp alone, without a barrier.
+  // most 32, and of no more groups than CTAs, is seen by each warp alone, without
+  // a barrier.
   // Where one pass will do it is made while the kernel before this one still
   // runs: the lengths of then say which rows to bring into L2 (a hint; page
   // numbers are checked), and if they are still those after the wait, the share
@@ -283,7 +284,7 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
   constexpr int kCount = 44;  // tiles and non-empty sequences are summed in one word: tiles + sequences * 2^44
   constexpr int kChunks = Sh::kRowBytes / 16, kLanes = 32 / kHalves, kCopies = 16 * kChunks / kLanes;
   const int half = kHalves == 2 ? lane >> 4 : 0, sub = lane % kLanes;
-  const bool alone = p.B <= 32;
+  const bool alone = p.B <= 32 && p.B * p.n_kv_head <= gridDim.x;  // (teams have to agree on the split)
   const int column = alone ? lane : tid, columns = alone ? 32 : Sh::kThreads;
   int64_t before = 0, mine = 0, own = 0;  // before this pass, before this thread's sequence, and its own
   int len = 0, most = 0;                  // most tiles of a sequence
@@ -300,7 +301,7 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
     const int top = __reduce_max_sync(0xffffffffu, n);
     int64_t sum = own;
 #pragma unroll 1
-    for (int o = 1; o < 32 && o < p.B; o <<= 1) {
+    for (int o = 1; o < (alone ? p.B : 32); o <<= 1) {
       const int64_t v = __shfl_up_sync(0xffffffffu, sum, o);
       if (lane >= o) sum += v;
     }
@@ -498,7 +499,32 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
   }
   if (one_pass) fill_idle(0);
   if ((int64_t)blockIdx.x >= ctas) return;
-  if (strided && !settle(b, g, seq)) return;
+  // A team goes where its first warp goes: its barriers count its warps, and a
+  // length that changes under the call (an error of the caller's) must not part
+  // them. (b, g and the length in one word; B and the heads fit 16 bits.)
+  uint64_t* next = reinterpret_cast<uint64_t*>(words + kW + 4 + (kW + 1) / 2) + (warp - lead);
+  auto team_sync = [&]() {
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + (warp - lead) / 2), "r"(team * 32) : "memory");
+  };
+  auto send = [&](bool any) {
+    if (lane == 0) *next = any ? (uint64_t)b << 48 | (uint64_t)g << 32 | (uint32_t)seq.len : ~0ull;
+  };
+  auto receive = [&]() {  // (after a barrier of the team)
+    const uint64_t word = *next;
+    b = (int)(word >> 48);
+    g = (int)(word >> 32) & 0xffff;
+    tiles_of<kRows>(p, (int)(uint32_t)word, &seq);
+    return word != ~0ull;
+  };
+  if (strided) {
+    bool any = lead == 0 && settle(b, g, seq);
+    if (team > 1) {
+      if (lead == 0) send(any);
+      team_sync();
+      any = receive();
+    }
+    if (!any) return;
+  }
   const int step = team;             // tiles between this warp's
   const int share = (int)(hi - lo);  // (below 2^31: checked on the host)
   int at = 0;                        // place in the share of the next tile to compute
@@ -878,9 +904,6 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
       }
       __syncwarp();  // the merge buffer is free
     } else if (strided) {
-      auto team_sync = [&]() {
-        asm volatile("bar.sync %0, %1;" ::"r"(1 + (warp - lead) / 2), "r"(team * 32) : "memory");
-      };
       team_sync();
       const int w0 = warp - lead;
       for (int i = lead * 32 + lane; i < items; i += team * 32) {
@@ -897,7 +920,6 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
         }
         store(i, r, ll);
       }
-      team_sync();  // the team's part of the merge buffer is free
     } else {
       __syncthreads();
       const bool whole = here == seq.tiles;
@@ -1054,7 +1076,14 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
     // --- the next group
     at += here + behind(seq);
     tile = 0;
-    if (!next_group(at, b, g, seq)) break;
+    bool any = true;
+    if (lead == 0 || !strided) any = next_group(at, b, g, seq);
+    if (__builtin_expect(strided && team > 1, 0)) {
+      if (lead == 0) send(any);
+      team_sync();  // and the team's part of the merge buffer is free
+      any = receive();
+    }
+    if (!any) break;
   }
   copy_wait<0>();
 }

@@ -457,7 +457,8 @@ DA_API size_t decode_attn_paged_workspace_size(int n_head, int n_kv_head, int he
  * DA_DEVERR_PAGE. window >= 0, sinks >= 0, and sinks > 0 needs window > 0
  * (else DA_ERR_SHAPE). No length bound is needed: the launch does not depend
  * on the lengths, so a captured graph serves any of them. Equal calls give
- * equal bits. out must not be q (DA_ERR_SHAPE).
+ * equal bits. kv_len and page_table must not change while the call runs, and
+ * out must not be q (DA_ERR_SHAPE).
  */
 DA_API int decode_attn_paged_fwd(const void* q, const void* k_pages, const void* v_pages, const int32_t* page_table,
                     const int32_t* kv_len, int B, int n_head, int n_kv_head, int head_dim, int num_pages,
