@@ -41,9 +41,9 @@
 // Measured (graph of calls, data from HBM, of the measured 6782 GB/s copy): 32
 // ragged sequences up to 32768 rows, 32 / 8 heads, 2.04 GB in 295 us (102%),
 // in 8 bits 1.02 GB in 153 us (98%); 8 ragged up to 8191, 16 / 8 heads, 159 MB
-// in 29.3 us (80%); 16 ragged with window 1021 and 16 / 8 heads, 68 MB in 12.5
-// us (80%); window 4096 in 8 bits, 16 ragged, 64 / 8 heads, 135 MB in 25.6 us
-// (78%); one of 1024 rows, 16 / 16 heads, 6.7 us. Short calls are a chain of
+// in 29.4 us (80%); 16 ragged with window 1021 and 16 / 8 heads, 68 MB in 12.7
+// us (79%); window 4096 in 8 bits, 16 ragged, 64 / 8 heads, 135 MB in 26.2 us
+// (76%); one of 1024 rows, 16 / 16 heads, 7.0 us. Short calls are a chain of
 // dependent steps, each about as long as a memory round trip: page numbers (0.6
 // us after the wait; lengths, share and L2 prefetch come before it), rows (0.8),
 // the tile, the join of the warps (0.7), arrival (1.0) and the join of the parts
@@ -73,8 +73,8 @@ constexpr int kJoinWide = 64, kJoinWidth = 16;
 // With more groups than CTAs, teams of 1, 2 or 4 warps may take whole groups: no
 // barrier of the CTA, nothing to join. The cost of either way is counted in tiles
 // a warp goes through, a group's end as one and an even share's joins as kTeamGain.
-// us in teams / in even shares, 8 KV heads: 256 ragged to 128 rows 19.0 / 42.7, 64 to
-// 400 14.0 / 19.9, 24 to 300 7.6 / 10.5, e4m3 64 to 800 20.6 / 24.9. With 3 for 6 the
+// us in teams / in even shares, 8 KV heads: 256 ragged to 128 rows 19.2 / 42.7, 64 to
+// 400 14.4 / 19.9, 24 to 300 8.1 / 10.5, e4m3 64 to 800 20.9 / 24.9. With 3 for 6 the
 // last three stay in even shares; with 10, e4m3 40 to 2000 of 64 goes in teams and
 // takes 23.0 for 20.8.
 constexpr int kTeamGain = 6;
