@@ -59,8 +59,9 @@ namespace da {
 
 constexpr int kHeads = 8;        // columns of the matrix instruction
 constexpr int kMaxCtas = 256;    // one for each SM; parts of one group, at most
-// The split, in tiles; each was swept on the device. A share of kFewestTiles: with
-// 4, 1 x 1024 of 16/8 heads takes 11.0 us for 6.8. The end of a group costs
+// The split, in tiles; each was swept on the device. A share of kFewestTiles (as
+// the only rule for short batches: 4 ragged to 200 rows of 32/8 heads 4.2 us, with 4
+// 5.9, with 16 9.0; 1 x 1024 of 16/16 6.7, 7.2, 7.5). The end of a group costs
 // kGroupCost, that of one in parts kJoinCost: without the latter 8 ragged to 8191
 // take 32.4 us for 29.2. With as many CTAs for every group a share saves kEvenGain,
 // and kAloneGain where there is then nothing to join; its tiles take 7/8 of the
