@@ -31,10 +31,12 @@
 // tile of one query token is too small: its 128-row operand would hold 8
 // pieces of different pages, and its accumulator would have to come back from
 // tensor memory for every softmax; here the tensor pipe is busy 11 to 25% of
-// the time.) Weights
-// are split in two 16-bit pieces, p = hi + lo, each multiplied with V: the sum
-// keeps the 16 (bf16) to 22 (fp16) bits of a weight that one 16-bit number
-// would round to 8 or 11. e4m3 is converted to fp16 (exact) on its way from
+// the time.) Weights are split in 16-bit pieces, each multiplied with V: three
+// of bf16, which hold all 24 bits of a float (two hold 16; then 0.21% of the
+// bf16 outputs of 8 ragged to 8191 differed from the rounded exact ones, for
+// 0.05% with three or in a plain fp32 form), or two of fp16, which hold 22. The
+// third costs bf16 caches 0 to 3% (64 ragged to 400 14.4 -> 14.9 us, 8 ragged to
+// 8191 29.9 -> 30.2). e4m3 is converted to fp16 (exact) on its way from
 // shared memory to the matrix instruction; the scales multiply scores and
 // sums.
 //
@@ -181,21 +183,25 @@ __device__ __forceinline__ uint32_t e4m3_high(uint32_t v) {
   return h;
 }
 
-// a and b rounded to 16 bits, packed; *rest their remainders, packed.
-template <bool BF16>
-__device__ __forceinline__ uint32_t split_pair(float a, float b, uint32_t* rest) {
-  if constexpr (BF16) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    const float2 f = __bfloat1622float2(h);
-    const __nv_bfloat162 r = __floats2bfloat162_rn(a - f.x, b - f.y);
-    *rest = *reinterpret_cast<const uint32_t*>(&r);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  } else {
-    const __half2 h = __floats2half2_rn(a, b);
-    const float2 f = __half22float2(h);
-    const __half2 r = __floats2half2_rn(a - f.x, b - f.y);
-    *rest = *reinterpret_cast<const uint32_t*>(&r);
-    return *reinterpret_cast<const uint32_t*>(&h);
+// a and b as sums of PIECES 16-bit numbers each, packed: each piece is what the
+// ones before leave, rounded to nearest. Three bf16 pieces hold all 24 bits of a
+// float (8, 8 and 8), two fp16 pieces 22.
+template <bool BF16, int PIECES>
+__device__ __forceinline__ void split_pair(float a, float b, uint32_t (&piece)[PIECES]) {
+#pragma unroll
+  for (int i = 0; i < PIECES; ++i) {
+    float2 f;
+    if constexpr (BF16) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+      piece[i] = *reinterpret_cast<const uint32_t*>(&h);
+      f = __bfloat1622float2(h);
+    } else {
+      const __half2 h = __floats2half2_rn(a, b);
+      piece[i] = *reinterpret_cast<const uint32_t*>(&h);
+      f = __half22float2(h);
+    }
+    a -= f.x;
+    b -= f.y;
   }
 }
 
@@ -254,6 +260,7 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
   using Sh = CacheAttnShape<E4M3, D>;
   constexpr bool kBf16 = !E4M3 && Storage<T>::kBf16;  // type of the matrix operands
   constexpr float kLift = kBf16 ? 0.f : kLiftF16;
+  constexpr int kPieces = kBf16 ? 3 : 2;  // of a weight
   constexpr int kW = Sh::kWarps, kS = Sh::kStages, kSteps = D / 16, kRows = Sh::kRows, kHalves = kRows / 16;
   constexpr uint32_t kFull = 0xffffffffu >> (32 - kRows);
   extern __shared__ __align__(128) uint8_t smem[];
@@ -777,7 +784,7 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
           o[k][3] *= c1;
         }
       }
-      uint32_t ph[kHalves][2], pl[kHalves][2];  // weights as the right operand, in two pieces
+      uint32_t pw[kHalves][2][kPieces];  // weights as the right operand, in pieces
 #pragma unroll
       for (int i = 0; i < kHalves; ++i) {
         x[i][0] = fast_exp2(x[i][0] + lift0);
@@ -789,9 +796,9 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
         if (bad[i]) l0 = l1 = NAN;  // a page outside the pool: these heads become NaN
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          ph[i][e] = split_pair<kBf16>(x[i][2 * e], x[i][2 * e + 1], &pl[i][e]);
-          ph[i][e] = transpose8x8(ph[i][e]);
-          pl[i][e] = transpose8x8(pl[i][e]);
+          split_pair<kBf16>(x[i][2 * e], x[i][2 * e + 1], pw[i][e]);
+#pragma unroll
+          for (int n = 0; n < kPieces; ++n) pw[i][e][n] = transpose8x8(pw[i][e][n]);
         }
       }
       const uint32_t vst = stage + Sh::kTileBytes;
@@ -804,8 +811,9 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
             uint32_t a[4];
             ldmatrix_x4_trans(vst + i * 16 * Sh::kRowBytes + chunk_offset<Sh::kRowBytes>(vr, 2 * k + ((lane >> 3) & 1)),
                               a);
-            mma_16x8x16<kBf16>(o[k], a[0], a[1], a[2], a[3], ph[i][0], ph[i][1]);
-            mma_16x8x16<kBf16>(o[k], a[0], a[1], a[2], a[3], pl[i][0], pl[i][1]);
+#pragma unroll
+            for (int n = 0; n < kPieces; ++n)
+              mma_16x8x16<kBf16>(o[k], a[0], a[1], a[2], a[3], pw[i][0][n], pw[i][1][n]);
           }
         }
       } else {
@@ -829,8 +837,9 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
             for (int n = 0; n < 2; ++n) {
               const uint32_t v0 = e4m3_low(a[2 * n]), v1 = e4m3_high(a[2 * n]), v2 = e4m3_low(a[2 * n + 1]),
                              v3 = e4m3_high(a[2 * n + 1]);
-              mma_16x8x16<false>(t[n], v0, v1, v2, v3, ph[i][0], ph[i][1]);
-              mma_16x8x16<false>(t[n], v0, v1, v2, v3, pl[i][0], pl[i][1]);
+#pragma unroll
+              for (int w = 0; w < kPieces; ++w)
+                mma_16x8x16<false>(t[n], v0, v1, v2, v3, pw[i][0][w], pw[i][1][w]);
             }
             if (i == 1 || apart) {
               const float vs = i ? vs1 : vs0;

@@ -1,0 +1,56 @@
+"""How many bits of a softmax weight reach the output of the paged and window
+attention: rows of nearly equal weight and opposite values, whose difference
+an output shows that is itself rounded to 8 or 11 bits."""
+import pytest
+import torch
+
+import decode_attention_static_gb300 as da
+import paged_reference as R
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"f16": torch.float16, "bf16": torch.bfloat16}
+# What a weight w = 2^x may be off by, relative: the base-2 exponential 2^-22,
+# and the two roundings of x, |x| < 2 (fp16: x + 7, below 8, half a step of
+# 2^-21), times ln 2; two pieces of fp16 leave 2^-23, three of bf16 nothing.
+WEIGHT = {"bf16": 2.0 ** -22 + 0.7 * 2 * 2.0 ** -24, "f16": 2.0 ** -22 + 0.7 * (2.0 ** -24 + 2.0 ** -22) + 2.0 ** -23}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _library():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    da.build_library()
+    da.load_library()
+
+
+@pytest.mark.parametrize("static", [False, True], ids=["pages", "static"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_weights_of_rows_that_cancel(dtype, D, static):
+    """Three rows: one of weight 1 and value 0, two of weights w and w (1 + d),
+    d < 2^-11, and values 1 and -1, so the output is about w d / (1 + 2 w). Every
+    product is exact, and so are the scores: an error of the weights or of the
+    sums (one step of 2^-23 for each of the three matrix instructions) is all
+    that the output can show beside its own rounding."""
+    dt, B, H = TYPES[dtype], 48, 8
+    gen = torch.Generator().manual_seed(D)
+    q, k, v = torch.zeros(B, H, D), torch.zeros(B, 1, 16, D), torch.zeros(B, 1, 16, D)
+    q[..., 0] = 1.0
+    q[..., D // 2 + 1] = 2.0 ** -10 * (1 + torch.arange(H) / 8)
+    k[:, 0, 1:3, 0] = -(0.25 + torch.arange(B) / 64)[:, None]
+    k[:, 0, 2, D // 2 + 1] = torch.randint(64, 128, (B,), generator=gen) / 512
+    v[:, 0, 1], v[:, 0, 2] = 1.0, -1.0
+    q, k, v = q.to(dt), k.to(dt), v.to(dt)
+    x = torch.einsum("bhd,bnd->bhn", q.double(), k[:, 0, :3].double())
+    p = torch.softmax(x, -1)
+    ref = torch.einsum("bhn,bnd->bhd", p, v[:, 0, :3].double())
+    assert ref.abs().max() < 2.0 ** -12
+    slack = ((p[..., 1] + p[..., 2]) * WEIGHT[dtype] + 3 * 2.0 ** -23 * p[..., 1])[..., None].expand(B, H, D)
+    n = torch.full((B,), 3, dtype=torch.int32, device="cuda")
+    if static:
+        out = da.decode_attn_window_fwd(q.cuda(), k.cuda(), v.cuda(), n, 3, scale=1.0)
+    else:
+        table = torch.arange(B, dtype=torch.int32, device="cuda")[:, None].contiguous()
+        out = da.decode_attn_paged_fwd(q.cuda(), k.cuda(), v.cuda(), table, n, scale=1.0)
+    R.assert_rows(out, ref, slack, "rows that cancel")
