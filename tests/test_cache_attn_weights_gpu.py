@@ -54,3 +54,36 @@ def test_weights_of_rows_that_cancel(dtype, D, static):
         table = torch.arange(B, dtype=torch.int32, device="cuda")[:, None].contiguous()
         out = da.decode_attn_paged_fwd(q.cuda(), k.cuda(), v.cuda(), table, n, scale=1.0)
     R.assert_rows(out, ref, slack, "rows that cancel")
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_long_sums_that_cancel(dtype):
+    """8192 rows in 512 tiles, the second half with the first one's keys (and so
+    its weights, bit for bit) and the opposite values: the output is 0, and every
+    error of the running sum stays in it. Rounded to nearest, the sum after k
+    tiles errs by up to half a step of 2^-23 of what it holds, in either
+    direction: independent errors, whose total stays within six standard
+    deviations (truncated ones would all point towards zero and add up). Within a
+    tile a sum may be truncated, by a step of it for each of its three matrix
+    instructions. Every sequence reads the same pages, so that one warp goes
+    through many tiles."""
+    dt, B, Hkv, G, D, page, n = TYPES[dtype], 152, 8, 2, 128, 64, 8192
+    gen = torch.Generator().manual_seed(1)
+    a = (torch.randint(-128, 129, (Hkv, n // 2), generator=gen) / 256)
+    order = torch.randperm(n // 2, generator=gen)
+    key = torch.cat([a, a[:, order]], dim=1)  # [Hkv, n]
+    k, v = (torch.zeros(n // page, Hkv, page, D) for _ in range(2))
+    k[..., 3] = key.view(Hkv, n // page, page).transpose(0, 1)
+    v[:n // page // 2], v[n // page // 2:] = 1.0, -1.0
+    q = torch.zeros(B, Hkv * G, D)
+    q[..., 3] = 1 + torch.arange(B * Hkv * G).view(B, -1) % 64 / 64
+    table = torch.arange(n // page, dtype=torch.int32).repeat(B, 1)
+    lens = torch.full((B,), n, dtype=torch.int32)
+    out = da.decode_attn_paged_fwd(*(t.cuda() for t in (q.to(dt), k.to(dt), v.to(dt), table, lens)), scale=1.0)
+    amplitude = q[..., 3].view(B, Hkv, G, 1).double()
+    p = torch.softmax(amplitude * key.double()[None, :, None], -1).flatten(1, 2)  # [B, H, n]
+    running = (p * v[:, 0, :, 0].reshape(-1).double()).view(B, Hkv * G, n // 16, 16).sum(-1).cumsum(-1)
+    assert running[..., -1].abs().max() < 1e-12
+    slack = 6 * (2.0 ** -46 * running.square() / 12).sum(-1).sqrt() + 3 * 2.0 ** -23
+    slack = slack[..., None].expand(-1, -1, D)
+    R.assert_rows(out, torch.zeros(B, Hkv * G, D).double(), slack, "sums that cancel")
