@@ -68,17 +68,17 @@ def build_fastcall(force: bool = False) -> pathlib.Path | None:
     if not force and not _stale(out):
         return out
     root = pathlib.Path(torch.__file__).parent
-    cuda = pathlib.Path(nvcc()).parent.parent
     tmp = out.with_name(out.name + f".tmp{os.getpid()}")
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-I{INCLUDE}",
-           f"-I{root / 'include'}", f"-I{root / 'include/torch/csrc/api/include'}",
-           f"-I{sysconfig.get_paths()['include']}", f"-I{cuda / 'include'}", str(CSRC / "fastcall.cpp"), "-o", str(tmp),
-           f"-L{root / 'lib'}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python",
-           f"-Wl,-rpath,{root / 'lib'}"]
     try:
+        cuda = pathlib.Path(nvcc()).parent.parent
+        cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-I{INCLUDE}",
+               f"-I{root / 'include'}", f"-I{root / 'include/torch/csrc/api/include'}",
+               f"-I{sysconfig.get_paths()['include']}", f"-I{cuda / 'include'}", str(CSRC / "fastcall.cpp"),
+               "-o", str(tmp), f"-L{root / 'lib'}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python",
+               f"-Wl,-rpath,{root / 'lib'}"]
         r = subprocess.run(cmd, capture_output=True, text=True)
-    except OSError as e:
+    except (OSError, RuntimeError) as e:  # no compiler, no CUDA toolkit
         warnings.warn(f"the binding's fast path was not built: {e}")
         return None
     if r.returncode != 0:
