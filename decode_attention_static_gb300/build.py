@@ -61,7 +61,8 @@ def fastcall_path() -> pathlib.Path:
 
 def build_fastcall(force: bool = False) -> pathlib.Path | None:
     """Compile the binding's fast path if a source is newer than it; None (and
-    a warning) where that does not work."""
+    a warning) where that does not work. No older module is left then: it calls
+    the library by addresses, with the argument lists of its own sources."""
     import torch
 
     out = fastcall_path()
@@ -78,11 +79,12 @@ def build_fastcall(force: bool = False) -> pathlib.Path | None:
                "-o", str(tmp), f"-L{root / 'lib'}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python",
                f"-Wl,-rpath,{root / 'lib'}"]
         r = subprocess.run(cmd, capture_output=True, text=True)
+        why = f"\n{' '.join(cmd)}\n{r.stderr[-2000:]}" if r.returncode != 0 else None
     except (OSError, RuntimeError) as e:  # no compiler, no CUDA toolkit
-        warnings.warn(f"the binding's fast path was not built: {e}")
-        return None
-    if r.returncode != 0:
-        warnings.warn(f"the binding's fast path was not built:\n{' '.join(cmd)}\n{r.stderr[-2000:]}")
+        why = str(e)
+    if why is not None:
+        out.unlink(missing_ok=True)
+        warnings.warn(f"the binding's fast path was not built: {why}")
         return None
     os.replace(tmp, out)
     return out

@@ -1,5 +1,7 @@
 """The binding's fast path is optional: where it cannot be built or loaded, the
 library and the Python path serve every call, with a warning. On the CPU."""
+import os
+
 import pytest
 
 from decode_attention_static_gb300 import build as da_build
@@ -30,6 +32,24 @@ def test_no_toolkit(elsewhere, monkeypatch):
 def test_no_compiler(elsewhere, monkeypatch):
     library, path = elsewhere
     monkeypatch.setenv("CXX", str(path.parent / "no-such-compiler"))
+    with pytest.warns(UserWarning, match="fast path was not built"):
+        assert da_build.build_library() == library
+    assert not path.exists()
+
+
+@pytest.mark.parametrize("how", ["no toolkit", "no compiler", "compile error"])
+def test_a_module_that_was_not_rebuilt_is_not_left(elsewhere, monkeypatch, how):
+    """A module older than its sources, whose argument lists may not be the
+    library's any more, does not outlive a build that fails."""
+    library, path = elsewhere
+    path.write_bytes(b"an older module")
+    os.utime(path, (0, 0))
+    if how == "no toolkit":
+        monkeypatch.setattr(da_build, "nvcc", lambda: (_ for _ in ()).throw(RuntimeError("nvcc not found")))
+    elif how == "no compiler":
+        monkeypatch.setenv("CXX", str(path.parent / "no-such-compiler"))
+    else:
+        monkeypatch.setenv("CXX", "false")
     with pytest.warns(UserWarning, match="fast path was not built"):
         assert da_build.build_library() == library
     assert not path.exists()
