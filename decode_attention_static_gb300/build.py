@@ -7,6 +7,7 @@ library needs only the CUDA driver at run time.
 from __future__ import annotations
 
 import concurrent.futures as cf
+import hashlib
 import os
 import pathlib
 import shutil
@@ -53,10 +54,12 @@ def _stale(output: pathlib.Path) -> bool:
 
 
 def fastcall_path() -> pathlib.Path:
-    """The fast path's module for this Python and torch (it is bound to both)."""
+    """The fast path's module for this Python, torch and C header: it is bound to
+    the first two, and its calls have the third one's argument lists."""
     import torch
 
-    return PKG / f"_fastcall.{sys.implementation.cache_tag}.torch-{torch.__version__}.so"
+    abi = hashlib.sha256((INCLUDE / "decode_attn.h").read_bytes()).hexdigest()[:8]
+    return PKG / f"_fastcall.{sys.implementation.cache_tag}.torch-{torch.__version__}.{abi}.so"
 
 
 def build_fastcall(force: bool = False) -> pathlib.Path | None:

@@ -53,3 +53,15 @@ def test_a_module_that_was_not_rebuilt_is_not_left(elsewhere, monkeypatch, how):
     with pytest.warns(UserWarning, match="fast path was not built"):
         assert da_build.build_library() == library
     assert not path.exists()
+
+
+def test_a_module_for_another_header_is_not_found(tmp_path, monkeypatch):
+    """A module left by another torch, or by sources that moved on, is known by
+    the header that its calls were compiled against."""
+    now = da_build.fastcall_path()
+    text = (da_build.INCLUDE / "decode_attn.h").read_text()
+    (tmp_path / "decode_attn.h").write_text(text.replace("int max_pages, int window", "int window, int max_pages"))
+    monkeypatch.setattr(da_build, "INCLUDE", tmp_path)
+    assert da_build.fastcall_path() != now and da_build.fastcall_path().parent == now.parent
+    (tmp_path / "decode_attn.h").write_text(text)
+    assert da_build.fastcall_path() == now
