@@ -10,8 +10,11 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import importlib.machinery
+import importlib.util
 import pathlib
 import threading
+import warnings
 
 import torch
 
@@ -97,26 +100,27 @@ def load_library() -> ctypes.CDLL:
 
 def _load_fast():
     """The binding's fast path (csrc/fastcall.cpp), bound to the library; False
-    where it has not been built. Its functions return NotImplemented for calls
-    that they leave to the Python path."""
+    where it has not been built or does not load (then with a warning). Its
+    functions return NotImplemented for calls that they leave to the Python path."""
     global _fast
     lib = load_library()
-    from .build import fastcall_path
+    try:
+        from .build import fastcall_path
 
-    path = fastcall_path()
-    if not path.exists():
+        path = fastcall_path()
+        if not path.exists():
+            _fast = False
+            return _fast
+        loader = importlib.machinery.ExtensionFileLoader("_fastcall", str(path))
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_fastcall", loader))
+        loader.exec_module(module)
+        module.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
+            "decode_attn_paged_fwd", "decode_attn_paged_q8_fwd", "decode_attn_window_fwd", "kvcache_append_paged",
+            "kvcache_append_paged_q8")))
+        _fast = module
+    except (ImportError, OSError, AttributeError) as e:
+        warnings.warn(f"the binding's fast path does not load, calls are made from Python: {e}")
         _fast = False
-        return _fast
-    import importlib.machinery
-    import importlib.util
-
-    loader = importlib.machinery.ExtensionFileLoader("_fastcall", str(path))
-    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_fastcall", loader))
-    loader.exec_module(module)
-    module.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
-        "decode_attn_paged_fwd", "decode_attn_paged_q8_fwd", "decode_attn_window_fwd", "kvcache_append_paged",
-        "kvcache_append_paged_q8")))
-    _fast = module
     return _fast
 
 

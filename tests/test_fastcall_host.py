@@ -1,9 +1,15 @@
 """The binding's fast path is optional: where it cannot be built or loaded, the
 library and the Python path serve every call, with a warning. On the CPU."""
+import importlib.util
 import os
+import pathlib
+import warnings
 
 import pytest
+import torch
 
+import decode_attention_static_gb300 as da
+from decode_attention_static_gb300 import _binding
 from decode_attention_static_gb300 import build as da_build
 
 
@@ -65,3 +71,33 @@ def test_a_module_for_another_header_is_not_found(tmp_path, monkeypatch):
     assert da_build.fastcall_path() != now and da_build.fastcall_path().parent == now.parent
     (tmp_path / "decode_attn.h").write_text(text)
     assert da_build.fastcall_path() == now
+
+
+@pytest.mark.parametrize("content", [None, b"", b"not an ELF file", "another module"],
+                         ids=["none", "empty", "garbage", "other"])
+def test_a_module_that_does_not_load(elsewhere, monkeypatch, content):
+    """The first call of an operator takes the Python path (which here says that
+    its tensors are not on a GPU) instead of failing on the module."""
+    _, path = elsewhere
+    if content == "another module":
+        content = pathlib.Path(_another_module()).read_bytes()
+    if content is not None:
+        path.write_bytes(content)
+    monkeypatch.setattr(_binding, "_fast", None)
+    q, cache = torch.zeros(1, 2, 64, dtype=torch.float16), torch.zeros(1, 1, 16, 64, dtype=torch.float16)
+    n = torch.ones(1, dtype=torch.int32)
+    with warnings.catch_warnings(record=True) as said:
+        warnings.simplefilter("always")
+        with pytest.raises(ValueError, match="CUDA"):
+            da.decode_attn_window_fwd(q, cache, cache, n, 4)
+    assert [w for w in said if "fast path does not load" in str(w.message)] or content is None
+    assert _binding._fast is False
+
+
+def _another_module():
+    """Some extension module of this Python that is not the fast path's."""
+    for name in ("_ctypes", "_json", "_zoneinfo", "_queue"):
+        spec = importlib.util.find_spec(name)
+        if spec and spec.origin and spec.origin.endswith(".so"):
+            return spec.origin
+    pytest.skip("every extension module is built in")
