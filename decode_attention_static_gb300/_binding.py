@@ -199,6 +199,13 @@ def _require(cond: bool, msg) -> None:
         raise ValueError(msg() if callable(msg) else msg)
 
 
+def _int32(name: str, value) -> int:
+    """value as the C int that it is passed as (ctypes would drop its upper bits)."""
+    value = int(value)
+    _require(-(1 << 31) <= value < 1 << 31, lambda: f"{name} = {value} does not fit 32 bits")
+    return value
+
+
 def _cuda_contig(name: str, t: torch.Tensor) -> None:
     _require(t.is_cuda, lambda: f"{name} must be a CUDA tensor")
     _require(t.is_contiguous(), lambda: f"{name} must be contiguous")
@@ -733,6 +740,7 @@ def _explain_attn_tail(q, kv_len, out, workspace, err_flag, **others):
 
 def _attn_paged(fn, q, k_pages, v_pages, k_scale, v_scale, eight, page_table, kv_len, window, sinks, out, scale,
                 workspace, err_flag):
+    window, sinks = _int32("window", window), _int32("sinks", sinks)
     dtype, shape, pool, table = q.dtype, q.shape, k_pages.shape, page_table.shape
     code, store = _DTYPE_CODE.get(dtype), _E4M3 if eight else dtype
     ix = q.get_device()
@@ -758,7 +766,7 @@ def _attn_paged(fn, q, k_pages, v_pages, k_scale, v_scale, eight, page_table, kv
     if workspace is None:
         workspace = alloc_paged_workspace(shape[1], pool[1], shape[2], q.device)
     tail = (page_table.data_ptr(), kv_len.data_ptr(), shape[0], shape[1], pool[1], shape[2], pool[0], pool[2],
-            table[1], int(window), int(sinks), shape[2] ** -0.5 if scale is None else float(scale), out.data_ptr(),
+            table[1], window, sinks, shape[2] ** -0.5 if scale is None else float(scale), out.data_ptr(),
             workspace.data_ptr(), workspace.numel() * workspace.element_size(), code,
             None if err_flag is None else err_flag.data_ptr(), _raw_stream(ix))
     if eight:
@@ -815,6 +823,7 @@ def decode_attn_window_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torc
         r = fast.attn_window(q, k_cache, v_cache, kv_len, window, sinks, out, scale, workspace, err_flag)
         if r is not NotImplemented:
             return r
+    window, sinks = _int32("window", window), _int32("sinks", sinks)
     dtype, shape, cache = q.dtype, q.shape, k_cache.shape
     code, ix = _DTYPE_CODE.get(dtype), q.get_device()
     if out is None:
@@ -839,7 +848,7 @@ def decode_attn_window_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torc
     if workspace is None:
         workspace = alloc_paged_workspace(shape[1], cache[1], shape[2], q.device)
     _call_on("decode_attn_window_fwd", ix, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), kv_len.data_ptr(),
-             shape[0], shape[1], cache[1], shape[2], cache[2], int(window), int(sinks),
+             shape[0], shape[1], cache[1], shape[2], cache[2], window, sinks,
              shape[2] ** -0.5 if scale is None else float(scale), out.data_ptr(), workspace.data_ptr(),
              workspace.numel() * workspace.element_size(), code, None if err_flag is None else err_flag.data_ptr(),
              _raw_stream(ix))
