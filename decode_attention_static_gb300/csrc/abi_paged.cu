@@ -27,11 +27,11 @@ int log2_of(int v) {
   return s;
 }
 
-// Sizes that the attention entry points share. B is the grid's y extent.
+// Sizes that the attention entry points share.
 int check_heads(int B, int n_head, int n_kv_head, int head_dim, int dtype) {
   if (dtype != DA_F16 && dtype != DA_BF16) return DA_ERR_DTYPE;
   if (B < 0 || n_head < 1 || n_kv_head < 1 || head_dim < 1) return DA_ERR_SHAPE;
-  if (n_head % n_kv_head != 0 || B > 65535 || n_kv_head > 65535) return DA_ERR_SHAPE;
+  if (n_head % n_kv_head != 0 || B > kMaxBatch || n_kv_head > kMaxBatch) return DA_ERR_SHAPE;
   if (!decode_supported(head_dim, n_head / n_kv_head)) return DA_ERR_UNSUPPORTED;
   return DA_OK;
 }

@@ -293,6 +293,8 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
   };
   Found* found = reinterpret_cast<Found*>(words + kW);
   constexpr int kCount = 44;  // tiles and non-empty sequences are summed in one word: tiles + sequences * 2^44
+  static_assert(kMaxBatch < 1 << (63 - kCount) && (int64_t)kMaxBatch << 27 <= 1ll << kCount,
+                "a batch of sequences of fewer than 2^31 rows, in tiles of 16, fits the word");
   constexpr int kChunks = Sh::kRowBytes / 16, kLanes = 32 / kHalves, kCopies = 16 * kChunks / kLanes;
   const int half = kHalves == 2 ? lane >> 4 : 0, sub = lane % kLanes;
   const bool alone = p.B <= 32 && p.B * p.n_kv_head <= gridDim.x;  // (teams have to agree on the split)
@@ -512,7 +514,9 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
   if ((int64_t)blockIdx.x >= ctas) return;
   // A team goes where its first warp goes: its barriers count its warps, and a
   // length that changes under the call (an error of the caller's) must not part
-  // them. (b, g and the length in one word; B and the heads fit 16 bits.)
+  // them. (b, g and the length in one word; all ones, which no group is, at the
+  // end.)
+  static_assert(kMaxBatch <= 0xffff, "b < B and g < n_kv_head are below 0xffff");
   uint64_t* next = reinterpret_cast<uint64_t*>(words + kW + 4 + (kW + 1) / 2) + (warp - lead);
   auto team_sync = [&]() {
     asm volatile("bar.sync %0, %1;" ::"r"(1 + (warp - lead) / 2), "r"(team * 32) : "memory");

@@ -11,6 +11,9 @@ namespace da {
 constexpr int kMinScaleExponent = -100;
 constexpr int kMinPageSize = 16;
 constexpr int kMaxPageSize = 256;
+// Most sequences, and most KV heads, of an attention call (cache_attn.cuh packs
+// a sequence number and a head into 16 bits each).
+constexpr int kMaxBatch = 65535;
 
 // Attention over a cache in pages, or (table == nullptr) over a static cache,
 // where sequence b is page b of `page_rows` = capacity rows.

@@ -382,9 +382,11 @@ DA_API int decode_attn_fwd_static_scratch(const void* q, const void* k_cache, co
  * infinities),
  *   k_scale, v_scale  fp32 [num_pages, n_kv_head]: element x of a page and KV
  *                     head stands for x * scale.
- * max_pages * page_size stays below 2^31 - 512, and B * n_kv_head times the
- * 16-row tiles of that below 2^37 (else DA_ERR_SHAPE). Arrays that a call
- * writes overlap no other argument, but for q_out, which may be q itself.
+ * max_pages * page_size stays below 2^31 - 512. The attentions (paged or over a
+ * static cache) take at most 65535 sequences and 65535 KV heads, and B *
+ * n_kv_head times the 16-row tiles of a longest sequence below 2^37. (Else
+ * DA_ERR_SHAPE.) Arrays that a call writes overlap no other argument, but for
+ * q_out, which may be q itself.
  */
 
 /*

@@ -5,6 +5,7 @@ import torch
 
 import decode_attention_static_gb300 as da
 import paged_reference as R
+import test_paged_host as P
 from decode_attention_static_gb300 import build as da_build
 
 
@@ -37,3 +38,13 @@ def test_windows_of_32_bits_are_not(value):
     for call in calls(window=value, sinks=value):
         with pytest.raises(ValueError, match="CUDA"):
             call()
+
+
+@pytest.mark.parametrize("fn", P.PAGED + ["decode_attn_window_fwd"])
+def test_batches_and_heads_past_16_bits_are_refused(fn):
+    """A sequence number and a head travel in 16 bits each."""
+    lib, rows = da.load_library(), {"capacity": 64} if "window" in fn else {"max_pages": 4}
+    assert P.call(lib, fn, B=65536, H=1, Hkv=1, **rows) == P.SHAPE
+    assert P.call(lib, fn, B=1, H=65536, Hkv=65536, **rows) == P.SHAPE
+    assert P.call(lib, fn, B=65535, H=1, Hkv=1, q=None, **rows) == P.NULL
+    assert P.call(lib, fn, B=1, H=65535, Hkv=65535, q=None, **rows) == P.NULL
