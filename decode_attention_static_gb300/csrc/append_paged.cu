@@ -238,17 +238,28 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t v) {
   return __half22float2(*reinterpret_cast<__half2*>(&h));
 }
 
-// 8 values over a scale. NaN becomes the type's NaN by the conversion;
-// infinities, which would be clamped to 448, only with INFINITIES (e4m3 has
-// none).
-template <bool INFINITIES>
-__device__ __forceinline__ uint2 quantise8(const float (&f)[8], float inv) {
+// Whether the reciprocal of a scale is exact: scales that this call makes are
+// powers of two, but a page may come with any other from elsewhere.
+__device__ __forceinline__ bool power_of_two(float scale) { return (__float_as_uint(scale) & 0x7fffffu) == 0; }
+
+// 8 values over a scale. NaN becomes the type's NaN by the conversion. CAREFUL:
+// infinities, which would be clamped to 448, become NaN too (e4m3 has none), and
+// the values are divided; else they are multiplied by the reciprocal of a power
+// of two.
+template <bool CAREFUL>
+__device__ __forceinline__ uint2 quantise8(const float (&f)[8], float scale) {
   float x[8];
+  const float inv = __uint_as_float((2u * 127 << 23) - __float_as_uint(scale));
 #pragma unroll
   for (int e = 0; e < 8; e += 2) {
-    const float2 v = __fmul2_rn(make_float2(f[e], f[e + 1]), make_float2(inv, inv));
-    x[e] = INFINITIES && fabsf(f[e]) == INFINITY ? NAN : v.x;
-    x[e + 1] = INFINITIES && fabsf(f[e + 1]) == INFINITY ? NAN : v.y;
+    if constexpr (CAREFUL) {
+      x[e] = fabsf(f[e]) == INFINITY ? NAN : f[e] / scale;
+      x[e + 1] = fabsf(f[e + 1]) == INFINITY ? NAN : f[e + 1] / scale;
+    } else {
+      const float2 v = __fmul2_rn(make_float2(f[e], f[e + 1]), make_float2(inv, inv));
+      x[e] = v.x;
+      x[e + 1] = v.y;
+    }
   }
   return make_uint2(to_e4m3x2(x[0], x[1]) | (to_e4m3x2(x[2], x[3]) << 16),
                     to_e4m3x2(x[4], x[5]) | (to_e4m3x2(x[6], x[7]) << 16));
@@ -348,14 +359,13 @@ __global__ void __launch_bounds__(kThreads)
     rescale_rows(at, n * p.head_dim, ratio, threadIdx.x % 32, 32);
   }
   if (write) {
-    const float inv = 1.f / scale;
     uint2* out = reinterpret_cast<uint2*>(rows + (int64_t)old_rows * p.head_dim) + c;
-    if (infinities) {
-      out[0] = quantise8<true>(a, inv);
-      out[half] = quantise8<true>(bb, inv);
+    if (infinities || !power_of_two(scale)) {
+      out[0] = quantise8<true>(a, scale);
+      out[half] = quantise8<true>(bb, scale);
     } else {
-      out[0] = quantise8<false>(a, inv);
-      out[half] = quantise8<false>(bb, inv);
+      out[0] = quantise8<false>(a, scale);
+      out[half] = quantise8<false>(bb, scale);
     }
     if (c == 0) *scale_at = scale;
   }
@@ -553,11 +563,12 @@ __global__ void __launch_bounds__(kThreads, prompt_ctas(R))
       __syncthreads();
       find_peaks(std::true_type());
     }
-    float scale[HC], inv[HC];
+    float scale[HC];
+    bool careful = infinities;
 #pragma unroll
     for (int k = 0; k < HC; ++k) {
       scale[k] = fmaxf(scale_of(peak[k]), old_scale[k]);
-      inv[k] = 1.f / scale[k];
+      careful |= !power_of_two(scale[k]);
       if (old_rows > 0 && k < live && scale[k] != old_scale[k])
         rescale_rows(rows + k * page_bytes, old_rows * p.head_dim, old_scale[k] / scale[k],
                      threadIdx.x % team, team);
@@ -571,12 +582,12 @@ __global__ void __launch_bounds__(kThreads, prompt_ctas(R))
         for (int k = 0; k < HC; ++k) {
           if (k >= live) break;
           uint2* out = reinterpret_cast<uint2*>(rows + k * page_bytes + (position - row0) * p.head_dim) + c;
-          out[0] = quantise8<decltype(some)::value>(va[i][k], inv[k]);
-          out[half] = quantise8<decltype(some)::value>(vb[i][k], inv[k]);
+          out[0] = quantise8<decltype(some)::value>(va[i][k], scale[k]);
+          out[half] = quantise8<decltype(some)::value>(vb[i][k], scale[k]);
         }
       }
     };
-    if (infinities) {
+    if (careful) {
       round_rows(std::true_type());
     } else {
       round_rows(std::false_type());

@@ -421,7 +421,8 @@ DA_API int kvcache_append_paged(void* k_pages, void* v_pages, const void* k_new,
  *           key before any rounding)
  *   scale = the smallest power of two >= peak / 448, at least 2^-100; and at
  *           least the page's present scale when rows before the first new one
- *           lie in the page (a page filled from its first row on starts anew)
+ *           lie in the page (a page filled from its first row on starts anew).
+ *           A present scale is finite and not negative, a power of two or not
  *   x is stored as e4m3(x / scale), nearest even; NaN and infinities as NaN.
  * Where the scale grows, the page's earlier rows are rounded to the new one
  * (a power of two: only exponents move, bits are lost below 2^-9 of the new
