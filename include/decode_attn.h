@@ -456,7 +456,8 @@ DA_API size_t decode_attn_paged_workspace_size(int n_head, int n_kv_head, int he
  * head; over bf16 caches all 24. Over 8-bit pages a bf16 query keeps what lies
  * above 2^-25 of its head's largest element.) Rows that are not visible are not
  * read; NaN among the visible ones reaches the heads that read it, and an
- * infinite element of V makes that element of its heads' outputs NaN.
+ * infinite element of V makes that element of its heads' outputs infinite or
+ * NaN (a weight reaches V in pieces, and a piece may be zero or negative).
  * kv_len[b] == 0 (an idle slot of a batch) gives a row of zeros;
  * kv_len[b] < 0 or > max_pages * page_size gives NaN and DA_DEVERR_KV_LEN; a
  * page id outside the pool gives NaN for the heads that would read it and
