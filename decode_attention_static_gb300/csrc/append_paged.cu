@@ -7,9 +7,9 @@
 // other lane. Every byte of q, k_new, v_new and the pages moves once (but for
 // the table rows, which come from L1 and L2 after the first head): prompts are
 // bound by HBM, single tokens by the chain of dependent loads (sequence,
-// position, page). Measured (of the measured 6782 GB/s copy): prompts of 8.4k
+// position, page). Measured (of the measured 6782 GB/s copy): prompts of 8.8k
 // tokens, 8 KV and 32 query heads of 128, fp16, 225 MB in 37.6 us (88%); the
-// same heads, 21k tokens into 8 bits, 482 MB in 86.4 us (82%; the 30% that are K
+// same heads, 20.8k tokens into 8 bits, 482 MB in 86.5 us (82%; the 30% that are K
 // and V take 35 us, bound by the chain of peaks and rounding at two CTAs an SM);
 // 8 sequences, one token each, 2.4 us, 64 into 8 bits 2.4 us.
 #include <stdint.h>
@@ -377,8 +377,9 @@ __global__ void __launch_bounds__(kThreads)
 // take further heads) and HC heads of a chunk. A thread's rows of the next item
 // are on their way into its own places in shared memory while it finds the
 // peaks of this one and rounds it: nothing is waited for but the peaks, once an
-// item. Two CTAs of 64 values a thread fill an SM's registers. (21k tokens of 8
-// KV and 32 query heads, us: pages of 16 / 64 / 128 87.2 / 86.4 / 88.3; one CTA for
+// item. Two CTAs of 64 values a thread fill an SM's registers (and spill a little:
+// 144 bytes with one row and four heads a unit, 40 with two and two). (21k tokens of 8
+// KV and 32 query heads, us: pages of 16 / 64 / 128 86.7 / 86.5 / 88.3; one CTA for
 // each page and K or V, with no load ahead of it, 97 / 87 / 93; three CTAs of 32
 // values 92 / 101 / 90; the values rotated twice instead of kept 98 / 97 / 102.)
 __host__ __device__ constexpr int prompt_heads(int R) { return R >= 4 ? 1 : 4 / R; }

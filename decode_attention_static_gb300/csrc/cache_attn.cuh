@@ -26,7 +26,7 @@
 //   S^T [16 rows x 8 heads] = K q^T        mma m16n8k16, K by ldmatrix
 //   p = 2^(x' - m), m raised only when a score passes it by 2^8 (a vote)
 //   out^T [D x 8 heads] += V^T P^T         V by ldmatrix.trans, P^T by movmatrix
-// The heads are the 8 columns of the instruction, so a group of any size
+// The heads are the 8 columns of the instruction, so a group of 1, 2, 4 or 8
 // costs the same, and scores and weights stay in registers. (For tcgen05 a
 // tile of one query token is too small: its 128-row operand would hold 8
 // pieces of different pages, and its accumulator would have to come back from
@@ -35,7 +35,7 @@
 // of bf16, which hold all 24 bits of a float (two hold 16; then 0.21% of the
 // bf16 outputs of 8 ragged to 8191 differed from the rounded exact ones, for
 // 0.05% with three or in a plain fp32 form), or two of fp16, which hold 22. The
-// third costs bf16 caches 0 to 3% (64 ragged to 400 14.4 -> 14.9 us, 8 ragged to
+// third costs bf16 caches 0 to 4% (64 ragged to 400 14.4 -> 14.9 us, 8 ragged to
 // 8191 29.9 -> 30.2). A tile's product starts from zero and is added to the
 // output in fp32: the matrix instruction truncates its sums, and 200 tiles on
 // one accumulator drift towards zero (32 ragged to 32768: 0.31% of the outputs
@@ -44,10 +44,10 @@
 // sums.
 //
 // Measured (graph of calls, data from HBM, of the measured 6782 GB/s copy): 32
-// ragged sequences up to 32768 rows, 32 / 8 heads, 2.04 GB in 295 us (102%),
+// ragged sequences up to 32768 rows, 32 / 8 heads, 2.04 GB in 298 us (101%),
 // in 8 bits 1.02 GB in 153 us (98%); 8 ragged up to 8191, 16 / 8 heads, 159 MB
-// in 29.4 us (80%); 16 ragged with window 1021 and 16 / 8 heads, 68 MB in 12.7
-// us (79%); window 4096 in 8 bits, 16 ragged, 64 / 8 heads, 135 MB in 26.2 us
+// in 30.2 us (78%); 16 ragged with window 1021 and 16 / 8 heads, 68 MB in 13.0
+// us (77%); window 4096 in 8 bits, 16 ragged, 64 / 8 heads, 135 MB in 26.3 us
 // (76%); one of 1024 rows, 16 / 16 heads, 7.0 us. Short calls are a chain of
 // dependent steps, each about as long as a memory round trip: page numbers (0.6
 // us after the wait; lengths, share and L2 prefetch come before it), rows (0.8),
@@ -64,7 +64,10 @@ namespace da {
 
 constexpr int kHeads = 8;        // columns of the matrix instruction
 constexpr int kMaxCtas = 256;    // one for each SM; parts of one group, at most
-// The split, in tiles; each was swept on the device. A share of kFewestTiles (as
+// The split, in tiles; each was swept on the device (with ragged lengths from an
+// eighth of the longest on, as lengths() of perf/operators.py draws them for lens
+// = 1; figures of bf16 caches from before their weights' third piece, which added
+// 0 to 5% with the rounded sums). A share of kFewestTiles (as
 // the only rule for short batches: 4 ragged to 200 rows of 32/8 heads 4.2 us, with 4
 // 5.9, with 16 9.0; 1 x 1024 of 16/16 6.7, 7.2, 7.5). The end of a group costs
 // kGroupCost, that of one in parts kJoinCost: without the latter 8 ragged to 8191
