@@ -238,9 +238,12 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t v) {
   return __half22float2(*reinterpret_cast<__half2*>(&h));
 }
 
-// Whether the reciprocal of a scale is exact: scales that this call makes are
-// powers of two, but a page may come with any other from elsewhere.
-__device__ __forceinline__ bool power_of_two(float scale) { return (__float_as_uint(scale) & 0x7fffffu) == 0; }
+// Whether a scale's reciprocal is exact and normal: scales that this call makes
+// are powers of two up to 2^120, but a page may come with any other from elsewhere.
+__device__ __forceinline__ bool power_of_two(float scale) {
+  const uint32_t u = __float_as_uint(scale);
+  return (u & 0x7fffffu) == 0 && u < 254u << 23;
+}
 
 // 8 values over a scale. NaN becomes the type's NaN by the conversion. CAREFUL:
 // infinities, which would be clamped to 448, become NaN too (e4m3 has none), and

@@ -50,3 +50,14 @@ def test_any_scale_grows_to_a_power_of_two(counts, positions):
     gen = torch.Generator().manual_seed(4)
     inp.ks, inp.vs = (torch.rand(inp.ks.shape, generator=gen) * 2.0 ** -6 + 2.0 ** -12 for _ in range(2))
     A.check(inp, "scales grow and stay")
+
+
+@pytest.mark.parametrize("counts,positions", PLACES, ids=["tokens", "prompts"])
+@pytest.mark.parametrize("scale", [2.0 ** 126, 2.0 ** 127, 1.5 * 2.0 ** 127])
+def test_scales_at_the_end_of_the_range(scale, counts, positions):
+    """Scales whose reciprocal is no normal number."""
+    inp = A.Inputs(counts, positions, 2, 2, 64, "bf16", 16, True, rope=False, with_q=False, seed=6)
+    inp.ks[:], inp.vs[:] = scale, scale
+    inp.k_new, inp.v_new = ((x.float() * 1.2 * 2.0 ** 125).bfloat16() for x in (inp.k_new, inp.v_new))
+    assert inp.k_new.isfinite().all() and inp.v_new.isfinite().all()
+    A.check(inp, f"scale {scale}")
