@@ -7,6 +7,7 @@ library needs only the CUDA driver at run time.
 from __future__ import annotations
 
 import concurrent.futures as cf
+import contextlib
 import hashlib
 import os
 import pathlib
@@ -86,7 +87,8 @@ def build_fastcall(force: bool = False) -> pathlib.Path | None:
     except (OSError, RuntimeError) as e:  # no compiler, no CUDA toolkit
         why = str(e)
     if why is not None:
-        out.unlink(missing_ok=True)
+        with contextlib.suppress(OSError):  # (a tree that cannot be written)
+            out.unlink()
         warnings.warn(f"the binding's fast path was not built: {why}")
         return None
     os.replace(tmp, out)

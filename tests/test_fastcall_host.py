@@ -101,3 +101,18 @@ def _another_module():
         if spec and spec.origin and spec.origin.endswith(".so"):
             return spec.origin
     pytest.skip("every extension module is built in")
+
+
+def test_a_tree_that_cannot_be_written(elsewhere, monkeypatch):
+    """A module that cannot be rebuilt and not be removed fails no build."""
+    library, path = elsewhere
+    path.write_bytes(b"an older module")
+    os.utime(path, (0, 0))
+    monkeypatch.setenv("CXX", "false")
+
+    def refused(self, missing_ok=False):
+        raise PermissionError("read-only")
+
+    monkeypatch.setattr(pathlib.Path, "unlink", refused)
+    with pytest.warns(UserWarning, match="fast path was not built"):
+        assert da_build.build_library() == library
