@@ -119,8 +119,8 @@ def _load_fast():
             "kvcache_append_paged_q8")))
         _fast = module
     except (ImportError, OSError, AttributeError) as e:
-        warnings.warn(f"the binding's fast path does not load, calls are made from Python: {e}")
         _fast = False
+        warnings.warn(f"the binding's fast path does not load, calls are made from Python: {e}")
     return _fast
 
 

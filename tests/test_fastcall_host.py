@@ -116,3 +116,16 @@ def test_a_tree_that_cannot_be_written(elsewhere, monkeypatch):
     monkeypatch.setattr(pathlib.Path, "unlink", refused)
     with pytest.warns(UserWarning, match="fast path was not built"):
         assert da_build.build_library() == library
+
+
+def test_a_warning_that_is_an_error_comes_once(elsewhere, monkeypatch):
+    """Where warnings are errors, the first call says that the module does not
+    load, and the next one is made."""
+    _, path = elsewhere
+    path.write_bytes(b"")
+    monkeypatch.setattr(_binding, "_fast", None)
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        with pytest.raises(UserWarning, match="does not load"):
+            _binding._load_fast()
+    assert _binding._fast is False
