@@ -24,7 +24,7 @@
 // up one tile ahead, over the ends of groups), and no barrier within a group.
 // Per tile and piece:
 //   S^T [16 rows x 8 heads] = K q^T        mma m16n8k16, K by ldmatrix
-//   p = 2^(x' - m), m raised only when a score passes it by 2^8 (a vote)
+//   p = 2^(x' - m), m raised only when a score passes it by some bits (a vote)
 //   out^T [D x 8 heads] += V^T P^T         V by ldmatrix.trans, P^T by movmatrix
 // The heads are the 8 columns of the instruction, so a group of 1, 2, 4 or 8
 // costs the same, and scores and weights stay in registers. (For tcgen05 a
@@ -87,10 +87,14 @@ constexpr int kJoinWide = 64, kJoinWidth = 16;
 // last three stay in even shares; with 10, e4m3 40 to 2000 of 64 goes in teams and
 // takes 23.0 for 20.8.
 constexpr int kTeamGain = 6;
-constexpr float kLazy = 8.f;     // m is raised when a score passes it by this (log2)
-// fp16 weights are 2^(x' - m + 7): at most 2^15, inside the type's range, and
-// 2^-32 of the largest one is still held. bf16 has fp32's range: no lift.
-constexpr float kLiftF16 = 7.f;
+// m is raised when a score passes it by kLazy (log2). bf16 weights have fp32's
+// range. fp16 weights are 2^13 2^(x' - m): at most 2^15, inside the type's range,
+// and what lies above 2^-38 of the largest one is held, so that the weights of
+// 16k rows together lose less than one fp32 rounding of it (with 8 and 2^7, 2^-32,
+// at the same time; with 1 and 2^14 8-bit caches take 0.5% longer). They are
+// scaled after the exponential: added to x' - m, 13 would round its last bits
+// away (twice as many outputs differ from the exact ones; 8-bit caches save 0.3%).
+constexpr float kLazyBf16 = 8.f, kLazyF16 = 2.f, kLiftF16 = 8192.f;
 
 template <bool E4M3, int D>
 struct CacheAttnShape {
@@ -265,7 +269,7 @@ template <typename T, bool E4M3, int D>
 __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_attn_kernel(const CacheAttnParams p) {
   using Sh = CacheAttnShape<E4M3, D>;
   constexpr bool kBf16 = !E4M3 && Storage<T>::kBf16;  // type of the matrix operands
-  constexpr float kLift = kBf16 ? 0.f : kLiftF16;
+  constexpr float kLift = kBf16 ? 1.f : kLiftF16, kLazy = kBf16 ? kLazyBf16 : kLazyF16;
   constexpr int kPieces = kBf16 ? 3 : 2;  // of a weight
   constexpr int kW = Sh::kWarps, kS = Sh::kStages, kSteps = D / 16, kRows = Sh::kRows, kHalves = kRows / 16;
   constexpr uint32_t kFull = 0xffffffffu >> (32 - kRows);
@@ -708,7 +712,7 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
         }
       }
     }
-    float o[kSteps][4], m0 = -INFINITY, m1 = -INFINITY, lift0 = kLift, lift1 = kLift, l0 = 0.f, l1 = 0.f;
+    float o[kSteps][4], m0 = -INFINITY, m1 = -INFINITY, base0 = 0.f, base1 = 0.f, l0 = 0.f, l1 = 0.f;
 #pragma unroll
     for (int k = 0; k < kSteps; ++k) o[k][0] = o[k][1] = o[k][2] = o[k][3] = 0.f;
 
@@ -782,8 +786,8 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
         const float c0 = a0 == m0 ? 1.f : fast_exp2(m0 - a0), c1 = a1 == m1 ? 1.f : fast_exp2(m1 - a1);
         m0 = a0;
         m1 = a1;
-        lift0 = kLift - (m0 == -INFINITY ? 0.f : m0);
-        lift1 = kLift - (m1 == -INFINITY ? 0.f : m1);
+        base0 = m0 == -INFINITY ? 0.f : m0;
+        base1 = m1 == -INFINITY ? 0.f : m1;
         l0 *= c0;
         l1 *= c1;
 #pragma unroll
@@ -797,10 +801,10 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
       uint32_t pw[kHalves][2][kPieces];  // weights as the right operand, in pieces
 #pragma unroll
       for (int i = 0; i < kHalves; ++i) {
-        x[i][0] = fast_exp2(x[i][0] + lift0);
-        x[i][1] = fast_exp2(x[i][1] + lift1);
-        x[i][2] = fast_exp2(x[i][2] + lift0);
-        x[i][3] = fast_exp2(x[i][3] + lift1);
+        x[i][0] = fast_exp2(x[i][0] - base0) * kLift;
+        x[i][1] = fast_exp2(x[i][1] - base1) * kLift;
+        x[i][2] = fast_exp2(x[i][2] - base0) * kLift;
+        x[i][3] = fast_exp2(x[i][3] - base1) * kLift;
         l0 += x[i][0] + x[i][2];
         l1 += x[i][1] + x[i][3];
         if (bad[i]) l0 = l1 = NAN;  // a page outside the pool: these heads become NaN
@@ -835,7 +839,7 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
         // elements 2 gr and 2 gr + 1. The scale multiplies the sum of the
         // pieces that share it (and takes the lift out of it: V may be as large
         // as fp32 holds).
-        const float vs0 = scales[1] * (1.f / (1 << (int)kLift)), vs1 = scales[3] * (1.f / (1 << (int)kLift));
+        const float vs0 = scales[1] * (1.f / kLift), vs1 = scales[3] * (1.f / kLift);
         const bool apart = vs0 != vs1;
 #pragma unroll
         for (int k = 0; k < kSteps; k += 2) {
@@ -872,8 +876,8 @@ __global__ void __launch_bounds__(CacheAttnShape<E4M3, D>::kThreads, 1) cache_at
 
     // --- join the warps' states
     if constexpr (E4M3) {
-      l0 *= 1.f / (1 << (int)kLift);
-      l1 *= 1.f / (1 << (int)kLift);
+      l0 *= 1.f / kLift;
+      l1 *= 1.f / kLift;
     }
 #pragma unroll
     for (int i = 4; i < 32; i <<= 1) {

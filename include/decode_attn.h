@@ -452,7 +452,7 @@ DA_API size_t decode_attn_paged_workspace_size(int n_head, int n_kv_head, int he
  * (the last `window` rows, the query's own among them, and the first `sinks`
  * ones), and out[b, h, :] = softmax_j(scale <q[b, h], K_j>) V_j over those
  * rows, fp32 arithmetic, rounded once. (Over fp16 and 8-bit caches a softmax
- * weight keeps 22 bits, and what lies above 2^-32 of the largest one of its
+ * weight keeps 22 bits, and what lies above 2^-38 of the largest one of its
  * head; over bf16 caches all 24. Over 8-bit pages a bf16 query keeps what lies
  * above 2^-25 of its head's largest element.) Rows that are not visible are not
  * read; NaN among the visible ones reaches the heads that read it, and an

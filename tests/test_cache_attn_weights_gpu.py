@@ -11,9 +11,9 @@ pytestmark = pytest.mark.gpu
 
 TYPES = {"f16": torch.float16, "bf16": torch.bfloat16}
 # What a weight w = 2^x may be off by, relative: the base-2 exponential 2^-22,
-# and the two roundings of x, |x| < 2 (fp16: x + 7, below 8, half a step of
-# 2^-21), times ln 2; two pieces of fp16 leave 2^-23, three of bf16 nothing.
-WEIGHT = {"bf16": 2.0 ** -22 + 0.7 * 2 * 2.0 ** -24, "f16": 2.0 ** -22 + 0.7 * (2.0 ** -24 + 2.0 ** -22) + 2.0 ** -23}
+# and the two roundings of x, |x| < 2, times ln 2; two pieces of fp16 leave 2^-23,
+# three of bf16 nothing.
+WEIGHT = {"bf16": 2.0 ** -22 + 0.7 * 2 * 2.0 ** -24, "f16": 2.0 ** -22 + 0.7 * 2 * 2.0 ** -24 + 2.0 ** -23}
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -87,3 +87,32 @@ def test_long_sums_that_cancel(dtype):
     slack = 6 * (2.0 ** -46 * running.square() / 12).sum(-1).sqrt() + 3 * 2.0 ** -23
     slack = slack[..., None].expand(-1, -1, D)
     R.assert_rows(out, torch.zeros(B, Hkv * G, D).double(), slack, "sums that cancel")
+
+
+@pytest.mark.parametrize("eight", [False, True], ids=["16bit", "e4m3"])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("rows", [2, 6, 40])
+def test_rows_beside_a_sink_without_a_value(rows, dtype, eight):
+    """One row takes nearly all of the weight, and its value is 0: the output is
+    what the others have, of weights around 2^-24. A score below 2^5 errs by half
+    a step of 2^-19 and by log2 e, which 32 bits hold to 2^-26, the base-2
+    exponential by 2^-22; 16-bit pieces leave 2^-38 of the largest weight."""
+    dt, B, H, D = TYPES[dtype], 24, 8, 64
+    q, k, v = torch.zeros(B, H, D), torch.zeros(B, 1, 48, D), torch.zeros(B, 1, 48, D)
+    q[..., 2] = (1 + torch.arange(B * H) / 512).view(B, H).to(dt).float()
+    key = -torch.tensor([15.0, 16.0])[torch.randint(0, 2, (B, rows - 1), generator=torch.Generator().manual_seed(rows))]
+    k[:, 0, 1:rows, 2], v[:, 0, 1:rows] = key, 1.0
+    x = q[..., 2, None].double() * k[:, :, :rows, 2].double()
+    p = torch.softmax(x, -1)
+    ref = p[..., 1:].sum(-1, keepdim=True).expand(B, H, D)
+    weight = 2.0 ** -22 + 0.7 * (2.0 ** -20 + 32 * 2.0 ** -26)
+    slack = ref * (weight + (rows / 16 + 4) * 2.0 ** -23) + (rows - 1) * 2.0 ** -38
+    store = R.E4M3 if eight else dt
+    pools = [t.view(B, 1, 3, 16, D).transpose(1, 2).reshape(B * 3, 1, 16, D).contiguous().to(store).cuda() for t in (k, v)]
+    assert torch.equal(pools[0].float().cpu().view(B, 48, D), k[:, 0])
+    if eight:
+        pools += [torch.ones(B * 3, 1, device="cuda") for _ in range(2)]
+    table = torch.arange(B * 3, dtype=torch.int32, device="cuda").view(B, 3)
+    n = torch.full((B,), rows, dtype=torch.int32, device="cuda")
+    attend = da.decode_attn_paged_q8_fwd if eight else da.decode_attn_paged_fwd
+    R.assert_rows(attend(q.to(dt).cuda(), *pools, table, n, scale=1.0), ref, slack, f"{rows} rows")
