@@ -458,6 +458,8 @@ DA_API size_t decode_attn_paged_workspace_size(int n_head, int n_kv_head, int he
  * read; NaN among the visible ones reaches the heads that read it, and an
  * infinite element of V makes that element of its heads' outputs infinite or
  * NaN (a weight reaches V in pieces, and a piece may be zero or negative).
+ * The weighted sums are held unnormalised: over bf16 and 8-bit caches kv_len
+ * times the largest |V| stays below 2^120, or they may overflow.
  * kv_len[b] == 0 (an idle slot of a batch) gives a row of zeros;
  * kv_len[b] < 0 or > max_pages * page_size gives NaN and DA_DEVERR_KV_LEN; a
  * page id outside the pool gives NaN for the heads that would read it and

@@ -5,6 +5,7 @@ import torch
 
 import decode_attention_static_gb300 as da
 import paged_reference as R
+import test_paged_attention_gpu as T
 
 pytestmark = pytest.mark.gpu
 
@@ -102,3 +103,26 @@ def test_no_row_has_a_weight(dtype, static):
     q, k, v = inputs(dtype, lens, H, Hkv, D, 8)
     q[..., 0], k[:, :, :, 0] = q[..., 0].abs() + 1, -float("inf")
     assert attend(q, k, v, lens, static).isnan().all()
+
+
+@CASES
+@pytest.mark.parametrize("lens", [[700, 33], [90] * 160])
+def test_large_values_do_not_overflow(lens, static):
+    """Values of 2^106 over 700 rows, with scores that spread over 2^30: every sum
+    stays in range, whatever the running reference is."""
+    q, k, v = inputs("bf16", lens, 8, 2, 64, 9)
+    q, v = (q.float() * 4).bfloat16(), (v.double() * 2.0 ** 106).bfloat16()
+    assert v.nan_to_num().abs().max().double() * max(lens) < 2.0 ** 120
+    want, got = reference(q, k, v, lens), attend(q, k, v, lens, static)
+    for b, (ref, slack) in enumerate(want):
+        R.assert_rows(got[b], ref, slack, f"{b}")
+
+
+@pytest.mark.parametrize("lens", [[700, 33], [90] * 160])
+def test_large_scales_do_not_overflow(lens):
+    """The same with 8-bit pages whose V scales are 2^98 to 2^101."""
+    case = T.Case(lens, 8, 2, 64, "bf16", 16, True, seed=10, spread=4.0)
+    up = 2.0 ** 106
+    case.vs = (case.vs.double() * up).float()
+    case.ref, case.slack = case.ref * up, case.slack * up
+    T.check(case, "large scales")
