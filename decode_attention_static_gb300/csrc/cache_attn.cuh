@@ -44,7 +44,7 @@
 // sums.
 //
 // Measured (graph of calls, data from HBM, of the measured 6782 GB/s copy): 32
-// ragged sequences up to 32768 rows, 32 / 8 heads, 2.04 GB in 298 us (101%),
+// ragged sequences up to 32768 rows, 32 / 8 heads, 2.04 GB in 297 us (101%),
 // in 8 bits 1.02 GB in 153 us (98%); 8 ragged up to 8191, 16 / 8 heads, 159 MB
 // in 30.2 us (78%); 16 ragged with window 1021 and 16 / 8 heads, 68 MB in 13.0
 // us (77%); window 4096 in 8 bits, 16 ragged, 64 / 8 heads, 135 MB in 26.3 us
