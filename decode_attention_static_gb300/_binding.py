@@ -27,6 +27,13 @@ DA_DEVERR_POSITION = 2
 DA_DEVERR_TIMEOUT = 4
 DA_DEVERR_WORKSPACE = 8
 DA_DEVERR_PAGE = 16
+DA_DEVERR_TOKENS = 32
+DA_DEVERR_SEQUENCE = 64
+DA_DEVERR_FULL = 128
+DA_DEVERR_POOL = 256
+DA_MAX_ROPE_AXES = 4
+DA_TREE_MAX_TOKENS = 256
+DA_POOL_HEADER = 4
 
 _DTYPE_CODE = {torch.float16: DA_F16, torch.bfloat16: DA_BF16}
 
@@ -76,6 +83,17 @@ _SIGNATURES = {
     "decode_attn_paged_fwd": ([_vp] * 5 + [_i] * 9 + [ctypes.c_float, _vp, _vp, ctypes.c_size_t, _i, _vp, _vp], _i),
     "decode_attn_paged_q8_fwd": ([_vp] * 7 + [_i] * 9 + [ctypes.c_float, _vp, _vp, ctypes.c_size_t, _i, _vp, _vp], _i),
     "decode_attn_window_fwd": ([_vp] * 4 + [_i] * 7 + [ctypes.c_float, _vp, _vp, ctypes.c_size_t, _i, _vp, _vp], _i),
+    "kvcache_append_paged_axes": ([_vp] * 8 + [_i] + [_vp] * 2 + [_i] + [_vp] * 3 + [_i] * 9 + [_vp, _vp], _i),
+    "kvcache_append_paged_q8_axes": ([_vp] * 10 + [_i] + [_vp] * 2 + [_i] + [_vp] * 3 + [_i] * 9 + [_vp, _vp], _i),
+    "decode_attn_tree_workspace_size": ([_i, _i, _i], ctypes.c_size_t),
+    "decode_attn_tree_fwd": ([_vp] * 7 + [_i] * 9 + [ctypes.c_float, _vp, _vp, ctypes.c_size_t, _i, _vp, _vp], _i),
+    "decode_attn_tree_q8_fwd": ([_vp] * 9 + [_i] * 9 + [ctypes.c_float, _vp, _vp, ctypes.c_size_t, _i, _vp, _vp], _i),
+    "kvcache_pool_init": ([_vp, _i, _vp], _i),
+    "kvcache_resize_paged": ([_vp] * 4 + [_i] * 4 + [_vp, _vp], _i),
+    "kvcache_fork_paged": ([_vp] * 6 + [_i] * 5 + [_vp, _vp], _i),
+    "kvcache_copy_pages": ([_vp] * 5 + [_i] * 7 + [_vp, _vp], _i),
+    "kvcache_compact_paged": ([_vp] * 6 + [_i] * 8 + [_vp, _vp], _i),
+    "kvcache_compact_paged_q8": ([_vp] * 8 + [_i] * 8 + [_vp, _vp], _i),
 }
 
 
@@ -583,7 +601,7 @@ def _explain_err_flag(err_flag):
 
 
 def _explain_append(k_pages, v_pages, k_scale, v_scale, eight, k_new, v_new, page_table, position_ids, token_start,
-                    rope_cos, rope_sin, q, q_out, err_flag):
+                    rope_cos, rope_sin, q, q_out, err_flag, turns=None):
     _cuda_contig("k_new", k_new)
     _code_for(k_new.dtype)
     _explain_pool(k_pages, v_pages, k_scale, v_scale, k_new.dtype, eight)
@@ -609,15 +627,26 @@ def _explain_append(k_pages, v_pages, k_scale, v_scale, eight, k_new, v_new, pag
     else:
         _require(q_out is None, "q_out comes with q")
     _explain_err_flag(err_flag)
+    others = {}
+    if turns is not None:
+        rope_position_ids, rope_axis = turns
+        _require(rope_cos is not None, "rotary positions need the rope tables")
+        _require(rope_position_ids.dtype == torch.int32 and rope_position_ids.dim() == 2
+                 and 1 <= rope_position_ids.shape[0] <= DA_MAX_ROPE_AXES
+                 and rope_position_ids.shape[1] == k_new.shape[0],
+                 f"rope_position_ids must be int32 [axes, tokens], at most {DA_MAX_ROPE_AXES} axes")
+        _require(rope_axis is None or (rope_axis.dtype == torch.int32 and rope_axis.numel() == D // 2),
+                 "rope_axis must be int32 [D / 2]")
+        others = dict(rope_position_ids=rope_position_ids, rope_axis=rope_axis)
     _explain_device(k_new.get_device(), dict(
         v_new=v_new, k_pages=k_pages, v_pages=v_pages, k_scale=k_scale, v_scale=v_scale, page_table=page_table,
         position_ids=position_ids, token_start=token_start, rope_cos=rope_cos, rope_sin=rope_sin, q=q, q_out=q_out,
-        err_flag=err_flag))
+        err_flag=err_flag, **others))
     raise ValueError("inconsistent arguments")
 
 
 def _append_paged(fn, k_pages, v_pages, k_scale, v_scale, eight, k_new, v_new, page_table, position_ids, token_start,
-                  rope_cos, rope_sin, q, q_out, err_flag):
+                  rope_cos, rope_sin, q, q_out, err_flag, turns=None):
     dtype, pool, new, table = k_new.dtype, k_pages.shape, k_new.shape, page_table.shape
     code, store = _DTYPE_CODE.get(dtype), _E4M3 if eight else dtype
     ix = k_new.get_device()
@@ -658,10 +687,21 @@ def _append_paged(fn, k_pages, v_pages, k_scale, v_scale, eight, k_new, v_new, p
                 ok = (q_out.shape == qs and q_out.dtype == dtype and q_out.get_device() == ix
                       and q_out.is_contiguous())
             n_head, q_ptr, out_ptr = qs[1], q.data_ptr(), q_out.data_ptr()
+    turn_args = ()
+    if ok and turns is not None:
+        rows, axis = turns
+        ok = (rope_cos is not None and rows.dtype == _I32 and rows.dim() == 2
+              and 1 <= rows.shape[0] <= DA_MAX_ROPE_AXES and rows.shape[1] == new[0] and rows.get_device() == ix
+              and rows.is_contiguous()
+              and (axis is None or (axis.dtype == _I32 and axis.numel() == new[2] // 2 and axis.get_device() == ix
+                                    and axis.is_contiguous())))
+        if ok:
+            turn_args = (rows.data_ptr(), None if axis is None else axis.data_ptr(), rows.shape[0])
     if not ok:
         _explain_append(k_pages, v_pages, k_scale, v_scale, eight, k_new, v_new, page_table, position_ids,
-                        token_start, rope_cos, rope_sin, q, q_out, err_flag)
-    tail = (k_new.data_ptr(), v_new.data_ptr(), q_ptr, out_ptr, cos_ptr, sin_ptr, rope_rows, page_table.data_ptr(),
+                        token_start, rope_cos, rope_sin, q, q_out, err_flag, turns)
+    tail = (k_new.data_ptr(), v_new.data_ptr(), q_ptr, out_ptr, cos_ptr, sin_ptr, rope_rows, *turn_args,
+            page_table.data_ptr(),
             position_ids.data_ptr(), None if token_start is None else token_start.data_ptr(), table[0], new[0],
             n_head, pool[1], pool[3], pool[0], pool[2], table[1], code,
             None if err_flag is None else err_flag.data_ptr(), _raw_stream(ix))
@@ -853,3 +893,293 @@ def decode_attn_window_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torc
              workspace.numel() * workspace.element_size(), code, None if err_flag is None else err_flag.data_ptr(),
              _raw_stream(ix))
     return out
+
+
+def kvcache_append_paged_axes(k_pages: torch.Tensor, v_pages: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
+                              page_table: torch.Tensor, position_ids: torch.Tensor, rope_position_ids: torch.Tensor,
+                              rope_cos: torch.Tensor, rope_sin: torch.Tensor, rope_axis: torch.Tensor | None = None,
+                              token_start: torch.Tensor | None = None, q: torch.Tensor | None = None,
+                              q_out: torch.Tensor | None = None,
+                              err_flag: torch.Tensor | None = None) -> torch.Tensor | None:
+    """kvcache_append_paged with rotary positions of their own: element pair i
+    of token t is rotated by row rope_position_ids[rope_axis[i], t] of the
+    tables (rope_position_ids int32 [axes, tokens], at most 4 axes; rope_axis
+    int32 [D / 2], None: the first axis for all)."""
+    return _append_paged("kvcache_append_paged_axes", k_pages, v_pages, None, None, False, k_new, v_new, page_table,
+                         position_ids, token_start, rope_cos, rope_sin, q, q_out, err_flag,
+                         (rope_position_ids, rope_axis))
+
+
+def kvcache_append_paged_q8_axes(k_pages: torch.Tensor, v_pages: torch.Tensor, k_scale: torch.Tensor,
+                                 v_scale: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
+                                 page_table: torch.Tensor, position_ids: torch.Tensor,
+                                 rope_position_ids: torch.Tensor, rope_cos: torch.Tensor, rope_sin: torch.Tensor,
+                                 rope_axis: torch.Tensor | None = None, token_start: torch.Tensor | None = None,
+                                 q: torch.Tensor | None = None, q_out: torch.Tensor | None = None,
+                                 err_flag: torch.Tensor | None = None) -> torch.Tensor | None:
+    """kvcache_append_paged_axes into float8_e4m3fn pools with their scales."""
+    return _append_paged("kvcache_append_paged_q8_axes", k_pages, v_pages, k_scale, v_scale, True, k_new, v_new,
+                         page_table, position_ids, token_start, rope_cos, rope_sin, q, q_out, err_flag,
+                         (rope_position_ids, rope_axis))
+
+
+def decode_attn_tree_workspace_size(n_head: int, n_kv_head: int, head_dim: int) -> int:
+    """Scratch bytes of one tree attention call on the current device (the same
+    for every batch, length, tree and page size)."""
+    n = load_library().decode_attn_tree_workspace_size(n_head, n_kv_head, head_dim)
+    if n == ctypes.c_size_t(-1).value:
+        raise DecodeAttnError("decode_attn_tree_workspace_size", -2, "invalid sizes or device query failed")
+    return int(n)
+
+
+def alloc_tree_workspace(n_head: int, n_kv_head: int, head_dim: int, device=None) -> torch.Tensor:
+    """A zero-filled device byte buffer of decode_attn_tree_workspace_size() bytes (torch owns it)."""
+    with torch.cuda.device(device):
+        n = decode_attn_tree_workspace_size(n_head, n_kv_head, head_dim)
+    return torch.zeros(max(n, 16), dtype=torch.uint8, device=device or "cuda")
+
+
+def _explain_tree(q, k_pages, v_pages, k_scale, v_scale, eight, page_table, kv_len, token_start, tree_mask, out,
+                  workspace, err_flag):
+    _cuda_contig("q", q)
+    _require(q.dim() == 3, "q must be [tokens, n_head, D]")
+    _code_for(q.dtype)
+    _explain_pool(k_pages, v_pages, k_scale, v_scale, q.dtype, eight)
+    _require(k_pages.shape[3] == q.shape[2], "head_dim of the pages must match q")
+    _require(page_table.dtype == torch.int32 and page_table.dim() == 2, "page_table must be int32 [B, max_pages]")
+    B = page_table.shape[0]
+    _require(kv_len.dtype == torch.int32 and kv_len.numel() == B, "kv_len must be int32 [B]")
+    if token_start is not None:
+        _require(token_start.dtype == torch.int32 and token_start.numel() == B + 1, "token_start must be int32 [B + 1]")
+    else:
+        _require(q.shape[0] == B, "without token_start there is one token per sequence")
+    _require(tree_mask is None or (tree_mask.dtype == torch.int64 and tree_mask.dim() == 2
+                                   and tree_mask.shape[0] == q.shape[0]
+                                   and 1 <= tree_mask.shape[1] <= DA_TREE_MAX_TOKENS // 64),
+             "tree_mask must be int64 [tokens, words], at most 4 words")
+    _require(out.shape == q.shape and out.dtype == q.dtype, "out must match q")
+    _explain_err_flag(err_flag)
+    _explain_device(q.get_device(), dict(
+        k_pages=k_pages, v_pages=v_pages, k_scale=k_scale, v_scale=v_scale, page_table=page_table, kv_len=kv_len,
+        token_start=token_start, tree_mask=tree_mask, out=out, workspace=workspace, err_flag=err_flag))
+    raise ValueError("inconsistent arguments")
+
+
+def _attn_tree(fn, q, k_pages, v_pages, k_scale, v_scale, eight, page_table, kv_len, token_start, tree_mask, out,
+               scale, workspace, err_flag):
+    dtype, shape, pool, table = q.dtype, q.shape, k_pages.shape, page_table.shape
+    code, store, ix = _DTYPE_CODE.get(dtype), _E4M3 if eight else dtype, q.get_device()
+    if out is None:
+        out = torch.empty_like(q)
+    if not (ix >= 0 and code is not None and len(shape) == 3 and len(pool) == 4 and len(table) == 2
+            and pool[3] == shape[2] and v_pages.shape == pool and k_pages.dtype == store and v_pages.dtype == store
+            and page_table.dtype == _I32 and kv_len.dtype == _I32 and kv_len.numel() == table[0]
+            and out.shape == shape and out.dtype == dtype
+            and k_pages.get_device() == ix and v_pages.get_device() == ix and page_table.get_device() == ix
+            and kv_len.get_device() == ix and out.get_device() == ix and q.is_contiguous()
+            and k_pages.is_contiguous() and v_pages.is_contiguous() and page_table.is_contiguous()
+            and kv_len.is_contiguous() and out.is_contiguous()
+            and (shape[0] == table[0] if token_start is None else
+                 (token_start.dtype == _I32 and token_start.numel() == table[0] + 1
+                  and token_start.get_device() == ix and token_start.is_contiguous()))
+            and (tree_mask is None or (tree_mask.dtype == torch.int64 and tree_mask.dim() == 2
+                                       and tree_mask.shape[0] == shape[0]
+                                       and 1 <= tree_mask.shape[1] <= DA_TREE_MAX_TOKENS // 64
+                                       and tree_mask.get_device() == ix and tree_mask.is_contiguous()))
+            and (workspace is None or (workspace.get_device() == ix and workspace.is_contiguous()))
+            and (not eight or (k_scale.dtype == _F32 and v_scale.dtype == _F32
+                               and k_scale.shape == pool[:2] and v_scale.shape == pool[:2]
+                               and k_scale.get_device() == ix and v_scale.get_device() == ix
+                               and k_scale.is_contiguous() and v_scale.is_contiguous()))
+            and (err_flag is None or (err_flag.dtype == _I32 and err_flag.numel() >= 1
+                                      and err_flag.get_device() == ix and err_flag.is_contiguous()))):
+        _explain_tree(q, k_pages, v_pages, k_scale, v_scale, eight, page_table, kv_len, token_start, tree_mask, out,
+                      workspace, err_flag)
+    if workspace is None:
+        workspace = alloc_tree_workspace(shape[1], pool[1], shape[2], q.device)
+    tail = (page_table.data_ptr(), kv_len.data_ptr(), None if token_start is None else token_start.data_ptr(),
+            None if tree_mask is None else tree_mask.data_ptr(), 0 if tree_mask is None else tree_mask.shape[1],
+            table[0], shape[0], shape[1], pool[1], shape[2], pool[0], pool[2], table[1],
+            shape[2] ** -0.5 if scale is None else float(scale), out.data_ptr(), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), code, None if err_flag is None else err_flag.data_ptr(),
+            _raw_stream(ix))
+    if eight:
+        _call_on(fn, ix, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(),
+                 v_scale.data_ptr(), *tail)
+    else:
+        _call_on(fn, ix, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), *tail)
+    return out
+
+
+def decode_attn_tree_fwd(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor,
+                         kv_len: torch.Tensor, token_start: torch.Tensor | None = None,
+                         tree_mask: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                         scale: float | None = None, workspace: torch.Tensor | None = None,
+                         err_flag: torch.Tensor | None = None) -> torch.Tensor:
+    """Attention of several new tokens of each sequence over a paged cache that
+    holds their rows already: q [tokens, n_head, D] packed, sequence b owning
+    tokens [token_start[b], token_start[b + 1]) (None: one each), which are the
+    last of its kv_len[b] rows. A token sees every row before them, and of them
+    those whose bit is set in its row of tree_mask (int64 [tokens, words], bit
+    i % 64 of word i / 64 for the sequence's i-th token; None: those up to
+    itself). A workspace comes from alloc_tree_workspace (reuse it)."""
+    return _attn_tree("decode_attn_tree_fwd", q, k_pages, v_pages, None, None, False, page_table, kv_len, token_start,
+                      tree_mask, out, scale, workspace, err_flag)
+
+
+def decode_attn_tree_q8_fwd(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, k_scale: torch.Tensor,
+                            v_scale: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tensor,
+                            token_start: torch.Tensor | None = None, tree_mask: torch.Tensor | None = None,
+                            out: torch.Tensor | None = None, scale: float | None = None,
+                            workspace: torch.Tensor | None = None,
+                            err_flag: torch.Tensor | None = None) -> torch.Tensor:
+    """decode_attn_tree_fwd over float8_e4m3fn pools with their scales float32
+    [num_pages, n_kv_head]."""
+    return _attn_tree("decode_attn_tree_q8_fwd", q, k_pages, v_pages, k_scale, v_scale, True, page_table, kv_len,
+                      token_start, tree_mask, out, scale, workspace, err_flag)
+
+
+def _ints(index: int, **tensors) -> None:
+    """Every given tensor is a contiguous int32 one on device `index`."""
+    for name, (t, shape) in tensors.items():
+        if t is None:
+            continue
+        _require(t.dtype == _I32 and tuple(t.shape) == tuple(shape), lambda: f"{name} must be int32 {list(shape)}")
+        if t.get_device() != index or not t.is_contiguous():
+            _explain_device(index, {name: t})
+
+
+def _pool_pages(pool: torch.Tensor) -> int:
+    """Pages of a pool's state."""
+    _cuda_contig("pool", pool)
+    _require(pool.dtype == _I32 and pool.dim() == 1 and pool.numel() > DA_POOL_HEADER
+             and (pool.numel() - DA_POOL_HEADER) % 2 == 0,
+             f"pool must be int32 [{DA_POOL_HEADER} + 2 * num_pages]")
+    return (pool.numel() - DA_POOL_HEADER) // 2
+
+
+def alloc_page_pool(num_pages: int, device=None) -> torch.Tensor:
+    """State of a pool of num_pages pages, all free, for kvcache_resize_paged and kvcache_fork_paged."""
+    _require(num_pages >= 1, "a pool needs a page")
+    pool = torch.empty(DA_POOL_HEADER + 2 * num_pages, dtype=torch.int32, device=device or "cuda")
+    _call_on("kvcache_pool_init", pool.get_device(), pool.data_ptr(), num_pages, _raw_stream(pool.get_device()))
+    return pool
+
+
+def page_pool_views(pool: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """(free [1], counts [num_pages], list [num_pages]) of a pool's state: views
+    of how many pages are free, how many table entries hold each page, and the
+    free pages (the list's first free[0] entries)."""
+    n = _pool_pages(pool)
+    return pool[:1], pool[DA_POOL_HEADER:DA_POOL_HEADER + n], pool[DA_POOL_HEADER + n:]
+
+
+def kvcache_resize_paged(page_table: torch.Tensor, held_len: torch.Tensor, wanted_len: torch.Tensor,
+                         pool: torch.Tensor, page_size: int, err_flag: torch.Tensor | None = None) -> None:
+    """Sequences whose first held_len[b] rows have pages become sequences of
+    wanted_len[b] rows: pages are released to the pool's state, then taken from
+    it (page_table int32 [B, max_pages], lengths int32 [B], pool from
+    alloc_page_pool; all updated in place)."""
+    pages, ix = _pool_pages(pool), pool.get_device()
+    _require(page_table.dim() == 2, "page_table must be int32 [B, max_pages]")
+    B, most = page_table.shape
+    _ints(ix, page_table=(page_table, (B, most)), held_len=(held_len, (B,)), wanted_len=(wanted_len, (B,)))
+    _err_ptr(err_flag, pool.device)
+    _call_on("kvcache_resize_paged", ix, page_table.data_ptr(), held_len.data_ptr(), wanted_len.data_ptr(),
+             pool.data_ptr(), B, pages, _int32("page_size", page_size), most,
+             None if err_flag is None else err_flag.data_ptr(), _raw_stream(ix))
+
+
+def kvcache_fork_paged(page_table: torch.Tensor, kv_len: torch.Tensor, parent: torch.Tensor, child: torch.Tensor,
+                       pool: torch.Tensor, page_size: int, copies: torch.Tensor | None = None,
+                       err_flag: torch.Tensor | None = None) -> torch.Tensor:
+    """Sequence child[i] becomes a copy of sequence parent[i] (int32 [forks]):
+    whole pages are shared, a partly filled last one is replaced by a page of
+    the pool. Returns copies int32 [3, forks] (source page, target page, rows),
+    for kvcache_copy_pages on every layer's pools; page_table, kv_len and pool
+    are updated in place."""
+    pages, ix = _pool_pages(pool), pool.get_device()
+    _require(page_table.dim() == 2, "page_table must be int32 [B, max_pages]")
+    (B, most), n = page_table.shape, parent.numel()
+    if copies is None:
+        copies = torch.empty((3, n), dtype=torch.int32, device=pool.device)
+    _ints(ix, page_table=(page_table, (B, most)), kv_len=(kv_len, (B,)), parent=(parent, (n,)), child=(child, (n,)),
+          copies=(copies, (3, n)))
+    _err_ptr(err_flag, pool.device)
+    _call_on("kvcache_fork_paged", ix, page_table.data_ptr(), kv_len.data_ptr(), parent.data_ptr(), child.data_ptr(),
+             pool.data_ptr(), copies.data_ptr(), n, B, pages, _int32("page_size", page_size), most,
+             None if err_flag is None else err_flag.data_ptr(), _raw_stream(ix))
+    return copies
+
+
+def _stacked_pools(k_pages, v_pages, k_scale, v_scale):
+    """(layers, pages, heads, page size, D, element size) of the pools of one
+    layer [num_pages, ...] or of several [layers, num_pages, ...]."""
+    _cuda_contig("k_pages", k_pages)
+    _on(k_pages.device, v_pages=v_pages)
+    _require(k_pages.dim() in (4, 5) and v_pages.shape == k_pages.shape and v_pages.dtype == k_pages.dtype,
+             "k_pages/v_pages must be [num_pages, n_kv_head, page_size, D], with a leading layer axis or without")
+    if k_pages.dtype not in (torch.float16, torch.bfloat16, _E4M3):
+        raise TypeError(f"pages of {k_pages.dtype} are not supported (float16, bfloat16 or float8_e4m3fn)")
+    _require((k_scale is None) == (v_scale is None), "k_scale and v_scale come together")
+    if k_scale is not None:
+        _on(k_pages.device, k_scale=k_scale, v_scale=v_scale)
+        _require(k_pages.dtype == _E4M3, "scales come with pages of float8_e4m3fn")
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            _require(t.dtype == _F32 and t.shape == k_pages.shape[:-2], lambda: f"{name} must be float32 "
+                     f"{list(k_pages.shape[:-2])}")
+    layers = k_pages.shape[0] if k_pages.dim() == 5 else 1
+    return (layers, *k_pages.shape[-4:], k_pages.element_size())
+
+
+def kvcache_copy_pages(k_pages: torch.Tensor, v_pages: torch.Tensor, copies: torch.Tensor,
+                       k_scale: torch.Tensor | None = None, v_scale: torch.Tensor | None = None,
+                       err_flag: torch.Tensor | None = None) -> None:
+    """Copy rows [0, copies[2, i]) of page copies[0, i] to page copies[1, i] in
+    the pools of one layer or (with a leading layer axis) of several, in place;
+    pages of 8 bits with their scales. Entries below 0 are skipped."""
+    layers, pages, Hkv, size, D, element = _stacked_pools(k_pages, v_pages, k_scale, v_scale)
+    _require(copies.dim() == 2 and copies.shape[0] == 3, "copies must be int32 [3, n]")
+    n, ix = copies.shape[1], k_pages.get_device()
+    _ints(ix, copies=(copies, (3, n)))
+    _err_ptr(err_flag, k_pages.device)
+    _call_on("kvcache_copy_pages", ix, k_pages.data_ptr(), v_pages.data_ptr(),
+             None if k_scale is None else k_scale.data_ptr(), None if v_scale is None else v_scale.data_ptr(),
+             copies.data_ptr(), n, layers, pages, Hkv, size, D, element,
+             None if err_flag is None else err_flag.data_ptr(), _raw_stream(ix))
+
+
+def _compact(fn, k_pages, v_pages, k_scale, v_scale, eight, page_table, keep, keep_start, position_ids, err_flag):
+    if (k_pages.dtype == _E4M3) != eight:
+        raise TypeError("pages must be float8_e4m3fn" if eight else "pages must be float16 or bfloat16")
+    layers, pages, Hkv, size, D, _ = _stacked_pools(k_pages, v_pages, k_scale, v_scale)
+    _require(page_table.dim() == 2, "page_table must be int32 [B, max_pages]")
+    (B, most), ix = page_table.shape, k_pages.get_device()
+    _ints(ix, page_table=(page_table, (B, most)), keep=(keep, (keep.numel(),)), keep_start=(keep_start, (B + 1,)),
+          position_ids=(position_ids, (B,)))
+    _err_ptr(err_flag, k_pages.device)
+    scales = (k_scale.data_ptr(), v_scale.data_ptr()) if eight else ()
+    _call_on(fn, ix, k_pages.data_ptr(), v_pages.data_ptr(), *scales, page_table.data_ptr(), keep.data_ptr(),
+             keep_start.data_ptr(), position_ids.data_ptr(), B, keep.numel(), layers, Hkv, D, pages, size, most,
+             None if err_flag is None else err_flag.data_ptr(), _raw_stream(ix))
+
+
+def kvcache_compact_paged(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor, keep: torch.Tensor,
+                          keep_start: torch.Tensor, position_ids: torch.Tensor,
+                          err_flag: torch.Tensor | None = None) -> None:
+    """Move row keep[keep_start[b] + i] of sequence b to row position_ids[b] + i
+    (rising rows, none moves up), in the pools of one layer or (with a leading
+    layer axis) of several, in place: accepted drafts behind the prefix."""
+    _compact("kvcache_compact_paged", k_pages, v_pages, None, None, False, page_table, keep, keep_start, position_ids,
+             err_flag)
+
+
+def kvcache_compact_paged_q8(k_pages: torch.Tensor, v_pages: torch.Tensor, k_scale: torch.Tensor,
+                             v_scale: torch.Tensor, page_table: torch.Tensor, keep: torch.Tensor,
+                             keep_start: torch.Tensor, position_ids: torch.Tensor,
+                             err_flag: torch.Tensor | None = None) -> None:
+    """kvcache_compact_paged over float8_e4m3fn pools: a page that takes rows of
+    pages with larger scales gets the largest one, its rows rounded to it."""
+    _require(k_scale is not None and v_scale is not None, "pages of 8 bits need their scales")
+    _compact("kvcache_compact_paged_q8", k_pages, v_pages, k_scale, v_scale, True, page_table, keep, keep_start,
+             position_ids, err_flag)

@@ -67,9 +67,71 @@ __device__ __forceinline__ void load_f32x4(const float* from, float (&out)[4]) {
   out[3] = __uint_as_float(v.w);
 }
 
+// Table rows of one token with positions on several axes (AX): element pairs
+// (i, i + D / 2) of axis a turn by the table row at[a].
+struct TurnRows {
+  int at[kMaxRopeAxes];
+  // The rows of token t; false when one is not in the tables.
+  __device__ __forceinline__ bool load(const AppendPagedParams& p, int t) {
+    bool ok = true;
+#pragma unroll
+    for (int a = 0; a < kMaxRopeAxes; ++a) {
+      at[a] = a < p.axes ? p.turn[(int64_t)a * p.tokens + t] : at[0];
+      ok = ok && at[a] >= 0 && at[a] < p.rope_rows;
+    }
+    return ok;
+  }
+  __device__ __forceinline__ int of(int axis) const {
+    int r = at[0];
+#pragma unroll
+    for (int a = 1; a < kMaxRopeAxes; ++a) r = axis == a ? at[a] : r;
+    return r;
+  }
+};
+
+// Axes of four pairs from pair i on (a multiple of four): an axis outside [0,
+// axes) counts as the first (the kernels' first units report it).
+__device__ __forceinline__ int4 pair_axes(const AppendPagedParams& p, int i) {
+  return p.axis ? __ldg(reinterpret_cast<const int4*>(p.axis + i)) : make_int4(0, 0, 0, 0);
+}
+__device__ __forceinline__ bool one_axis(const int4& a) { return a.x == a.y && a.x == a.z && a.x == a.w; }
+
+// Four elements at column `col` of a table, for pairs of axes `a`: one vector
+// where the pairs share an axis (sections of whole vectors), else gathered.
+__device__ __forceinline__ void load_turn4(const float* table, int D, const TurnRows& rows, const int4& a, int col,
+                                           float (&out)[4]) {
+  if (one_axis(a)) {
+    load_f32x4(table + (int64_t)rows.of(a.x) * D + col, out);
+  } else {
+    out[0] = __ldg(table + (int64_t)rows.of(a.x) * D + col);
+    out[1] = __ldg(table + (int64_t)rows.of(a.y) * D + col + 1);
+    out[2] = __ldg(table + (int64_t)rows.of(a.z) * D + col + 2);
+    out[3] = __ldg(table + (int64_t)rows.of(a.w) * D + col + 3);
+  }
+}
+
+// The first CTA's threads report axes outside [0, axes).
+__device__ __forceinline__ void check_axes(const AppendPagedParams& p) {
+  if (blockIdx.x == 0 && p.err_flag && p.axis && (int)threadIdx.x < p.head_dim / 2) {
+    const int a = p.axis[threadIdx.x];
+    if (a < 0 || a >= p.axes) atomicOr(p.err_flag, kErrPosition);
+  }
+}
+
 // cos and sin of one row at a lane's two vectors.
 struct RopeRow {
   float c0[8], s0[8], c1[8], s1[8];
+  __device__ __forceinline__ void load_axes(const AppendPagedParams& p, const TurnRows& rows, int c) {
+    const int D = p.head_dim;
+#pragma unroll
+    for (int e = 0; e < 8; e += 4) {
+      const int4 a = pair_axes(p, 8 * c + e);
+      load_turn4(p.cos, D, rows, a, 8 * c + e, *reinterpret_cast<float(*)[4]>(c0 + e));
+      load_turn4(p.sin, D, rows, a, 8 * c + e, *reinterpret_cast<float(*)[4]>(s0 + e));
+      load_turn4(p.cos, D, rows, a, D / 2 + 8 * c + e, *reinterpret_cast<float(*)[4]>(c1 + e));
+      load_turn4(p.sin, D, rows, a, D / 2 + 8 * c + e, *reinterpret_cast<float(*)[4]>(s1 + e));
+    }
+  }
   __device__ __forceinline__ void load(const AppendPagedParams& p, int position, int c) {
     const int D = p.head_dim;
     load_f32x8(p.cos, position, D, 8 * c, c0);
@@ -94,17 +156,26 @@ struct RopeRow {
 
 // The same for a row's unpacked vectors of N heads, in place; 4 elements at a
 // time, so that few registers hold the table row.
-template <int N>
-__device__ __forceinline__ void rotate_rows(const AppendPagedParams& p, int position, int c, float (&a)[N][8],
-                                            float (&b)[N][8]) {
+template <bool AX, int N>
+__device__ __forceinline__ void rotate_rows(const AppendPagedParams& p, int position, const TurnRows& rows, int c,
+                                            float (&a)[N][8], float (&b)[N][8]) {
   const int64_t at = (int64_t)position * p.head_dim + 8 * c;
 #pragma unroll
   for (int q = 0; q < 8; q += 4) {
     float c0[4], s0[4], c1[4], s1[4];
-    load_f32x4(p.cos + at + q, c0);
-    load_f32x4(p.sin + at + q, s0);
-    load_f32x4(p.cos + at + p.head_dim / 2 + q, c1);
-    load_f32x4(p.sin + at + p.head_dim / 2 + q, s1);
+    if constexpr (AX) {
+      const int D = p.head_dim;
+      const int4 axes = pair_axes(p, 8 * c + q);
+      load_turn4(p.cos, D, rows, axes, 8 * c + q, c0);
+      load_turn4(p.sin, D, rows, axes, 8 * c + q, s0);
+      load_turn4(p.cos, D, rows, axes, D / 2 + 8 * c + q, c1);
+      load_turn4(p.sin, D, rows, axes, D / 2 + 8 * c + q, s1);
+    } else {
+      load_f32x4(p.cos + at + q, c0);
+      load_f32x4(p.sin + at + q, s0);
+      load_f32x4(p.cos + at + p.head_dim / 2 + q, c1);
+      load_f32x4(p.sin + at + p.head_dim / 2 + q, s1);
+    }
 #pragma unroll
     for (int k = 0; k < N; ++k) {
 #pragma unroll
@@ -138,7 +209,7 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
 // token's place is looked up, and the table row serves all of them.
 constexpr int kAtOnce = 6;
 
-template <typename T>
+template <typename T, bool AX>
 __device__ __forceinline__ void move_token(const AppendPagedParams& p, int t, int first, int stride, int c) {
   const int row_vecs = p.head_dim / 8, half = row_vecs / 2, Hkv = p.n_kv_head;
   const int heads = 2 * Hkv + (p.q ? p.n_head : 0);
@@ -166,9 +237,15 @@ __device__ __forceinline__ void move_token(const AppendPagedParams& p, int t, in
       int from = 0, count = 0, p0 = 0;
       ok = sequence_rows(p, b, &from, &count, &p0) && t >= from && t < from + count;
       position = p0 + (t - from);
+      TurnRows rows;
+      if constexpr (AX) ok = rows.load(p, t) && ok;
       if (!ok && first == 0 && c == 0 && p.err_flag) atomicOr(p.err_flag, kErrPosition);
       if (ok) {
-        if (p.cos) rope.load(p, position, c);
+        if constexpr (AX) {
+          rope.load_axes(p, rows, c);
+        } else {
+          if (p.cos) rope.load(p, position, c);
+        }
         page = p.table[(int64_t)b * p.max_pages + (position >> p.page_shift)];
         page_ok = page >= 0 && page < p.num_pages;
         if (!page_ok && first == 0 && c == 0 && p.err_flag) atomicOr(p.err_flag, kErrPage);
@@ -204,14 +281,15 @@ __device__ __forceinline__ void move_token(const AppendPagedParams& p, int t, in
 }
 
 // 16-bit pages: `stride` units for each token.
-template <typename T>
+template <typename T, bool AX>
 __global__ void __launch_bounds__(kThreads, 2) append_paged_kernel(const AppendPagedParams p, int stride) {
   pdl_wait();
   pdl_trigger();
+  if constexpr (AX) check_axes(p);
   const int half = p.head_dim / 16;
   const int64_t unit = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / half;
   const int64_t t = unit / stride;
-  if (t < p.tokens) move_token<T>(p, (int)t, (int)(unit - t * stride), stride, threadIdx.x % half);
+  if (t < p.tokens) move_token<T, AX>(p, (int)t, (int)(unit - t * stride), stride, threadIdx.x % half);
 }
 
 // Exponent of the smallest power of two s with peak <= 448 s (448 = 1.75 *
@@ -305,16 +383,17 @@ __device__ __forceinline__ float finite_peak(float peak, const float (&f)[8]) {
 // head), and `stride` units for the query heads of each token. A unit finds
 // its row's peak with shuffles; where a scale grows, its whole warp rounds the
 // page's older rows.
-template <typename T>
+template <typename T, bool AX>
 __global__ void __launch_bounds__(kThreads)
     append_token_q8_kernel(const AppendPagedParams p, int row_ctas, int stride) {
   pdl_wait();
   pdl_trigger();
+  if constexpr (AX) check_axes(p);
   const int row_vecs = p.head_dim / 8, half = row_vecs / 2, Hkv = p.n_kv_head, c = threadIdx.x % half;
   if ((int)blockIdx.x >= row_ctas) {
     const int64_t unit = ((int64_t)(blockIdx.x - row_ctas) * kThreads + threadIdx.x) / half;
     const int64_t t = unit / stride;
-    if (t < p.tokens) move_token<T>(p, (int)t, 2 * Hkv + (int)(unit - t * stride), stride, c);
+    if (t < p.tokens) move_token<T, AX>(p, (int)t, 2 * Hkv + (int)(unit - t * stride), stride, c);
     return;
   }
   const int64_t unit = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / half;
@@ -324,7 +403,9 @@ __global__ void __launch_bounds__(kThreads)
   const uint4* in = reinterpret_cast<const uint4*>(is_k ? p.k_new : p.v_new) + ((int64_t)b * Hkv + g) * row_vecs + c;
   const uint4 x = in[0], y = in[half];
   const int position = p.pos[b];
-  const bool ok = position >= 0 && position < p.limit;
+  TurnRows turn;
+  bool ok = position >= 0 && position < p.limit;
+  if constexpr (AX) ok = turn.load(p, b) && ok;
   int page = ok ? p.table[(int64_t)b * p.max_pages + (position >> p.page_shift)] : 0;
   const bool page_ok = page >= 0 && page < p.num_pages;
   if (live && hk == 0 && c == 0 && p.err_flag && !(ok && page_ok)) atomicOr(p.err_flag, ok ? kErrPage : kErrPosition);
@@ -333,7 +414,7 @@ __global__ void __launch_bounds__(kThreads)
   float a[8], bb[8];
   if (write && is_k && p.cos) {
     RopeRow rope;
-    rope.load(p, position, c);
+    if constexpr (AX) rope.load_axes(p, turn, c); else rope.load(p, position, c);
     rope.rotate<T>(x, y, a, bb);
   } else {
     Storage<T>::unpack(x, a);
@@ -389,7 +470,7 @@ __host__ __device__ constexpr int prompt_heads(int R) { return R >= 4 ? 1 : 4 / 
 __host__ __device__ constexpr int prompt_smem(int R) { return 2 * kThreads * R * prompt_heads(R) * 32; }
 __host__ __device__ constexpr int prompt_ctas(int R) { return R == 8 ? 1 : 2; }  // on an SM
 
-template <typename T, int R>
+template <typename T, int R, bool AX>
 __global__ void __launch_bounds__(kThreads, prompt_ctas(R))
     append_prompt_q8_kernel(const AppendPagedParams p, int page_ctas, int chunks, int stride) {
   constexpr int HC = prompt_heads(R), kWarps = kThreads / 32;
@@ -399,12 +480,13 @@ __global__ void __launch_bounds__(kThreads, prompt_ctas(R))
   __shared__ uint32_t sh_peak[2][HC][kWarps];
   pdl_wait();
   pdl_trigger();
+  if constexpr (AX) check_axes(p);
   const int row_vecs = p.head_dim / 8, half = row_vecs / 2, Hkv = p.n_kv_head;
   const int units = kThreads / half, unit = threadIdx.x / half, c = threadIdx.x % half;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if ((int)blockIdx.x >= page_ctas) {
     const int64_t u = (int64_t)(blockIdx.x - page_ctas) * units + unit, t = u / stride;
-    if (t < p.tokens) move_token<T>(p, (int)t, 2 * Hkv + (int)(u - t * stride), stride, c);
+    if (t < p.tokens) move_token<T, AX>(p, (int)t, 2 * Hkv + (int)(u - t * stride), stride, c);
     return;
   }
   int first = 0, count = 0, p0 = 0;  // new rows of the sequence at hand
@@ -456,6 +538,7 @@ __global__ void __launch_bounds__(kThreads, prompt_ctas(R))
   const int slots = p.page_rows / R, slot = unit % slots, at_once = units / slots;
   struct Item {
     int row0, lo, hi, page, which, g0;  // first row of the page, rows [lo, hi) of it, first head of the unit
+    int token0;                         // AX: the packed token of position 0 would be (rows' turns are looked up by it)
   };
   auto place = [&](int stage, int i, int k, int which) {
     return staged + (((stage * R + i) * HC + k) * 2 + which) * kThreads + threadIdx.x;
@@ -467,6 +550,7 @@ __global__ void __launch_bounds__(kThreads, prompt_ctas(R))
     it.hi = min(p0 + count, it.row0 + p.page_rows);
     it.which = which;
     it.g0 = (chunk * at_once + unit / slots) * HC;
+    if constexpr (AX) it.token0 = first - p0;
     const uint4* in = reinterpret_cast<const uint4*>(which ? p.v_new : p.k_new);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
@@ -517,10 +601,19 @@ __global__ void __launch_bounds__(kThreads, prompt_ctas(R))
     const int old_rows = lo - row0;
     // the rows' values, kept between the peaks and the rounding
     float va[R][HC][8], vb[R][HC][8], peak[HC];
+    uint32_t skipped = 0;  // AX: rows of this unit whose turn is not in the tables
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       const int position = row0 + slot + i * slots;
-      const bool on = position >= lo && position < hi;
+      bool on = position >= lo && position < hi;
+      TurnRows turn_rows;
+      if constexpr (AX) {
+        if (on && !turn_rows.load(p, it.token0 + position)) {
+          on = false;
+          skipped |= 1u << i;
+          if (c == 0 && p.err_flag) atomicOr(p.err_flag, kErrPosition);
+        }
+      }
 #pragma unroll
       for (int k = 0; k < HC; ++k) {
         const uint4 none = make_uint4(0u, 0u, 0u, 0u);
@@ -528,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, prompt_ctas(R))
         Storage<T>::unpack(in ? *place(n & 1, i, k, 0) : none, va[i][k]);
         Storage<T>::unpack(in ? *place(n & 1, i, k, 1) : none, vb[i][k]);
       }
-      if (on && rotate) rotate_rows<HC>(p, position, c, va[i], vb[i]);
+      if (on && rotate) rotate_rows<AX, HC>(p, position, turn_rows, c, va[i], vb[i]);
     }
     auto find_peaks = [&](auto finite) {
 #pragma unroll
@@ -581,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, prompt_ctas(R))
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         const int position = row0 + slot + i * slots;
-        if (position < lo || position >= hi) continue;
+        if (position < lo || position >= hi || (AX && (skipped >> i & 1))) continue;
 #pragma unroll
         for (int k = 0; k < HC; ++k) {
           if (k >= live) break;
@@ -605,10 +698,10 @@ __global__ void __launch_bounds__(kThreads, prompt_ctas(R))
   }
 }
 
-template <typename T, int R>
+template <typename T, int R, bool AX>
 cudaError_t launch_prompt_q8(cudaLaunchConfig_t cfg, const AppendPagedParams& p, int page_ctas, int chunks,
                              int stride) {
-  auto* fn = append_prompt_q8_kernel<T, R>;
+  auto* fn = append_prompt_q8_kernel<T, R, AX>;
   cfg.dynamicSmemBytes = prompt_smem(R);
   static std::atomic<bool> ready[64];  // per device: the shared-memory opt-in is applied
   int device = 0;
@@ -638,8 +731,10 @@ int units_per_token(int64_t tokens, int heads, int half, int sms) {
 
 }  // namespace
 
-cudaError_t launch_append_paged(const AppendPagedParams& p, int dtype, int sms, cudaStream_t stream) {
-  const bool f16 = dtype == DA_F16;
+namespace {
+
+template <typename T, bool AX>
+cudaError_t launch_append_as(const AppendPagedParams& p, int sms, cudaStream_t stream) {
   const int half = p.head_dim / 16, units = kThreads / half, query_heads = p.q ? p.n_head : 0;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kThreads);
@@ -657,16 +752,14 @@ cudaError_t launch_append_paged(const AppendPagedParams& p, int dtype, int sms, 
   if (!p.k_scale) {
     const int heads = 2 * p.n_kv_head + query_heads, stride = units_per_token(p.tokens, heads, half, sms);
     if (!grid(ctas_of((int64_t)p.tokens * stride))) return cudaErrorInvalidConfiguration;
-    return f16 ? cudaLaunchKernelEx(&cfg, append_paged_kernel<__half>, p, stride)
-               : cudaLaunchKernelEx(&cfg, append_paged_kernel<__nv_bfloat16>, p, stride);
+    return cudaLaunchKernelEx(&cfg, append_paged_kernel<T, AX>, p, stride);
   }
   const int stride = query_heads ? units_per_token(p.tokens, query_heads, half, sms) : 1;
   const int64_t query_ctas = query_heads ? ctas_of((int64_t)p.tokens * stride) : 0;
   if (!p.start) {
     const int64_t rows = ctas_of((int64_t)p.B * 2 * p.n_kv_head);
     if (!grid(rows + query_ctas)) return cudaErrorInvalidConfiguration;
-    return f16 ? cudaLaunchKernelEx(&cfg, append_token_q8_kernel<__half>, p, (int)rows, stride)
-               : cudaLaunchKernelEx(&cfg, append_token_q8_kernel<__nv_bfloat16>, p, (int)rows, stride);
+    return cudaLaunchKernelEx(&cfg, append_token_q8_kernel<T, AX>, p, (int)rows, stride);
   }
   // n rows touch at most (n - 2) / page + 2 pages
   const int64_t tasks = std::min<int64_t>((int64_t)p.tokens / p.page_rows + 2 * (int64_t)p.B, p.tokens);
@@ -677,8 +770,7 @@ cudaError_t launch_append_paged(const AppendPagedParams& p, int dtype, int sms, 
   if (!grid(page_ctas + query_ctas)) return cudaErrorInvalidConfiguration;
   auto launch = [&](auto rows) {
     constexpr int kR = decltype(rows)::value;
-    return f16 ? launch_prompt_q8<__half, kR>(cfg, p, (int)page_ctas, chunks, stride)
-               : launch_prompt_q8<__nv_bfloat16, kR>(cfg, p, (int)page_ctas, chunks, stride);
+    return launch_prompt_q8<T, kR, AX>(cfg, p, (int)page_ctas, chunks, stride);
   };
   switch (R) {
     case 1: return launch(std::integral_constant<int, 1>());
@@ -686,6 +778,16 @@ cudaError_t launch_append_paged(const AppendPagedParams& p, int dtype, int sms, 
     case 4: return launch(std::integral_constant<int, 4>());
     default: return launch(std::integral_constant<int, 8>());
   }
+}
+
+}  // namespace
+
+cudaError_t launch_append_paged(const AppendPagedParams& p, int dtype, int sms, cudaStream_t stream) {
+  if (p.turn)
+    return dtype == DA_F16 ? launch_append_as<__half, true>(p, sms, stream)
+                           : launch_append_as<__nv_bfloat16, true>(p, sms, stream);
+  return dtype == DA_F16 ? launch_append_as<__half, false>(p, sms, stream)
+                         : launch_append_as<__nv_bfloat16, false>(p, sms, stream);
 }
 
 }  // namespace da

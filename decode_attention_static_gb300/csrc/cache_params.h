@@ -14,6 +14,8 @@ constexpr int kMaxPageSize = 256;
 // Most sequences, and most KV heads, of an attention call (cache_attn.cuh packs
 // a sequence number and a head into 16 bits each).
 constexpr int kMaxBatch = 65535;
+// Most rotary axes of an append.
+constexpr int kMaxRopeAxes = 4;
 
 // Attention over a cache in pages, or (table == nullptr) over a static cache,
 // where sequence b is page b of `page_rows` = capacity rows.
@@ -54,6 +56,9 @@ struct AppendPagedParams {
   int B, tokens, n_head, n_kv_head, head_dim;
   int num_pages, page_rows, page_shift, max_pages;
   int limit;               // positions must lie in [0, limit)
+  const int32_t* turn;     // rows of the tables: [axes, tokens] (null: a token's row is its position)
+  const int32_t* axis;     // [D / 2]: axis of each element pair (null: the first)
+  int axes, rope_rows;
   int32_t* err_flag;       // may be null
 };
 

@@ -18,6 +18,10 @@ constexpr int32_t kErrPosition = 2;
 constexpr int32_t kErrTimeout = 4;
 constexpr int32_t kErrWorkspace = 8;
 constexpr int32_t kErrPage = 16;
+constexpr int32_t kErrTokens = 32;
+constexpr int32_t kErrSequence = 64;
+constexpr int32_t kErrFull = 128;
+constexpr int32_t kErrPool = 256;
 
 // A pipeline wait gives up after this long and reports kErrTimeout.
 constexpr unsigned long long kWaitLimitNs = 1000ull * 1000ull * 1000ull;  // 1 s

@@ -1,0 +1,372 @@
+// Bookkeeping of a paged cache on the device: taking, sharing and releasing
+// pages. Everything is whole numbers in an order that the header fixes, so that
+// equal calls give equal states.
+//
+// Every call is one thread-block cluster: the steps (release, collect, take)
+// need a barrier over all threads, and the cluster's is in hardware, without
+// counters in memory or a promise that CTAs run at the same time. The bytes (a table
+// entry, a count and a list entry for each page) are few; what a call
+// costs is the chain of dependent loads (length, entry, count) and barriers.
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "page_params.h"
+
+namespace da {
+
+namespace {
+
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kClusterMax = 8;  // the portable size
+
+__device__ __forceinline__ void cluster_sync() {
+  cluster_arrive_release();
+  cluster_wait_acquire();
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_addr(const void* local, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr(local)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void cluster_or(uint32_t addr, uint32_t v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ int cluster_load(uint32_t addr) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ void report(int32_t* err_flag, int bits) {
+  if (bits && err_flag) atomicOr(err_flag, bits);
+}
+
+// Sum of v over the threads before this one, and (in *all) over all of them.
+// `scratch` holds kWarps + 1 numbers; every thread takes part.
+__device__ __forceinline__ int scan_threads(int v, int* scratch, int* all) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  int sum = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int up = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += up;
+  }
+  __syncthreads();  // (the last call's sums have been read)
+  if (lane == 31) scratch[warp] = sum;
+  __syncthreads();
+  const int w = lane < kWarps ? scratch[lane] : 0;
+  const int before = __reduce_add_sync(0xffffffffu, lane < warp ? w : 0);
+  *all = __reduce_add_sync(0xffffffffu, w);
+  return before + sum - v;
+}
+
+// Pages of a sequence before and after, and its number among the pages taken;
+// of the kThreads sequences that a pass looks at.
+struct Span {
+  int held, wanted, rank;
+};
+
+// The sequences [first, first + kThreads): their spans into shared memory;
+// returns the pages they take, and adds those they release to *released.
+__device__ __forceinline__ int find_spans(const PoolParams& p, int first, int taken, Span* spans, int* scratch,
+                                          int* released, int* errors) {
+  const int b = first + threadIdx.x, most = p.max_pages << p.page_shift, size = 1 << p.page_shift;
+  Span s = {0, 0, 0};
+  if (b < p.B) {
+    const int h = p.a[b], w = p.b[b];
+    if (h < 0 || h > most || w < 0 || w > most) {
+      *errors |= kErrKvLen;
+    } else {
+      s.held = (h + size - 1) >> p.page_shift;
+      s.wanted = (w + size - 1) >> p.page_shift;
+    }
+  }
+  int take, drop;
+  scan_threads(max(0, s.held - s.wanted), scratch, &drop);
+  s.rank = taken + scan_threads(max(0, s.wanted - s.held), scratch, &take);
+  *released += drop;
+  spans[threadIdx.x] = s;
+  __syncthreads();
+  return take;
+}
+
+// One cluster. A page that becomes free sets its bit in the shared memory of
+// the CTA that owns its part of the pool; the CTAs then list their bits.
+__global__ void __launch_bounds__(kThreads) resize_kernel(const PoolParams p, int ctas, int words) {
+  extern __shared__ uint32_t freed[];  // [words]: bits of this CTA's pages
+  __shared__ Span spans[kThreads];
+  __shared__ int scratch[kWarps + 1];
+  __shared__ int listed;
+  const int lane = threadIdx.x % 32, cta = ctas > 1 ? (int)cluster_rank() : 0;
+  const int warps = ctas * kWarps, warp = cta * kWarps + threadIdx.x / 32;
+  for (int i = threadIdx.x; i < words; i += kThreads) freed[i] = 0;
+  pdl_wait();
+  pdl_trigger();
+  int32_t* const counts = p.pool + kPoolHeader;
+  int32_t* const list = counts + p.num_pages;
+  int errors = 0, released = 0, taken = 0;
+  const int free_now = __ldcg(p.pool);
+  const int free0 = min(max(free_now, 0), p.num_pages);
+  if (free0 != free_now) errors |= kErrPool;
+  if (ctas > 1) cluster_sync();  // every CTA's bits are zero, and the free pages have been read
+  // as many warps for a sequence as there are for each of a pass
+  const int pass = min(p.B, kThreads), each = max(1, warps / max(1, pass));
+  // releases
+  for (int first = 0; first < p.B; first += kThreads) {
+    taken += find_spans(p, first, taken, spans, scratch, &released, &errors);
+    for (int i = warp / each; i < min(kThreads, p.B - first) && warp < each * pass; i += warps / each) {
+      const Span s = spans[i];
+      int32_t* const row = p.table + (int64_t)(first + i) * p.max_pages;
+      for (int j = s.wanted + warp % each * 32 + lane; j < s.held; j += each * 32) {
+        const int id = row[j];
+        row[j] = -1;
+        if (id < 0 || id >= p.num_pages) {
+          if (id != -1) errors |= kErrPage;
+          continue;
+        }
+        const int before = atomicSub(counts + id, 1);
+        if (before == 1) {
+          const uint32_t word = (uint32_t)id >> 5;
+          if (ctas > 1) {
+            cluster_or(cluster_addr(freed + word % words, word / words), 1u << (id & 31));
+          } else {
+            atomicOr(freed + word, 1u << (id & 31));
+          }
+        } else if (before < 1) {
+          atomicAdd(counts + id, 1);
+          errors |= kErrPool;
+        }
+      }
+    }
+    if (first + kThreads < p.B) __syncthreads();
+  }
+  int top = free0;
+  if (released > 0) {  // (the same in every CTA)
+    if (ctas > 1) cluster_sync(); else __syncthreads();
+    const int per = (words + kThreads - 1) / kThreads;  // words of a thread
+    const int lo = min(words, (int)threadIdx.x * per), hi = min(words, lo + per);
+    int mine = 0;
+    for (int i = lo; i < hi; ++i) mine += __popc(freed[i]);
+    int all;
+    int at = scan_threads(mine, scratch, &all);
+    if (ctas > 1) {
+      if (threadIdx.x == 0) listed = all;
+      cluster_sync();
+      const int n = lane < ctas ? cluster_load(cluster_addr(&listed, lane)) : 0;
+      at += __reduce_add_sync(0xffffffffu, lane < cta ? n : 0);
+      all = __reduce_add_sync(0xffffffffu, n);
+    }
+    at += free0;
+    for (int i = lo; i < hi; ++i) {
+      for (uint32_t bits = freed[i]; bits; bits &= bits - 1) {
+        const int id = ((cta * words + i) << 5) + __ffs(bits) - 1;
+        if (at < p.num_pages) list[at] = id; else errors |= kErrPool;
+        ++at;
+      }
+    }
+    top = min(free0 + all, p.num_pages);
+    if (ctas > 1) cluster_sync(); else __syncthreads();
+  }
+  if (taken > 0) {
+    int rank0 = 0, none = 0;
+    for (int first = 0; first < p.B; first += kThreads) {
+      if (p.B > kThreads) {
+        __syncthreads();
+        rank0 += find_spans(p, first, rank0, spans, scratch, &none, &none);
+      }
+      for (int i = warp / each; i < min(kThreads, p.B - first) && warp < each * pass; i += warps / each) {
+        const Span s = spans[i];
+        int32_t* const row = p.table + (int64_t)(first + i) * p.max_pages;
+        for (int j = s.held + warp % each * 32 + lane; j < s.wanted; j += each * 32) {
+          const int rank = s.rank + j - s.held;
+          int id = -1;
+          if (rank < top) {
+            id = __ldcg(list + top - 1 - rank);
+            if (id < 0 || id >= p.num_pages) {
+              errors |= kErrPool;
+              id = -1;
+            } else {
+              atomicAdd(counts + id, 1);
+            }
+          } else {
+            errors |= kErrFull;
+          }
+          row[j] = id;
+        }
+      }
+    }
+  }
+  if (cta == 0 && threadIdx.x == 0) p.pool[0] = top - min(taken, top);
+  report(p.err_flag, errors);
+  if (ctas > 1 && released > 0) cluster_sync();  // shared memory that other CTAs read is there until they have
+}
+
+// One cluster. Every CTA finds which forks are valid and how many pages those
+// before each one take (bits of the children in shared memory); the warps then
+// copy table rows.
+__global__ void __launch_bounds__(kThreads) fork_kernel(const PoolParams p, int ctas, int words) {
+  extern __shared__ uint32_t bits[];  // [words] children, [words] children of more than one fork
+  __shared__ int scratch[kWarps + 1];
+  struct Fork {
+    int parent, child, rows, rank;  // rows -1: skipped
+  };
+  __shared__ Fork forks[kThreads];
+  const int lane = threadIdx.x % 32, cta = ctas > 1 ? (int)cluster_rank() : 0;
+  const int warps = ctas * kWarps, warp = cta * kWarps + threadIdx.x / 32;
+  for (int i = threadIdx.x; i < 2 * words; i += kThreads) bits[i] = 0;
+  __syncthreads();
+  pdl_wait();
+  pdl_trigger();
+  int32_t* const counts = p.pool + kPoolHeader;
+  const int32_t* const list = counts + p.num_pages;
+  int errors = 0;
+  const int free_now = __ldcg(p.pool);
+  const int free0 = min(max(free_now, 0), p.num_pages);
+  if (free0 != free_now) errors |= kErrPool;
+  for (int i = threadIdx.x; i < p.n; i += kThreads) {
+    const int c = p.b[i];
+    if (c >= 0 && c < p.B && (atomicOr(bits + (c >> 5), 1u << (c & 31)) >> (c & 31) & 1))
+      atomicOr(bits + words + (c >> 5), 1u << (c & 31));
+  }
+  __syncthreads();
+  const int pass = min(p.n, kThreads), each = max(1, warps / max(1, pass));
+  const int size = 1 << p.page_shift;
+  int taken = 0;
+  for (int first = 0; first < p.n; first += kThreads) {
+    const int mine = first + threadIdx.x;
+    Fork f = {0, 0, -1, 0};
+    if (mine < p.n) {
+      f.parent = p.a[mine];
+      f.child = p.b[mine];
+      if (f.parent < 0 || f.parent >= p.B || f.child < 0 || f.child >= p.B ||
+          (bits[words + (f.child >> 5)] >> (f.child & 31) & 1) || (bits[f.parent >> 5] >> (f.parent & 31) & 1)) {
+        errors |= kErrSequence;
+      } else {
+        f.rows = __ldcg(p.kv_len + f.parent);
+        if (f.rows < 0 || f.rows > p.max_pages << p.page_shift) {
+          errors |= kErrKvLen;
+          f.rows = -1;
+        }
+      }
+    }
+    int need = f.rows > 0 && (f.rows & (size - 1)) ? 1 : 0, all;
+    f.rank = taken + scan_threads(need, scratch, &all);
+    taken += all;
+    if (need && f.rank >= free0) {
+      errors |= kErrFull;
+      f.rows = -1;
+    }
+    forks[threadIdx.x] = f;
+    __syncthreads();
+    for (int i = warp / each; i < min(kThreads, p.n - first) && warp < each * pass; i += warps / each) {
+      const Fork k = forks[i];
+      const int full = k.rows >> p.page_shift, rest = k.rows & (size - 1);
+      const int32_t* const from = p.table + (int64_t)k.parent * p.max_pages;
+      int32_t* const to = p.table + (int64_t)k.child * p.max_pages;
+      if (k.rows > 0) {
+        for (int j = warp % each * 32 + lane; j < full; j += each * 32) {
+          const int id = from[j];
+          to[j] = id;
+          if (id >= 0 && id < p.num_pages) atomicAdd(counts + id, 1); else errors |= kErrPage;
+        }
+      }
+      if (warp % each == 0 && lane == 0) {
+        int src = -1, dst = -1, rows = 0;
+        if (k.rows > 0 && rest) {
+          src = from[full];
+          dst = list[free0 - 1 - k.rank];
+          rows = rest;
+          if (dst < 0 || dst >= p.num_pages) {
+            errors |= kErrPool;
+            dst = -1;
+          } else {
+            atomicAdd(counts + dst, 1);
+          }
+          to[full] = dst;
+          if (src < 0 || src >= p.num_pages) errors |= kErrPage;
+          if (src < 0 || src >= p.num_pages || dst < 0) {
+            src = dst = -1;
+            rows = 0;
+          }
+        }
+        const int at = first + i;
+        p.copies[at] = src;
+        p.copies[p.n + at] = dst;
+        p.copies[2 * (int64_t)p.n + at] = rows;
+        if (k.rows >= 0) p.kv_len[k.child] = k.rows;
+      }
+    }
+    __syncthreads();
+  }
+  if (ctas > 1) cluster_sync();  // every CTA has read the free pages
+  if (cta == 0 && threadIdx.x == 0) p.pool[0] = free0 - min(taken, free0);
+  report(p.err_flag, errors);
+}
+
+__global__ void __launch_bounds__(256) init_kernel(int32_t* pool, int num_pages) {
+  pdl_wait();
+  pdl_trigger();
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  if (i < kPoolHeader) pool[i] = i == 0 ? num_pages : 0;
+  if (i < num_pages) {
+    pool[kPoolHeader + i] = 0;
+    pool[kPoolHeader + num_pages + i] = i;
+  }
+}
+
+// CTAs of a call: one where its table entries are few (no cluster barriers),
+// else a cluster.
+constexpr int64_t kOneCtaEntries = 4096;
+
+template <typename K>
+cudaError_t launch_cluster(K* kernel, const PoolParams& p, int ctas, int words, size_t smem, cudaStream_t stream) {
+  if (smem > 32 * 1024) {  // (static arrays come on top)
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attrs[2];
+  attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attrs[0].val.programmaticStreamSerializationAllowed = 1;
+  attrs[1].id = cudaLaunchAttributeClusterDimension;
+  attrs[1].val.clusterDim.x = ctas;
+  attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
+  cfg.attrs = attrs;
+  cfg.numAttrs = ctas > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p, ctas, words);
+}
+
+}  // namespace
+
+cudaError_t launch_pool_init(int32_t* pool, int num_pages, cudaStream_t stream) {
+  const int n = std::max(num_pages, kPoolHeader);
+  init_kernel<<<(n + 255) / 256, 256, 0, stream>>>(pool, num_pages);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pool_resize(const PoolParams& p, cudaStream_t stream) {
+  const int64_t entries = (int64_t)p.B * p.max_pages;
+  const int all_words = (p.num_pages + 31) / 32;
+  const int ctas = entries <= kOneCtaEntries && all_words <= 8192 ? 1 : kClusterMax;
+  const int words = (all_words + ctas - 1) / ctas;
+  return launch_cluster(resize_kernel, p, ctas, words, (size_t)words * 4, stream);
+}
+
+cudaError_t launch_pool_fork(const PoolParams& p, cudaStream_t stream) {
+  const int ctas = (int64_t)p.n * p.max_pages <= kOneCtaEntries ? 1 : kClusterMax;
+  const int words = (p.B + 31) / 32;
+  return launch_cluster(fork_kernel, p, ctas, words, (size_t)words * 8, stream);
+}
+
+}  // namespace da

@@ -75,6 +75,10 @@ typedef enum {
 #define DA_DEVERR_TIMEOUT 4u  /* a pipeline wait hit its time limit: rows are NaN */
 #define DA_DEVERR_WORKSPACE 8u /* the workspace counters were not zero: rows of the group are NaN */
 #define DA_DEVERR_PAGE 16u /* a page id in use lies outside [0, num_pages): rows are NaN, writes skipped */
+#define DA_DEVERR_TOKENS 32u /* a sequence's range of packed tokens is not valid, or too long: skipped, or rows are NaN */
+#define DA_DEVERR_SEQUENCE 64u /* a fork's parent or child is no sequence, or one that another fork writes: skipped */
+#define DA_DEVERR_FULL 128u /* the pool has too few free pages: entries are -1, forks skipped */
+#define DA_DEVERR_POOL 256u /* a pool's counts or list of free pages are not consistent */
 
 /* Human-readable name of a da_status value (static string). */
 DA_API const char* da_status_string(int status);
@@ -496,6 +500,209 @@ DA_API int decode_attn_paged_q8_fwd(const void* q, const void* k_pages, const vo
 DA_API int decode_attn_window_fwd(const void* q, const void* k_cache, const void* v_cache, const int32_t* kv_len,
                     int B, int n_head, int n_kv_head, int head_dim, int capacity, int window, int sinks, float scale,
                     void* out, void* workspace, size_t workspace_bytes, int dtype, int32_t* err_flag, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Serving steps with drafted tokens, over the paged caches above (the same
+ * conventions and layouts). A step takes pages for the drafts
+ * (kvcache_resize_paged), appends them with rotary positions by their depth
+ * (kvcache_append_paged_axes), verifies them in one pass over the cache
+ * (decode_attn_tree_fwd), moves the accepted rows together
+ * (kvcache_compact_paged) and gives the pages behind them back. No call needs
+ * a length on the host, so that one captured graph serves every step.
+ */
+
+/*
+ * kvcache_append_paged with rotary positions of their own: element pair (i, i +
+ * head_dim / 2) of token t's key (and q) heads is rotated by row
+ * rope_position_ids[a, t] of the tables, a = rope_axis[i], whatever row of the
+ * cache the token goes to.
+ *   rope_position_ids  int32 [axes, tokens], 1 <= axes <= DA_MAX_ROPE_AXES:
+ *                      time, height and width of an image's patches, or one
+ *                      axis with the depth of a drafted token
+ *   rope_axis          int32 [head_dim / 2], 16-byte aligned, any order
+ *                      (sections, interleaved); NULL: axis 0 for all
+ * The tables are required. A token with a position (on any axis) outside [0,
+ * rope_rows) is skipped whole (its q_out row becomes NaN) and sets
+ * DA_DEVERR_POSITION; an entry of rope_axis outside [0, axes) sets it too and
+ * counts as axis 0. position_ids alone decide where rows go; rope_rows does not
+ * bound them. Everything else as in kvcache_append_paged (whose results it
+ * has when every rope position is the token's position).
+ */
+#define DA_MAX_ROPE_AXES 4
+DA_API int kvcache_append_paged_axes(void* k_pages, void* v_pages, const void* k_new, const void* v_new, const void* q,
+                    void* q_out, const float* rope_cos, const float* rope_sin, int rope_rows,
+                    const int32_t* rope_position_ids, const int32_t* rope_axis, int axes, const int32_t* page_table,
+                    const int32_t* position_ids, const int32_t* token_start, int B, int tokens, int n_head,
+                    int n_kv_head, int head_dim, int num_pages, int page_size, int max_pages, int dtype,
+                    int32_t* err_flag, void* stream);
+
+/* kvcache_append_paged_axes into pages of e4m3, as kvcache_append_paged_q8. */
+DA_API int kvcache_append_paged_q8_axes(void* k_pages, void* v_pages, float* k_scale, float* v_scale,
+                    const void* k_new, const void* v_new, const void* q, void* q_out, const float* rope_cos,
+                    const float* rope_sin, int rope_rows, const int32_t* rope_position_ids, const int32_t* rope_axis,
+                    int axes, const int32_t* page_table, const int32_t* position_ids, const int32_t* token_start,
+                    int B, int tokens, int n_head, int n_kv_head, int head_dim, int num_pages, int page_size,
+                    int max_pages, int dtype, int32_t* err_flag, void* stream);
+
+/* Most tokens of one sequence in a call of decode_attn_tree_fwd. */
+#define DA_TREE_MAX_TOKENS 256
+
+/* Bytes of scratch of one call of decode_attn_tree_fwd or
+ * decode_attn_tree_q8_fwd on the current device; it depends on the heads alone.
+ * Zero-fill it once before its first use; every call that completes leaves it
+ * ready for the next. Calls that share it must not overlap on the GPU.
+ * Returns (size_t)-1 for invalid sizes or a failed device query. */
+DA_API size_t decode_attn_tree_workspace_size(int n_head, int n_kv_head, int head_dim);
+
+/*
+ * Attention of several new tokens of each sequence over a paged cache that
+ * holds their rows already. q and out are packed, [tokens, n_head, head_dim];
+ * sequence b owns tokens [token_start[b], token_start[b + 1]) (int32 [B + 1],
+ * rising; NULL: one token per sequence), n_b of them, and they are its last
+ * n_b rows: token i of it is row base_b + i, base_b = kv_len[b] - n_b. It sees
+ * every row j < base_b, and of the new rows those of its mask: row base_b + i'
+ * for i' in [0, n_b) where
+ *   tree_mask == NULL   i' <= i (a chain of drafts)
+ *   else                bit i' mod 64 of tree_mask[t, i' / 64] is set (int64
+ *                       [tokens, mask_words], 1 <= mask_words <= 4; bits at
+ *                       or past n_b do not matter): a tree's ancestors and
+ *                       the token itself, or any other set
+ *   out[t, h, :] = softmax_j(scale <q[t, h], K_j>) V_j over the rows seen
+ * Products of the storage type, sums, maxima and exponentials in fp32; a
+ * weight is rounded to the storage type, relative to its row's running
+ * maximum, before it reaches V, and the output is rounded once. A token that sees
+ * nothing gets a row of zeros. Rows that a token does not see do not reach
+ * it, whatever they hold (NaN and infinities among them). Rows of q and out
+ * that no sequence owns are left alone. Facts only the device knows:
+ * kv_len[b] < n_b or > max_pages * page_size gives NaN rows and
+ * DA_DEVERR_KV_LEN; n_b above DA_TREE_MAX_TOKENS or 64 * mask_words gives NaN
+ * rows and DA_DEVERR_TOKENS; a token range that is not inside the packed
+ * tokens is skipped and sets DA_DEVERR_TOKENS; a page id outside the pool
+ * among the first ceil(kv_len / page_size) of a sequence gives NaN for its
+ * tokens and DA_DEVERR_PAGE. kv_len times the largest |V| stays below 2^110,
+ * or sums may overflow. Equal calls give equal bits. Lengths, table, tokens
+ * and masks must not change while the call runs, and out must not be q
+ * (DA_ERR_SHAPE).
+ */
+DA_API int decode_attn_tree_fwd(const void* q, const void* k_pages, const void* v_pages, const int32_t* page_table,
+                    const int32_t* kv_len, const int32_t* token_start, const int64_t* tree_mask, int mask_words,
+                    int B, int tokens, int n_head, int n_kv_head, int head_dim, int num_pages, int page_size,
+                    int max_pages, float scale, void* out, void* workspace, size_t workspace_bytes, int dtype,
+                    int32_t* err_flag, void* stream);
+
+/* decode_attn_tree_fwd over pages of e4m3 with their scales (finite), as
+ * decode_attn_paged_q8_fwd. dtype is that of q and out. */
+DA_API int decode_attn_tree_q8_fwd(const void* q, const void* k_pages, const void* v_pages, const float* k_scale,
+                    const float* v_scale, const int32_t* page_table, const int32_t* kv_len,
+                    const int32_t* token_start, const int64_t* tree_mask, int mask_words, int B, int tokens,
+                    int n_head, int n_kv_head, int head_dim, int num_pages, int page_size, int max_pages, float scale,
+                    void* out, void* workspace, size_t workspace_bytes, int dtype, int32_t* err_flag, void* stream);
+
+/*
+ * A pool's state, `pool`: int32 [DA_POOL_HEADER + 2 * num_pages]
+ *   pool[0]                      number of free pages, f
+ *   pool[1 .. DA_POOL_HEADER)    zero
+ *   then [num_pages]             how many table entries hold each page
+ *   then [num_pages]             the free pages, in entries [0, f)
+ * The program may read it, or make it by itself (for a cache that exists). One
+ * state serves the pools of all layers, which share page numbers. Calls on
+ * one state must not overlap on the GPU. num_pages <= DA_POOL_MAX_PAGES.
+ */
+#define DA_POOL_HEADER 4
+#define DA_POOL_MAX_PAGES (1 << 22)
+
+/* A state whose pages are all free, listed in rising order (the last page is
+ * taken first). */
+DA_API int kvcache_pool_init(int32_t* pool, int num_pages, void* stream);
+
+/*
+ * Sequence b, whose first held_len[b] rows have pages, becomes one of
+ * wanted_len[b] rows: table entries [ceil(wanted / page_size), ceil(held /
+ * page_size)) are released (and become -1) where it shrinks, entries
+ * [ceil(held / page_size), ceil(wanted / page_size)) get free pages where it
+ * grows. Freeing a sequence is wanted 0, taking pages for new ones held 0.
+ * First all releases: each lowers its page's count, and the pages whose count
+ * becomes zero are put at the end of the list, in rising order. Then all
+ * pages are taken from the end of the list, in the order of sequences and
+ * rows (the first one gets the last entry), their counts raised by one. So
+ * equal calls give equal states. Where the list runs out the entry becomes -1
+ * and DA_DEVERR_FULL is set. A length outside [0, max_pages * page_size]
+ * leaves the sequence as it was and sets DA_DEVERR_KV_LEN; a released entry
+ * outside the pool sets DA_DEVERR_PAGE (-1: nothing); a page released more
+ * often than it is counted, or a list with entries outside the pool, sets
+ * DA_DEVERR_POOL. held_len and wanted_len int32 [B], may not overlap what the
+ * call writes.
+ */
+DA_API int kvcache_resize_paged(int32_t* page_table, const int32_t* held_len, const int32_t* wanted_len,
+                    int32_t* pool, int B, int num_pages, int page_size, int max_pages, int32_t* err_flag,
+                    void* stream);
+
+/*
+ * Fork i (i < forks): sequence child[i] becomes a copy of sequence parent[i], n
+ * = kv_len[parent[i]] rows. Their first floor(n / page_size) pages are shared
+ * (the child's table entries are the parent's, their counts raised by one); a
+ * page that is partly filled is not: the child gets one from the end of the
+ * list of free pages (in the order of i), and copies[0, i] (the parent's page),
+ * copies[1, i] (the child's) and copies[2, i] = n mod page_size say what
+ * kvcache_copy_pages has to copy in every layer's pools (-1, -1, 0 where there
+ * is nothing). kv_len[child[i]] becomes n; further entries of the child's table
+ * row are left as they were. A child holds no pages before (release them with
+ * kvcache_resize_paged). A fork is skipped, with copies -1, -1, 0, when parent or
+ * child lie outside [0, B), when its child is the child or the parent of
+ * another fork, or its parent is a child (DA_DEVERR_SEQUENCE), when the parent's length is outside [0,
+ * max_pages * page_size] (DA_DEVERR_KV_LEN), or when it needs a page and none is
+ * left (DA_DEVERR_FULL). A table entry outside the pool is shared without a count, or
+ * not copied (the child's entry becomes -1), and sets DA_DEVERR_PAGE.
+ *   parent, child int32 [forks]; copies int32 [3, forks]
+ */
+DA_API int kvcache_fork_paged(int32_t* page_table, int32_t* kv_len, const int32_t* parent, const int32_t* child,
+                    int32_t* pool, int32_t* copies, int forks, int B, int num_pages, int page_size, int max_pages,
+                    int32_t* err_flag, void* stream);
+
+/*
+ * Copy i (i < n): rows [0, copies[2, i]) of page copies[0, i] to page copies[1,
+ * i], for every KV head of the K and V pools of `layers` layers (pools [layers,
+ * num_pages, n_kv_head, page_size, head_dim] of elements of element_size bytes:
+ * 2, or 1 with scales [layers, num_pages, n_kv_head], which are copied too; both
+ * scales NULL: none). Rows behind the copied ones are left as they were (in 8
+ * bits they then count under the new scale). A source or target below 0 skips
+ * the entry, one past the pool, or a row count outside [0, page_size], too, and
+ * sets DA_DEVERR_PAGE. A page that one entry writes and another one reads or
+ * writes ends up with unspecified rows.
+ */
+DA_API int kvcache_copy_pages(void* k_pages, void* v_pages, float* k_scale, float* v_scale, const int32_t* copies,
+                    int n, int layers, int num_pages, int n_kv_head, int page_size, int head_dim, int element_size,
+                    int32_t* err_flag, void* stream);
+
+/*
+ * Move rows of sequences together: row keep[keep_start[b] + i] of sequence b goes to
+ * row position_ids[b] + i, for i in [0, keep_start[b + 1] - keep_start[b]), in the K
+ * and V pools of `layers` layers (as in kvcache_copy_pages, 16 bits). keep
+ * (int32 [kept], packed; keep_start int32 [B + 1], rising) holds the rows of
+ * accepted drafts, or what stays of a longer part: rising for each sequence,
+ * never below the row it goes to. A sequence's rows from the first one on that
+ * breaks this, or lies outside [0, max_pages * page_size), are not moved
+ * (DA_DEVERR_POSITION), nor is a range that is not inside [0, kept]
+ * (DA_DEVERR_TOKENS), nor rows from or to a page outside the pool (DA_DEVERR_PAGE).
+ * Every other row is left as it was. Pages that rows move into belong to one
+ * sequence (a shared one ends up with unspecified rows).
+ */
+DA_API int kvcache_compact_paged(void* k_pages, void* v_pages, const int32_t* page_table, const int32_t* keep,
+                    const int32_t* keep_start, const int32_t* position_ids, int B, int kept, int layers,
+                    int n_kv_head, int head_dim, int num_pages, int page_size, int max_pages, int32_t* err_flag,
+                    void* stream);
+
+/*
+ * kvcache_compact_paged over pages of e4m3. A page that rows move into gets the
+ * largest of its own scale and those of the pages the rows come from (finite, not
+ * negative); rows of a smaller scale, the page's other rows among them (all
+ * of them, those behind the new ones too), are rounded to it, e4m3(x * old /
+ * new). Where no scale differs nothing but the moved rows changes.
+ */
+DA_API int kvcache_compact_paged_q8(void* k_pages, void* v_pages, float* k_scale, float* v_scale,
+                    const int32_t* page_table, const int32_t* keep, const int32_t* keep_start,
+                    const int32_t* position_ids, int B, int kept, int layers, int n_kv_head, int head_dim,
+                    int num_pages, int page_size, int max_pages, int32_t* err_flag, void* stream);
 
 #ifdef __cplusplus
 }
