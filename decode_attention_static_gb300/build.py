@@ -26,7 +26,7 @@ LIBRARY = PKG / "libdecode_attn.so"
 
 SOURCES = ["abi.cu", "decode_f16.cu", "decode_bf16.cu", "decode_f16_rope.cu", "decode_bf16_rope.cu", "append.cu",
            "static_scratch.cu", "abi_paged.cu", "append_paged.cu", "cache_attn_f16.cu", "cache_attn_bf16.cu",
-           "tree_attn.cu", "abi_pages.cu", "page_pool.cu", "page_rows.cu"]
+           "tree_attn.cu", "tree_attn_f16.cu", "tree_attn_bf16.cu", "abi_pages.cu", "page_pool.cu", "page_rows.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          f"-I{INCLUDE}", f"-I{CSRC}"]

@@ -148,6 +148,26 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 
 static_assert(sizeof(TensorMap) == sizeof(CUtensorMap), "TensorMap holds a CUtensorMap");
 
+}  // namespace
+
+// Rows of head_dim 16-bit elements, boxes of 64 columns by box_rows, 128-byte
+// swizzle.
+bool encode_rows_map(TensorMap* map, const void* base, int dtype, int64_t rows, int head_dim, int box_rows) {
+  const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)head_dim, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)head_dim * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+  const cuuint32_t unit[2] = {1, 1};
+  return enc(reinterpret_cast<CUtensorMap*>(map),
+             dtype == DA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+             const_cast<void*>(base), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+namespace {
+
 // The two K-cache tensor maps of the tensor-core instances: the cache as
 // [groups][capacity][head_dim] elements, boxes of 64 columns by one tile's
 // rows and by 8 rows, 128-byte swizzle, zero fill past the capacity.

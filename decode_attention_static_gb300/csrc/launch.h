@@ -32,6 +32,9 @@ cudaError_t launch_append(void* k_cache, void* v_cache, const void* k_new, const
                           const int32_t* pos, int B, int n_kv_head, int head_dim, int capacity,
                           int32_t* err_flag, cudaStream_t stream);
 
+// abi.cu: a tensor map over rows of head_dim 16-bit elements.
+bool encode_rows_map(TensorMap* map, const void* base, int dtype, int64_t rows, int head_dim, int box_rows);
+
 // Per-dtype halves of launch_decode / decode_kernel_info (one translation
 // unit each, compiled in parallel); `flavor` selects the flavour where an
 // instance has several.
