@@ -4,16 +4,16 @@
 // The query rows that share a KV head (its G heads for each token) are the rows of
 // the products: 128 to a tile, row = token * G + head. A unit is (sequence, KV
 // head, 256 query rows) over all tiles of 128 cache rows; the launch's CTAs (one
-// an SM) take equal runs of the tiles of all units, whatever the lengths, and a
-// unit that several CTAs take is joined from their partial states by a second
-// small kernel (tree_attn.cu).
+// an SM) take equal runs of the tiles of all units, whatever the lengths. A unit
+// that several CTAs take is joined from their partial states by the last of them
+// to arrive, with the help of those that are still there (a row for each warp).
 //
 //   warps 0-7   two groups of 128 threads, a query row each: softmax with a
 //               running maximum, weights to tensor memory, output
 //   warp 8      page numbers and copies of K and V tiles into a ring
 //   warp 9      the products: S = Q K^T (both in shared memory), O += P V (P in
 //               tensor memory, V in shared memory as it lies, read transposed)
-//   warps 10-13 8-bit pages: e4m3 to fp16 (exact), raw ring to operand ring
+//   warps 12-15 8-bit pages: e4m3 to fp16 (exact), raw ring to operand ring
 //
 // Units of more than 128 rows ("two") give each group its own query tile and every
 // K and V tile is used twice; smaller ones share the query tile, the groups take
@@ -23,6 +23,8 @@
 
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "tree_params.h"
 
@@ -30,16 +32,22 @@ namespace da {
 
 constexpr int kTreeTile = 128;             // cache rows of a tile, query rows of a tile
 constexpr int kTreeUnitRows = 256;         // query rows of a unit
+constexpr unsigned long long kTreeHelpNs = 20000;  // how long a CTA waits for a unit's other parts, to help with their join
 constexpr float kTreeLazy = 8.f;           // a running maximum is raised when a score passes it by 2^8
 
-// A partial state: O [2][D / 4][128] float4, then (m, m of l, l) [256] float4.
+// A partial state: O [256][D], then (m, m of l, l) [256] float4.
 __host__ __device__ constexpr int tree_slot_floats(int D) { return kTreeUnitRows * D + kTreeUnitRows * 4; }
-// What the merge needs of a unit that several CTAs take, by the CTA that begins it.
-struct TreeJoin {
-  int token0;   // first packed token of the unit
-  int rows;     // query rows (0: nothing to join)
-  int g;        // KV head
-  int last;     // the last CTA of the unit
+// Where the CTAs of one unit meet, by the CTA that begins it. All zero before the first call; the last to arrive
+// zeroes the first and the third and raises the second.
+struct alignas(16) TreeMeet {
+  unsigned arrived, generation, ticket, unused;
+};
+// A unit that this CTA has a part of.
+struct TreePending {
+  int c0, parts;           // its first CTA, and how many take part
+  unsigned generation;     // of its meeting place before this CTA arrived
+  int last;                // this CTA arrived last
+  int rows, token0, g;
 };
 
 struct alignas(64) TreeLaunch {
@@ -47,9 +55,9 @@ struct alignas(64) TreeLaunch {
   TreeParams p;
 };
 
-cudaError_t launch_tree_f16(const TreeLaunch& l, int head_dim, bool e4m3, int ctas, TreeJoin* joins, float* partials,
+cudaError_t launch_tree_f16(const TreeLaunch& l, int head_dim, bool e4m3, int ctas, TreeMeet* meets, float* partials,
                             cudaStream_t stream);
-cudaError_t launch_tree_bf16(const TreeLaunch& l, int head_dim, bool e4m3, int ctas, TreeJoin* joins, float* partials,
+cudaError_t launch_tree_bf16(const TreeLaunch& l, int head_dim, bool e4m3, int ctas, TreeMeet* meets, float* partials,
                              cudaStream_t stream);
 
 template <int D, bool EIGHT>
@@ -60,10 +68,20 @@ struct TreeShape {
   static constexpr int kRawBytes = kTreeTile * D;          // e4m3 tile
   static constexpr int kSlots = EIGHT ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 8);
   static constexpr int kRaw = EIGHT ? (D == 128 ? 4 : 6) : 0;
-  static constexpr int kThreads = EIGHT ? 448 : 320;
+  // whole warpgroups (setmaxnreg); registers of a thread: at launch, of the softmax groups, of the others
+  static constexpr int kThreads = EIGHT ? 512 : 384;
+  static constexpr int kRegsSoftmax = EIGHT ? 192 : 224, kRegsOther = EIGHT ? 64 : 56;
   static constexpr int kQ = 0, kRing = 2 * kTileBytes, kRawRing = kRing + kSlots * kTileBytes;
   static constexpr int kControl = kRawRing + kRaw * kRawBytes;
-  static constexpr int kSmem = 1024 + kControl + 2048;
+  // At the end of a segment the query tiles are free: weighted outputs [2][128][32] for the exchange, and behind
+  // them (or behind the control area) the states.
+  static constexpr int kExchange = kQ, kExchangeBytes = 2 * kTreeTile * 32 * 4;
+  static constexpr int kStateBytes = 2 * kTreeTile * 16 + kTreeUnitRows * 4;
+  static constexpr int kStates = D == 128 ? kQ + kExchangeBytes : kControl + 2048;
+  static constexpr int kSmem = 1024 + kControl + 2048 + (D == 128 ? 0 : kStateBytes);
+  // bf16 weights of units with one query tile are held in two pieces (16 bits): the products have time for it, and
+  // the columns behind the weights are free where they lie over the scores
+  static constexpr bool kTwoPieces = D == 128 && !EIGHT;
   // tensor memory columns: scores of the groups, outputs, weights (in place of the scores where D is 128, whose two
   // products have one shape and therefore run in order)
   static constexpr int kS = 0, kO = 256, kP = D == 128 ? 0 : 384;
@@ -75,13 +93,17 @@ struct TreeControl {
   uint64_t s_full[2], p_full[2], q_full, o_final, o_free, drain;
   uint32_t tmem;
   int abort;
-  int start_b, start_off;
+  int start[8];           // of this CTA's tiles: sequence, its first token, tokens, rows; KV head, unit, tile
+  TreePending pending[2];
+  int pendings, ready, ticket;
+  float2 scales[8][8];    // 8 bits: of a warp's column groups: factor of a score, log2 of V's scale
   int sums[16];
   // of segment s, in entry s % 8: drafted rows whose V is not finite, and whether a page lies outside the pool
   uint32_t bad[8][8];
   int bad_page[8];
 };
 static_assert(sizeof(TreeControl) <= 2048, "control area");
+static_assert(128 * (2 * 224 + 56) <= 384 * 168 && 128 * (2 * 192 + 2 * 64) <= 512 * 128, "registers of the launch");
 
 // Tokens and rows of a sequence; kt tiles for each of mps units a KV head.
 struct TreeSeq {
@@ -132,16 +154,18 @@ struct TreeCursor {
   int b, g, mp, tile, left;
   TreeSeq s;
 
-  __device__ __forceinline__ void begin(const TreeParams& p, int b0, int off, int tiles) {
+  __device__ __forceinline__ void begin(const TreeParams& p, const int (&start)[8], int tiles) {
     left = tiles;
     if (tiles == 0) return;
-    int none = 0;
-    b = b0;
-    s = tree_sequence(p, b, &none);
-    const int unit = off / s.kt;
-    tile = off - unit * s.kt;
-    g = unit / s.mps;
-    mp = unit - g * s.mps;
+    b = start[0];
+    s.first = start[1];
+    s.n = start[2];
+    s.rows = start[3];
+    s.kt = (s.rows + kTreeTile - 1) / kTreeTile;
+    s.mps = (s.n * p.group + kTreeUnitRows - 1) / kTreeUnitRows;
+    g = start[4];
+    mp = start[5];
+    tile = start[6];
   }
   __device__ __forceinline__ bool next(const TreeParams& p, TreeSegment* out) {
     if (left == 0) return false;
@@ -210,17 +234,16 @@ __device__ __forceinline__ void tmem_load32(uint32_t taddr, uint32_t* r) {
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tmem_store32(uint32_t taddr, const uint32_t* r) {
+__device__ __forceinline__ void tmem_load16(uint32_t taddr, uint32_t* r) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
       : "memory");
 }
+__device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_store16(uint32_t taddr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
@@ -231,15 +254,33 @@ __device__ __forceinline__ void tmem_store16(uint32_t taddr, const uint32_t* r) 
 }
 __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// D (tensor memory) = A (tensor memory) B (+ D), issued by one thread.
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                          bool accumulate) {
+// D (tensor memory) = A B^T (+ D), A in shared or in tensor memory. The whole warp comes here, converged and with
+// the same operands, and its leader issues: so the operands stay in uniform registers (issued under a branch for one
+// lane, each product cost 125 cycles to issue, twice what it takes).
+__device__ __forceinline__ void tree_mma_ss(uint32_t leader, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                            uint32_t idesc, bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred acc;\n\tsetp.ne.b32 acc, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, acc;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
+      "{\n\t.reg .pred acc, one;\n\tsetp.ne.b32 acc, %4, 0;\n\tsetp.ne.b32 one, %5, 0;\n\t"
+      "@one tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, acc;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate), "r"(leader)
       : "memory");
 }
+__device__ __forceinline__ void tree_mma_ts(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                            uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred acc, one;\n\tsetp.ne.b32 acc, %4, 0;\n\tsetp.ne.b32 one, %5, 0;\n\t"
+      "@one tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, acc;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void tree_commit(uint32_t leader, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred one;\n\tsetp.ne.b32 one, %1, 0;\n\t"
+      "@one tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 // M = 128; B transposed (its rows are the contracted ones) where `transpose`.
 __host__ __device__ constexpr uint32_t tree_idesc(bool bf16, int n, bool transpose) {
   return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((transpose ? 1u : 0u) << 16) |
@@ -313,19 +354,267 @@ __device__ __forceinline__ uint32_t seen_bits(const TreeParams& p, const TreeSeg
   return prefix | draft_bits(p, token, local, s.rows - s.base, -before);
 }
 
+template <int REGS>
+__device__ __forceinline__ void raise_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+template <int REGS>
+__device__ __forceinline__ void lower_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+
 // A row's softmax state: m for the output and the weights, ml for l (they differ with scales of V).
 struct TreeState {
   float m, ml, l;
 };
 
+// Tensor-memory column of the weights of cache row k of a tile (two to a column). In two pieces they lie by halves of
+// the tile, first pieces, then second ones: the half of the scores that is still to be read is not written over.
+template <int PIECES>
+__device__ __forceinline__ int weight_column(int k) {
+  return PIECES == 2 ? k / 64 * 64 + k % 64 / 2 : k / 2;
+}
+
+// COLS columns of scores, from column `col` on, to weights in tensor memory: the running maximum, the sum, and the
+// rescaling of the output where the maximum was raised. a: factor of a score (positive); seen(k): bits of the k-th 32
+// columns, looked at where `masked`. 8 bits: scales holds the factor that K's scale is and log2 |V's scale| of each 16
+// rows, sign (in lanes 0 to 7) the sign of V's scale or zero; PLAIN: all of K's are positive, and so are V's (a branch
+// for every 16 columns took 4000 cycles an item). Straight code, held in registers: as a loop over 32 columns at a time, read
+// twice, 128 columns took 4000 cycles instead of 1700.
+template <bool BF16, int D, bool EIGHT, int COLS, int PIECES, bool PLAIN, typename Seen>
+__device__ __forceinline__ void softmax_columns(TreeState& st, uint32_t s_at, uint32_t p_at, uint32_t o_at, int col,
+                                                bool first, float a, bool masked, const Seen& seen,
+                                                const float2* scales, float sign) {
+  // fp16 weights are held 2^7 times as large: the largest one of a row lies in [2^7, 2^15]
+  constexpr float kLift = BF16 ? 0.f : 7.f;
+  // (8 bits: fewer registers, 128 columns are read twice, by halves)
+  constexpr int kHold = EIGHT && COLS == 128 ? 64 : COLS;
+  // (a NaN of no other origin where factors may be zero or negative)
+  constexpr uint32_t kHidden = EIGHT && !PLAIN ? 0x7fdeadedu : 0xff800000u;
+  constexpr int kGroups = EIGHT ? kHold / 16 : 1, kPart = kHold / kGroups;
+  uint32_t r[kHold];
+  float ak[kGroups], vk[kGroups];
+  auto load = [&](int from) {
+#pragma unroll
+    for (int k = 0; k < kHold / 32; ++k) tmem_load32(s_at + col + from + 32 * k, r + 32 * k);
+    if constexpr (EIGHT) {
+#pragma unroll
+      for (int g = 0; g < kGroups; g += 2) {
+        const float4 x = *reinterpret_cast<const float4*>(scales + (col + from) / 16 + g);
+        ak[g] = PLAIN ? fmaxf(a * x.x, 1.2e-38f) : a * x.x;  // (never zero, which would make hidden scores NaN)
+        vk[g] = x.y;
+        ak[g + 1] = PLAIN ? fmaxf(a * x.z, 1.2e-38f) : a * x.z;
+        vk[g + 1] = x.w;
+      }
+    } else {
+      ak[0] = a;
+      vk[0] = 0.f;
+    }
+    tmem_wait_load();
+    if (masked) {
+#pragma unroll
+      for (int k = 0; k < kHold / 32; ++k) {
+        const uint32_t bits = seen(from / 32 + k);
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (!(bits >> i & 1)) r[32 * k + i] = kHidden;
+      }
+    }
+  };
+  float m_tile = -INFINITY, ml_tile = -INFINITY;
+#pragma unroll
+  for (int from = 0; from < COLS; from += kHold) {
+    load(from);
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int i = 0; i < kPart; i += 2)
+        top[i / 2 % 4] = fmaxf(fmaxf(__uint_as_float(r[kPart * g + i]), __uint_as_float(r[kPart * g + i + 1])), top[i / 2 % 4]);
+      top[0] = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+      if (EIGHT && !PLAIN && ak[g] < 0.f) {
+        top[0] = INFINITY;
+#pragma unroll
+        for (int i = 0; i < kPart; ++i) top[0] = fminf(top[0], __uint_as_float(r[kPart * g + i]));
+      }
+      // (nothing seen: no product with a factor that may be zero)
+      if (!EIGHT || PLAIN) {
+        top[0] *= ak[g];
+      } else {
+        top[0] = fabsf(top[0]) < INFINITY ? top[0] * ak[g] : top[0] == INFINITY && ak[g] > 0.f ? INFINITY : -INFINITY;
+      }
+      if constexpr (EIGHT) ml_tile = fmaxf(ml_tile, top[0]);
+      m_tile = fmaxf(m_tile, EIGHT ? top[0] + vk[g] : top[0]);
+    }
+  }
+  if constexpr (!EIGHT) ml_tile = m_tile;
+  // raise the maximum where a score passes it by 2^8 (or is the first one)
+  const bool up = m_tile > st.m + kTreeLazy || (st.m == -INFINITY && m_tile > -INFINITY);
+  if (__any_sync(0xffffffffu, up)) {
+    const float factor = !up ? 1.f : st.m == -INFINITY ? 0.f : fast_exp2(st.m - m_tile);
+    if (up) st.m = m_tile;
+    if constexpr (!EIGHT) st.l *= factor;
+    if (!first) {
+#pragma unroll 1
+      for (int k = 0; k < D; k += 16) {
+        uint32_t o[16];
+        tmem_load16(o_at + k, o);
+        tmem_wait_load();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * factor);
+        tmem_store16(o_at + k, o);
+      }
+    }
+  }
+  if constexpr (EIGHT) {
+    if (ml_tile > st.ml + kTreeLazy || (st.ml == -INFINITY && ml_tile > -INFINITY)) {
+      st.l *= st.ml == -INFINITY ? 0.f : fast_exp2(st.ml - ml_tile);
+      st.ml = ml_tile;
+    }
+  } else {
+    st.ml = st.m;
+  }
+  const float ref = st.m == -INFINITY ? 0.f : st.m - kLift;
+  const float lref = st.ml == -INFINITY ? 0.f : st.ml;
+#pragma unroll
+  for (int h = 0; h < COLS; h += 32) {
+    if (kHold < COLS && h % kHold == 0) load(h);
+    uint32_t hi[16];
+    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      const int at = h % kHold + i, g = EIGHT ? at / 16 : 0;
+      float2 y = __ffma2_rn(make_float2(__uint_as_float(r[at]), __uint_as_float(r[at + 1])),
+                            make_float2(ak[g], ak[g]), make_float2(vk[g] - ref, vk[g] - ref));
+      if (EIGHT && !PLAIN && masked) {
+        if (r[at] == kHidden) y.x = -INFINITY;
+        if (r[at + 1] == kHidden) y.y = -INFINITY;
+      }
+      y.x = fast_exp2(y.x);
+      y.y = fast_exp2(y.y);
+      sum[i / 16] = __fadd2_rn(sum[i / 16], y);
+      hi[i / 2] = pack2<BF16>(y.x, y.y);
+      if constexpr (PIECES == 2) {
+        r[at] = __float_as_uint(y.x);
+        r[at + 1] = __float_as_uint(y.y);
+      }
+    }
+    if constexpr (EIGHT) {
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        // l counts the weights without the scale of V
+        st.l += (sum[g].x + sum[g].y) * fast_exp2(fminf(ref - lref - vk[h % kHold / 16 + g], 126.f));
+        if constexpr (!PLAIN) {
+          const float sg = __shfl_sync(0xffffffffu, sign, (col + h) / 16 + g);
+          if (sg != 1.f) {
+#pragma unroll
+            for (int i = 8 * g; i < 8 * g + 8; ++i) hi[i] = sg == 0.f ? 0u : hi[i] ^ 0x80008000u;
+          }
+        }
+      }
+    } else {
+      st.l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+    }
+    tmem_store16(p_at + weight_column<PIECES>(col + h), hi);
+    if constexpr (PIECES == 2) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        hi[i] = pack2<true>(__uint_as_float(r[h + 2 * i]) - __uint_as_float(hi[i] << 16),
+                            __uint_as_float(r[h + 2 * i + 1]) - __uint_as_float(hi[i] & 0xffff0000u));
+      tmem_store16(p_at + weight_column<PIECES>(col + h) + 32, hi);
+    }
+  }
+  if constexpr (COLS < 128) {
+    // the other columns of this row belong to its copies
+    uint32_t none[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) none[i] = 0;
+#pragma unroll
+    for (int k = 0; k < 128; k += 32) {
+      if (k >= col && k < col + COLS) continue;
+      tmem_store16(p_at + weight_column<PIECES>(k), none);
+      if constexpr (PIECES == 2) tmem_store16(p_at + weight_column<PIECES>(k) + 32, none);
+    }
+  }
+  tmem_wait_store();
+}
+
+__device__ __forceinline__ unsigned arrive_acq_rel(unsigned* at) {
+  unsigned before;
+  asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(before) : "l"(at) : "memory");
+  return before;
+}
+__device__ __forceinline__ void store_release(unsigned* at, unsigned v) {
+  asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(at), "r"(v) : "memory");
+}
+__device__ __forceinline__ unsigned load_acquire(const unsigned* at) {
+  unsigned v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(at) : "memory");
+  return v;
+}
+
+// One row of a unit from its parts, by a warp: a lane for each part's state, then four columns a lane over the parts.
+// The first CTA's part is its second state, the others' their first.
+template <typename T, int D>
+__device__ __forceinline__ void tree_join_row(const TreeParams& p, const float* partials, const TreePending& x, int row,
+                                              int lane) {
+  constexpr int kLanes = D / 4, kAtOnce = 32 / kLanes;  // lanes of a row, parts that a warp reads side by side
+  auto slot = [&](int i) { return partials + ((int64_t)(x.c0 + i) * 2 + (i == 0 ? 1 : 0)) * tree_slot_floats(D); };
+  auto state = [&](int i) { return __ldcg(reinterpret_cast<const float4*>(slot(i) + kTreeUnitRows * D) + row); };
+  const float4 none = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
+  float m = -INFINITY, ml = -INFINITY, l = 0.f;
+  float4 s = none, acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = lane; i < x.parts; i += 32) {
+    s = state(i);
+    m = fmaxf(m, s.x);
+    ml = fmaxf(ml, s.y);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    ml = fmaxf(ml, __shfl_xor_sync(0xffffffffu, ml, o));
+  }
+  const float m0 = m == -INFINITY ? 0.f : m, ml0 = ml == -INFINITY ? 0.f : ml;
+  for (int base = 0; base < x.parts; base += 32) {
+    if (x.parts > 32) s = base + lane < x.parts ? state(base + lane) : none;
+    const float w = fast_exp2(s.x - m0);
+    l += s.z * fast_exp2(s.y - ml0);
+    const int n = min(32, x.parts - base);
+#pragma unroll 4
+    for (int i = 0; i < n; i += kAtOnce) {
+      const int k = i + lane / kLanes;
+      const float wk = __shfl_sync(0xffffffffu, w, min(k, 31));
+      if (k < n) {
+        const float4 o = __ldcg(reinterpret_cast<const float4*>(slot(base + k) + row * D) + lane % kLanes);
+        acc.x = fmaf(o.x, wk, acc.x);
+        acc.y = fmaf(o.y, wk, acc.y);
+        acc.z = fmaf(o.z, wk, acc.z);
+        acc.w = fmaf(o.w, wk, acc.w);
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  if constexpr (kAtOnce == 2) {
+    acc.x += __shfl_xor_sync(0xffffffffu, acc.x, 16);
+    acc.y += __shfl_xor_sync(0xffffffffu, acc.y, 16);
+    acc.z += __shfl_xor_sync(0xffffffffu, acc.z, 16);
+    acc.w += __shfl_xor_sync(0xffffffffu, acc.w, 16);
+  }
+  const float inv = l == 0.f ? 0.f : fast_exp2(m0 - ml0) / l;
+  const int shift = __ffs(p.group) - 1;
+  const int64_t at = ((int64_t)(x.token0 + (row >> shift)) * p.n_head + x.g * p.group + (row & (p.group - 1))) * D;
+  if (lane < kLanes)
+    *reinterpret_cast<uint2*>(p.out + (at + 4 * lane) * 2) =
+        make_uint2(pack2<Storage<T>::kBf16>(acc.x * inv, acc.y * inv), pack2<Storage<T>::kBf16>(acc.z * inv, acc.w * inv));
+}
+
 template <typename T, int D, bool EIGHT>
 __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
-    tree_kernel(const __grid_constant__ TreeLaunch launch, TreeJoin* joins, float* partials) {
+    tree_kernel(const __grid_constant__ TreeLaunch launch, TreeMeet* meets, float* partials) {
   using Shape = TreeShape<D, EIGHT>;
   using S = Storage<T>;
   constexpr bool kBf16 = S::kBf16 && !EIGHT;  // type of the products
-  // fp16 weights are held 2^7 times as large: the largest one of a row lies in [2^7, 2^15]
-  constexpr float kLift = kBf16 ? 0.f : 7.f;
   constexpr int kThreads = Shape::kThreads, kWarps = kThreads / 32;
   const TreeParams& p = launch.p;
   extern __shared__ uint8_t smem_raw[];
@@ -403,8 +692,15 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
       const int w = lane < kWarps ? c->sums[lane] : 0;
       const int at = before + __reduce_add_sync(0xffffffffu, lane < warp ? w : 0) + scan - v;
       if (begin >= at && begin < at + v) {
-        c->start_b = base + threadIdx.x;
-        c->start_off = begin - at;
+        const TreeSeq x = tree_sequence(p, base + threadIdx.x, &errors);
+        const int off = begin - at, unit = off / x.kt, head = unit / x.mps;
+        c->start[0] = base + threadIdx.x;
+        c->start[1] = x.first;
+        c->start[2] = x.n;
+        c->start[3] = x.rows;
+        c->start[4] = head;
+        c->start[5] = unit - head * x.mps;
+        c->start[6] = off - unit * x.kt;
       }
       before += __reduce_add_sync(0xffffffffu, w);
     }
@@ -412,11 +708,12 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
   }
   if (blockIdx.x == 0 && errors && p.err_flag) atomicOr(p.err_flag, errors);
   TreeCursor cursor;
-  cursor.begin(p, c->start_b, c->start_off, end - begin);
+  cursor.begin(p, c->start, end - begin);
   TreeSegment seg;
 
   if (warp == 8) {
     // ---------------- producer ----------------
+    lower_registers<Shape::kRegsOther>();
     const int step = min(p.page_rows, kTreeTile);  // rows of a page in a tile
     uint8_t* const pools[2] = {const_cast<uint8_t*>(p.k), const_cast<uint8_t*>(p.v)};
     constexpr int kStages = EIGHT ? Shape::kRaw : Shape::kSlots;
@@ -472,63 +769,93 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
     __syncwarp();
   } else if (warp == 9) {
     // ---------------- products ----------------
-    if (lane == 0) {
-      constexpr uint32_t kScores = tree_idesc(kBf16, kTreeTile, false), kOut = tree_idesc(kBf16, D, true);
-      int tau = 0, phase_p[2] = {0, 0};
-      bool ok = true;
-      for (int s = 0; ok && cursor.next(p, &seg); ++s) {
-        const bool two = seg.count > kTreeTile;
-        const int tiles = seg.t1 - seg.t0, items = two ? 2 * tiles : tiles;
-        ok = tree_wait(c, p, &c->q_full, s & 1);
-        for (int u = 0; ok && u <= items; ++u) {
-          if (u < items) {
-            const int use = 2 * (tau + (two ? u >> 1 : u)), slot = use % Shape::kSlots;
-            if (!two || !(u & 1)) ok = tree_wait(c, p, &c->full[slot], (use / Shape::kSlots) & 1);
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t a = sw128_desc_at(q_tiles + (two ? (u & 1) * Shape::kTileBytes : 0));
-            const uint64_t b = sw128_desc_at(ring + slot * Shape::kTileBytes);
+    lower_registers<Shape::kRegsOther>();
+    constexpr uint32_t kScores = tree_idesc(kBf16, kTreeTile, false), kOut = tree_idesc(kBf16, D, true);
+    const uint32_t leader = lane == 0;
+    const uint32_t tm = uniform(tmem), q0 = uniform(q_tiles), ring0 = uniform(ring), bars = uniform(smem_addr(c));
+    auto bar = [&](uint64_t* b) { return bars + (uint32_t)(reinterpret_cast<uint8_t*>(b) - reinterpret_cast<uint8_t*>(c)); };
+    int tau = 0, phase_p[2] = {0, 0};
+    bool ok = true;
+    for (int s = 0; ok && cursor.next(p, &seg); ++s) {
+      const bool two = uniform(seg.count) > kTreeTile;
+      const int tiles = uniform(seg.t1 - seg.t0), items = two ? 2 * tiles : tiles;
+      const int last_steps = (uniform(min(kTreeTile, seg.rows - (seg.t1 - 1) * kTreeTile)) + 15) / 16;
+      const bool pieces = kBf16 && Shape::kTwoPieces && !two;
+      ok = __all_sync(0xffffffffu, tree_wait(c, p, &c->q_full, s & 1));
+      for (int u = 0; ok && u <= items; ++u) {
+        if (u < items) {
+          const int use = 2 * (tau + (two ? u >> 1 : u)), slot = use % Shape::kSlots;
+          if (!two || !(u & 1)) ok = __all_sync(0xffffffffu, tree_wait(c, p, &c->full[slot], (use / Shape::kSlots) & 1));
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t a = sw128_desc_at(q0 + (two ? (u & 1) * Shape::kTileBytes : 0));
+          const uint64_t b = sw128_desc_at(ring0 + slot * Shape::kTileBytes);
+          const uint32_t to = tm + Shape::kS + (u & 1) * 128;
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const uint64_t off = (uint64_t)(((k / 4) * Shape::kBlockBytes + (k % 4) * 32) >> 4);
-              mma_f16_ss(tmem + Shape::kS + (u & 1) * 128, a + off, b + off, kScores, k > 0);
-            }
-            mma_commit(&c->s_full[u & 1]);
-            if (!two || (u & 1)) mma_commit(&c->empty[slot]);
+          for (int k = 0; k < D / 16; ++k) {
+            const uint64_t off = (uint64_t)(((k / 4) * Shape::kBlockBytes + (k % 4) * 32) >> 4);
+            tree_mma_ss(leader, to, a + off, b + off, kScores, k > 0);
           }
-          if (u > 0) {
-            const int v = u - 1, grp = v & 1, t = two ? v >> 1 : v;
-            const int use = 2 * (tau + t) + 1, slot = use % Shape::kSlots;
-            if (v == 0 && s > 0) ok = tree_wait(c, p, &c->o_free, (s - 1) & 1);
-            if (ok) ok = tree_wait(c, p, &c->full[slot], (use / Shape::kSlots) & 1);
-            if (ok) ok = tree_wait(c, p, &c->p_full[grp], phase_p[grp] & 1);
-            if (!ok) break;
-            ++phase_p[grp];
-            tc_fence_after();
-            const int steps = (min(kTreeTile, seg.rows - (seg.t0 + t) * kTreeTile) + 15) / 16;
-            const uint64_t b = sw128_desc_rows(ring + slot * Shape::kTileBytes, Shape::kBlockBytes);
-            for (int k = 0; k < steps; ++k)
-              mma_f16_ts(tmem + Shape::kO + grp * D, tmem + Shape::kP + grp * Shape::kPStride + k * 8,
-                         b + (uint64_t)((k * 2048) >> 4), kOut, v >= 2 || k > 0);
-            if (!two || (v & 1)) mma_commit(&c->empty[slot]);
-          }
+          tree_commit(leader, bar(&c->s_full[u & 1]));
+          if (!two || (u & 1)) tree_commit(leader, bar(&c->empty[slot]));
         }
-        if (!ok) break;
-        mma_commit(&c->o_final);
-        mbar_arrive(&c->o_final);
-        tau += tiles;
+        if (u > 0) {
+          const int v = u - 1, grp = v & 1, t = two ? v >> 1 : v;
+          const int use = 2 * (tau + t) + 1, slot = use % Shape::kSlots;
+          if (v == 0 && s > 0) ok = tree_wait(c, p, &c->o_free, (s - 1) & 1);
+          if (ok) ok = tree_wait(c, p, &c->full[slot], (use / Shape::kSlots) & 1);
+          if (ok) ok = tree_wait(c, p, &c->p_full[grp], phase_p[grp] & 1);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          ++phase_p[grp];
+          tc_fence_after();
+          const int steps = t == tiles - 1 ? last_steps : kTreeTile / 16;
+          const uint64_t b = sw128_desc_rows(ring0 + slot * Shape::kTileBytes, Shape::kBlockBytes);
+          const uint32_t weights = tm + Shape::kP + grp * Shape::kPStride, to = tm + Shape::kO + grp * D;
+          auto product = [&](int k, bool add) {
+            const uint64_t rows = b + (uint64_t)((k * 2048) >> 4);
+            tree_mma_ts(leader, to, weights + (pieces ? weight_column<2>(16 * k) : weight_column<1>(16 * k)), rows, kOut, add);
+            if (pieces) tree_mma_ts(leader, to, weights + weight_column<2>(16 * k) + 32, rows, kOut, true);
+          };
+          product(0, v >= 2);
+          if (steps == kTreeTile / 16) {
+#pragma unroll
+            for (int k = 1; k < kTreeTile / 16; ++k) product(k, true);
+          } else {
+#pragma unroll 1
+            for (int k = 1; k < steps; ++k) product(k, true);
+          }
+          if (!two || (v & 1)) tree_commit(leader, bar(&c->empty[slot]));
+        }
       }
-      if (!ok) {
-        // products in flight end before the memory is freed (bounded)
-        mma_commit(&c->drain);
-        mbar_wait(&c->drain, 0);
-      }
+      if (!ok) break;
+      tree_commit(leader, bar(&c->o_final));
+      if (lane == 0) mbar_arrive(&c->o_final);
+      __syncwarp();
+      tau += tiles;
+    }
+    if (!ok) {
+      // products in flight end before the memory is freed (bounded)
+      tree_commit(leader, bar(&c->drain));
+      mbar_wait(&c->drain, 0);
     }
     __syncwarp();
   } else if (warp >= 10) {
-    // ---------------- e4m3 to fp16 ----------------
-    if constexpr (EIGHT) {
-      const int th = threadIdx.x - 320;
+    // ---------------- e4m3 to fp16 (and two warps that complete a group) ----------------
+    lower_registers<Shape::kRegsOther>();
+    if (warp < 12) {
+      // sequences that are refused: NaN rows
+      for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+        int none = 0;
+        const TreeSeq x = tree_sequence(p, b, &none);
+        if (x.state >= 0) continue;
+        const uint32_t n = (uint32_t)S::kNaN * 0x10001u;
+        uint4* const out = reinterpret_cast<uint4*>(p.out + (int64_t)x.first * p.n_head * D * 2);
+        for (int64_t i = threadIdx.x - 320; i < (int64_t)x.n * p.n_head * (D / 8); i += 64) out[i] = make_uint4(n, n, n, n);
+      }
+    }
+    if constexpr (EIGHT) if (warp >= 12) {
+      const int th = threadIdx.x - 384;
       constexpr int kChunks = D / 16;  // 16-byte chunks of a raw row, and of a thread
       int use = 0;
       bool ok = true;
@@ -543,28 +870,8 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
             if (!ok) break;
             const uint8_t* const from = smem + Shape::kRawRing + raw * Shape::kRawBytes;
             uint8_t* const to = smem + Shape::kRing + slot * Shape::kTileBytes;
-            const bool special = kv == 1 && j0 + kTreeTile > seg.base;
-#pragma unroll
-            for (int i = 0; i < kChunks; ++i) {
-              const int idx = th + i * 128, r = idx / kChunks, ch = idx % kChunks;
-              uint4 x = ld_shared_v4(from + idx * 16);
-              if (special) {
-                uint32_t* const w = &x.x;
-                if (r >= valid) {
-                  x = make_uint4(0u, 0u, 0u, 0u);
-                } else if (j0 + r >= seg.base) {
-                  // drafted rows: NaN reaches only those who see it (added at the end)
-                  bool nan = false;
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    const uint32_t m = __vcmpeq4(w[k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                    nan |= m != 0;
-                    w[k] &= ~m;
-                  }
-                  const int d = j0 + r - seg.base;
-                  if (nan) atomicOr(&c->bad[s & 7][d >> 5], 1u << (d & 31));
-                }
-              }
+            auto convert = [&](const uint4& x, int idx) {
+              const int r = idx / kChunks, ch = idx % kChunks;
               uint32_t h[8];
               const uint32_t* const w = &x.x;
 #pragma unroll
@@ -574,6 +881,32 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
               }
               *reinterpret_cast<uint4*>(to + chunk_at<D>(r, 2 * ch)) = make_uint4(h[0], h[1], h[2], h[3]);
               *reinterpret_cast<uint4*>(to + chunk_at<D>(r, 2 * ch + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
+            };
+            if (kv == 0 || j0 + kTreeTile <= seg.base) {
+#pragma unroll
+              for (int i = 0; i < kChunks; ++i) convert(ld_shared_v4(from + (th + i * 128) * 16), th + i * 128);
+            } else {
+#pragma unroll 1
+              for (int i = 0; i < kChunks; ++i) {
+                const int idx = th + i * 128, r = idx / kChunks;
+                uint4 x = ld_shared_v4(from + idx * 16);
+                if (r >= valid) {
+                  x = make_uint4(0u, 0u, 0u, 0u);
+                } else if (j0 + r >= seg.base) {
+                  // drafted rows: NaN reaches only those who see it (added at the end)
+                  bool nan = false;
+                  uint32_t* const w = &x.x;
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    const uint32_t m = __vcmpeq4(w[k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                    nan |= m != 0;
+                    w[k] &= ~m;
+                  }
+                  const int d = j0 + r - seg.base;
+                  if (nan) atomicOr(&c->bad[s & 7][d >> 5], 1u << (d & 31));
+                }
+                convert(x, idx);
+              }
             }
             fence_proxy_async_shared();
             mbar_arrive(&c->full[slot]);
@@ -584,202 +917,162 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
     }
   } else {
     // ---------------- softmax and output ----------------
+    raise_registers<Shape::kRegsSoftmax>();
     const int grp = warp / 4, row = (warp % 4) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp % 4) * 32) << 16;
     const uint32_t s_at = tmem + lanes + Shape::kS + grp * 128, p_at = tmem + lanes + Shape::kP + grp * Shape::kPStride;
-    const uint32_t o_at = tmem + lanes + Shape::kO;  // outputs of group 0; of group 1 D columns on
-    const float qscale = fabsf(p.qscale);
-    const bool negate = p.qscale < 0.f;
+    const uint32_t o_at = tmem + lanes + Shape::kO + grp * D;
+    const bool negate = p.qscale < 0.f, flat = p.qscale == 0.f;
+    const int gshift = __ffs(p.group) - 1;
     int phase_s = 0, tau = 0;
     bool dead = false;
+    int pos = begin;  // of a segment's first tile among all tiles
+    if (threadIdx.x == 0) c->pendings = 0;
     for (int s = 0; cursor.next(p, &seg); ++s) {
       const bool two = seg.count > kTreeTile;
       const int tiles = seg.t1 - seg.t0, items = two ? 2 * tiles : tiles;
-      const int urow = (two ? grp * kTreeTile : 0) + row;  // row of the unit
+      // A unit of few rows has them several times in its tile: each copy takes its part of a cache tile's columns, so
+      // that all warps work on the exponentials.
+      const int copies = seg.count <= 32 ? 4 : seg.count <= 64 ? 2 : 1;
+      const int own = kTreeTile / copies;                  // rows of a copy, and columns it takes
+      const int urow = two ? grp * kTreeTile + row : row & (own - 1);
+      const int col = two ? 0 : row / own * own;
       const bool live = urow < seg.count;
       const bool busy = urow - lane < seg.count;           // any row of the warp
-      const int token = seg.token0 + urow / p.group, local = seg.local0 + urow / p.group;
-      const int head = seg.g * p.group + urow % p.group;
-      const int64_t out_row = ((int64_t)token * p.n_head + head) * D;
-      float a = qscale;  // of a score
-      // the query tile
+      const int token = seg.token0 + (urow >> gshift), local = seg.local0 + (urow >> gshift);
+      float a = flat ? 1.f : fabsf(p.qscale);  // of a score (flat: the query is zero)
+      int e_row = 14;
+      // The query tile: a warp brings its 32 rows, D / 8 lanes to a row.
       if (busy) {
-        const uint4* const from = reinterpret_cast<const uint4*>(p.q + out_row * 2);
+        constexpr int kRowLanes = D / 8, kStep = 32 / kRowLanes;  // lanes of a row, rows at once
         uint8_t* const to = smem + Shape::kQ + (two ? grp * Shape::kTileBytes : 0);
-        const bool writes = two || grp == 0;
-        uint4 x[D / 8];
+        const int ch = lane % kRowLanes, sub = lane / kRowLanes;
+        auto source = [&](int i, bool* there) {
+          const int r = urow - lane + i * kStep + sub;
+          *there = r < seg.count && !flat;
+          return p.q + (((int64_t)(seg.token0 + (r >> gshift)) * p.n_head + seg.g * p.group + (r & (p.group - 1))) * D + ch * 8) * 2;
+        };
+        auto target = [&](int i) { return to + chunk_at<D>((warp % 4) * 32 + i * kStep + sub, ch); };
+        if constexpr (!(EIGHT && S::kBf16)) {
+          if (two || grp == 0) {
+#pragma unroll 4
+            for (int i = 0; i < kRowLanes; ++i) {
+              bool there;
+              const uint8_t* const from = source(i, &there);
+              copy16_or_zero(smem_addr(target(i)), there ? from : p.q, there ? 16 : 0);
+            }
+            copy_commit();
+            copy_wait<0>();
+            if (negate) {
+              for (int i = 0; i < kRowLanes; ++i) {
+                uint4* const at = reinterpret_cast<uint4*>(target(i));
+                *at = make_uint4(at->x ^ 0x80008000u, at->y ^ 0x80008000u, at->z ^ 0x80008000u, at->w ^ 0x80008000u);
+              }
+            }
+          }
+        } else {
+          constexpr int kBatch = 8;
+#pragma unroll 1
+          for (int i0 = 0; i0 < kRowLanes; i0 += kBatch) {
+            uint4 x[kBatch];
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) x[i] = live ? ld_global_nc_v4(from + i) : make_uint4(0u, 0u, 0u, 0u);
-        uint32_t* const w = &x[0].x;
-        if constexpr (EIGHT && S::kBf16) {
-          // to fp16 with the row's largest element in [2^14, 2^15): exact above 2^-39 of it
-          uint32_t top = 0;
+            for (int i = 0; i < kBatch; ++i) {
+              bool there;
+              const uint8_t* const from = source(i0 + i, &there);
+              x[i] = there ? ld_global_nc_v4(from) : make_uint4(0u, 0u, 0u, 0u);
+            }
 #pragma unroll
-          for (int i = 0; i < D / 2; ++i) top = max(top, max(w[i] & 0x7fffu, w[i] >> 16 & 0x7fffu));
-          int e = (int)(top >> 7) - 127;  // exponent of the largest one
-          if (top == 0 || e == 128) e = 14;
-          const float up = __uint_as_float((uint32_t)(min(14 - e, 100) + 127) << 23);
-          const float more = __uint_as_float((uint32_t)(max(14 - e, 100) - 100 + 127) << 23);
+            for (int i = 0; i < kBatch; ++i) {
+              uint32_t* const w = &x[i].x;
+              // to fp16 with the row's largest element in [2^14, 2^15): exact above 2^-39 of it
+              uint32_t top = 0;
 #pragma unroll
-          for (int i = 0; i < D / 2; ++i)
-            w[i] = pack2<false>(__uint_as_float(w[i] << 16) * up * more, __uint_as_float(w[i] & 0xffff0000u) * up * more);
-          a = a / up / more;
-        }
-        if (negate) {
+              for (int k = 0; k < 4; ++k) top = max(top, max(w[k] & 0x7fffu, w[k] >> 16 & 0x7fffu));
 #pragma unroll
-          for (int i = 0; i < D / 2; ++i) w[i] ^= 0x80008000u;
-        }
-        if (writes) {
+              for (int o = kRowLanes / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+              int e = (int)(top >> 7) - 127;  // exponent of the largest one
+              if (top == 0 || e == 128) e = 14;
+              const float up = __uint_as_float((uint32_t)(min(14 - e, 100) + 127) << 23);
+              const float more = __uint_as_float((uint32_t)(max(14 - e, 100) - 100 + 127) << 23);
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i) *reinterpret_cast<uint4*>(to + chunk_at<D>(row, i)) = x[i];
+              for (int k = 0; k < 4; ++k) {
+                w[k] = pack2<false>(__uint_as_float(w[k] << 16) * up * more, __uint_as_float(w[k] & 0xffff0000u) * up * more);
+                if (negate) w[k] ^= 0x80008000u;
+              }
+              // to the row's own thread: row i * kStep + h of the warp was read by lanes [h * kRowLanes, ...)
+              const int own_e = __shfl_sync(0xffffffffu, e, (lane & (kStep - 1)) * kRowLanes);
+              if (lane / kStep == i0 + i) e_row = own_e;
+              if (two || grp == 0) *reinterpret_cast<uint4*>(target(i0 + i)) = x[i];
+            }
+          }
         }
       }
+      if constexpr (EIGHT && S::kBf16)
+        a = a / __uint_as_float((uint32_t)(min(14 - e_row, 100) + 127) << 23) /
+            __uint_as_float((uint32_t)(max(14 - e_row, 100) - 100 + 127) << 23);
       fence_proxy_async_shared();
       mbar_arrive(&c->q_full);
 
+      // Scales of 16 rows, in lanes 0 to 7, are on their way an item ahead, their pages' numbers two.
+      const int32_t* const table = p.table + (int64_t)seg.b * p.max_pages;
+      auto page_of = [&](int u) {
+        const int j = (seg.t0 + (two ? u >> 1 : u)) * kTreeTile + lane * 16;
+        return u < items && lane < 8 && j < seg.rows ? table[j >> p.page_shift] : -1;
+      };
+      int id_next = -1;
+      float k_next = 0.f, v_next = 0.f;
+      auto scales_of = [&](int id) {
+        const bool fine = id >= 0 && id < p.num_pages;
+        const int64_t at = (int64_t)id * p.n_kv_head + seg.g;
+        k_next = fine ? p.k_scale[at] : 0.f;
+        v_next = fine ? p.v_scale[at] : 1.f;
+        if (!fine) k_next = 1.f;  // (columns that nobody sees)
+      };
+      if constexpr (EIGHT) {
+        scales_of(page_of(grp));
+        id_next = page_of(grp + 2);
+      }
       TreeState st = {-INFINITY, -INFINITY, 0.f};
       for (int u = grp; u < items; u += 2) {
         const int t = seg.t0 + (two ? u >> 1 : u), j0 = t * kTreeTile;
         const bool masked = j0 + kTreeTile > seg.base;
-        float sk = 0.f, lv = 0.f, sv = 1.f;  // scales of 16 rows, in lanes 0 to 7
+        float sign = 1.f;
+        bool plain = true;
         if constexpr (EIGHT) {
-          if (lane < 8 && j0 + lane * 16 < seg.rows) {
-            const int id = p.table[(int64_t)seg.b * p.max_pages + ((j0 + lane * 16) >> p.page_shift)];
-            if (id >= 0 && id < p.num_pages) {
-              const int64_t at = (int64_t)id * p.n_kv_head + seg.g;
-              sk = p.k_scale[at];
-              const float v = p.v_scale[at];
-              lv = v == 0.f ? 0.f : log2f(fabsf(v));
-              sv = v == 0.f ? 0.f : v < 0.f ? -1.f : 1.f;
-            }
-          }
-        }
-        uint32_t seen[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
-        if (masked) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) seen[k] = live ? seen_bits(p, seg, token, local, j0 + 32 * k) : 0u;
+          sign = v_next == 0.f ? 0.f : v_next < 0.f ? -1.f : 1.f;
+          plain = __all_sync(0xffffffffu, lane >= 8 || (k_next > 0.f && sign == 1.f));
+          __syncwarp();
+          if (lane < 8) c->scales[warp][lane] = make_float2(k_next, v_next == 0.f ? 0.f : log2f(fabsf(v_next)));
+          __syncwarp();
+          scales_of(id_next);
+          id_next = page_of(u + 4);
         }
         if (!dead) dead = !__all_sync(0xffffffffu, tree_wait(c, p, &c->s_full[grp], phase_s & 1));
         ++phase_s;
         if (dead) continue;
         tc_fence_after();
         if (busy) {
-          uint32_t r[EIGHT ? 32 : 128];
-          float m_tile = -INFINITY, ml_tile = -INFINITY;
-          if constexpr (!EIGHT) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) tmem_load32(s_at + 32 * k, r + 32 * k);
-            tmem_wait_load();
-            if (masked) {
-#pragma unroll
-              for (int i = 0; i < 128; ++i)
-                if (!(seen[i / 32] >> (i % 32) & 1)) r[i] = 0xff800000u;
+          auto seen = [&](int k) { return live ? seen_bits(p, seg, token, local, j0 + col + 32 * k) : 0u; };
+          auto columns = [&](auto cols, auto pieces) {
+            constexpr int kCols = decltype(cols)::value, kPieces = decltype(pieces)::value;
+            const float2* const scales = c->scales[warp];
+            if (!EIGHT || plain) {
+              softmax_columns<kBf16, D, EIGHT, kCols, kPieces, true>(st, s_at, p_at, o_at, col, u < 2, a, masked, seen, scales, sign);
+            } else {
+              softmax_columns<kBf16, D, EIGHT, kCols, kPieces, !EIGHT>(st, s_at, p_at, o_at, col, u < 2, a, masked, seen, scales, sign);
             }
-            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int i = 0; i < 128; ++i) top[i % 4] = fmaxf(top[i % 4], __uint_as_float(r[i]));
-            const float top1 = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-            m_tile = top1 == -INFINITY ? -INFINITY : top1 * a;
-            ml_tile = m_tile;
+          };
+          using std::integral_constant;
+          constexpr integral_constant<int, kBf16 && Shape::kTwoPieces ? 2 : 1> kPieces;
+          if (two) {
+            columns(integral_constant<int, 128>(), integral_constant<int, 1>());
+          } else if (copies == 1) {
+            columns(integral_constant<int, 128>(), kPieces);
+          } else if (copies == 2) {
+            columns(integral_constant<int, 64>(), kPieces);
           } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              tmem_load32(s_at + 32 * k, r);
-              tmem_wait_load();
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const float ak = a * __shfl_sync(0xffffffffu, sk, 2 * k + h);
-                const float vk = __shfl_sync(0xffffffffu, lv, 2 * k + h);
-                const uint32_t bits = seen[k] >> (16 * h) & 0xffffu;
-                float top = -INFINITY;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  const float x = __uint_as_float(r[16 * h + i]) * ak;
-                  top = fmaxf(top, !masked || (bits >> i & 1) ? x : -INFINITY);
-                }
-                ml_tile = fmaxf(ml_tile, top);
-                m_tile = fmaxf(m_tile, top + vk);
-              }
-            }
+            columns(integral_constant<int, 32>(), kPieces);
           }
-          // raise the maximum where a score passes it by 2^8 (or is the first one)
-          const bool up = m_tile > st.m + kTreeLazy || (st.m == -INFINITY && m_tile > -INFINITY);
-          if (__any_sync(0xffffffffu, up)) {
-            const float factor = !up ? 1.f : st.m == -INFINITY ? 0.f : fast_exp2(st.m - m_tile);
-            if (up) st.m = m_tile;
-            if constexpr (!EIGHT) st.l *= factor;
-            if (u >= 2) {
-              uint32_t o[32];
-#pragma unroll
-              for (int k = 0; k < D / 32; ++k) {
-                tmem_load32(o_at + grp * D + 32 * k, o);
-                tmem_wait_load();
-#pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * factor);
-                tmem_store32(o_at + grp * D + 32 * k, o);
-              }
-            }
-          }
-          if constexpr (EIGHT) {
-            if (ml_tile > st.ml + kTreeLazy || (st.ml == -INFINITY && ml_tile > -INFINITY)) {
-              st.l *= st.ml == -INFINITY ? 0.f : fast_exp2(st.ml - ml_tile);
-              st.ml = ml_tile;
-            }
-          } else {
-            st.ml = st.m;
-          }
-          const float ref = st.m == -INFINITY ? 0.f : st.m - kLift;
-          if constexpr (!EIGHT) {
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int i = 0; i < 128; ++i) {
-              float x = fmaf(__uint_as_float(r[i]), a, -ref);
-              if (masked && !(seen[i / 32] >> (i % 32) & 1)) x = -INFINITY;
-              x = fast_exp2(x);
-              sum[i % 4] += x;
-              r[i] = __float_as_uint(x);
-            }
-            st.l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-#pragma unroll
-            for (int i = 0; i < 64; ++i)
-              r[i] = pack2<kBf16>(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
-            tmem_store32(p_at, r);
-            tmem_store32(p_at + 32, r + 32);
-          } else {
-            const float lref = st.ml == -INFINITY ? 0.f : st.ml;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              tmem_load32(s_at + 32 * k, r);
-              tmem_wait_load();
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const float ak = a * __shfl_sync(0xffffffffu, sk, 2 * k + h);
-                const float vk = __shfl_sync(0xffffffffu, lv, 2 * k + h);
-                const float sg = __shfl_sync(0xffffffffu, sv, 2 * k + h);
-                const uint32_t bits = seen[k] >> (16 * h) & 0xffffu;
-                float sum = 0.f;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  float x = fmaf(__uint_as_float(r[16 * h + i]), ak, vk - ref);
-                  if (masked && !(bits >> i & 1)) x = -INFINITY;
-                  x = fast_exp2(x);
-                  sum += x;
-                  r[16 * h + i] = __float_as_uint(x);
-                }
-                // l counts the weights without the scale of V
-                if (sum != 0.f) st.l += sum * fast_exp2(ref - lref - vk);
-                if (sg != 1.f) {
-#pragma unroll
-                  for (int i = 0; i < 16; ++i) r[16 * h + i] = __float_as_uint(__uint_as_float(r[16 * h + i]) * sg);
-                }
-              }
-#pragma unroll
-              for (int i = 0; i < 16; ++i)
-                r[i] = pack2<false>(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
-              tmem_store16(p_at + 16 * k, r);
-            }
-          }
-          tmem_wait_store();
         }
         if constexpr (!EIGHT) {
           // V rows behind the last one become zero, elements of drafted rows that are not finite too: they
@@ -818,139 +1111,182 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
       }
 
       // ---- the segment's output ----
-      if constexpr (EIGHT) st.m -= kLift;
+      if constexpr (EIGHT) st.m -= 7.f;  // (weights were held 2^7 times as large, and l was not)
       if (!dead) dead = !__all_sync(0xffffffffu, tree_wait(c, p, &c->o_final, s & 1));
       tc_fence_after();
-      bool nan = dead || c->bad_page[s & 7] != 0;
+      const bool nan = dead || c->bad_page[s & 7] != 0;
       const bool whole = seg.t0 == 0 && seg.t1 == seg.kt;
-      float w0 = 1.f, w1 = 0.f;
+      float* const slot = partials + ((int64_t)blockIdx.x * 2 + (seg.t0 == 0 ? 1 : 0)) * tree_slot_floats(D);
+      // Values of drafted V rows that are not finite, for a row that sees them: columns [at, at + 32) of o.
+      auto add_bad = [&](uint32_t (&o)[32], int at) {
+        for (int k = 0; k < 8; ++k) {
+          uint32_t left = c->bad[s & 7][k];
+          if (left) left &= draft_bits(p, token, local, seg.rows - seg.base, 32 * k);
+          for (; left; left &= left - 1) {
+            const int j = seg.base + 32 * k + __ffs(left) - 1;
+            if (j < seg.t0 * kTreeTile || j >= seg.t1 * kTreeTile) continue;
+            const int id = table[j >> p.page_shift];
+            if (id < 0 || id >= p.num_pages) continue;
+            const int64_t from = (((int64_t)id * p.n_kv_head + seg.g) * p.page_rows + (j & (p.page_rows - 1))) * D + at;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              float x;
+              if constexpr (EIGHT) {
+                x = (p.v[from + i] & 0x7f) == 0x7f ? NAN : 0.f;
+              } else {
+                x = (float)reinterpret_cast<const T*>(p.v)[from + i];
+              }
+              if (!(fabsf(x) < INFINITY)) o[i] = __float_as_uint(__uint_as_float(o[i]) + x);
+            }
+          }
+        }
+      };
+      bool any_bad = false;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) any_bad |= c->bad[s & 7][k] != 0;
+      // The state of the row: this thread's own (two), or that of both groups and of the copies.
+      float4* const states = reinterpret_cast<float4*>(smem + Shape::kStates);
+      float* const inverse = reinterpret_cast<float*>(states + 2 * kTreeTile);
+      float m = st.m, ml = st.ml, l = st.l, w0 = 1.f, w1 = 0.f;
       if (!two) {
-        // both groups have states of the same rows: each writes half of the columns
-        float4* const states = reinterpret_cast<float4*>(smem + Shape::kQ + Shape::kTileBytes);
+        const int groups = tiles > 1 ? 2 : 1;
         states[grp * kTreeTile + row] = make_float4(st.m, st.ml, st.l, 0.f);
         named_barrier_sync<1, 256>();
-        const float4 x = states[row], y = states[kTreeTile + row];
-        st.m = fmaxf(x.x, y.x);
-        st.ml = fmaxf(x.y, y.y);
-        const float m = st.m == -INFINITY ? 0.f : st.m, ml = st.ml == -INFINITY ? 0.f : st.ml;
-        w0 = fast_exp2(x.x - m);
-        w1 = fast_exp2(y.x - m);
-        st.l = x.z * fast_exp2(x.y - ml) + y.z * fast_exp2(y.y - ml);
-      }
-      const int c0 = two ? 0 : grp * (D / 2), c1 = two ? D : c0 + D / 2;
-      if (busy) {
-        const bool second = !two && tiles > 1;
-        const float inv = st.l == 0.f ? 0.f : (EIGHT ? fast_exp2(st.m - st.ml) : 1.f) / st.l;
-        // which drafted rows with values that are not finite this row sees
-        uint32_t bad[8], any = 0;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          bad[k] = c->bad[s & 7][k];
-          if (bad[k]) bad[k] &= draft_bits(p, token, local, seg.rows - seg.base, 32 * k);
-          any |= bad[k];
+        m = ml = -INFINITY;
+        l = 0.f;
+        for (int i = urow; i < groups * kTreeTile; i += own) {
+          m = fmaxf(m, states[i].x);
+          ml = fmaxf(ml, states[i].y);
         }
-        float* const slot = partials + ((int64_t)blockIdx.x * 2 + (seg.t0 == 0 ? 1 : 0)) * tree_slot_floats(D);
-        float4* const part = reinterpret_cast<float4*>(slot) + (two ? grp : 0) * (D / 4) * kTreeTile + row;
-        for (int col = c0; col < c1; col += 32) {
-          uint32_t o[32];
+        const float m0 = m == -INFINITY ? 0.f : m, ml0 = ml == -INFINITY ? 0.f : ml;
+        for (int i = urow; i < groups * kTreeTile; i += own) l += states[i].z * fast_exp2(states[i].y - ml0);
+        w0 = fast_exp2(states[row].x - m0);
+        w1 = groups > 1 ? fast_exp2(states[kTreeTile + row].x - m0) : 0.f;
+      }
+      const float inv = nan ? NAN : l == 0.f ? 0.f : (EIGHT ? fast_exp2(m - ml) : 1.f) / l;
+      const bool first_copy = two || row < own;
+      if (two || (grp == 0 && first_copy)) {
+        inverse[urow] = inv;
+        if (live && !whole) reinterpret_cast<float4*>(slot + kTreeUnitRows * D)[urow] = make_float4(m, ml, nan ? NAN : l, 0.f);
+      }
+      named_barrier_sync<1, 256>();
+      // 32 columns at a time through shared memory, so that rows are written in whole lines: of its own group's output
+      // (two), or of both groups' for half of the columns; copies are summed on the way out.
+      uint8_t* const exchange = smem + Shape::kExchange + (grp * kTreeTile) * 128;  // rows of this group
+      const int c0 = two ? 0 : grp * (D / 2), c1 = two ? D : c0 + D / 2;
+      const uint32_t o0 = two ? o_at : tmem + lanes + Shape::kO;
+#pragma unroll 1
+      for (int at = c0; at < c1; at += 32) {
+        if (busy) {
+          uint32_t o[32], o1[32];
           __syncwarp();
           if (!dead) {
-            tmem_load32(o_at + (two ? grp * D : 0) + col, o);
+            tmem_load32(o0 + at, o);
+            if (!two && tiles > 1) tmem_load32(o0 + D + at, o1);
             tmem_wait_load();
-            if (!two) {
+          }
+          if (!two) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * w0);
-              if (second) {
-                uint32_t o1[32];
-                tmem_load32(o_at + D + col, o1);
-                tmem_wait_load();
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * w0);
+            if (tiles > 1) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  o[i] = __float_as_uint(fmaf(__uint_as_float(o1[i]), w1, __uint_as_float(o[i])));
-              }
+              for (int i = 0; i < 32; ++i)
+                o[i] = __float_as_uint(fmaf(__uint_as_float(o1[i]), w1, __uint_as_float(o[i])));
             }
           }
-          if (any && live) {
+          if (any_bad && live && first_copy) add_bad(o, at);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              for (uint32_t left = bad[k]; left; left &= left - 1) {
-                const int j = seg.base + 32 * k + __ffs(left) - 1;
-                if (j < seg.t0 * kTreeTile || j >= seg.t1 * kTreeTile) continue;
-                const int id = p.table[(int64_t)seg.b * p.max_pages + (j >> p.page_shift)];
-                if (id < 0 || id >= p.num_pages) continue;
-                const int64_t at = (((int64_t)id * p.n_kv_head + seg.g) * p.page_rows + (j & (p.page_rows - 1))) * D + col;
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                  float x;
-                  if constexpr (EIGHT) {
-                    x = (p.v[at + i] & 0x7f) == 0x7f ? NAN : 0.f;
-                  } else {
-                    x = (float)reinterpret_cast<const T*>(p.v)[at + i];
-                  }
-                  if (!(fabsf(x) < INFINITY)) o[i] = __float_as_uint(__uint_as_float(o[i]) + x);
-                }
-              }
-            }
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<uint4*>(exchange + row * 128 + ((i ^ (row & 7)) << 4)) =
+                make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        }
+        if (two || copies == 1) __syncwarp(); else if (grp == 0) named_barrier_sync<3, 128>(); else named_barrier_sync<4, 128>();
+        // (a warp's own rows, or the group's first copy)
+        const int from = two || copies == 1 ? row - lane : 0, rows = two || copies == 1 ? 32 : own;
+        const int th = two || copies == 1 ? lane : (int)threadIdx.x % 128, step = two || copies == 1 ? 4 : 16;
+        for (int r = from + th / 8; r < from + rows; r += step) {
+          const int ur = (two ? grp * kTreeTile : 0) + r, ch = th % 8;
+          if (ur >= seg.count) break;
+          float4 sum = *reinterpret_cast<const float4*>(exchange + r * 128 + ((ch ^ (r & 7)) << 4));
+          for (int k = r + own; copies > 1 && k < kTreeTile; k += own) {
+            const float4 x = *reinterpret_cast<const float4*>(exchange + k * 128 + ((ch ^ (r & 7)) << 4));
+            sum.x += x.x;
+            sum.y += x.y;
+            sum.z += x.z;
+            sum.w += x.w;
           }
-          if (live && whole) {
-            uint32_t h[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float x = nan ? NAN : __uint_as_float(o[2 * i]) * inv, y = nan ? NAN : __uint_as_float(o[2 * i + 1]) * inv;
-              h[i] = pack2<S::kBf16>(x, y);
-            }
-            uint4* const out = reinterpret_cast<uint4*>(p.out + (out_row + col) * 2);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) out[i] = make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
-          } else if (live) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              part[(col / 4 + i) * kTreeTile] =
-                  make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]), __uint_as_float(o[4 * i + 2]),
-                              __uint_as_float(o[4 * i + 3]));
+          if (whole) {
+            const float f = inverse[ur];
+            const int64_t to = ((int64_t)(seg.token0 + (ur >> gshift)) * p.n_head + seg.g * p.group + (ur & (p.group - 1))) * D;
+            *reinterpret_cast<uint2*>(p.out + (to + at + 4 * ch) * 2) =
+                make_uint2(pack2<S::kBf16>(sum.x * f, sum.y * f), pack2<S::kBf16>(sum.z * f, sum.w * f));
+          } else {
+            *reinterpret_cast<float4*>(slot + ur * D + at + 4 * ch) = sum;
           }
         }
-        if (!whole && live && c0 == 0)
-          reinterpret_cast<float4*>(slot + kTreeUnitRows * D)[urow] = make_float4(st.m, st.ml, nan ? NAN : st.l, 0.f);
+        if (two || copies == 1) __syncwarp(); else if (grp == 0) named_barrier_sync<3, 128>(); else named_barrier_sync<4, 128>();
       }
       tc_fence_before();
       named_barrier_sync<2, 256>();  // the states, and the notes on the segment's rows, have been read
       if (threadIdx.x < 8) c->bad[s & 7][threadIdx.x] = 0;
       if (threadIdx.x == 0) c->bad_page[s & 7] = 0;
       mbar_arrive(&c->o_free);
+      if (!whole && threadIdx.x == 0) {
+        // this CTA's part of the unit is written: arrive where its CTAs meet
+        const int ctas = min((int)gridDim.x, total);
+        auto owner = [&](int64_t tile) { return (int)(((tile + 1) * ctas + total - 1) / total) - 1; };
+        TreePending x;
+        x.c0 = seg.t0 == 0 ? (int)blockIdx.x : owner((int64_t)pos - seg.t0);
+        x.parts = owner((int64_t)pos - seg.t0 + seg.kt - 1) - x.c0 + 1;
+        x.rows = seg.count;
+        x.token0 = seg.token0;
+        x.g = seg.g;
+        TreeMeet* const meet = meets + x.c0;
+        x.generation = *reinterpret_cast<volatile unsigned*>(&meet->generation);
+        const unsigned before = arrive_acq_rel(&meet->arrived);
+        x.last = before + 1 == (unsigned)x.parts;
+        if (before >= (unsigned)x.parts && p.err_flag) atomicOr(p.err_flag, kErrWorkspace);
+        if (x.last) {
+          meet->arrived = 0;
+          meet->ticket = 0;
+          store_release(&meet->generation, x.generation + 1);
+        }
+        c->pending[c->pendings++] = x;
+      }
+      pos += tiles;
       tau += tiles;
+    }
+    named_barrier_sync<2, 256>();
+    const int pendings = c->pendings;
+    for (int i = 0; i < pendings; ++i) {
+      const TreePending x = c->pending[i];
+      TreeMeet* const meet = meets + x.c0;
+      named_barrier_sync<1, 256>();
+      if (threadIdx.x == 0) {
+        // The last to arrive joins the unit. The others wait for it a while, to help: it does without them, so that no
+        // CTA depends on another one being there.
+        bool ready = x.last;
+        const unsigned long long t0 = global_ns();
+        while (!ready && global_ns() - t0 < kTreeHelpNs) ready = load_acquire(&meet->generation) != x.generation;
+        c->ready = ready;
+      }
+      named_barrier_sync<1, 256>();
+      if (!c->ready) continue;
+      const int share = max(16, ((x.rows + x.parts - 1) / x.parts + 7) & ~7), shares = (x.rows + share - 1) / share;
+      for (;;) {
+        if (threadIdx.x == 0) c->ticket = (int)atomicAdd(&meet->ticket, 1u);
+        named_barrier_sync<1, 256>();
+        const int ticket = c->ticket;
+        named_barrier_sync<1, 256>();
+        if (ticket >= shares) break;
+        for (int r = ticket * share + warp; r < min(x.rows, (ticket + 1) * share); r += 8)
+          tree_join_row<T, D>(p, partials, x, r, lane);
+      }
     }
   }
   __syncthreads();
   tc_fence_after();
   if (warp == 9) tmem_free(tmem, 512);
-
-  // What the merge has to join, as far as this CTA begins it: its last unit, if it does not finish it.
-  if (threadIdx.x == 0) {
-    TreeJoin join = {0, 0, 0, 0};
-    TreeCursor walk;
-    walk.begin(p, c->start_b, c->start_off, end - begin);
-    while (walk.next(p, &seg)) {
-      if (seg.t0 == 0 && seg.t1 < seg.kt) {
-        const int ctas = min((int)gridDim.x, total);
-        const int64_t last_tile = (int64_t)end - seg.t1 + seg.kt - 1;  // of the unit, among all tiles
-        join.token0 = seg.token0;
-        join.rows = seg.count;
-        join.g = seg.g;
-        join.last = (int)(((last_tile + 1) * ctas + total - 1) / total) - 1;
-      }
-    }
-    joins[blockIdx.x] = join;
-  }
-  // Sequences that are refused: NaN rows.
-  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-    int none = 0;
-    const TreeSeq x = tree_sequence(p, b, &none);
-    if (x.state >= 0) continue;
-    const uint32_t n = (uint32_t)S::kNaN * 0x10001u;
-    uint4* const out = reinterpret_cast<uint4*>(p.out + (int64_t)x.first * p.n_head * D * 2);
-    for (int64_t i = threadIdx.x; i < (int64_t)x.n * p.n_head * (D / 8); i += kThreads) out[i] = make_uint4(n, n, n, n);
-  }
 }
 
 }  // namespace da
