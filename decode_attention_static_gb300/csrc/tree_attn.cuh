@@ -21,6 +21,7 @@
 // one group's exponentials run under the other's products.
 #pragma once
 
+#include <stddef.h>
 #include <stdint.h>
 
 #include <type_traits>
@@ -33,6 +34,8 @@ namespace da {
 constexpr int kTreeTile = 128;             // cache rows of a tile, query rows of a tile
 constexpr int kTreeUnitRows = 256;         // query rows of a unit
 constexpr unsigned long long kTreeHelpNs = 20000;  // how long a CTA waits for a unit's other parts, to help with their join
+constexpr int kTreeMinTiles = 1;            // a part of a unit has at least as many tiles
+constexpr int kTreeJoinTiles = 8;           // what the ends of a share inside units cost, in tiles (at most the warps)
 constexpr float kTreeLazy = 8.f;           // a running maximum is raised when a score passes it by 2^8
 
 // A partial state: O [256][D], then (m, m of l, l) [256] float4.
@@ -93,16 +96,19 @@ struct TreeControl {
   uint64_t s_full[2], p_full[2], q_full, o_final, o_free, drain;
   uint32_t tmem;
   int abort;
-  int start[8];           // of this CTA's tiles: sequence, its first token, tokens, rows; KV head, unit, tile
+  int start[8];           // of this CTA's tiles: sequence, its first token, tokens, rows; KV head, unit, tile; tiles
+  int piece, pieces;      // ... as a part of its unit
+  int counts[16];
   TreePending pending[2];
   int pendings, ready, ticket;
-  float2 scales[8][8];    // 8 bits: of a warp's column groups: factor of a score, log2 of V's scale
+  int16_t exponent[kTreeTile];  // 8 bits: of a query row's largest element
+  alignas(16) float2 scales[8][8];  // 8 bits: of a warp's column groups: factor of a score, log2 of V's scale
   int sums[16];
   // of segment s, in entry s % 8: drafted rows whose V is not finite, and whether a page lies outside the pool
   uint32_t bad[8][8];
   int bad_page[8];
 };
-static_assert(sizeof(TreeControl) <= 2048, "control area");
+static_assert(sizeof(TreeControl) <= 2048 && offsetof(TreeControl, scales) % 16 == 0, "control area");
 static_assert(128 * (2 * 224 + 56) <= 384 * 168 && 128 * (2 * 192 + 2 * 64) <= 512 * 128, "registers of the launch");
 
 // Tokens and rows of a sequence; kt tiles for each of mps units a KV head.
@@ -553,60 +559,52 @@ __device__ __forceinline__ unsigned load_acquire(const unsigned* at) {
   return v;
 }
 
-// One row of a unit from its parts, by a warp: a lane for each part's state, then four columns a lane over the parts.
-// The first CTA's part is its second state, the others' their first.
+// Rows [r0, r1) of a unit from its parts, by the 256 softmax threads: the parts' weights of each row into shared memory
+// (a thread for each row), then four columns a thread over the parts. The first CTA's part is its second state, the
+// others' their first.
 template <typename T, int D>
-__device__ __forceinline__ void tree_join_row(const TreeParams& p, const float* partials, const TreePending& x, int row,
-                                              int lane) {
-  constexpr int kLanes = D / 4, kAtOnce = 32 / kLanes;  // lanes of a row, parts that a warp reads side by side
+__device__ __forceinline__ void tree_join_rows(const TreeParams& p, const float* partials, const TreePending& x, int r0,
+                                               int r1, float* weights) {
+  const int rows = r1 - r0, parts = x.parts;
   auto slot = [&](int i) { return partials + ((int64_t)(x.c0 + i) * 2 + (i == 0 ? 1 : 0)) * tree_slot_floats(D); };
-  auto state = [&](int i) { return __ldcg(reinterpret_cast<const float4*>(slot(i) + kTreeUnitRows * D) + row); };
-  const float4 none = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
-  float m = -INFINITY, ml = -INFINITY, l = 0.f;
-  float4 s = none, acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i = lane; i < x.parts; i += 32) {
-    s = state(i);
-    m = fmaxf(m, s.x);
-    ml = fmaxf(ml, s.y);
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    ml = fmaxf(ml, __shfl_xor_sync(0xffffffffu, ml, o));
-  }
-  const float m0 = m == -INFINITY ? 0.f : m, ml0 = ml == -INFINITY ? 0.f : ml;
-  for (int base = 0; base < x.parts; base += 32) {
-    if (x.parts > 32) s = base + lane < x.parts ? state(base + lane) : none;
-    const float w = fast_exp2(s.x - m0);
-    l += s.z * fast_exp2(s.y - ml0);
-    const int n = min(32, x.parts - base);
+  for (int r = threadIdx.x; r < rows; r += 256) {
+    auto state = [&](int i) { return __ldcg(reinterpret_cast<const float4*>(slot(i) + kTreeUnitRows * D) + r0 + r); };
+    float m = -INFINITY, ml = -INFINITY, l = 0.f;
 #pragma unroll 4
-    for (int i = 0; i < n; i += kAtOnce) {
-      const int k = i + lane / kLanes;
-      const float wk = __shfl_sync(0xffffffffu, w, min(k, 31));
-      if (k < n) {
-        const float4 o = __ldcg(reinterpret_cast<const float4*>(slot(base + k) + row * D) + lane % kLanes);
-        acc.x = fmaf(o.x, wk, acc.x);
-        acc.y = fmaf(o.y, wk, acc.y);
-        acc.z = fmaf(o.z, wk, acc.z);
-        acc.w = fmaf(o.w, wk, acc.w);
-      }
+    for (int i = 0; i < parts; ++i) {
+      const float4 s = state(i);
+      m = fmaxf(m, s.x);
+      ml = fmaxf(ml, s.y);
     }
+    const float m0 = m == -INFINITY ? 0.f : m, ml0 = ml == -INFINITY ? 0.f : ml;
+#pragma unroll 4
+    for (int i = 0; i < parts; ++i) {
+      const float4 s = state(i);
+      weights[i * rows + r] = fast_exp2(s.x - m0);
+      l += s.z * fast_exp2(s.y - ml0);
+    }
+    weights[parts * rows + r] = l == 0.f ? 0.f : fast_exp2(m0 - ml0) / l;
   }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  if constexpr (kAtOnce == 2) {
-    acc.x += __shfl_xor_sync(0xffffffffu, acc.x, 16);
-    acc.y += __shfl_xor_sync(0xffffffffu, acc.y, 16);
-    acc.z += __shfl_xor_sync(0xffffffffu, acc.z, 16);
-    acc.w += __shfl_xor_sync(0xffffffffu, acc.w, 16);
-  }
-  const float inv = l == 0.f ? 0.f : fast_exp2(m0 - ml0) / l;
-  const int shift = __ffs(p.group) - 1;
-  const int64_t at = ((int64_t)(x.token0 + (row >> shift)) * p.n_head + x.g * p.group + (row & (p.group - 1))) * D;
-  if (lane < kLanes)
-    *reinterpret_cast<uint2*>(p.out + (at + 4 * lane) * 2) =
+  named_barrier_sync<1, 256>();
+  const int shift = __ffs(p.group) - 1, col = threadIdx.x % (D / 4);
+#pragma unroll 2
+  for (int r = threadIdx.x / (D / 4); r < rows; r += 256 / (D / 4)) {
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = 0; i < parts; ++i) {
+      const float4 o = __ldcg(reinterpret_cast<const float4*>(slot(i) + (r0 + r) * D) + col);
+      const float w = weights[i * rows + r];
+      acc.x = fmaf(o.x, w, acc.x);
+      acc.y = fmaf(o.y, w, acc.y);
+      acc.z = fmaf(o.z, w, acc.z);
+      acc.w = fmaf(o.w, w, acc.w);
+    }
+    const float inv = weights[parts * rows + r];
+    const int row = r0 + r;
+    const int64_t at = ((int64_t)(x.token0 + (row >> shift)) * p.n_head + x.g * p.group + (row & (p.group - 1))) * D;
+    *reinterpret_cast<uint2*>(p.out + (at + 4 * col) * 2) =
         make_uint2(pack2<Storage<T>::kBf16>(acc.x * inv, acc.y * inv), pack2<Storage<T>::kBf16>(acc.z * inv, acc.w * inv));
+  }
 }
 
 template <typename T, int D, bool EIGHT>
@@ -657,29 +655,67 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
   pdl_wait();
   pdl_trigger();
 
-  // This CTA's share of all tiles, and where it begins.
-  int errors = 0, begin = 0, end = 0, total = 0;
+  // This CTA's share of all tiles, and where it begins: an even share of the list of all units' tiles, or a part of one
+  // unit. Even shares end and begin inside units, which costs a CTA two partial states and joins, as long as some
+  // kTreeJoinTiles tiles: so every unit is cut into parts of its own, a CTA each, where the largest part is not longer
+  // than an even share by that much (and there are not more parts than CTAs).
+  int errors = 0, begin = 0, end = 0, total = 0, part_tiles = 0;
   {
-    auto tiles_of = [&](int b) {
+    auto units_of = [&](int b, int* kt) {
+      *kt = 1;
       if (b >= p.B) return 0;
       const TreeSeq s = tree_sequence(p, b, &errors);
-      return p.n_kv_head * s.mps * s.kt;
+      if (s.kt) *kt = s.kt;
+      return s.kt ? p.n_kv_head * s.mps : 0;
     };
-    const int mine = tiles_of(threadIdx.x);
-    int sum = mine;
-    for (int b = threadIdx.x + kThreads; b < p.B; b += kThreads) sum += tiles_of(b);
+    int my_kt, kt;
+    const int my_units = units_of(threadIdx.x, &my_kt);
+    int sum = my_units * my_kt, units = my_units;
+    for (int b = threadIdx.x + kThreads; b < p.B; b += kThreads) {
+      const int n = units_of(b, &kt);
+      sum += n * kt;
+      units += n;
+    }
+    // the sequences' units and tiles, as far as one pass goes, for the search of the parts' size
+    int2* const table = reinterpret_cast<int2*>(smem + Shape::kQ);
+    table[threadIdx.x] = make_int2(my_units, my_kt);
     sum = __reduce_add_sync(0xffffffffu, sum);
-    if (lane == 0) c->sums[warp] = sum;
+    units = __reduce_add_sync(0xffffffffu, units);
+    if (lane == 0) {
+      c->sums[warp] = sum;
+      c->counts[warp] = units;
+    }
     __syncthreads();
     total = __reduce_add_sync(0xffffffffu, lane < kWarps ? c->sums[lane] : 0);
-    const int ctas = min((int)gridDim.x, total);
-    if ((int)blockIdx.x < ctas) {
-      begin = (int)((int64_t)total * blockIdx.x / ctas);
-      end = (int)((int64_t)total * (blockIdx.x + 1) / ctas);
+    units = __reduce_add_sync(0xffffffffu, lane < kWarps ? c->counts[lane] : 0);
+    const int grid = gridDim.x, share = max((total + grid - 1) / grid, kTreeMinTiles);
+    if (units <= grid && p.B <= kThreads) {  // (the same in every thread)
+      // one candidate for each warp: share, share + 1, ...
+      int parts = 0;
+      for (int i = lane; i < p.B; i += 32) parts += table[i].x * ((table[i].y + share + warp - 1) / (share + warp));
+      parts = __reduce_add_sync(0xffffffffu, parts);
+      __syncthreads();
+      if (lane == 0) c->counts[warp] = parts;
+      __syncthreads();
+      const uint32_t fits = __ballot_sync(0xffffffffu, lane < kTreeJoinTiles && c->counts[lane] <= grid);
+      if (fits) part_tiles = share + __ffs(fits) - 1;
+    }
+    const int ctas = min(grid, total);
+    int want = blockIdx.x;  // the part, or the first tile
+    if (part_tiles == 0) {
+      if ((int)blockIdx.x < ctas) {
+        begin = (int)((int64_t)total * blockIdx.x / ctas);
+        end = (int)((int64_t)total * (blockIdx.x + 1) / ctas);
+      }
+      want = begin;
     }
     int before = 0;
-    for (int base = 0; base < p.B && before <= begin && end > 0; base += kThreads) {
-      const int v = base == 0 ? mine : tiles_of(base + threadIdx.x);
+    if (threadIdx.x == 0) c->start[7] = 0;
+    for (int base = 0; base < p.B && before <= want && (end > 0 || part_tiles > 0); base += kThreads) {
+      int n = my_units;
+      kt = my_kt;
+      if (base > 0) n = units_of(base + threadIdx.x, &kt);
+      const int pieces = part_tiles > 0 ? (kt + part_tiles - 1) / part_tiles : kt, v = n * pieces;
       int scan = v;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -691,16 +727,21 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
       __syncthreads();
       const int w = lane < kWarps ? c->sums[lane] : 0;
       const int at = before + __reduce_add_sync(0xffffffffu, lane < warp ? w : 0) + scan - v;
-      if (begin >= at && begin < at + v) {
-        const TreeSeq x = tree_sequence(p, base + threadIdx.x, &errors);
-        const int off = begin - at, unit = off / x.kt, head = unit / x.mps;
+      if (want >= at && want < at + v) {
+        int none = 0;
+        const TreeSeq x = tree_sequence(p, base + threadIdx.x, &none);
+        const int off = want - at, unit = off / pieces, piece = off - unit * pieces, head = unit / x.mps;
         c->start[0] = base + threadIdx.x;
         c->start[1] = x.first;
         c->start[2] = x.n;
         c->start[3] = x.rows;
         c->start[4] = head;
         c->start[5] = unit - head * x.mps;
-        c->start[6] = off - unit * x.kt;
+        c->start[6] = part_tiles > 0 ? (int)((int64_t)x.kt * piece / pieces) : piece;
+        // tiles of the part; its number and how many there are
+        c->start[7] = part_tiles > 0 ? (int)((int64_t)x.kt * (piece + 1) / pieces) - c->start[6] : end - begin;
+        c->piece = piece;
+        c->pieces = pieces;
       }
       before += __reduce_add_sync(0xffffffffu, w);
     }
@@ -708,7 +749,7 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
   }
   if (blockIdx.x == 0 && errors && p.err_flag) atomicOr(p.err_flag, errors);
   TreeCursor cursor;
-  cursor.begin(p, c->start, end - begin);
+  cursor.begin(p, c->start, c->start[7]);
   TreeSegment seg;
 
   if (warp == 8) {
@@ -953,59 +994,52 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
           return p.q + (((int64_t)(seg.token0 + (r >> gshift)) * p.n_head + seg.g * p.group + (r & (p.group - 1))) * D + ch * 8) * 2;
         };
         auto target = [&](int i) { return to + chunk_at<D>((warp % 4) * 32 + i * kStep + sub, ch); };
-        if constexpr (!(EIGHT && S::kBf16)) {
-          if (two || grp == 0) {
+        if (two || grp == 0) {
 #pragma unroll 4
-            for (int i = 0; i < kRowLanes; ++i) {
-              bool there;
-              const uint8_t* const from = source(i, &there);
-              copy16_or_zero(smem_addr(target(i)), there ? from : p.q, there ? 16 : 0);
-            }
-            copy_commit();
-            copy_wait<0>();
-            if (negate) {
-              for (int i = 0; i < kRowLanes; ++i) {
-                uint4* const at = reinterpret_cast<uint4*>(target(i));
-                *at = make_uint4(at->x ^ 0x80008000u, at->y ^ 0x80008000u, at->z ^ 0x80008000u, at->w ^ 0x80008000u);
-              }
-            }
+          for (int i = 0; i < kRowLanes; ++i) {
+            bool there;
+            const uint8_t* const from = source(i, &there);
+            copy16_or_zero(smem_addr(target(i)), there ? from : p.q, there ? 16 : 0);
           }
-        } else {
-          constexpr int kBatch = 8;
-#pragma unroll 1
-          for (int i0 = 0; i0 < kRowLanes; i0 += kBatch) {
-            uint4 x[kBatch];
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-              bool there;
-              const uint8_t* const from = source(i0 + i, &there);
-              x[i] = there ? ld_global_nc_v4(from) : make_uint4(0u, 0u, 0u, 0u);
+          copy_commit();
+          copy_wait<0>();
+          if (EIGHT && S::kBf16) {
+            // To fp16 with the row's largest element in [2^14, 2^15), exact above 2^-39 of it: a thread its own row.
+            __syncwarp();
+            uint32_t top = 0;
+            auto at = [&](int i) { return reinterpret_cast<uint4*>(to + chunk_at<D>(row, i)); };
+#pragma unroll 4
+            for (int i = 0; i < D / 8; ++i) {
+              const uint4 x = *at(i);
+              top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                                           __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
             }
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-              uint32_t* const w = &x[i].x;
-              // to fp16 with the row's largest element in [2^14, 2^15): exact above 2^-39 of it
-              uint32_t top = 0;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) top = max(top, max(w[k] & 0x7fffu, w[k] >> 16 & 0x7fffu));
-#pragma unroll
-              for (int o = kRowLanes / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-              int e = (int)(top >> 7) - 127;  // exponent of the largest one
-              if (top == 0 || e == 128) e = 14;
-              const float up = __uint_as_float((uint32_t)(min(14 - e, 100) + 127) << 23);
-              const float more = __uint_as_float((uint32_t)(max(14 - e, 100) - 100 + 127) << 23);
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                w[k] = pack2<false>(__uint_as_float(w[k] << 16) * up * more, __uint_as_float(w[k] & 0xffff0000u) * up * more);
-                if (negate) w[k] ^= 0x80008000u;
-              }
-              // to the row's own thread: row i * kStep + h of the warp was read by lanes [h * kRowLanes, ...)
-              const int own_e = __shfl_sync(0xffffffffu, e, (lane & (kStep - 1)) * kRowLanes);
-              if (lane / kStep == i0 + i) e_row = own_e;
-              if (two || grp == 0) *reinterpret_cast<uint4*>(target(i0 + i)) = x[i];
+            top = max(top & 0xffffu, top >> 16);
+            if (top != 0 && (int)(top >> 7) != 255) e_row = (int)(top >> 7) - 127;  // exponent of the largest one
+            const float up = __uint_as_float((uint32_t)(min(14 - e_row, 100) + 127) << 23);
+            const float more = __uint_as_float((uint32_t)(max(14 - e_row, 100) - 100 + 127) << 23);
+            auto half2 = [&](uint32_t w) {
+              return pack2<false>(__uint_as_float(w << 16) * up * more, __uint_as_float(w & 0xffff0000u) * up * more);
+            };
+#pragma unroll 4
+            for (int i = 0; i < D / 8; ++i) {
+              const uint4 x = *at(i);
+              *at(i) = make_uint4(half2(x.x), half2(x.y), half2(x.z), half2(x.w));
+            }
+            if (!two) c->exponent[row] = (int16_t)e_row;
+            __syncwarp();
+          }
+          if (negate) {
+            for (int i = 0; i < kRowLanes; ++i) {
+              uint4* const at = reinterpret_cast<uint4*>(target(i));
+              *at = make_uint4(at->x ^ 0x80008000u, at->y ^ 0x80008000u, at->z ^ 0x80008000u, at->w ^ 0x80008000u);
             }
           }
         }
+      }
+      if (EIGHT && S::kBf16 && !two) {
+        named_barrier_sync<1, 256>();  // the groups share the query tile
+        e_row = c->exponent[row];
       }
       if constexpr (EIGHT && S::kBf16)
         a = a / __uint_as_float((uint32_t)(min(14 - e_row, 100) + 127) << 23) /
@@ -1031,6 +1065,24 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
       if constexpr (EIGHT) {
         scales_of(page_of(grp));
         id_next = page_of(grp + 2);
+      }
+      const bool whole = seg.t0 == 0 && seg.t1 == seg.kt;
+      TreePending part;
+      if (threadIdx.x == 0 && !whole) {
+        // where the CTAs of the unit meet
+        const int ctas = min((int)gridDim.x, total);
+        auto owner = [&](int64_t tile) { return (int)(((tile + 1) * ctas + total - 1) / total) - 1; };
+        if (part_tiles > 0) {
+          part.c0 = blockIdx.x - c->piece;
+          part.parts = c->pieces;
+        } else {
+          part.c0 = seg.t0 == 0 ? (int)blockIdx.x : owner((int64_t)pos - seg.t0);
+          part.parts = owner((int64_t)pos - seg.t0 + seg.kt - 1) - part.c0 + 1;
+        }
+        part.rows = seg.count;
+        part.token0 = seg.token0;
+        part.g = seg.g;
+        part.generation = *reinterpret_cast<volatile unsigned*>(&meets[part.c0].generation);
       }
       TreeState st = {-INFINITY, -INFINITY, 0.f};
       for (int u = grp; u < items; u += 2) {
@@ -1115,7 +1167,6 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
       if (!dead) dead = !__all_sync(0xffffffffu, tree_wait(c, p, &c->o_final, s & 1));
       tc_fence_after();
       const bool nan = dead || c->bad_page[s & 7] != 0;
-      const bool whole = seg.t0 == 0 && seg.t1 == seg.kt;
       float* const slot = partials + ((int64_t)blockIdx.x * 2 + (seg.t0 == 0 ? 1 : 0)) * tree_slot_floats(D);
       // Values of drafted V rows that are not finite, for a row that sees them: columns [at, at + 32) of o.
       auto add_bad = [&](uint32_t (&o)[32], int at) {
@@ -1202,19 +1253,12 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
         }
         if (two || copies == 1) __syncwarp(); else if (grp == 0) named_barrier_sync<3, 128>(); else named_barrier_sync<4, 128>();
         // (a warp's own rows, or the group's first copy)
-        const int from = two || copies == 1 ? row - lane : 0, rows = two || copies == 1 ? 32 : own;
-        const int th = two || copies == 1 ? lane : (int)threadIdx.x % 128, step = two || copies == 1 ? 4 : 16;
-        for (int r = from + th / 8; r < from + rows; r += step) {
-          const int ur = (two ? grp * kTreeTile : 0) + r, ch = th % 8;
-          if (ur >= seg.count) break;
-          float4 sum = *reinterpret_cast<const float4*>(exchange + r * 128 + ((ch ^ (r & 7)) << 4));
-          for (int k = r + own; copies > 1 && k < kTreeTile; k += own) {
-            const float4 x = *reinterpret_cast<const float4*>(exchange + k * 128 + ((ch ^ (r & 7)) << 4));
-            sum.x += x.x;
-            sum.y += x.y;
-            sum.z += x.z;
-            sum.w += x.w;
-          }
+        const bool alone = two || copies == 1;
+        const int th = alone ? lane : (int)threadIdx.x % 128, ch = th % 8, step = alone ? 4 : 16;
+        const int r0 = (alone ? row - lane : 0) + th / 8, rows = alone ? 32 : own;
+        auto emit = [&](int r, float4 sum) {
+          const int ur = (two ? grp * kTreeTile : 0) + r;
+          if (ur >= seg.count) return;
           if (whole) {
             const float f = inverse[ur];
             const int64_t to = ((int64_t)(seg.token0 + (ur >> gshift)) * p.n_head + seg.g * p.group + (ur & (p.group - 1))) * D;
@@ -1222,6 +1266,26 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
                 make_uint2(pack2<S::kBf16>(sum.x * f, sum.y * f), pack2<S::kBf16>(sum.z * f, sum.w * f));
           } else {
             *reinterpret_cast<float4*>(slot + ur * D + at + 4 * ch) = sum;
+          }
+        };
+        auto place = [&](int r) { return *reinterpret_cast<const float4*>(exchange + r * 128 + ((ch ^ (r & 7)) << 4)); };
+        if (alone) {
+          float4 x[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = place(r0 + 4 * i);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) emit(r0 + 4 * i, x[i]);
+        } else {
+          for (int r = r0; r < rows; r += step) {
+            float4 sum = place(r);
+            for (int k = r + own; k < kTreeTile; k += own) {
+              const float4 x = place(k);
+              sum.x += x.x;
+              sum.y += x.y;
+              sum.z += x.z;
+              sum.w += x.w;
+            }
+            emit(r, sum);
           }
         }
         if (two || copies == 1) __syncwarp(); else if (grp == 0) named_barrier_sync<3, 128>(); else named_barrier_sync<4, 128>();
@@ -1233,25 +1297,16 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
       mbar_arrive(&c->o_free);
       if (!whole && threadIdx.x == 0) {
         // this CTA's part of the unit is written: arrive where its CTAs meet
-        const int ctas = min((int)gridDim.x, total);
-        auto owner = [&](int64_t tile) { return (int)(((tile + 1) * ctas + total - 1) / total) - 1; };
-        TreePending x;
-        x.c0 = seg.t0 == 0 ? (int)blockIdx.x : owner((int64_t)pos - seg.t0);
-        x.parts = owner((int64_t)pos - seg.t0 + seg.kt - 1) - x.c0 + 1;
-        x.rows = seg.count;
-        x.token0 = seg.token0;
-        x.g = seg.g;
-        TreeMeet* const meet = meets + x.c0;
-        x.generation = *reinterpret_cast<volatile unsigned*>(&meet->generation);
+        TreeMeet* const meet = meets + part.c0;
         const unsigned before = arrive_acq_rel(&meet->arrived);
-        x.last = before + 1 == (unsigned)x.parts;
-        if (before >= (unsigned)x.parts && p.err_flag) atomicOr(p.err_flag, kErrWorkspace);
-        if (x.last) {
+        part.last = before + 1 == (unsigned)part.parts;
+        if (before >= (unsigned)part.parts && p.err_flag) atomicOr(p.err_flag, kErrWorkspace);
+        if (part.last) {
           meet->arrived = 0;
           meet->ticket = 0;
-          store_release(&meet->generation, x.generation + 1);
+          store_release(&meet->generation, part.generation + 1);
         }
-        c->pending[c->pendings++] = x;
+        c->pending[c->pendings++] = part;
       }
       pos += tiles;
       tau += tiles;
@@ -1279,8 +1334,9 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
         const int ticket = c->ticket;
         named_barrier_sync<1, 256>();
         if (ticket >= shares) break;
-        for (int r = ticket * share + warp; r < min(x.rows, (ticket + 1) * share); r += 8)
-          tree_join_row<T, D>(p, partials, x, r, lane);
+        // (weights: at most max(16 parts, rows + 8 parts) + rows floats)
+        tree_join_rows<T, D>(p, partials, x, ticket * share, min(x.rows, (ticket + 1) * share),
+                             reinterpret_cast<float*>(smem + Shape::kExchange));
       }
     }
   }
