@@ -73,7 +73,8 @@ struct TreeShape {
   static constexpr int kRaw = EIGHT ? (D == 128 ? 4 : 6) : 0;
   // whole warpgroups (setmaxnreg); registers of a thread: at launch, of the softmax groups, of the others
   static constexpr int kThreads = EIGHT ? 512 : 384;
-  static constexpr int kRegsSoftmax = EIGHT ? 192 : 224, kRegsOther = EIGHT ? 64 : 56;
+  static constexpr int kRegsSoftmax = EIGHT ? 184 : 224, kRegsOther = EIGHT ? 72 : 56;
+  static constexpr int kConverters = kThreads - 384;  // threads
   static constexpr int kQ = 0, kRing = 2 * kTileBytes, kRawRing = kRing + kSlots * kTileBytes;
   static constexpr int kControl = kRawRing + kRaw * kRawBytes;
   // At the end of a segment the query tiles are free: weighted outputs [2][128][32] for the exchange, and behind
@@ -98,18 +99,18 @@ struct TreeControl {
   int abort;
   int start[8];           // of this CTA's tiles: sequence, its first token, tokens, rows; KV head, unit, tile; tiles
   int piece, pieces;      // ... as a part of its unit
-  int counts[16];
+  int counts[32];
   TreePending pending[2];
   int pendings, ready, ticket;
   int16_t exponent[kTreeTile];  // 8 bits: of a query row's largest element
   alignas(16) float2 scales[8][8];  // 8 bits: of a warp's column groups: factor of a score, log2 of V's scale
-  int sums[16];
+  int sums[32];
   // of segment s, in entry s % 8: drafted rows whose V is not finite, and whether a page lies outside the pool
   uint32_t bad[8][8];
   int bad_page[8];
 };
 static_assert(sizeof(TreeControl) <= 2048 && offsetof(TreeControl, scales) % 16 == 0, "control area");
-static_assert(128 * (2 * 224 + 56) <= 384 * 168 && 128 * (2 * 192 + 2 * 64) <= 512 * 128, "registers of the launch");
+static_assert(128 * (2 * 224 + 56) <= 384 * 168 && 128 * (2 * 184 + 2 * 72) <= 512 * 128, "registers of the launch");
 
 // Tokens and rows of a sequence; kt tiles for each of mps units a KV head.
 struct TreeSeq {
@@ -428,7 +429,7 @@ __device__ __forceinline__ void softmax_columns(TreeState& st, uint32_t s_at, ui
     }
   };
   float m_tile = -INFINITY, ml_tile = -INFINITY;
-#pragma unroll
+#pragma unroll 1
   for (int from = 0; from < COLS; from += kHold) {
     load(from);
 #pragma unroll
@@ -482,14 +483,16 @@ __device__ __forceinline__ void softmax_columns(TreeState& st, uint32_t s_at, ui
   }
   const float ref = st.m == -INFINITY ? 0.f : st.m - kLift;
   const float lref = st.ml == -INFINITY ? 0.f : st.ml;
+#pragma unroll 1
+  for (int from = 0; from < COLS; from += kHold) {
+    if (kHold < COLS) load(from);
 #pragma unroll
-  for (int h = 0; h < COLS; h += 32) {
-    if (kHold < COLS && h % kHold == 0) load(h);
+    for (int h = 0; h < kHold; h += 32) {
     uint32_t hi[16];
     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
     for (int i = 0; i < 32; i += 2) {
-      const int at = h % kHold + i, g = EIGHT ? at / 16 : 0;
+      const int at = h + i, g = EIGHT ? at / 16 : 0;
       float2 y = __ffma2_rn(make_float2(__uint_as_float(r[at]), __uint_as_float(r[at + 1])),
                             make_float2(ak[g], ak[g]), make_float2(vk[g] - ref, vk[g] - ref));
       if (EIGHT && !PLAIN && masked) {
@@ -509,9 +512,9 @@ __device__ __forceinline__ void softmax_columns(TreeState& st, uint32_t s_at, ui
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         // l counts the weights without the scale of V
-        st.l += (sum[g].x + sum[g].y) * fast_exp2(fminf(ref - lref - vk[h % kHold / 16 + g], 126.f));
+        st.l += (sum[g].x + sum[g].y) * fast_exp2(fminf(ref - lref - vk[h / 16 + g], 126.f));
         if constexpr (!PLAIN) {
-          const float sg = __shfl_sync(0xffffffffu, sign, (col + h) / 16 + g);
+          const float sg = __shfl_sync(0xffffffffu, sign, (col + from + h) / 16 + g);
           if (sg != 1.f) {
 #pragma unroll
             for (int i = 8 * g; i < 8 * g + 8; ++i) hi[i] = sg == 0.f ? 0u : hi[i] ^ 0x80008000u;
@@ -521,13 +524,14 @@ __device__ __forceinline__ void softmax_columns(TreeState& st, uint32_t s_at, ui
     } else {
       st.l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
     }
-    tmem_store16(p_at + weight_column<PIECES>(col + h), hi);
+    tmem_store16(p_at + weight_column<PIECES>(col + from + h), hi);
     if constexpr (PIECES == 2) {
 #pragma unroll
       for (int i = 0; i < 16; ++i)
         hi[i] = pack2<true>(__uint_as_float(r[h + 2 * i]) - __uint_as_float(hi[i] << 16),
                             __uint_as_float(r[h + 2 * i + 1]) - __uint_as_float(hi[i] & 0xffff0000u));
-      tmem_store16(p_at + weight_column<PIECES>(col + h) + 32, hi);
+      tmem_store16(p_at + weight_column<PIECES>(col + from + h) + 32, hi);
+    }
     }
   }
   if constexpr (COLS < 128) {
@@ -587,7 +591,7 @@ __device__ __forceinline__ void tree_join_rows(const TreeParams& p, const float*
   }
   named_barrier_sync<1, 256>();
   const int shift = __ffs(p.group) - 1, col = threadIdx.x % (D / 4);
-#pragma unroll 2
+#pragma unroll 4
   for (int r = threadIdx.x / (D / 4); r < rows; r += 256 / (D / 4)) {
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
@@ -624,10 +628,10 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 8; ++i) {
-      mbar_init(&c->full[i], EIGHT ? 128 : 1);
+      mbar_init(&c->full[i], EIGHT ? Shape::kConverters : 1);
       mbar_init(&c->empty[i], 1);
       mbar_init(&c->raw_full[i], 1);
-      mbar_init(&c->raw_empty[i], 128);
+      mbar_init(&c->raw_empty[i], max(Shape::kConverters, 1));
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&c->s_full[i], 1);
@@ -737,9 +741,10 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
         c->start[3] = x.rows;
         c->start[4] = head;
         c->start[5] = unit - head * x.mps;
-        c->start[6] = part_tiles > 0 ? (int)((int64_t)x.kt * piece / pieces) : piece;
+        const int each = x.kt / pieces, more = x.kt - each * pieces;
+        c->start[6] = part_tiles > 0 ? piece * each + min(piece, more) : piece;
         // tiles of the part; its number and how many there are
-        c->start[7] = part_tiles > 0 ? (int)((int64_t)x.kt * (piece + 1) / pieces) - c->start[6] : end - begin;
+        c->start[7] = part_tiles > 0 ? each + (piece < more ? 1 : 0) : end - begin;
         c->piece = piece;
         c->pieces = pieces;
       }
@@ -897,13 +902,14 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
     }
     if constexpr (EIGHT) if (warp >= 12) {
       const int th = threadIdx.x - 384;
-      constexpr int kChunks = D / 16;  // 16-byte chunks of a raw row, and of a thread
+      constexpr int kChunks = D / 16;                                       // 16-byte chunks of a raw row
+      constexpr int kEach = kTreeTile * kChunks / Shape::kConverters;       // ... of a thread
       int use = 0;
       bool ok = true;
       for (int s = 0; ok && cursor.next(p, &seg); ++s) {
         for (int t = seg.t0; ok && t < seg.t1; ++t) {
           const int j0 = t * kTreeTile, valid = min(kTreeTile, seg.rows - j0);
-#pragma unroll
+#pragma unroll 1
           for (int kv = 0; kv < 2; ++kv, ++use) {
             const int raw = use % Shape::kRaw, slot = use % Shape::kSlots, round = use / Shape::kSlots;
             ok = tree_wait(c, p, &c->raw_full[raw], (use / Shape::kRaw) & 1);
@@ -911,38 +917,44 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
             if (!ok) break;
             const uint8_t* const from = smem + Shape::kRawRing + raw * Shape::kRawBytes;
             uint8_t* const to = smem + Shape::kRing + slot * Shape::kTileBytes;
-            auto convert = [&](const uint4& x, int idx) {
+            auto store = [&](const uint32_t (&h)[8], int idx) {
               const int r = idx / kChunks, ch = idx % kChunks;
+              *reinterpret_cast<uint4*>(to + chunk_at<D>(r, 2 * ch)) = make_uint4(h[0], h[1], h[2], h[3]);
+              *reinterpret_cast<uint4*>(to + chunk_at<D>(r, 2 * ch + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
+            };
+            auto convert = [&](const uint4& x, int idx) {
+              const uint32_t w[4] = {x.x, x.y, x.z, x.w};
               uint32_t h[8];
-              const uint32_t* const w = &x.x;
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[2 * k]) : "h"((uint16_t)(w[k] & 0xffffu)));
                 asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[2 * k + 1]) : "h"((uint16_t)(w[k] >> 16)));
               }
-              *reinterpret_cast<uint4*>(to + chunk_at<D>(r, 2 * ch)) = make_uint4(h[0], h[1], h[2], h[3]);
-              *reinterpret_cast<uint4*>(to + chunk_at<D>(r, 2 * ch + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
+              store(h, idx);
             };
             if (kv == 0 || j0 + kTreeTile <= seg.base) {
 #pragma unroll
-              for (int i = 0; i < kChunks; ++i) convert(ld_shared_v4(from + (th + i * 128) * 16), th + i * 128);
+              for (int i = 0; i < kEach; ++i)
+                convert(ld_shared_v4(from + (th + i * Shape::kConverters) * 16), th + i * Shape::kConverters);
             } else {
 #pragma unroll 1
-              for (int i = 0; i < kChunks; ++i) {
-                const int idx = th + i * 128, r = idx / kChunks;
+              for (int i = 0; i < kEach; ++i) {
+                const int idx = th + i * Shape::kConverters, r = idx / kChunks;
                 uint4 x = ld_shared_v4(from + idx * 16);
                 if (r >= valid) {
                   x = make_uint4(0u, 0u, 0u, 0u);
                 } else if (j0 + r >= seg.base) {
                   // drafted rows: NaN reaches only those who see it (added at the end)
                   bool nan = false;
-                  uint32_t* const w = &x.x;
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    const uint32_t m = __vcmpeq4(w[k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                  auto clean = [&](uint32_t& w) {
+                    const uint32_t m = __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
                     nan |= m != 0;
-                    w[k] &= ~m;
-                  }
+                    w &= ~m;
+                  };
+                  clean(x.x);
+                  clean(x.y);
+                  clean(x.z);
+                  clean(x.w);
                   const int d = j0 + r - seg.base;
                   if (nan) atomicOr(&c->bad[s & 7][d >> 5], 1u << (d & 31));
                 }
