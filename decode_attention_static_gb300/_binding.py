@@ -134,7 +134,9 @@ def _load_fast():
         loader.exec_module(module)
         module.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
             "decode_attn_paged_fwd", "decode_attn_paged_q8_fwd", "decode_attn_window_fwd", "kvcache_append_paged",
-            "kvcache_append_paged_q8")))
+            "kvcache_append_paged_q8", "kvcache_append_paged_axes", "kvcache_append_paged_q8_axes",
+            "decode_attn_tree_fwd", "decode_attn_tree_q8_fwd", "kvcache_resize_paged", "kvcache_fork_paged",
+            "kvcache_copy_pages", "kvcache_compact_paged", "kvcache_compact_paged_q8")))
         _fast = module
     except (ImportError, OSError, AttributeError) as e:
         _fast = False
@@ -905,6 +907,12 @@ def kvcache_append_paged_axes(k_pages: torch.Tensor, v_pages: torch.Tensor, k_ne
     of token t is rotated by row rope_position_ids[rope_axis[i], t] of the
     tables (rope_position_ids int32 [axes, tokens], at most 4 axes; rope_axis
     int32 [D / 2], None: the first axis for all)."""
+    fast = _load_fast() if _fast is None else _fast
+    if fast:
+        r = fast.append(k_pages, v_pages, None, None, k_new, v_new, page_table, position_ids, token_start, rope_cos,
+                        rope_sin, q, q_out, err_flag, rope_position_ids, rope_axis)
+        if r is not NotImplemented:
+            return r
     return _append_paged("kvcache_append_paged_axes", k_pages, v_pages, None, None, False, k_new, v_new, page_table,
                          position_ids, token_start, rope_cos, rope_sin, q, q_out, err_flag,
                          (rope_position_ids, rope_axis))
@@ -918,6 +926,12 @@ def kvcache_append_paged_q8_axes(k_pages: torch.Tensor, v_pages: torch.Tensor, k
                                  q: torch.Tensor | None = None, q_out: torch.Tensor | None = None,
                                  err_flag: torch.Tensor | None = None) -> torch.Tensor | None:
     """kvcache_append_paged_axes into float8_e4m3fn pools with their scales."""
+    fast = _load_fast() if _fast is None else _fast
+    if fast and k_scale is not None:
+        r = fast.append(k_pages, v_pages, k_scale, v_scale, k_new, v_new, page_table, position_ids, token_start,
+                        rope_cos, rope_sin, q, q_out, err_flag, rope_position_ids, rope_axis)
+        if r is not NotImplemented:
+            return r
     return _append_paged("kvcache_append_paged_q8_axes", k_pages, v_pages, k_scale, v_scale, True, k_new, v_new,
                          page_table, position_ids, token_start, rope_cos, rope_sin, q, q_out, err_flag,
                          (rope_position_ids, rope_axis))
@@ -1023,6 +1037,12 @@ def decode_attn_tree_fwd(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.
     those whose bit is set in its row of tree_mask (int64 [tokens, words], bit
     i % 64 of word i / 64 for the sequence's i-th token; None: those up to
     itself). A workspace comes from alloc_tree_workspace (reuse it)."""
+    fast = _load_fast() if _fast is None else _fast
+    if fast:
+        r = fast.attn_tree(q, k_pages, v_pages, None, None, page_table, kv_len, token_start, tree_mask, out, scale,
+                           workspace, err_flag)
+        if r is not NotImplemented:
+            return r
     return _attn_tree("decode_attn_tree_fwd", q, k_pages, v_pages, None, None, False, page_table, kv_len, token_start,
                       tree_mask, out, scale, workspace, err_flag)
 
@@ -1035,6 +1055,12 @@ def decode_attn_tree_q8_fwd(q: torch.Tensor, k_pages: torch.Tensor, v_pages: tor
                             err_flag: torch.Tensor | None = None) -> torch.Tensor:
     """decode_attn_tree_fwd over float8_e4m3fn pools with their scales float32
     [num_pages, n_kv_head]."""
+    fast = _load_fast() if _fast is None else _fast
+    if fast and k_scale is not None:
+        r = fast.attn_tree(q, k_pages, v_pages, k_scale, v_scale, page_table, kv_len, token_start, tree_mask, out, scale,
+                           workspace, err_flag)
+        if r is not NotImplemented:
+            return r
     return _attn_tree("decode_attn_tree_q8_fwd", q, k_pages, v_pages, k_scale, v_scale, True, page_table, kv_len,
                       token_start, tree_mask, out, scale, workspace, err_flag)
 
@@ -1080,6 +1106,9 @@ def kvcache_resize_paged(page_table: torch.Tensor, held_len: torch.Tensor, wante
     wanted_len[b] rows: pages are released to the pool's state, then taken from
     it (page_table int32 [B, max_pages], lengths int32 [B], pool from
     alloc_page_pool; all updated in place)."""
+    fast = _load_fast() if _fast is None else _fast
+    if fast and fast.resize(page_table, held_len, wanted_len, pool, page_size, err_flag) is not NotImplemented:
+        return
     pages, ix = _pool_pages(pool), pool.get_device()
     _require(page_table.dim() == 2, "page_table must be int32 [B, max_pages]")
     B, most = page_table.shape
@@ -1098,6 +1127,11 @@ def kvcache_fork_paged(page_table: torch.Tensor, kv_len: torch.Tensor, parent: t
     the pool. Returns copies int32 [3, forks] (source page, target page, rows),
     for kvcache_copy_pages on every layer's pools; page_table, kv_len and pool
     are updated in place."""
+    fast = _load_fast() if _fast is None else _fast
+    if fast:
+        r = fast.fork(page_table, kv_len, parent, child, pool, page_size, copies, err_flag)
+        if r is not NotImplemented:
+            return r
     pages, ix = _pool_pages(pool), pool.get_device()
     _require(page_table.dim() == 2, "page_table must be int32 [B, max_pages]")
     (B, most), n = page_table.shape, parent.numel()
@@ -1138,6 +1172,9 @@ def kvcache_copy_pages(k_pages: torch.Tensor, v_pages: torch.Tensor, copies: tor
     """Copy rows [0, copies[2, i]) of page copies[0, i] to page copies[1, i] in
     the pools of one layer or (with a leading layer axis) of several, in place;
     pages of 8 bits with their scales. Entries below 0 are skipped."""
+    fast = _load_fast() if _fast is None else _fast
+    if fast and fast.copy_pages(k_pages, v_pages, k_scale, v_scale, copies, err_flag) is not NotImplemented:
+        return
     layers, pages, Hkv, size, D, element = _stacked_pools(k_pages, v_pages, k_scale, v_scale)
     _require(copies.dim() == 2 and copies.shape[0] == 3, "copies must be int32 [3, n]")
     n, ix = copies.shape[1], k_pages.get_device()
@@ -1150,6 +1187,10 @@ def kvcache_copy_pages(k_pages: torch.Tensor, v_pages: torch.Tensor, copies: tor
 
 
 def _compact(fn, k_pages, v_pages, k_scale, v_scale, eight, page_table, keep, keep_start, position_ids, err_flag):
+    fast = _load_fast() if _fast is None else _fast
+    if fast and (k_scale is not None) == eight and fast.compact(
+            k_pages, v_pages, k_scale, v_scale, page_table, keep, keep_start, position_ids, err_flag) is not NotImplemented:
+        return
     if (k_pages.dtype == _E4M3) != eight:
         raise TypeError("pages must be float8_e4m3fn" if eight else "pages must be float16 or bfloat16")
     layers, pages, Hkv, size, D, _ = _stacked_pools(k_pages, v_pages, k_scale, v_scale)

@@ -289,3 +289,52 @@ def test_plain_compaction():
     errors = Q.compact([pool, pool.clone()], table, torch.tensor([3, 6, 17]), [0, 3], [3], 16)
     assert not errors and pool[0, 1, 0, :7, 0].tolist() == [16, 17, 18, 19, 22, 1, 22]
     assert Q.compact([pool, pool.clone()], table, torch.tensor([3, 3]), [0, 2], [3], 16) == {"position"}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("eight", [False, True], ids=["16bit", "e4m3"])
+def test_both_paths_of_the_binding(eight, monkeypatch):
+    """The calls made in C++ and those made from Python do the same, and the C++ path takes them all."""
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from decode_attention_static_gb300 import _binding
+
+    da_build.build_library()
+    assert _binding._load_fast()
+    taken = []
+
+    class Counted:
+        def __init__(self, module):
+            self.module = module
+
+        def __getattr__(self, name):
+            def call(*args):
+                r = getattr(self.module, name)(*args)
+                taken.append(r is not NotImplemented)
+                return r
+            return call
+
+    def run():
+        gen = torch.Generator().manual_seed(0)
+        got = []
+        for fn, good in arguments("cuda", eight).items():
+            for name in ("q", "k_new", "v_new", "k_pages", "v_pages", "rope_cos", "rope_sin"):
+                if name in good:
+                    good[name].copy_(torch.randn(good[name].shape, generator=gen).to(good[name].dtype))
+            if "tree" in fn:
+                good["workspace"] = da.alloc_tree_workspace(4, 2, 64)
+            for drop in ("err_flag", "out", "q_out", "copies") if fn != "kvcache_copy_pages" else ("err_flag",):
+                r = getattr(da, fn)(**{k: v for k, v in good.items() if k != drop})
+                got += [t for t in good.values() if isinstance(t, torch.Tensor) and t is not good.get("workspace")]
+                got += [r] if r is not None else []
+                got = [t.clone() for t in got]
+        return [R.bits(t.view(torch.uint8)) for t in got]
+
+    monkeypatch.setattr(_binding, "_fast", Counted(_binding._fast))
+    fast = run()
+    assert all(taken) and len(taken) >= 13
+    monkeypatch.setattr(_binding, "_fast", False)
+    slow = run()
+    assert len(fast) == len(slow)
+    for f, s in zip(fast, slow):
+        assert torch.equal(f, s)
