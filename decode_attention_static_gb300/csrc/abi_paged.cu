@@ -193,7 +193,7 @@ int tree_attention(const void* q, const void* k_pages, const void* v_pages, cons
   // tokens and rows of pools are 32-bit coordinates of tensor copies, tiles are numbered in 32 bits
   if ((int64_t)num_pages * n_kv_head * page_size > INT32_MAX) return DA_ERR_SHAPE;
   if ((int64_t)B * n_kv_head * (kTreeMaxTokens * (n_head / n_kv_head) / 256) *
-          (((int64_t)max_pages * page_size + 127) / 128) > INT32_MAX)
+          (((int64_t)max_pages * page_size + 127) / 128 + 8) > INT32_MAX)
     return DA_ERR_SHAPE;
   if (B == 0 || tokens == 0) return DA_OK;
   if (!q || !k_pages || !v_pages || !page_table || !kv_len || !out || (e4m3 && (!k_scale || !v_scale)))

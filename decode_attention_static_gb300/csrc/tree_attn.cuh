@@ -36,6 +36,7 @@ constexpr int kTreeUnitRows = 256;         // query rows of a unit
 constexpr unsigned long long kTreeHelpNs = 20000;  // how long a CTA waits for a unit's other parts, to help with their join
 constexpr int kTreeMinTiles = 1;            // a part of a unit has at least as many tiles
 constexpr int kTreeJoinTiles = 8;           // what the ends of a share inside units cost, in tiles (at most the warps)
+constexpr int kTreeUnitTiles = 6;           // ... what beginning and ending a unit takes
 constexpr float kTreeLazy = 8.f;           // a running maximum is raised when a score passes it by 2^8
 
 // A partial state: O [256][D], then (m, m of l, l) [256] float4.
@@ -98,7 +99,8 @@ struct TreeControl {
   uint32_t tmem;
   int abort;
   int start[8];           // of this CTA's tiles: sequence, its first token, tokens, rows; KV head, unit, tile; tiles
-  int piece, pieces;      // ... as a part of its unit
+  int piece, pieces;      // ... as a part of its unit; or where its first unit begins in the list, and its last tile + 1
+  int unit_at, end_tile;
   int counts[32];
   TreePending pending[2];
   int pendings, ready, ticket;
@@ -659,11 +661,12 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
   pdl_wait();
   pdl_trigger();
 
-  // This CTA's share of all tiles, and where it begins: an even share of the list of all units' tiles, or a part of one
-  // unit. Even shares end and begin inside units, which costs a CTA two partial states and joins, as long as some
-  // kTreeJoinTiles tiles: so every unit is cut into parts of its own, a CTA each, where the largest part is not longer
-  // than an even share by that much (and there are not more parts than CTAs).
-  int errors = 0, begin = 0, end = 0, total = 0, part_tiles = 0;
+  // This CTA's share of all tiles, and where it begins: a part of one unit, or an even share of the list of all units.
+  // Every unit is cut into parts of its own, a CTA each, where there are not more of them than CTAs and the largest is
+  // longer than an even share by less than kTreeJoinTiles tiles: even shares end and begin inside units, which costs a
+  // CTA partial states and joins. In the list a unit counts for its tiles and kTreeUnitTiles more, which is what
+  // beginning and ending one takes; a share that would begin within those begins with the unit.
+  int errors = 0, total = 0, part_tiles = 0, ctas = 0;  // total: of the list, with what units count for
   {
     auto units_of = [&](int b, int* kt) {
       *kt = 1;
@@ -674,25 +677,27 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
     };
     int my_kt, kt;
     const int my_units = units_of(threadIdx.x, &my_kt);
-    int sum = my_units * my_kt, units = my_units;
+    int tiles = my_units * my_kt, units = my_units;
     for (int b = threadIdx.x + kThreads; b < p.B; b += kThreads) {
       const int n = units_of(b, &kt);
-      sum += n * kt;
+      tiles += n * kt;
       units += n;
     }
     // the sequences' units and tiles, as far as one pass goes, for the search of the parts' size
     int2* const table = reinterpret_cast<int2*>(smem + Shape::kQ);
     table[threadIdx.x] = make_int2(my_units, my_kt);
-    sum = __reduce_add_sync(0xffffffffu, sum);
+    tiles = __reduce_add_sync(0xffffffffu, tiles);
     units = __reduce_add_sync(0xffffffffu, units);
     if (lane == 0) {
-      c->sums[warp] = sum;
+      c->sums[warp] = tiles;
       c->counts[warp] = units;
     }
     __syncthreads();
-    total = __reduce_add_sync(0xffffffffu, lane < kWarps ? c->sums[lane] : 0);
+    tiles = __reduce_add_sync(0xffffffffu, lane < kWarps ? c->sums[lane] : 0);
     units = __reduce_add_sync(0xffffffffu, lane < kWarps ? c->counts[lane] : 0);
-    const int grid = gridDim.x, share = max((total + grid - 1) / grid, kTreeMinTiles);
+    const int grid = gridDim.x, share = max((tiles + grid - 1) / grid, kTreeMinTiles);
+    total = tiles + kTreeUnitTiles * units;
+    ctas = min(grid, total);
     if (units <= grid && p.B <= kThreads) {  // (the same in every thread)
       // one candidate for each warp: share, share + 1, ...
       int parts = 0;
@@ -704,57 +709,80 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
       const uint32_t fits = __ballot_sync(0xffffffffu, lane < kTreeJoinTiles && c->counts[lane] <= grid);
       if (fits) part_tiles = share + __ffs(fits) - 1;
     }
-    const int ctas = min(grid, total);
-    int want = blockIdx.x;  // the part, or the first tile
+    // the part's number; or where the share begins in the list, and the next one
+    int want = blockIdx.x, next = 0;
     if (part_tiles == 0) {
-      if ((int)blockIdx.x < ctas) {
-        begin = (int)((int64_t)total * blockIdx.x / ctas);
-        end = (int)((int64_t)total * (blockIdx.x + 1) / ctas);
-      }
-      want = begin;
+      const bool on = (int)blockIdx.x < ctas;
+      want = on ? (int)((int64_t)total * blockIdx.x / ctas) : total;
+      next = on ? (int)((int64_t)total * (blockIdx.x + 1) / ctas) : total;
     }
-    int before = 0;
-    if (threadIdx.x == 0) c->start[7] = 0;
-    for (int base = 0; base < p.B && before <= want && (end > 0 || part_tiles > 0); base += kThreads) {
+    if (threadIdx.x == 0) {
+      c->start[7] = 0;
+      c->end_tile = tiles;
+    }
+    int before = 0, units_before = 0;
+    for (int base = 0; base < p.B && before <= max(want, next); base += kThreads) {
       int n = my_units;
       kt = my_kt;
       if (base > 0) n = units_of(base + threadIdx.x, &kt);
-      const int pieces = part_tiles > 0 ? (kt + part_tiles - 1) / part_tiles : kt, v = n * pieces;
-      int scan = v;
+      // what a unit counts for, and all of the sequence
+      const int each = part_tiles > 0 ? (kt + part_tiles - 1) / part_tiles : kt + kTreeUnitTiles, v = n * each;
+      int scan = v, scan_units = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int up = __shfl_up_sync(0xffffffffu, scan, o);
-        if (lane >= o) scan += up;
+        const int up = __shfl_up_sync(0xffffffffu, scan, o), up_units = __shfl_up_sync(0xffffffffu, scan_units, o);
+        if (lane >= o) {
+          scan += up;
+          scan_units += up_units;
+        }
       }
       __syncthreads();
-      if (lane == 31) c->sums[warp] = scan;
+      if (lane == 31) {
+        c->sums[warp] = scan;
+        c->counts[warp] = scan_units;
+      }
       __syncthreads();
-      const int w = lane < kWarps ? c->sums[lane] : 0;
+      const int w = lane < kWarps ? c->sums[lane] : 0, wu = lane < kWarps ? c->counts[lane] : 0;
       const int at = before + __reduce_add_sync(0xffffffffu, lane < warp ? w : 0) + scan - v;
+      const int first_unit = units_before + __reduce_add_sync(0xffffffffu, lane < warp ? wu : 0) + scan_units - n;
+      // (tiles before the sequence's, in the list)
+      const int tiles_at = at - kTreeUnitTiles * first_unit;
       if (want >= at && want < at + v) {
         int none = 0;
         const TreeSeq x = tree_sequence(p, base + threadIdx.x, &none);
-        const int off = want - at, unit = off / pieces, piece = off - unit * pieces, head = unit / x.mps;
+        const int off = want - at, unit = off / each, piece = off - unit * each, head = unit / x.mps;
         c->start[0] = base + threadIdx.x;
         c->start[1] = x.first;
         c->start[2] = x.n;
         c->start[3] = x.rows;
         c->start[4] = head;
         c->start[5] = unit - head * x.mps;
-        const int each = x.kt / pieces, more = x.kt - each * pieces;
-        c->start[6] = part_tiles > 0 ? piece * each + min(piece, more) : piece;
-        // tiles of the part; its number and how many there are
-        c->start[7] = part_tiles > 0 ? each + (piece < more ? 1 : 0) : end - begin;
-        c->piece = piece;
-        c->pieces = pieces;
+        if (part_tiles > 0) {
+          const int share_tiles = x.kt / each, more = x.kt - share_tiles * each;
+          c->start[6] = piece * share_tiles + min(piece, more);
+          c->start[7] = share_tiles + (piece < more ? 1 : 0);
+          c->piece = piece;
+          c->pieces = each;
+        } else {
+          const int tile = max(0, piece - kTreeUnitTiles);
+          c->start[6] = tile;
+          c->start[7] = -(tiles_at + unit * x.kt + tile) - 1;  // (the number of tiles once the end is known)
+          c->unit_at = at + unit * each;
+        }
+      }
+      if (part_tiles == 0 && next >= at && next < at + v) {
+        const int off = next - at, unit = off / each;
+        c->end_tile = tiles_at + unit * kt + max(0, off - unit * each - kTreeUnitTiles);
       }
       before += __reduce_add_sync(0xffffffffu, w);
+      units_before += __reduce_add_sync(0xffffffffu, wu);
     }
     __syncthreads();
   }
+  const int my_tiles = c->start[7] >= 0 ? c->start[7] : c->end_tile + c->start[7] + 1;
   if (blockIdx.x == 0 && errors && p.err_flag) atomicOr(p.err_flag, errors);
   TreeCursor cursor;
-  cursor.begin(p, c->start, c->start[7]);
+  cursor.begin(p, c->start, my_tiles);
   TreeSegment seg;
 
   if (warp == 8) {
@@ -979,7 +1007,7 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
     const int gshift = __ffs(p.group) - 1;
     int phase_s = 0, tau = 0;
     bool dead = false;
-    int pos = begin;  // of a segment's first tile among all tiles
+    int unit_at = c->unit_at;  // where the unit at hand begins in the list
     if (threadIdx.x == 0) c->pendings = 0;
     for (int s = 0; cursor.next(p, &seg); ++s) {
       const bool two = seg.count > kTreeTile;
@@ -1082,14 +1110,14 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
       TreePending part;
       if (threadIdx.x == 0 && !whole) {
         // where the CTAs of the unit meet
-        const int ctas = min((int)gridDim.x, total);
-        auto owner = [&](int64_t tile) { return (int)(((tile + 1) * ctas + total - 1) / total) - 1; };
+        // (the last CTA whose share begins at or before a place in the list)
+        auto owner = [&](int64_t place) { return (int)(((place + 1) * ctas + total - 1) / total) - 1; };
         if (part_tiles > 0) {
           part.c0 = blockIdx.x - c->piece;
           part.parts = c->pieces;
         } else {
-          part.c0 = seg.t0 == 0 ? (int)blockIdx.x : owner((int64_t)pos - seg.t0);
-          part.parts = owner((int64_t)pos - seg.t0 + seg.kt - 1) - part.c0 + 1;
+          part.c0 = seg.t0 == 0 ? (int)blockIdx.x : owner((int64_t)unit_at + kTreeUnitTiles);
+          part.parts = owner((int64_t)unit_at + kTreeUnitTiles + seg.kt - 1) - part.c0 + 1;
         }
         part.rows = seg.count;
         part.token0 = seg.token0;
@@ -1320,7 +1348,7 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
         }
         c->pending[c->pendings++] = part;
       }
-      pos += tiles;
+      if (seg.t1 == seg.kt) unit_at += seg.kt + kTreeUnitTiles;
       tau += tiles;
     }
     named_barrier_sync<2, 256>();
