@@ -592,24 +592,39 @@ __device__ __forceinline__ void tree_join_rows(const TreeParams& p, const float*
     weights[parts * rows + r] = l == 0.f ? 0.f : fast_exp2(m0 - ml0) / l;
   }
   named_barrier_sync<1, 256>();
+  // four rows of a thread at once, so that as many loads of each part are on their way
+  constexpr int kStep = 256 / (D / 4), kRows = 4;
   const int shift = __ffs(p.group) - 1, col = threadIdx.x % (D / 4);
-#pragma unroll 4
-  for (int r = threadIdx.x / (D / 4); r < rows; r += 256 / (D / 4)) {
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 1
+  for (int first = threadIdx.x / (D / 4); first < rows; first += kRows * kStep) {
+    float4 acc[kRows];
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
     for (int i = 0; i < parts; ++i) {
-      const float4 o = __ldcg(reinterpret_cast<const float4*>(slot(i) + (r0 + r) * D) + col);
-      const float w = weights[i * rows + r];
-      acc.x = fmaf(o.x, w, acc.x);
-      acc.y = fmaf(o.y, w, acc.y);
-      acc.z = fmaf(o.z, w, acc.z);
-      acc.w = fmaf(o.w, w, acc.w);
+      const float4* const from = reinterpret_cast<const float4*>(slot(i) + r0 * D) + col;
+      float4 o[kRows];
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) o[k] = __ldcg(from + min(first + k * kStep, rows - 1) * (D / 4));
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) {
+        const float w = weights[i * rows + min(first + k * kStep, rows - 1)];
+        acc[k].x = fmaf(o[k].x, w, acc[k].x);
+        acc[k].y = fmaf(o[k].y, w, acc[k].y);
+        acc[k].z = fmaf(o[k].z, w, acc[k].z);
+        acc[k].w = fmaf(o[k].w, w, acc[k].w);
+      }
     }
-    const float inv = weights[parts * rows + r];
-    const int row = r0 + r;
-    const int64_t at = ((int64_t)(x.token0 + (row >> shift)) * p.n_head + x.g * p.group + (row & (p.group - 1))) * D;
-    *reinterpret_cast<uint2*>(p.out + (at + 4 * col) * 2) =
-        make_uint2(pack2<Storage<T>::kBf16>(acc.x * inv, acc.y * inv), pack2<Storage<T>::kBf16>(acc.z * inv, acc.w * inv));
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      const int r = first + k * kStep, row = r0 + r;
+      if (r >= rows) break;
+      const float inv = weights[parts * rows + r];
+      const int64_t at = ((int64_t)(x.token0 + (row >> shift)) * p.n_head + x.g * p.group + (row & (p.group - 1))) * D;
+      *reinterpret_cast<uint2*>(p.out + (at + 4 * col) * 2) =
+          make_uint2(pack2<Storage<T>::kBf16>(acc[k].x * inv, acc[k].y * inv),
+                     pack2<Storage<T>::kBf16>(acc[k].z * inv, acc[k].w * inv));
+    }
   }
 }
 
