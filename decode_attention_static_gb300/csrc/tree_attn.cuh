@@ -37,7 +37,8 @@ constexpr unsigned long long kTreeHelpNs = 20000;  // how long a CTA waits for a
 constexpr int kTreeMinTiles = 1;            // a part of a unit has at least as many tiles
 constexpr int kTreeJoinTiles = 8;           // what the ends of a share inside units cost, in tiles (at most the warps)
 constexpr int kTreeUnitTiles = 6;           // ... what beginning and ending a unit takes
-constexpr float kTreeLazy = 8.f;           // a running maximum is raised when a score passes it by 2^8
+constexpr float kTreeLazy = 7.f;            // a running maximum is raised when a score passes it by 2^7
+constexpr float kTreeLift = 8.f;            // fp16 weights are held 2^8 times as large: a row's largest lies in [2^7, 2^15]
 
 // A partial state: O [256][D], then (m, m of l, l) [256] float4.
 __host__ __device__ constexpr int tree_slot_floats(int D) { return kTreeUnitRows * D + kTreeUnitRows * 4; }
@@ -384,28 +385,29 @@ __device__ __forceinline__ int weight_column(int k) {
   return PIECES == 2 ? k / 64 * 64 + k % 64 / 2 : k / 2;
 }
 
-// COLS columns of scores, from column `col` on, to weights in tensor memory: the running maximum, the sum, and the
-// rescaling of the output where the maximum was raised. a: factor of a score (positive); seen(k): bits of the k-th 32
-// columns, looked at where `masked`. 8 bits: scales holds the factor that K's scale is and log2 |V's scale| of each 16
-// rows, sign (in lanes 0 to 7) the sign of V's scale or zero; PLAIN: all of K's are positive, and so are V's (a branch
-// for every 16 columns took 4000 cycles an item). Straight code, held in registers: as a loop over 32 columns at a time, read
-// twice, 128 columns took 4000 cycles instead of 1700.
-template <bool BF16, int D, bool EIGHT, int COLS, int PIECES, bool PLAIN, typename Seen>
+// COLS columns of scores, from column `col` on, to weights in tensor memory, their sum to the state. The weights are
+// taken against a running maximum; where a score passes it by 2^7 (or is the row's first) it is raised to the next
+// whole number, and the output, the sum and earlier weights of the tile are rescaled (by powers of two: exact). a: factor
+// of a score (positive); seen: bits of the columns, looked at where `masked`. 8 bits: scales holds the factor that K's scale is and log2 |V's scale|
+// of each 16 rows, sign (in lanes 0 to 7) the sign of V's scale or zero; PLAIN: all of K's are positive, and so are V's
+// (a branch for every 16 columns took 4000 cycles an item). Straight code for the columns held in registers: as a loop
+// over 32 at a time, 128 took 4000 cycles instead of 1700.
+template <bool BF16, int D, bool EIGHT, int COLS, int PIECES, bool PLAIN>
 __device__ __forceinline__ void softmax_columns(TreeState& st, uint32_t s_at, uint32_t p_at, uint32_t o_at, int col,
-                                                bool first, float a, bool masked, const Seen& seen,
+                                                bool first, float a, bool masked, const uint32_t (&seen)[4],
                                                 const float2* scales, float sign) {
-  // fp16 weights are held 2^7 times as large: the largest one of a row lies in [2^7, 2^15]
-  constexpr float kLift = BF16 ? 0.f : 7.f;
-  // (8 bits: fewer registers, 128 columns are read twice, by halves)
+  constexpr float kLift = BF16 ? 0.f : kTreeLift;
+  // (8 bits have fewer registers: 128 columns by halves)
   constexpr int kHold = EIGHT && COLS == 128 ? 64 : COLS;
   // (a NaN of no other origin where factors may be zero or negative)
   constexpr uint32_t kHidden = EIGHT && !PLAIN ? 0x7fdeadedu : 0xff800000u;
   constexpr int kGroups = EIGHT ? kHold / 16 : 1, kPart = kHold / kGroups;
-  uint32_t r[kHold];
-  float ak[kGroups], vk[kGroups];
-  auto load = [&](int from) {
+#pragma unroll 1
+  for (int from = 0; from < COLS; from += kHold) {
+    uint32_t r[kHold];
 #pragma unroll
     for (int k = 0; k < kHold / 32; ++k) tmem_load32(s_at + col + from + 32 * k, r + 32 * k);
+    float ak[kGroups], vk[kGroups];
     if constexpr (EIGHT) {
 #pragma unroll
       for (int g = 0; g < kGroups; g += 2) {
@@ -423,17 +425,13 @@ __device__ __forceinline__ void softmax_columns(TreeState& st, uint32_t s_at, ui
     if (masked) {
 #pragma unroll
       for (int k = 0; k < kHold / 32; ++k) {
-        const uint32_t bits = seen(from / 32 + k);
+        const uint32_t bits = kHold < COLS && from > 0 ? seen[2 + k] : seen[k];
 #pragma unroll
         for (int i = 0; i < 32; ++i)
           if (!(bits >> i & 1)) r[32 * k + i] = kHidden;
       }
     }
-  };
-  float m_tile = -INFINITY, ml_tile = -INFINITY;
-#pragma unroll 1
-  for (int from = 0; from < COLS; from += kHold) {
-    load(from);
+    float m_tile = -INFINITY, ml_tile = -INFINITY;
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
       float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -452,89 +450,98 @@ __device__ __forceinline__ void softmax_columns(TreeState& st, uint32_t s_at, ui
       } else {
         top[0] = fabsf(top[0]) < INFINITY ? top[0] * ak[g] : top[0] == INFINITY && ak[g] > 0.f ? INFINITY : -INFINITY;
       }
-      if constexpr (EIGHT) ml_tile = fmaxf(ml_tile, top[0]);
+      ml_tile = fmaxf(ml_tile, top[0]);
       m_tile = fmaxf(m_tile, EIGHT ? top[0] + vk[g] : top[0]);
     }
-  }
-  if constexpr (!EIGHT) ml_tile = m_tile;
-  // raise the maximum where a score passes it by 2^8 (or is the first one)
-  const bool up = m_tile > st.m + kTreeLazy || (st.m == -INFINITY && m_tile > -INFINITY);
-  if (__any_sync(0xffffffffu, up)) {
-    const float factor = !up ? 1.f : st.m == -INFINITY ? 0.f : fast_exp2(st.m - m_tile);
-    if (up) st.m = m_tile;
-    if constexpr (!EIGHT) st.l *= factor;
-    if (!first) {
+    const bool up = m_tile > st.m + kTreeLazy || (st.m == -INFINITY && m_tile > -INFINITY);
+    const bool up_l = EIGHT && (ml_tile > st.ml + kTreeLazy || (st.ml == -INFINITY && ml_tile > -INFINITY));
+    if (__any_sync(0xffffffffu, up || up_l)) {
+      const float m_new = up ? ceilf(m_tile) : st.m;
+      const float factor = !up ? 1.f : st.m == -INFINITY ? 0.f : fast_exp2(st.m - m_new);
+      st.m = m_new;
+      if constexpr (EIGHT) {
+        if (up_l) {
+          const float ml_new = ceilf(ml_tile);
+          st.l *= st.ml == -INFINITY ? 0.f : fast_exp2(st.ml - ml_new);
+          st.ml = ml_new;
+        }
+      } else {
+        st.l *= factor;
+        st.ml = st.m;
+      }
+      if (kHold < COLS && from > 0) {
+        tmem_wait_store();
+        // the weights of the first half, two fp16 numbers to a column
 #pragma unroll 1
-      for (int k = 0; k < D; k += 16) {
-        uint32_t o[16];
-        tmem_load16(o_at + k, o);
-        tmem_wait_load();
+        for (int k = 0; k < from / 2; k += 16) {
+          uint32_t w[16];
+          tmem_load16(p_at + k, w);
+          tmem_wait_load();
+          const __half2 f = __float2half2_rn(factor);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * factor);
-        tmem_store16(o_at + k, o);
-      }
-    }
-  }
-  if constexpr (EIGHT) {
-    if (ml_tile > st.ml + kTreeLazy || (st.ml == -INFINITY && ml_tile > -INFINITY)) {
-      st.l *= st.ml == -INFINITY ? 0.f : fast_exp2(st.ml - ml_tile);
-      st.ml = ml_tile;
-    }
-  } else {
-    st.ml = st.m;
-  }
-  const float ref = st.m == -INFINITY ? 0.f : st.m - kLift;
-  const float lref = st.ml == -INFINITY ? 0.f : st.ml;
-#pragma unroll 1
-  for (int from = 0; from < COLS; from += kHold) {
-    if (kHold < COLS) load(from);
-#pragma unroll
-    for (int h = 0; h < kHold; h += 32) {
-    uint32_t hi[16];
-    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-      const int at = h + i, g = EIGHT ? at / 16 : 0;
-      float2 y = __ffma2_rn(make_float2(__uint_as_float(r[at]), __uint_as_float(r[at + 1])),
-                            make_float2(ak[g], ak[g]), make_float2(vk[g] - ref, vk[g] - ref));
-      if (EIGHT && !PLAIN && masked) {
-        if (r[at] == kHidden) y.x = -INFINITY;
-        if (r[at + 1] == kHidden) y.y = -INFINITY;
-      }
-      y.x = fast_exp2(y.x);
-      y.y = fast_exp2(y.y);
-      sum[i / 16] = __fadd2_rn(sum[i / 16], y);
-      hi[i / 2] = pack2<BF16>(y.x, y.y);
-      if constexpr (PIECES == 2) {
-        r[at] = __float_as_uint(y.x);
-        r[at + 1] = __float_as_uint(y.y);
-      }
-    }
-    if constexpr (EIGHT) {
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        // l counts the weights without the scale of V
-        st.l += (sum[g].x + sum[g].y) * fast_exp2(fminf(ref - lref - vk[h / 16 + g], 126.f));
-        if constexpr (!PLAIN) {
-          const float sg = __shfl_sync(0xffffffffu, sign, (col + from + h) / 16 + g);
-          if (sg != 1.f) {
-#pragma unroll
-            for (int i = 8 * g; i < 8 * g + 8; ++i) hi[i] = sg == 0.f ? 0u : hi[i] ^ 0x80008000u;
+          for (int i = 0; i < 16; ++i) {
+            const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&w[i]), f);
+            w[i] = *reinterpret_cast<const uint32_t*>(&x);
           }
+          tmem_store16(p_at + k, w);
         }
       }
-    } else {
-      st.l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-    }
-    tmem_store16(p_at + weight_column<PIECES>(col + from + h), hi);
-    if constexpr (PIECES == 2) {
+      if (!first) {
+#pragma unroll 1
+        for (int k = 0; k < D; k += 16) {
+          uint32_t o[16];
+          tmem_load16(o_at + k, o);
+          tmem_wait_load();
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        hi[i] = pack2<true>(__uint_as_float(r[h + 2 * i]) - __uint_as_float(hi[i] << 16),
-                            __uint_as_float(r[h + 2 * i + 1]) - __uint_as_float(hi[i] & 0xffff0000u));
-      tmem_store16(p_at + weight_column<PIECES>(col + from + h) + 32, hi);
+          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * factor);
+          tmem_store16(o_at + k, o);
+        }
+      }
     }
+    const float ref = st.m == -INFINITY ? 0.f : st.m - kLift, lref = st.ml == -INFINITY ? 0.f : st.ml;
+    float total = 0.f;
+#pragma unroll
+    for (int h = 0; h < kHold; h += 32) {
+      uint32_t hi[16], lo[16];
+      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        const int at = h + i, g = EIGHT ? at / 16 : 0;
+        float2 y = __ffma2_rn(make_float2(__uint_as_float(r[at]), __uint_as_float(r[at + 1])),
+                              make_float2(ak[g], ak[g]), make_float2(vk[g] - ref, vk[g] - ref));
+        if (EIGHT && !PLAIN && masked) {
+          if (r[at] == kHidden) y.x = -INFINITY;
+          if (r[at + 1] == kHidden) y.y = -INFINITY;
+        }
+        y.x = fast_exp2(y.x);
+        y.y = fast_exp2(y.y);
+        sum[i / 16] = __fadd2_rn(sum[i / 16], y);
+        const uint32_t v = pack2<BF16>(y.x, y.y);
+        hi[i / 2] = v;
+        if constexpr (PIECES == 2)
+          lo[i / 2] = pack2<true>(y.x - __uint_as_float(v << 16), y.y - __uint_as_float(v & 0xffff0000u));
+      }
+      if constexpr (EIGHT) {
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          // l counts the weights without the scale of V
+          total += (sum[g].x + sum[g].y) * fast_exp2(fminf(ref - lref - vk[h / 16 + g], 126.f));
+          if constexpr (!PLAIN) {
+            const float sg = __shfl_sync(0xffffffffu, sign, (col + from + h) / 16 + g);
+            if (sg != 1.f) {
+#pragma unroll
+              for (int i = 8 * g; i < 8 * g + 8; ++i) hi[i] = sg == 0.f ? 0u : hi[i] ^ 0x80008000u;
+            }
+          }
+        }
+      } else {
+        total += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+      }
+      // (over scores that are in registers, or were used)
+      tmem_store16(p_at + weight_column<PIECES>(col + from + h), hi);
+      if constexpr (PIECES == 2) tmem_store16(p_at + weight_column<PIECES>(col + from + h) + 32, lo);
     }
+    st.l += total;
   }
   if constexpr (COLS < 128) {
     // the other columns of this row belong to its copies
@@ -1154,12 +1161,53 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
           scales_of(id_next);
           id_next = page_of(u + 4);
         }
+        uint32_t seen[4] = {0u, 0u, 0u, 0u};
+        if (masked && live) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (32 * k < own) seen[k] = seen_bits(p, seg, token, local, j0 + col + 32 * k);
+        }
+        if constexpr (!EIGHT) {
+          // V rows behind the last one become zero, elements of drafted rows that are not finite too: they are added at
+          // the end for those who see them. (Before the wait for the scores, which are being made meanwhile.)
+          if (masked && !dead && (!two || grp == 0)) {
+            const int use = 2 * (tau + t - seg.t0) + 1, slot = use % Shape::kSlots, j = j0 + row;
+            const int valid = min(kTreeTile, seg.rows - j0);
+            if (row < (valid + 15) / 16 * 16 && j >= seg.base) {
+              if (!tree_wait(c, p, &c->full[slot], (use / Shape::kSlots) & 1)) dead = true;
+              uint8_t* const v = smem + Shape::kRing + slot * Shape::kTileBytes;
+              auto at = [&](int i) { return reinterpret_cast<uint4*>(v + chunk_at<D>(row, i)); };
+              if (row >= valid) {
+                for (int i = 0; i < D / 8; ++i) *at(i) = make_uint4(0u, 0u, 0u, 0u);
+              } else {
+                // (an exponent of ones, and one more, carries into the sign's place)
+                constexpr uint32_t kExp = kBf16 ? 0x7f807f80u : 0x7c007c00u, kOne = kBf16 ? 0x00800080u : 0x04000400u;
+                uint32_t bad = 0;
+#pragma unroll 4
+                for (int i = 0; i < D / 8; ++i) {
+                  const uint4 x = *at(i);
+                  bad |= ((x.x & kExp) + kOne) | ((x.y & kExp) + kOne) | ((x.z & kExp) + kOne) | ((x.w & kExp) + kOne);
+                }
+                if (bad & 0x80008000u) {
+                  for (int i = 0; i < D / 8; ++i) {
+                    const uint4 x = *at(i);
+                    *at(i) = make_uint4(x.x & finite_pair_mask<kBf16>(x.x), x.y & finite_pair_mask<kBf16>(x.y),
+                                        x.z & finite_pair_mask<kBf16>(x.z), x.w & finite_pair_mask<kBf16>(x.w));
+                  }
+                  const int d = j - seg.base;
+                  atomicOr(&c->bad[s & 7][d >> 5], 1u << (d & 31));
+                }
+              }
+              fence_proxy_async_shared();
+            }
+            dead = __any_sync(0xffffffffu, dead);
+          }
+        }
         if (!dead) dead = !__all_sync(0xffffffffu, tree_wait(c, p, &c->s_full[grp], phase_s & 1));
         ++phase_s;
         if (dead) continue;
         tc_fence_after();
         if (busy) {
-          auto seen = [&](int k) { return live ? seen_bits(p, seg, token, local, j0 + col + 32 * k) : 0u; };
           auto columns = [&](auto cols, auto pieces) {
             constexpr int kCols = decltype(cols)::value, kPieces = decltype(pieces)::value;
             const float2* const scales = c->scales[warp];
@@ -1181,44 +1229,12 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
             columns(integral_constant<int, 32>(), kPieces);
           }
         }
-        if constexpr (!EIGHT) {
-          // V rows behind the last one become zero, elements of drafted rows that are not finite too: they
-          // are added at the end for those who see them
-          if (masked && (!two || grp == 0)) {
-            const int use = 2 * (tau + t - seg.t0) + 1, slot = use % Shape::kSlots, j = j0 + row;
-            const int valid = min(kTreeTile, seg.rows - j0);
-            if (row < (valid + 15) / 16 * 16 && j >= seg.base) {
-              if (!tree_wait(c, p, &c->full[slot], (use / Shape::kSlots) & 1)) dead = true;
-              uint8_t* const v = smem + Shape::kRing + slot * Shape::kTileBytes;
-              bool bad = false;
-#pragma unroll 4
-              for (int i = 0; i < D / 8; ++i) {
-                uint4* const at = reinterpret_cast<uint4*>(v + chunk_at<D>(row, i));
-                if (row >= valid) {
-                  *at = make_uint4(0u, 0u, 0u, 0u);
-                } else {
-                  uint4 x = *at;
-                  const uint4 m = make_uint4(finite_pair_mask<kBf16>(x.x), finite_pair_mask<kBf16>(x.y),
-                                             finite_pair_mask<kBf16>(x.z), finite_pair_mask<kBf16>(x.w));
-                  if ((m.x & m.y & m.z & m.w) != 0xffffffffu) {
-                    bad = true;
-                    *at = make_uint4(x.x & m.x, x.y & m.y, x.z & m.z, x.w & m.w);
-                  }
-                }
-              }
-              const int d = j - seg.base;
-              if (bad) atomicOr(&c->bad[s & 7][d >> 5], 1u << (d & 31));
-              fence_proxy_async_shared();
-            }
-            dead = __any_sync(0xffffffffu, dead);
-          }
-        }
         tc_fence_before();
         mbar_arrive(&c->p_full[grp]);
       }
 
       // ---- the segment's output ----
-      if constexpr (EIGHT) st.m -= 7.f;  // (weights were held 2^7 times as large, and l was not)
+      if constexpr (EIGHT) st.m -= kTreeLift;  // (of which l knows nothing)
       if (!dead) dead = !__all_sync(0xffffffffu, tree_wait(c, p, &c->o_final, s & 1));
       tc_fence_after();
       const bool nan = dead || c->bad_page[s & 7] != 0;
