@@ -18,7 +18,8 @@ namespace da {
 
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kThreads = 1024, kWarps = kThreads / 32;
+constexpr int kAtOnce = 4;  // entries of a lane on their way at once: a call's time is its chain of loads
 constexpr int kClusterMax = 8;  // the portable size
 
 __device__ __forceinline__ void cluster_sync() {
@@ -124,24 +125,37 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(const PoolParams p, in
     for (int i = warp / each; i < min(kThreads, p.B - first) && warp < each * pass; i += warps / each) {
       const Span s = spans[i];
       int32_t* const row = p.table + (int64_t)(first + i) * p.max_pages;
-      for (int j = s.wanted + warp % each * 32 + lane; j < s.held; j += each * 32) {
-        const int id = row[j];
-        row[j] = -1;
-        if (id < 0 || id >= p.num_pages) {
-          if (id != -1) errors |= kErrPage;
-          continue;
+      for (int j0 = s.wanted + warp % each * 32 + lane; j0 < s.held; j0 += each * 32 * kAtOnce) {
+        int id[kAtOnce], before[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+          const int j = j0 + k * each * 32;
+          id[k] = j < s.held ? row[j] : -1;
         }
-        const int before = atomicSub(counts + id, 1);
-        if (before == 1) {
-          const uint32_t word = (uint32_t)id >> 5;
-          if (ctas > 1) {
-            cluster_or(cluster_addr(freed + word % words, word / words), 1u << (id & 31));
-          } else {
-            atomicOr(freed + word, 1u << (id & 31));
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+          const int j = j0 + k * each * 32;
+          if (j < s.held) row[j] = -1;
+          before[k] = 2;  // (nothing to do)
+          if (id[k] >= 0 && id[k] < p.num_pages) {
+            before[k] = atomicSub(counts + id[k], 1);
+          } else if (id[k] != -1) {
+            errors |= kErrPage;
           }
-        } else if (before < 1) {
-          atomicAdd(counts + id, 1);
-          errors |= kErrPool;
+        }
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+          if (before[k] == 1) {
+            const uint32_t word = (uint32_t)id[k] >> 5;
+            if (ctas > 1) {
+              cluster_or(cluster_addr(freed + word % words, word / words), 1u << (id[k] & 31));
+            } else {
+              atomicOr(freed + word, 1u << (id[k] & 31));
+            }
+          } else if (before[k] < 1) {
+            atomicAdd(counts + id[k], 1);
+            errors |= kErrPool;
+          }
         }
       }
     }
@@ -184,21 +198,27 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(const PoolParams p, in
       for (int i = warp / each; i < min(kThreads, p.B - first) && warp < each * pass; i += warps / each) {
         const Span s = spans[i];
         int32_t* const row = p.table + (int64_t)(first + i) * p.max_pages;
-        for (int j = s.held + warp % each * 32 + lane; j < s.wanted; j += each * 32) {
-          const int rank = s.rank + j - s.held;
-          int id = -1;
-          if (rank < top) {
-            id = __ldcg(list + top - 1 - rank);
-            if (id < 0 || id >= p.num_pages) {
-              errors |= kErrPool;
-              id = -1;
-            } else {
-              atomicAdd(counts + id, 1);
-            }
-          } else {
-            errors |= kErrFull;
+        for (int j0 = s.held + warp % each * 32 + lane; j0 < s.wanted; j0 += each * 32 * kAtOnce) {
+          int id[kAtOnce];
+#pragma unroll
+          for (int k = 0; k < kAtOnce; ++k) {
+            const int rank = s.rank + j0 + k * each * 32 - s.held;
+            id[k] = j0 + k * each * 32 < s.wanted && rank < top ? __ldcg(list + top - 1 - rank) : -1;
           }
-          row[j] = id;
+#pragma unroll
+          for (int k = 0; k < kAtOnce; ++k) {
+            const int j = j0 + k * each * 32, rank = s.rank + j - s.held;
+            if (j >= s.wanted) break;
+            if (rank >= top) {
+              errors |= kErrFull;
+            } else if (id[k] < 0 || id[k] >= p.num_pages) {
+              errors |= kErrPool;
+              id[k] = -1;
+            } else {
+              atomicAdd(counts + id[k], 1);
+            }
+            row[j] = id[k];
+          }
         }
       }
     }
@@ -271,10 +291,17 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const PoolParams p, int 
       const int32_t* const from = p.table + (int64_t)k.parent * p.max_pages;
       int32_t* const to = p.table + (int64_t)k.child * p.max_pages;
       if (k.rows > 0) {
-        for (int j = warp % each * 32 + lane; j < full; j += each * 32) {
-          const int id = from[j];
-          to[j] = id;
-          if (id >= 0 && id < p.num_pages) atomicAdd(counts + id, 1); else errors |= kErrPage;
+        for (int j0 = warp % each * 32 + lane; j0 < full; j0 += each * 32 * kAtOnce) {
+          int id[kAtOnce];
+#pragma unroll
+          for (int k = 0; k < kAtOnce; ++k) id[k] = j0 + k * each * 32 < full ? from[j0 + k * each * 32] : 0;
+#pragma unroll
+          for (int k = 0; k < kAtOnce; ++k) {
+            const int j = j0 + k * each * 32;
+            if (j >= full) break;
+            to[j] = id[k];
+            if (id[k] >= 0 && id[k] < p.num_pages) atomicAdd(counts + id[k], 1); else errors |= kErrPage;
+          }
         }
       }
       if (warp % each == 0 && lane == 0) {

@@ -145,6 +145,7 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const MoveParams p) {
     // the lanes of a unit share its page scales: they are read by all before one writes them
     const uint32_t team = (p.row_vecs == 32 ? 0xffffffffu : (1u << p.row_vecs) - 1) << (threadIdx.x % 32 / p.row_vecs * p.row_vecs);
     bool ok = true;
+    int pages[kBatch];
     for (int i0 = 0; i0 < n && ok;) {
       // rows of one target page
       const int target0 = first + i0;
@@ -158,43 +159,79 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const MoveParams p) {
       const bool d_ok = inside(d);
       const float own = d_ok ? scales[block(d)] : 0.f;
       float scale = own;
-      const int before = last;
+      // Rows of the first kBatch on their way at once: their numbers, pages, scales, then the rows themselves; of further
+      // ones in the page only the scales at first.
       int end = i0;  // rows [i0, end) are valid
-      for (; end < i1; ++end) {
-        const int row = keep[end];
-        if (!valid(end, row)) break;
-        last = row;
-        const int a = table[row >> p.page_shift];
-        if (inside(a)) scale = fmaxf(scale, scales[block(a)]);
+      int src[kBatch];
+      float from[kBatch];
+      for (int j0 = i0; j0 < i1 && end == j0; j0 += kBatch) {
+        int row[kBatch], a[kBatch];
+        float s[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) row[k] = j0 + k < i1 ? keep[j0 + k] : -1;
+        int good = 0;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          if (good == k && j0 + k < i1 && valid(j0 + k, row[k])) {
+            last = row[k];
+            ++good;
+          }
+        }
+        end = j0 + good;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) a[k] = k < good ? table[row[k] >> p.page_shift] : -1;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const bool in = k < good && inside(a[k]);
+          if (k < good && !in) errors |= kErrPage;
+          s[k] = in ? scales[block(a[k])] : 0.f;
+          scale = fmaxf(scale, s[k]);
+          if (j0 == i0) {
+            // (a row that stays, or cannot be had, is one of the page's other rows)
+            const int target = first + j0 + k;
+            const bool moves = in && row[k] != target;
+            src[k] = moves ? row[k] : target;
+            from[k] = moves ? s[k] : own;
+            a[k] = moves ? a[k] : d;
+            row[k] = k < good ? a[k] : -1;
+          }
+        }
+        if (j0 == i0) {
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) pages[k] = row[k];
+        }
       }
-      last = before;
       __syncwarp(team);
-      if (d_ok) {
+      if (d_ok && end > i0) {
         uint4* const out = pool + block(d) * page_vecs + c;
         for (int j0 = i0; j0 < end; j0 += kBatch) {
+          if (j0 > i0) {
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+              const int row = j0 + k < end ? keep[j0 + k] : -1, target = first + j0 + k;
+              const int a = row >= 0 ? table[row >> p.page_shift] : -1;
+              const bool moves = inside(a) && row != target;
+              src[k] = moves ? row : target;
+              pages[k] = row < 0 ? -1 : moves ? a : d;
+              from[k] = moves ? (a == d ? own : scales[block(a)]) : own;
+            }
+          }
           uint4 x[kBatch];
-          bool have[kBatch];
 #pragma unroll
           for (int k = 0; k < kBatch; ++k) {
-            have[k] = false;
-            if (j0 + k >= end) continue;
-            const int row = keep[j0 + k], target = first + j0 + k;
-            int a = table[row >> p.page_shift];
-            if (!inside(a)) errors |= kErrPage;
-            const bool moves = inside(a) && row != target;
-            if (!moves && scale == own) continue;
-            if (!moves) a = d;  // stays, as one of the page's other rows
-            have[k] = true;
-            x[k] = rescaled(pool[block(a) * page_vecs + (int64_t)((moves ? row : target) & (p.page_rows - 1)) * p.row_vecs + c],
-                            a == d ? own : scales[block(a)], scale);
+            if (pages[k] >= 0 && (pages[k] != d || src[k] != first + j0 + k || scale != own))
+              x[k] = pool[block(pages[k]) * page_vecs + (int64_t)(src[k] & (p.page_rows - 1)) * p.row_vecs + c];
           }
 #pragma unroll
-          for (int k = 0; k < kBatch; ++k)
-            if (have[k]) out[(int64_t)((first + j0 + k) & (p.page_rows - 1)) * p.row_vecs] = x[k];
+          for (int k = 0; k < kBatch; ++k) {
+            if (pages[k] >= 0 && (pages[k] != d || src[k] != first + j0 + k || scale != own))
+              out[(int64_t)((first + j0 + k) & (p.page_rows - 1)) * p.row_vecs] = rescaled(x[k], from[k], scale);
+          }
         }
-        if (end > i0 && scale != own) {
+        if (scale != own) {
           // the page's other rows
           const int lo = target0 & (p.page_rows - 1), hi = lo + (end - i0);
+#pragma unroll 4
           for (int r = 0; r < p.page_rows; ++r)
             if (r < lo || r >= hi) out[(int64_t)r * p.row_vecs] = rescaled(out[(int64_t)r * p.row_vecs], own, scale);
         }
@@ -204,7 +241,6 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const MoveParams p) {
       __syncwarp(team);
       if (d_ok && end > i0 && scale != own && c == 0) scales[block(d)] = scale;
       __syncwarp(team);
-      if (end > i0) last = keep[end - 1];
       ok = end == i1;
       i0 = i1;
     }

@@ -34,7 +34,7 @@ namespace da {
 constexpr int kTreeTile = 128;             // cache rows of a tile, query rows of a tile
 constexpr int kTreeUnitRows = 256;         // query rows of a unit
 constexpr unsigned long long kTreeHelpNs = 20000;  // how long a CTA waits for a unit's other parts, to help with their join
-constexpr int kTreeMinTiles = 1;            // a part of a unit has at least as many tiles
+constexpr int kTreeMinTiles = 2;            // a part of a unit has at least as many tiles
 constexpr int kTreeJoinTiles = 8;           // what the ends of a share inside units cost, in tiles (at most the warps)
 constexpr int kTreeUnitTiles = 6;           // ... what beginning and ending a unit takes
 constexpr float kTreeLazy = 7.f;            // a running maximum is raised when a score passes it by 2^7
