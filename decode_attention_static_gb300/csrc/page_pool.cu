@@ -6,7 +6,9 @@
 // need a barrier over all threads, and the cluster's is in hardware, without
 // counters in memory or a promise that CTAs run at the same time. The bytes (a table
 // entry, a count and a list entry for each page) are few; what a call
-// costs is the chain of dependent loads (length, entry, count) and barriers.
+// costs is the chain of dependent loads (length, entry, count) and barriers. A
+// resize that moves few pages (a step's drafts), which only the lengths say, is
+// therefore left to the first CTA alone.
 #include <stdint.h>
 
 #include <algorithm>
@@ -31,16 +33,10 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ uint32_t cluster_addr(const void* local, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr(local)), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ void cluster_or(uint32_t addr, uint32_t v) {
-  asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
-__device__ __forceinline__ int cluster_load(uint32_t addr) {
+__device__ __forceinline__ int cluster_load(const int* local, uint32_t rank) {
+  uint32_t addr;
   int v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_addr(local)), "r"(rank));
   asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
@@ -49,9 +45,17 @@ __device__ __forceinline__ void report(int32_t* err_flag, int bits) {
   if (bits && err_flag) atomicOr(err_flag, bits);
 }
 
-// Sum of v over the threads before this one, and (in *all) over all of them.
-// `scratch` holds kWarps + 1 numbers; every thread takes part.
-__device__ __forceinline__ int scan_threads(int v, int* scratch, int* all) {
+// Threads for each of n sequences (of a pass over at most kThreads): a power of two.
+__device__ __forceinline__ int team_of(int ctas, int n) {
+  return 1 << (31 - __clz(ctas * kThreads / max(1, min(n, kThreads))));
+}
+
+// Sum of v over the threads before this one; in *all and *all_other the sums
+// of v and `other` over all of them. Every thread takes part.
+struct ScanArea {
+  int v[kWarps], other[kWarps];
+};
+__device__ __forceinline__ int scan_threads(int v, int other, ScanArea& area, int* all, int* all_other) {
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   int sum = v;
 #pragma unroll
@@ -59,12 +63,17 @@ __device__ __forceinline__ int scan_threads(int v, int* scratch, int* all) {
     const int up = __shfl_up_sync(0xffffffffu, sum, o);
     if (lane >= o) sum += up;
   }
+  other = __reduce_add_sync(0xffffffffu, other);
   __syncthreads();  // (the last call's sums have been read)
-  if (lane == 31) scratch[warp] = sum;
+  if (lane == 31) {
+    area.v[warp] = sum;
+    area.other[warp] = other;
+  }
   __syncthreads();
-  const int w = lane < kWarps ? scratch[lane] : 0;
+  const int w = lane < kWarps ? area.v[lane] : 0;
   const int before = __reduce_add_sync(0xffffffffu, lane < warp ? w : 0);
   *all = __reduce_add_sync(0xffffffffu, w);
+  *all_other = __reduce_add_sync(0xffffffffu, lane < kWarps ? area.other[lane] : 0);
   return before + sum - v;
 }
 
@@ -76,7 +85,7 @@ struct Span {
 
 // The sequences [first, first + kThreads): their spans into shared memory;
 // returns the pages they take, and adds those they release to *released.
-__device__ __forceinline__ int find_spans(const PoolParams& p, int first, int taken, Span* spans, int* scratch,
+__device__ __forceinline__ int find_spans(const PoolParams& p, int first, int taken, Span* spans, ScanArea& area,
                                           int* released, int* errors) {
   const int b = first + threadIdx.x, most = p.max_pages << p.page_shift, size = 1 << p.page_shift;
   Span s = {0, 0, 0};
@@ -90,24 +99,28 @@ __device__ __forceinline__ int find_spans(const PoolParams& p, int first, int ta
     }
   }
   int take, drop;
-  scan_threads(max(0, s.held - s.wanted), scratch, &drop);
-  s.rank = taken + scan_threads(max(0, s.wanted - s.held), scratch, &take);
+  s.rank = taken + scan_threads(max(0, s.wanted - s.held), max(0, s.held - s.wanted), area, &take, &drop);
   *released += drop;
   spans[threadIdx.x] = s;
   __syncthreads();
   return take;
 }
 
-// One cluster. A page that becomes free sets its bit in the shared memory of
-// the CTA that owns its part of the pool; the CTAs then list their bits.
-__global__ void __launch_bounds__(kThreads) resize_kernel(const PoolParams p, int ctas, int words) {
-  extern __shared__ uint32_t freed[];  // [words]: bits of this CTA's pages
+// A page whose count has just become zero is marked by a count of kFreed (or
+// near it, where it is released once too often in the same call) until it is listed.
+constexpr int kFreed = INT32_MIN / 2;
+__device__ __forceinline__ bool just_freed(int count) { return count < kFreed / 2; }
+
+// Pages that a resize releases and takes at most for it to be the first CTA's alone.
+constexpr int kSoloReleases = kThreads, kSoloTakes = 4 * kThreads;
+
+__global__ void __launch_bounds__(kThreads) resize_kernel(const PoolParams p, int ctas) {
   __shared__ Span spans[kThreads];
-  __shared__ int scratch[kWarps + 1];
+  __shared__ ScanArea area;
   __shared__ int listed;
-  const int lane = threadIdx.x % 32, cta = ctas > 1 ? (int)cluster_rank() : 0;
-  const int warps = ctas * kWarps, warp = cta * kWarps + threadIdx.x / 32;
-  for (int i = threadIdx.x; i < words; i += kThreads) freed[i] = 0;
+  __shared__ __align__(16) int freed[kSoloReleases + 4];  // the first CTA alone: pages that became free
+  const int lane = threadIdx.x % 32;
+  int cta = ctas > 1 ? (int)cluster_rank() : 0;
   pdl_wait();
   pdl_trigger();
   int32_t* const counts = p.pool + kPoolHeader;
@@ -116,25 +129,38 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(const PoolParams p, in
   const int free_now = __ldcg(p.pool);
   const int free0 = min(max(free_now, 0), p.num_pages);
   if (free0 != free_now) errors |= kErrPool;
-  if (ctas > 1) cluster_sync();  // every CTA's bits are zero, and the free pages have been read
-  // as many warps for a sequence as there are for each of a pass
-  const int pass = min(p.B, kThreads), each = max(1, warps / max(1, pass));
+  bool solo = false;
+  if (p.B <= kThreads) {
+    taken = find_spans(p, 0, 0, spans, area, &released, &errors);
+    solo = released <= kSoloReleases && taken <= kSoloTakes;  // (the same in every CTA)
+    if (solo) {
+      if (cta > 0) return;
+      ctas = 1;
+    }
+  }
+  auto barrier = [&]() {
+    if (ctas > 1) cluster_sync(); else __syncthreads();
+  };
+  if (threadIdx.x == 0) listed = 0;
+  barrier();  // every CTA has read the free pages
+  // as many threads for a sequence as there are for each of a pass
+  const int thread = cta * kThreads + threadIdx.x, team = team_of(ctas, p.B), mine = thread / team, at0 = thread % team;
   // releases
   for (int first = 0; first < p.B; first += kThreads) {
-    taken += find_spans(p, first, taken, spans, scratch, &released, &errors);
-    for (int i = warp / each; i < min(kThreads, p.B - first) && warp < each * pass; i += warps / each) {
-      const Span s = spans[i];
-      int32_t* const row = p.table + (int64_t)(first + i) * p.max_pages;
-      for (int j0 = s.wanted + warp % each * 32 + lane; j0 < s.held; j0 += each * 32 * kAtOnce) {
+    if (p.B > kThreads) taken += find_spans(p, first, taken, spans, area, &released, &errors);
+    if (mine < min(kThreads, p.B - first)) {
+      const Span s = spans[mine];
+      int32_t* const row = p.table + (int64_t)(first + mine) * p.max_pages;
+      for (int j0 = s.wanted + at0; j0 < s.held; j0 += team * kAtOnce) {
         int id[kAtOnce], before[kAtOnce];
 #pragma unroll
         for (int k = 0; k < kAtOnce; ++k) {
-          const int j = j0 + k * each * 32;
+          const int j = j0 + k * team;
           id[k] = j < s.held ? row[j] : -1;
         }
 #pragma unroll
         for (int k = 0; k < kAtOnce; ++k) {
-          const int j = j0 + k * each * 32;
+          const int j = j0 + k * team;
           if (j < s.held) row[j] = -1;
           before[k] = 2;  // (nothing to do)
           if (id[k] >= 0 && id[k] < p.num_pages) {
@@ -146,11 +172,10 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(const PoolParams p, in
 #pragma unroll
         for (int k = 0; k < kAtOnce; ++k) {
           if (before[k] == 1) {
-            const uint32_t word = (uint32_t)id[k] >> 5;
-            if (ctas > 1) {
-              cluster_or(cluster_addr(freed + word % words, word / words), 1u << (id[k] & 31));
+            if (solo) {
+              freed[atomicAdd(&listed, 1)] = id[k];
             } else {
-              atomicOr(freed + word, 1u << (id[k] & 31));
+              atomicAdd(counts + id[k], kFreed);
             }
           } else if (before[k] < 1) {
             atomicAdd(counts + id[k], 1);
@@ -162,52 +187,78 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(const PoolParams p, in
     if (first + kThreads < p.B) __syncthreads();
   }
   int top = free0;
-  if (released > 0) {  // (the same in every CTA)
-    if (ctas > 1) cluster_sync(); else __syncthreads();
-    const int per = (words + kThreads - 1) / kThreads;  // words of a thread
-    const int lo = min(words, (int)threadIdx.x * per), hi = min(words, lo + per);
-    int mine = 0;
-    for (int i = lo; i < hi; ++i) mine += __popc(freed[i]);
-    int all;
-    int at = scan_threads(mine, scratch, &all);
+  if (solo) {
+    if (released > 0) {
+      __syncthreads();
+      // in rising order: a page's place is the number of smaller ones
+      const int n = listed, id = (int)threadIdx.x < n ? freed[threadIdx.x] : 0;
+      if (threadIdx.x < 4) freed[n + threadIdx.x] = INT32_MAX;
+      __syncthreads();
+      int place = 0;
+      if (threadIdx.x / 32 * 32 < n) {
+#pragma unroll 4
+        for (int i = 0; i < n; i += 4) {
+          const int4 x = *reinterpret_cast<const int4*>(freed + i);
+          place += (x.x < id) + (x.y < id) + (x.z < id) + (x.w < id);
+        }
+      }
+      if ((int)threadIdx.x < n && free0 + place < p.num_pages) list[free0 + place] = id;
+      if (free0 + n > p.num_pages) errors |= kErrPool;
+      top = min(free0 + n, p.num_pages);
+      __syncthreads();
+    }
+  } else if (released > 0) {
+    barrier();
+    // each CTA lists its part of the pool
+    const int per = ((p.num_pages + ctas - 1) / ctas + kThreads - 1) / kThreads * kThreads;
+    const int lo = min(p.num_pages, cta * per), hi = min(p.num_pages, lo + per);
+    int found = 0;
+#pragma unroll 4
+    for (int i = lo + threadIdx.x; i < hi; i += kThreads) found += just_freed(__ldcg(counts + i));
+    int all, none;
+    scan_threads(0, found, area, &none, &all);
+    int at = free0;
     if (ctas > 1) {
       if (threadIdx.x == 0) listed = all;
       cluster_sync();
-      const int n = lane < ctas ? cluster_load(cluster_addr(&listed, lane)) : 0;
+      const int n = lane < ctas ? cluster_load(&listed, lane) : 0;
       at += __reduce_add_sync(0xffffffffu, lane < cta ? n : 0);
       all = __reduce_add_sync(0xffffffffu, n);
     }
-    at += free0;
-    for (int i = lo; i < hi; ++i) {
-      for (uint32_t bits = freed[i]; bits; bits &= bits - 1) {
-        const int id = ((cta * words + i) << 5) + __ffs(bits) - 1;
-        if (at < p.num_pages) list[at] = id; else errors |= kErrPool;
-        ++at;
+    for (int i0 = lo; i0 < hi; i0 += kThreads) {
+      const int id = i0 + threadIdx.x, count = id < hi ? __ldcg(counts + id) : 0;
+      const bool is = just_freed(count);
+      int here;
+      const int place = at + scan_threads(is, 0, area, &here, &none);
+      if (is) {
+        counts[id] = 0;
+        if (place < p.num_pages) list[place] = id; else errors |= kErrPool;
       }
+      at += here;
     }
     top = min(free0 + all, p.num_pages);
-    if (ctas > 1) cluster_sync(); else __syncthreads();
+    barrier();
   }
   if (taken > 0) {
     int rank0 = 0, none = 0;
     for (int first = 0; first < p.B; first += kThreads) {
       if (p.B > kThreads) {
         __syncthreads();
-        rank0 += find_spans(p, first, rank0, spans, scratch, &none, &none);
+        rank0 += find_spans(p, first, rank0, spans, area, &none, &none);
       }
-      for (int i = warp / each; i < min(kThreads, p.B - first) && warp < each * pass; i += warps / each) {
-        const Span s = spans[i];
-        int32_t* const row = p.table + (int64_t)(first + i) * p.max_pages;
-        for (int j0 = s.held + warp % each * 32 + lane; j0 < s.wanted; j0 += each * 32 * kAtOnce) {
+      if (mine < min(kThreads, p.B - first)) {
+        const Span s = spans[mine];
+        int32_t* const row = p.table + (int64_t)(first + mine) * p.max_pages;
+        for (int j0 = s.held + at0; j0 < s.wanted; j0 += team * kAtOnce) {
           int id[kAtOnce];
 #pragma unroll
           for (int k = 0; k < kAtOnce; ++k) {
-            const int rank = s.rank + j0 + k * each * 32 - s.held;
-            id[k] = j0 + k * each * 32 < s.wanted && rank < top ? __ldcg(list + top - 1 - rank) : -1;
+            const int rank = s.rank + j0 + k * team - s.held;
+            id[k] = j0 + k * team < s.wanted && rank < top ? __ldcg(list + top - 1 - rank) : -1;
           }
 #pragma unroll
           for (int k = 0; k < kAtOnce; ++k) {
-            const int j = j0 + k * each * 32, rank = s.rank + j - s.held;
+            const int j = j0 + k * team, rank = s.rank + j - s.held;
             if (j >= s.wanted) break;
             if (rank >= top) {
               errors |= kErrFull;
@@ -233,13 +284,12 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(const PoolParams p, in
 // copy table rows.
 __global__ void __launch_bounds__(kThreads) fork_kernel(const PoolParams p, int ctas, int words) {
   extern __shared__ uint32_t bits[];  // [words] children, [words] children of more than one fork
-  __shared__ int scratch[kWarps + 1];
+  __shared__ ScanArea area;
   struct Fork {
     int parent, child, rows, rank;  // rows -1: skipped
   };
   __shared__ Fork forks[kThreads];
-  const int lane = threadIdx.x % 32, cta = ctas > 1 ? (int)cluster_rank() : 0;
-  const int warps = ctas * kWarps, warp = cta * kWarps + threadIdx.x / 32;
+  const int cta = ctas > 1 ? (int)cluster_rank() : 0;
   for (int i = threadIdx.x; i < 2 * words; i += kThreads) bits[i] = 0;
   __syncthreads();
   pdl_wait();
@@ -256,7 +306,7 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const PoolParams p, int 
       atomicOr(bits + words + (c >> 5), 1u << (c & 31));
   }
   __syncthreads();
-  const int pass = min(p.n, kThreads), each = max(1, warps / max(1, pass));
+  const int thread = cta * kThreads + threadIdx.x, team = team_of(ctas, p.n), my_fork = thread / team, at0 = thread % team;
   const int size = 1 << p.page_shift;
   int taken = 0;
   for (int first = 0; first < p.n; first += kThreads) {
@@ -276,8 +326,8 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const PoolParams p, int 
         }
       }
     }
-    int need = f.rows > 0 && (f.rows & (size - 1)) ? 1 : 0, all;
-    f.rank = taken + scan_threads(need, scratch, &all);
+    int need = f.rows > 0 && (f.rows & (size - 1)) ? 1 : 0, all, none;
+    f.rank = taken + scan_threads(need, 0, area, &all, &none);
     taken += all;
     if (need && f.rank >= free0) {
       errors |= kErrFull;
@@ -285,26 +335,26 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const PoolParams p, int 
     }
     forks[threadIdx.x] = f;
     __syncthreads();
-    for (int i = warp / each; i < min(kThreads, p.n - first) && warp < each * pass; i += warps / each) {
-      const Fork k = forks[i];
+    if (my_fork < min(kThreads, p.n - first)) {
+      const Fork k = forks[my_fork];
       const int full = k.rows >> p.page_shift, rest = k.rows & (size - 1);
       const int32_t* const from = p.table + (int64_t)k.parent * p.max_pages;
       int32_t* const to = p.table + (int64_t)k.child * p.max_pages;
       if (k.rows > 0) {
-        for (int j0 = warp % each * 32 + lane; j0 < full; j0 += each * 32 * kAtOnce) {
+        for (int j0 = at0; j0 < full; j0 += team * kAtOnce) {
           int id[kAtOnce];
 #pragma unroll
-          for (int k = 0; k < kAtOnce; ++k) id[k] = j0 + k * each * 32 < full ? from[j0 + k * each * 32] : 0;
+          for (int k = 0; k < kAtOnce; ++k) id[k] = j0 + k * team < full ? from[j0 + k * team] : 0;
 #pragma unroll
           for (int k = 0; k < kAtOnce; ++k) {
-            const int j = j0 + k * each * 32;
+            const int j = j0 + k * team;
             if (j >= full) break;
             to[j] = id[k];
             if (id[k] >= 0 && id[k] < p.num_pages) atomicAdd(counts + id[k], 1); else errors |= kErrPage;
           }
         }
       }
-      if (warp % each == 0 && lane == 0) {
+      if (at0 == 0) {
         int src = -1, dst = -1, rows = 0;
         if (k.rows > 0 && rest) {
           src = from[full];
@@ -323,7 +373,7 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const PoolParams p, int 
             rows = 0;
           }
         }
-        const int at = first + i;
+        const int at = first + my_fork;
         p.copies[at] = src;
         p.copies[p.n + at] = dst;
         p.copies[2 * (int64_t)p.n + at] = rows;
@@ -352,12 +402,8 @@ __global__ void __launch_bounds__(256) init_kernel(int32_t* pool, int num_pages)
 // else a cluster.
 constexpr int64_t kOneCtaEntries = 4096;
 
-template <typename K>
-cudaError_t launch_cluster(K* kernel, const PoolParams& p, int ctas, int words, size_t smem, cudaStream_t stream) {
-  if (smem > 32 * 1024) {  // (static arrays come on top)
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
+template <typename K, typename... A>
+cudaError_t launch_cluster(K* kernel, int ctas, size_t smem, cudaStream_t stream, A... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kThreads);
@@ -371,7 +417,7 @@ cudaError_t launch_cluster(K* kernel, const PoolParams& p, int ctas, int words, 
   attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
   cfg.attrs = attrs;
   cfg.numAttrs = ctas > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p, ctas, words);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 }  // namespace
@@ -383,17 +429,14 @@ cudaError_t launch_pool_init(int32_t* pool, int num_pages, cudaStream_t stream) 
 }
 
 cudaError_t launch_pool_resize(const PoolParams& p, cudaStream_t stream) {
-  const int64_t entries = (int64_t)p.B * p.max_pages;
-  const int all_words = (p.num_pages + 31) / 32;
-  const int ctas = entries <= kOneCtaEntries && all_words <= 8192 ? 1 : kClusterMax;
-  const int words = (all_words + ctas - 1) / ctas;
-  return launch_cluster(resize_kernel, p, ctas, words, (size_t)words * 4, stream);
+  const int ctas = (int64_t)p.B * p.max_pages <= kOneCtaEntries && p.num_pages <= kOneCtaEntries ? 1 : kClusterMax;
+  return launch_cluster(resize_kernel, ctas, 0, stream, p, ctas);
 }
 
 cudaError_t launch_pool_fork(const PoolParams& p, cudaStream_t stream) {
   const int ctas = (int64_t)p.n * p.max_pages <= kOneCtaEntries ? 1 : kClusterMax;
-  const int words = (p.B + 31) / 32;
-  return launch_cluster(fork_kernel, p, ctas, words, (size_t)words * 8, stream);
+  const int words = (p.B + 31) / 32;  // (at most 16 KiB of bits)
+  return launch_cluster(fork_kernel, ctas, (size_t)words * 8, stream, p, ctas, words);
 }
 
 }  // namespace da

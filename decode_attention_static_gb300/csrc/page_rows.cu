@@ -78,8 +78,8 @@ __device__ __forceinline__ uint4 rescaled(const uint4& v, float from, float to) 
 
 // Column c of (sequence b, layer, K or V, head g), as numbered by thread.
 template <bool EIGHT>
-__global__ void __launch_bounds__(kThreads) compact_kernel(const MoveParams p) {
-  constexpr int kBatch = 8;  // rows on their way at once
+__global__ void __launch_bounds__(kThreads, EIGHT ? 4 : 3) compact_kernel(const MoveParams p) {
+  constexpr int kBatch = EIGHT ? 4 : 8;  // rows on their way at once
   pdl_wait();
   pdl_trigger();
   const int64_t unit = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / p.row_vecs;
