@@ -97,7 +97,10 @@ __device__ __forceinline__ int4 pair_axes(const AppendPagedParams& p, int i) {
 __device__ __forceinline__ bool one_axis(const int4& a) { return a.x == a.y && a.x == a.z && a.x == a.w; }
 
 // Four elements at column `col` of a table, for pairs of axes `a`: one vector
-// where the pairs share an axis (sections of whole vectors), else gathered.
+// where the pairs share an axis (sections of whole vectors), else gathered (keys
+// and values of 27k tokens into 8 bits, us: one axis 48, sections of whole
+// vectors 52, sections that end inside vectors 71, interleaved 72; a vector of
+// each axis that the pairs have, and its elements of it, spilled: 59, 73, 73, 80).
 __device__ __forceinline__ void load_turn4(const float* table, int D, const TurnRows& rows, const int4& a, int col,
                                            float (&out)[4]) {
   if (one_axis(a)) {
@@ -216,6 +219,10 @@ __device__ __forceinline__ void move_token(const AppendPagedParams& p, int t, in
   RopeRow rope;
   int b = 0, page = 0, position = 0;
   bool ok = false, page_ok = false;
+  // AX: the table rows do not depend on the token's place, and are asked for first
+  TurnRows rows;
+  bool turns_ok = true;
+  if constexpr (AX) turns_ok = rows.load(p, t);
   for (int h0 = first, turn = 0; h0 < heads; h0 += kAtOnce * stride, ++turn) {
     // (q may be rotated in place: plain loads, not the read-only path)
     uint4 x[kAtOnce], y[kAtOnce];
@@ -232,18 +239,18 @@ __device__ __forceinline__ void move_token(const AppendPagedParams& p, int t, in
       }
     }
     if (turn == 0) {
+      if constexpr (AX) {
+        if (turns_ok) rope.load_axes(p, rows, c);
+      }
       b = sequence_of(p, t);
       if (b < 0) return;
       int from = 0, count = 0, p0 = 0;
       ok = sequence_rows(p, b, &from, &count, &p0) && t >= from && t < from + count;
       position = p0 + (t - from);
-      TurnRows rows;
-      if constexpr (AX) ok = rows.load(p, t) && ok;
+      ok = ok && turns_ok;
       if (!ok && first == 0 && c == 0 && p.err_flag) atomicOr(p.err_flag, kErrPosition);
       if (ok) {
-        if constexpr (AX) {
-          rope.load_axes(p, rows, c);
-        } else {
+        if constexpr (!AX) {
           if (p.cos) rope.load(p, position, c);
         }
         page = p.table[(int64_t)b * p.max_pages + (position >> p.page_shift)];
