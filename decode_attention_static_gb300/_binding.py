@@ -524,8 +524,8 @@ def prefix_ready():
 
 
 def test_skip_slot(slot: int) -> None:
-    """Failure-detection test hook: with slot >= 0, later decode calls of this
-    thread leave that ring slot of one CTA unfilled, so its bounded waits
+    """Failure-detection test hook: with slot >= 0, later decode (and tree) calls of
+    this thread leave that ring slot of one CTA unfilled, so its bounded waits
     expire and the call reports DA_DEVERR_TIMEOUT (-1 turns it off)."""
     load_library().da_test_skip_slot(int(slot))
 

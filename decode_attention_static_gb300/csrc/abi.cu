@@ -364,6 +364,8 @@ cudaError_t current_device_sms(int* sms) {
   return e != cudaSuccess ? e : device_sms(device, sms);
 }
 
+int skipped_slot() { return t_skip_slot; }
+
 }  // namespace da
 
 extern "C" {

@@ -234,6 +234,7 @@ int tree_attention(const void* q, const void* k_pages, const void* v_pages, cons
   p.out = static_cast<uint8_t*>(out);
   p.workspace = workspace;
   p.err_flag = err_flag;
+  p.skip_slot = skipped_slot();
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (!record_timing_before(st)) return DA_ERR_CUDA;
   if (launch_tree(p, dtype, head_dim, e4m3, sms, st) != cudaSuccess) return DA_ERR_CUDA;

@@ -83,5 +83,7 @@ cudaError_t launch_append_paged(const AppendPagedParams& p, int dtype, int sms, 
 bool record_timing_before(cudaStream_t stream);
 bool record_timing_after(cudaStream_t stream);
 cudaError_t current_device_sms(int* sms);
+// abi.cu: the ring slot that this host thread's failure tests leave unfilled (< 0: none).
+int skipped_slot();
 
 }  // namespace da

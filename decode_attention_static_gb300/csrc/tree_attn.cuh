@@ -833,10 +833,11 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
           if (round > 0) ok = __all_sync(0xffffffffu, tree_wait(c, p, &empty[stage], (round - 1) & 1));
           if (!ok) break;
           const int row_bytes = EIGHT ? D : 2 * D;
-          if (lane == 0) mbar_arrive_expect_tx(&full[stage], __popc(on) * step * row_bytes);
+          const bool skipped = issued == p.skip_slot && blockIdx.x == 0;  // (failure test: a copy that never comes)
+          if (lane == 0 && !skipped) mbar_arrive_expect_tx(&full[stage], __popc(on) * step * row_bytes);
           __syncwarp();
           if constexpr (EIGHT) {
-            if (lane < pages && fine) {
+            if (lane < pages && fine && !skipped) {
               const int64_t row = ((int64_t)id * p.n_kv_head + seg.g) * p.page_rows + ((j0 + lane * step) & (p.page_rows - 1));
               bulk_load_plain(smem + Shape::kRawRing + stage * Shape::kRawBytes + lane * step * D, pools[kv] + row * D,
                               step * D, &full[stage]);
@@ -844,7 +845,7 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
           } else {
             const int page = lane / Shape::kBlocks, block = lane % Shape::kBlocks;
             const int at = __shfl_sync(0xffffffffu, id, page);
-            if (page < pages && (on >> page & 1)) {
+            if (page < pages && (on >> page & 1) && !skipped) {
               const int row = (at * p.n_kv_head + seg.g) * p.page_rows + ((j0 + page * step) & (p.page_rows - 1));
               tensor_load_2d(ring + stage * Shape::kTileBytes + block * Shape::kBlockBytes + page * step * 128,
                              kv ? &launch.v_map : &launch.k_map, block * 64, row, &full[stage]);

@@ -27,6 +27,7 @@ struct TreeParams {
   uint8_t* out;            // [tokens, n_head, D]
   void* workspace;
   int32_t* err_flag;       // may be null
+  int skip_slot;           // test hook: copy of the first CTA that is left out (< 0: none)
 };
 
 size_t tree_workspace_bytes(int sms, int group, int head_dim);

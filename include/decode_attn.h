@@ -205,7 +205,8 @@ DA_API int da_set_prefix_ready(int on);
  * (about one second), the CTA publishes NaN and the call sets
  * DA_DEVERR_TIMEOUT; nothing faults and the context stays usable. Zero the
  * workspace afterwards (as after any DA_DEVERR_TIMEOUT). slot < 0 turns the
- * hook off (the default). Returns DA_OK.
+ * hook off (the default). A tree attention call leaves out that copy of its
+ * first CTA in the same way. Returns DA_OK.
  */
 DA_API int da_test_skip_slot(int slot);
 
@@ -570,7 +571,8 @@ DA_API size_t decode_attn_tree_workspace_size(int n_head, int n_kv_head, int hea
  *   out[t, h, :] = softmax_j(scale <q[t, h], K_j>) V_j over the rows seen
  * Products of the storage type, sums, maxima and exponentials in fp32; a
  * weight is rounded to the storage type, relative to its row's running
- * maximum, before it reaches V, and the output is rounded once. A token that sees
+ * maximum, before it reaches V (bf16, head_dim 128, sequences of at most 128 query
+ * heads times tokens for each KV head: to 16 bits), and the output is rounded once. A token that sees
  * nothing gets a row of zeros. Rows that a token does not see do not reach
  * it, whatever they hold (NaN and infinities among them). Rows of q and out
  * that no sequence owns are left alone. Facts only the device knows:
@@ -579,10 +581,15 @@ DA_API size_t decode_attn_tree_workspace_size(int n_head, int n_kv_head, int hea
  * rows and DA_DEVERR_TOKENS; a token range that is not inside the packed
  * tokens is skipped and sets DA_DEVERR_TOKENS; a page id outside the pool
  * among the first ceil(kv_len / page_size) of a sequence gives NaN for its
- * tokens and DA_DEVERR_PAGE. kv_len times the largest |V| stays below 2^110,
- * or sums may overflow. Equal calls give equal bits. Lengths, table, tokens
- * and masks must not change while the call runs, and out must not be q
- * (DA_ERR_SHAPE).
+ * tokens and DA_DEVERR_PAGE; a wait that hits its time limit gives NaN for some
+ * units of tokens and DA_DEVERR_TIMEOUT (zero the workspace then). An infinite
+ * element of V in a row that a token sees makes that element of its output infinite
+ * or NaN. kv_len times the largest |V| stays below 2^110, or sums may
+ * overflow. Equal calls give equal bits. Lengths, table, tokens and masks must
+ * not change while the call runs, and out must not be q (DA_ERR_SHAPE).
+ * The pool has at most 2^31 - 1 rows of all KV heads, and B * n_kv_head * (n_head /
+ * n_kv_head) times the 128-row tiles of a longest sequence, and 8 more, stay below
+ * 2^31 (DA_ERR_SHAPE).
  */
 DA_API int decode_attn_tree_fwd(const void* q, const void* k_pages, const void* v_pages, const int32_t* page_table,
                     const int32_t* kv_len, const int32_t* token_start, const int64_t* tree_mask, int mask_words,
@@ -591,7 +598,10 @@ DA_API int decode_attn_tree_fwd(const void* q, const void* k_pages, const void* 
                     int32_t* err_flag, void* stream);
 
 /* decode_attn_tree_fwd over pages of e4m3 with their scales (finite), as
- * decode_attn_paged_q8_fwd. dtype is that of q and out. */
+ * decode_attn_paged_q8_fwd. dtype is that of q and out. The products are of fp16:
+ * a bf16 query keeps what lies above 2^-39 of its head's largest element, a weight,
+ * with the scale of its V row, 11 bits above 2^-21 of its row's largest. Scales of V that
+ * a token sees lie within 2^100 of one another. */
 DA_API int decode_attn_tree_q8_fwd(const void* q, const void* k_pages, const void* v_pages, const float* k_scale,
                     const float* v_scale, const int32_t* page_table, const int32_t* kv_len,
                     const int32_t* token_start, const int64_t* tree_mask, int mask_words, int B, int tokens,

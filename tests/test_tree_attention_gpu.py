@@ -390,3 +390,70 @@ def test_graph_replays_with_new_lengths(eight):
         for o in (out, out2):
             assert torch.equal(R.bits(o), R.bits(want[id(case)]))
         assert torch.equal(R.bits(other), R.bits(want[id(a)]))
+
+
+@BOTH
+@pytest.mark.parametrize("slot", [0, 1, 4])
+def test_a_copy_that_never_comes(slot, eight):
+    """One copy of one CTA is left out: its bounded waits run out, NaN rows and the error bit, nothing faults, and the
+    next call is right."""
+    case = Case([2000, 900], [20, 9], 8, 2, 128, "bf16", 64, eight, seed=4).cuda()
+    ws = da.alloc_tree_workspace(8, 2, 128)
+    clean = case.check(workspace=ws)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = torch.full_like(case.q, 7.0)
+    da.test_skip_slot(slot)
+    try:
+        case.call(out=out, err_flag=err, workspace=ws)
+        torch.cuda.synchronize()
+    finally:
+        da.test_skip_slot(-1)
+    bad = out.isnan().all(dim=-1)
+    assert (R.bits(out) == R.bits(clean)).all(dim=-1)[~bad.cpu()].all()
+    if bad.any():  # (a CTA of fewer copies never comes to a later one)
+        assert int(err.item()) & da.DA_DEVERR_TIMEOUT and bad[:20, :4].all()
+    else:
+        assert slot > 1 and int(err.item()) == 0
+    ws.zero_()
+    assert torch.equal(R.bits(case.check(workspace=ws)), R.bits(clean))
+
+
+@BOTH
+def test_large_pools(eight):
+    """Rows and pages whose offsets pass 32 bits: a pool of more than 2^32 elements, its last pages in use."""
+    Hkv, D, page, n = 16, 128, 256, 700
+    pages = (1 << 32) // (Hkv * D * page) + 5
+    if torch.cuda.mem_get_info()[0] < 5 * pages * Hkv * D * page:
+        pytest.skip("not enough free memory")
+    small = Case([n], [7], 32, Hkv, D, "f16", page, eight, seed=8)
+    dt = small.k.dtype
+    big = [torch.zeros(pages, Hkv, page, D, dtype=torch.uint8 if eight else torch.int16, device="cuda") for _ in range(2)]
+    scale = [torch.ones(pages, Hkv, device="cuda") for _ in range(2)]
+    table = torch.arange(pages - 1, pages - 4, -1, dtype=torch.int32)[None]
+    for i in range(3):
+        src = int(small.table[0, i])
+        for x, pool in zip((small.k, small.v), big):
+            pool[pages - 1 - i] = x.view(pool.dtype)[src].cuda()
+        for x, s in zip((small.ks, small.vs), scale):
+            s[pages - 1 - i] = x[src].cuda()
+    small.table, small.k, small.v = table, big[0].view(dt), big[1].view(dt)
+    small.ks, small.vs = scale
+    small.cuda().check()
+
+
+def test_concurrent_calls_on_two_streams():
+    """Calls with workspaces of their own side by side, longer than the time that a CTA waits for a unit's other parts."""
+    cases = [Case([9000, 4000], [64, 40], 16, 4, 128, "bf16", 64, False, seed=s).cuda() for s in (1, 2)]
+    want = [c.check() for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    spaces = [da.alloc_tree_workspace(16, 4, 128) for _ in cases]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(30):
+        for i, c in enumerate(cases):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(c.call(workspace=spaces[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for g in got[i]:
+            assert torch.equal(R.bits(g), R.bits(want[i]))
