@@ -37,6 +37,7 @@ constexpr unsigned long long kTreeHelpNs = 20000;  // how long a CTA waits for a
 constexpr int kTreeMinTiles = 2;            // a part of a unit has at least as many tiles
 constexpr int kTreeJoinTiles = 8;           // what the ends of a share inside units cost, in tiles (at most the warps)
 constexpr int kTreeUnitTiles = 6;           // ... what beginning and ending a unit takes
+constexpr int kTreeAloneRows = 32;          // a unit of few rows is joined by the last CTA alone
 constexpr float kTreeLazy = 7.f;            // a running maximum is raised when a score passes it by 2^7
 constexpr float kTreeLift = 8.f;            // fp16 weights are held 2^8 times as large: a row's largest lies in [2^7, 2^15]
 
@@ -697,8 +698,10 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
       if (s.kt) *kt = s.kt;
       return s.kt ? p.n_kv_head * s.mps : 0;
     };
+    // (up to 32 sequences every warp looks at them by itself, without barriers)
+    const bool small = p.B <= 32;
     int my_kt, kt;
-    const int my_units = units_of(threadIdx.x, &my_kt);
+    const int my_units = units_of(small ? lane : threadIdx.x, &my_kt);
     int tiles = my_units * my_kt, units = my_units;
     for (int b = threadIdx.x + kThreads; b < p.B; b += kThreads) {
       const int n = units_of(b, &kt);
@@ -707,20 +710,26 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
     }
     // the sequences' units and tiles, as far as one pass goes, for the search of the parts' size
     int2* const table = reinterpret_cast<int2*>(smem + Shape::kQ);
-    table[threadIdx.x] = make_int2(my_units, my_kt);
     tiles = __reduce_add_sync(0xffffffffu, tiles);
     units = __reduce_add_sync(0xffffffffu, units);
-    if (lane == 0) {
-      c->sums[warp] = tiles;
-      c->counts[warp] = units;
+    if (!small) {
+      table[threadIdx.x] = make_int2(my_units, my_kt);
+      if (lane == 0) {
+        c->sums[warp] = tiles;
+        c->counts[warp] = units;
+      }
+      __syncthreads();
+      tiles = __reduce_add_sync(0xffffffffu, lane < kWarps ? c->sums[lane] : 0);
+      units = __reduce_add_sync(0xffffffffu, lane < kWarps ? c->counts[lane] : 0);
     }
-    __syncthreads();
-    tiles = __reduce_add_sync(0xffffffffu, lane < kWarps ? c->sums[lane] : 0);
-    units = __reduce_add_sync(0xffffffffu, lane < kWarps ? c->counts[lane] : 0);
     const int grid = gridDim.x, share = max((tiles + grid - 1) / grid, kTreeMinTiles);
     total = tiles + kTreeUnitTiles * units;
     ctas = min(grid, total);
-    if (units <= grid && p.B <= kThreads) {  // (the same in every thread)
+    if (small && units <= grid) {
+      for (int size = share; size < share + kTreeJoinTiles && part_tiles == 0; ++size) {
+        if (__reduce_add_sync(0xffffffffu, my_units * ((my_kt + size - 1) / size)) <= grid) part_tiles = size;
+      }
+    } else if (units <= grid && p.B <= kThreads) {  // (the same in every thread)
       // one candidate for each warp: share, share + 1, ...
       int parts = 0;
       for (int i = lane; i < p.B; i += 32) parts += table[i].x * ((table[i].y + share + warp - 1) / (share + warp));
@@ -742,6 +751,7 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
       c->start[7] = 0;
       c->end_tile = tiles;
     }
+    __syncwarp();
     int before = 0, units_before = 0;
     for (int base = 0; base < p.B && before <= max(want, next); base += kThreads) {
       int n = my_units;
@@ -758,18 +768,23 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
           scan_units += up_units;
         }
       }
-      __syncthreads();
-      if (lane == 31) {
-        c->sums[warp] = scan;
-        c->counts[warp] = scan_units;
+      int w = 0, wu = 0;
+      if (!small) {
+        __syncthreads();
+        if (lane == 31) {
+          c->sums[warp] = scan;
+          c->counts[warp] = scan_units;
+        }
+        __syncthreads();
+        w = lane < kWarps ? c->sums[lane] : 0;
+        wu = lane < kWarps ? c->counts[lane] : 0;
       }
-      __syncthreads();
-      const int w = lane < kWarps ? c->sums[lane] : 0, wu = lane < kWarps ? c->counts[lane] : 0;
       const int at = before + __reduce_add_sync(0xffffffffu, lane < warp ? w : 0) + scan - v;
       const int first_unit = units_before + __reduce_add_sync(0xffffffffu, lane < warp ? wu : 0) + scan_units - n;
       // (tiles before the sequence's, in the list)
       const int tiles_at = at - kTreeUnitTiles * first_unit;
-      if (want >= at && want < at + v) {
+      const bool writes = !small || warp == 0;
+      if (writes && want >= at && want < at + v) {
         int none = 0;
         const TreeSeq x = tree_sequence(p, base + threadIdx.x, &none);
         const int off = want - at, unit = off / each, piece = off - unit * each, head = unit / x.mps;
@@ -792,7 +807,7 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
           c->unit_at = at + unit * each;
         }
       }
-      if (part_tiles == 0 && next >= at && next < at + v) {
+      if (writes && part_tiles == 0 && next >= at && next < at + v) {
         const int off = next - at, unit = off / each;
         c->end_tile = tiles_at + unit * kt + max(0, off - unit * each - kTreeUnitTiles);
       }
@@ -1388,17 +1403,22 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
     for (int i = 0; i < pendings; ++i) {
       const TreePending x = c->pending[i];
       TreeMeet* const meet = meets + x.c0;
+      const bool alone = x.rows <= kTreeAloneRows;  // few rows: the last to arrive joins them, nobody waits
       named_barrier_sync<1, 256>();
       if (threadIdx.x == 0) {
         // The last to arrive joins the unit. The others wait for it a while, to help: it does without them, so that no
         // CTA depends on another one being there.
         bool ready = x.last;
         const unsigned long long t0 = global_ns();
-        while (!ready && global_ns() - t0 < kTreeHelpNs) ready = load_acquire(&meet->generation) != x.generation;
+        while (!alone && !ready && global_ns() - t0 < kTreeHelpNs) ready = load_acquire(&meet->generation) != x.generation;
         c->ready = ready;
       }
       named_barrier_sync<1, 256>();
       if (!c->ready) continue;
+      if (alone) {
+        tree_join_rows<T, D>(p, partials, x, 0, x.rows, reinterpret_cast<float*>(smem + Shape::kExchange));
+        continue;
+      }
       const int share = max(16, ((x.rows + x.parts - 1) / x.parts + 7) & ~7), shares = (x.rows + share - 1) / share;
       for (;;) {
         if (threadIdx.x == 0) c->ticket = (int)atomicAdd(&meet->ticket, 1u);
