@@ -266,29 +266,54 @@ __device__ __forceinline__ void tmem_store16(uint32_t taddr, const uint32_t* r) 
 __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // D (tensor memory) = A B^T (+ D), A in shared or in tensor memory. The whole warp comes here, converged and with
-// the same operands, and its leader issues: so the operands stay in uniform registers (issued under a branch for one
-// lane, each product cost 125 cycles to issue, twice what it takes).
-__device__ __forceinline__ void tree_mma_ss(uint32_t leader, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                            uint32_t idesc, bool accumulate) {
+// the same operands, and one elected lane issues: so the operands stay in uniform registers. What it costs to issue a
+// product is what the kernel would wait for (64 cycles would do for one of 128 x 128 x 16; under a branch for one lane
+// it cost 125, with a predicate made of the lane's number as much, whatever the product's size), so one vote serves
+// several products.
+// Four products along the contracted axis: of a 64-column block of both operands ...
+__device__ __forceinline__ void tree_mma_ss4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                             bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred acc, one;\n\tsetp.ne.b32 acc, %4, 0;\n\tsetp.ne.b32 one, %5, 0;\n\t"
-      "@one tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, acc;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate), "r"(leader)
+      "{\n\t.reg .pred acc, add, one;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 acc, %4, 0;\n\tsetp.eq.b32 add, 0, 0;\n\t"
+      "elect.sync _|one, 0xffffffff;\n\t"
+      "@one tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, acc;\n\t"
+      "add.s64 a, %1, 2;\n\tadd.s64 b, %2, 2;\n\t"
+      "@one tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, add;\n\t"
+      "add.s64 a, %1, 4;\n\tadd.s64 b, %2, 4;\n\t"
+      "@one tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, add;\n\t"
+      "add.s64 a, %1, 6;\n\tadd.s64 b, %2, 6;\n\t"
+      "@one tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, add;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
       : "memory");
 }
-__device__ __forceinline__ void tree_mma_ts(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                            uint32_t idesc, bool accumulate) {
+// ... of 64 rows of the second one and 32 columns of tensor memory.
+__device__ __forceinline__ void tree_mma_ts4(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                             bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred acc, one;\n\tsetp.ne.b32 acc, %4, 0;\n\tsetp.ne.b32 one, %5, 0;\n\t"
+      "{\n\t.reg .pred acc, add, one;\n\t.reg .b32 a;\n\t.reg .b64 b;\n\tsetp.ne.b32 acc, %4, 0;\n\tsetp.eq.b32 add, 0, 0;\n\t"
+      "elect.sync _|one, 0xffffffff;\n\t"
+      "@one tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, acc;\n\t"
+      "add.s32 a, %1, 8;\n\tadd.s64 b, %2, 128;\n\t"
+      "@one tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, add;\n\t"
+      "add.s32 a, %1, 16;\n\tadd.s64 b, %2, 256;\n\t"
+      "@one tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, add;\n\t"
+      "add.s32 a, %1, 24;\n\tadd.s64 b, %2, 384;\n\t"
+      "@one tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, add;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tree_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred acc, one;\n\tsetp.ne.b32 acc, %4, 0;\n\telect.sync _|one, 0xffffffff;\n\t"
       "@one tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, acc;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate), "r"(leader)
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"((uint32_t)accumulate)
       : "memory");
 }
-__device__ __forceinline__ void tree_commit(uint32_t leader, uint32_t bar) {
+__device__ __forceinline__ void tree_commit(uint32_t bar) {
   asm volatile(
-      "{\n\t.reg .pred one;\n\tsetp.ne.b32 one, %1, 0;\n\t"
-      "@one tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
-      "r"(leader)
+      "{\n\t.reg .pred one;\n\telect.sync _|one, 0xffffffff;\n\t"
+      "@one tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
       : "memory");
 }
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
@@ -883,7 +908,6 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
     // ---------------- products ----------------
     lower_registers<Shape::kRegsOther>();
     constexpr uint32_t kScores = tree_idesc(kBf16, kTreeTile, false), kOut = tree_idesc(kBf16, D, true);
-    const uint32_t leader = lane == 0;
     const uint32_t tm = uniform(tmem), q0 = uniform(q_tiles), ring0 = uniform(ring), bars = uniform(smem_addr(c));
     auto bar = [&](uint64_t* b) { return bars + (uint32_t)(reinterpret_cast<uint8_t*>(b) - reinterpret_cast<uint8_t*>(c)); };
     int tau = 0, phase_p[2] = {0, 0};
@@ -904,12 +928,12 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
           const uint64_t b = sw128_desc_at(ring0 + slot * Shape::kTileBytes);
           const uint32_t to = tm + Shape::kS + (u & 1) * 128;
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint64_t off = (uint64_t)(((k / 4) * Shape::kBlockBytes + (k % 4) * 32) >> 4);
-            tree_mma_ss(leader, to, a + off, b + off, kScores, k > 0);
+          for (int k = 0; k < Shape::kBlocks; ++k) {
+            const uint64_t off = (uint64_t)(k * Shape::kBlockBytes >> 4);
+            tree_mma_ss4(to, a + off, b + off, kScores, k > 0);
           }
-          tree_commit(leader, bar(&c->s_full[u & 1]));
-          if (!two || (u & 1)) tree_commit(leader, bar(&c->empty[slot]));
+          tree_commit(bar(&c->s_full[u & 1]));
+          if (!two || (u & 1)) tree_commit(bar(&c->empty[slot]));
         }
         if (u > 0) {
           const int v = u - 1, grp = v & 1, t = two ? v >> 1 : v;
@@ -924,31 +948,35 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
           const int steps = t == tiles - 1 ? last_steps : kTreeTile / 16;
           const uint64_t b = sw128_desc_rows(ring0 + slot * Shape::kTileBytes, Shape::kBlockBytes);
           const uint32_t weights = tm + Shape::kP + grp * Shape::kPStride, to = tm + Shape::kO + grp * D;
-          auto product = [&](int k, bool add) {
-            const uint64_t rows = b + (uint64_t)((k * 2048) >> 4);
-            tree_mma_ts(leader, to, weights + (pieces ? weight_column<2>(16 * k) : weight_column<1>(16 * k)), rows, kOut, add);
-            if (pieces) tree_mma_ts(leader, to, weights + weight_column<2>(16 * k) + 32, rows, kOut, true);
-          };
-          product(0, v >= 2);
           if (steps == kTreeTile / 16) {
 #pragma unroll
-            for (int k = 1; k < kTreeTile / 16; ++k) product(k, true);
+            for (int k = 0; k < 2; ++k) {
+              const uint64_t rows = b + (uint64_t)((k * 64 * 128) >> 4);
+              const uint32_t at = weights + (pieces ? weight_column<2>(64 * k) : weight_column<1>(64 * k));
+              tree_mma_ts4(to, at, rows, kOut, k > 0 || v >= 2);
+              if (pieces) tree_mma_ts4(to, at + 32, rows, kOut, true);
+            }
           } else {
 #pragma unroll 1
-            for (int k = 1; k < steps; ++k) product(k, true);
+            for (int k = 0; k < steps; ++k) {
+              const uint64_t rows = b + (uint64_t)((k * 2048) >> 4);
+              const uint32_t at = weights + (pieces ? weight_column<2>(16 * k) : weight_column<1>(16 * k));
+              tree_mma_ts(to, at, rows, kOut, k > 0 || v >= 2);
+              if (pieces) tree_mma_ts(to, at + 32, rows, kOut, true);
+            }
           }
-          if (!two || (v & 1)) tree_commit(leader, bar(&c->empty[slot]));
+          if (!two || (v & 1)) tree_commit(bar(&c->empty[slot]));
         }
       }
       if (!ok) break;
-      tree_commit(leader, bar(&c->o_final));
+      tree_commit(bar(&c->o_final));
       if (lane == 0) mbar_arrive(&c->o_final);
       __syncwarp();
       tau += tiles;
     }
     if (!ok) {
       // products in flight end before the memory is freed (bounded)
-      tree_commit(leader, bar(&c->drain));
+      tree_commit(bar(&c->drain));
       mbar_wait(&c->drain, 0);
     }
     __syncwarp();
