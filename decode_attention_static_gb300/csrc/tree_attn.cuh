@@ -41,8 +41,12 @@ constexpr int kTreeAloneRows = 32;          // a unit of few rows is joined by t
 constexpr float kTreeLazy = 7.f;            // a running maximum is raised when a score passes it by 2^7
 constexpr float kTreeLift = 8.f;            // fp16 weights are held 2^8 times as large: a row's largest lies in [2^7, 2^15]
 
-// A partial state: O [256][D], then (m, m of l, l) [256] float4.
+// A partial state: O in blocks of 32 columns [D / 32][256][32], as it lies in shared memory on its way (the 16-byte
+// chunks of a row exchanged by the row's lowest bits), then (m, m of l, l) [256] float4.
 __host__ __device__ constexpr int tree_slot_floats(int D) { return kTreeUnitRows * D + kTreeUnitRows * 4; }
+__device__ __forceinline__ int tree_slot_at(int row, int column) {
+  return (column / 32 * kTreeUnitRows + row) * 32 + (((column / 4 % 8) ^ (row & 7)) << 2);
+}
 // Where the CTAs of one unit meet, by the CTA that begins it. All zero before the first call; the last to arrive
 // zeroes the first and the third and raises the second.
 struct alignas(16) TreeMeet {
@@ -232,6 +236,15 @@ __device__ __forceinline__ void tensor_load_2d(uint32_t smem_dst, const TensorMa
       "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
       : "memory");
 }
+
+// From shared memory to `to`, and this thread's waits: until what it copies has been read, until it is written.
+__device__ __forceinline__ void bulk_store(float* to, const void* from, int bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(to), "r"(smem_addr(from)), "r"(bytes)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // 32 (or 16) columns of this warp's lanes; the caller waits with tmem_wait_load.
 __device__ __forceinline__ void tmem_load32(uint32_t taddr, uint32_t* r) {
@@ -633,12 +646,13 @@ __device__ __forceinline__ void tree_join_rows(const TreeParams& p, const float*
     float4 acc[kRows];
 #pragma unroll
     for (int k = 0; k < kRows; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
+#pragma unroll 4
     for (int i = 0; i < parts; ++i) {
-      const float4* const from = reinterpret_cast<const float4*>(slot(i) + r0 * D) + col;
+      const float* const from = slot(i);
       float4 o[kRows];
 #pragma unroll
-      for (int k = 0; k < kRows; ++k) o[k] = __ldcg(from + min(first + k * kStep, rows - 1) * (D / 4));
+      for (int k = 0; k < kRows; ++k)
+        o[k] = __ldcg(reinterpret_cast<const float4*>(from + tree_slot_at(r0 + min(first + k * kStep, rows - 1), 4 * col)));
 #pragma unroll
       for (int k = 0; k < kRows; ++k) {
         const float w = weights[i * rows + min(first + k * kStep, rows - 1)];
@@ -1341,8 +1355,12 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
       uint8_t* const exchange = smem + Shape::kExchange + (grp * kTreeTile) * 128;  // rows of this group
       const int c0 = two ? 0 : grp * (D / 2), c1 = two ? D : c0 + D / 2;
       const uint32_t o0 = two ? o_at : tmem + lanes + Shape::kO;
+      // A warp's own rows of a partial state leave by a bulk copy: stores of the threads, and the wait for them at the
+      // arrival, took 15 000 cycles for 256 rows of 128; what an SM can write takes 5 900.
+      const bool copied = !whole && (two || copies == 1);
 #pragma unroll 1
       for (int at = c0; at < c1; at += 32) {
+        if (copied && lane == 0) bulk_wait_read();
         if (busy) {
           uint32_t o[32], o1[32];
           __syncwarp();
@@ -1366,6 +1384,15 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
             *reinterpret_cast<uint4*>(exchange + row * 128 + ((i ^ (row & 7)) << 4)) =
                 make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
         }
+        if (copied) {
+          const int first = (two ? grp * kTreeTile : 0) + row - lane;
+          if (first < seg.count) {
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) bulk_store(slot + tree_slot_at(first, at), exchange + (row - lane) * 128, 32 * 128);
+          }
+          continue;
+        }
         if (two || copies == 1) __syncwarp(); else if (grp == 0) named_barrier_sync<3, 128>(); else named_barrier_sync<4, 128>();
         // (a warp's own rows, or the group's first copy)
         const bool alone = two || copies == 1;
@@ -1380,7 +1407,7 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
             *reinterpret_cast<uint2*>(p.out + (to + at + 4 * ch) * 2) =
                 make_uint2(pack2<S::kBf16>(sum.x * f, sum.y * f), pack2<S::kBf16>(sum.z * f, sum.w * f));
           } else {
-            *reinterpret_cast<float4*>(slot + ur * D + at + 4 * ch) = sum;
+            *reinterpret_cast<float4*>(slot + tree_slot_at(ur, at + 4 * ch)) = sum;
           }
         };
         auto place = [&](int r) { return *reinterpret_cast<const float4*>(exchange + r * 128 + ((ch ^ (r & 7)) << 4)); };
@@ -1405,6 +1432,7 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
         }
         if (two || copies == 1) __syncwarp(); else if (grp == 0) named_barrier_sync<3, 128>(); else named_barrier_sync<4, 128>();
       }
+      if (copied && lane == 0) bulk_wait();
       tc_fence_before();
       named_barrier_sync<2, 256>();  // the states, and the notes on the segment's rows, have been read
       if (threadIdx.x < 8) c->bad[s & 7][threadIdx.x] = 0;
