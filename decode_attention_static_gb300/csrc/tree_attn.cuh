@@ -41,11 +41,13 @@ constexpr int kTreeAloneRows = 32;          // a unit of few rows is joined by t
 constexpr float kTreeLazy = 7.f;            // a running maximum is raised when a score passes it by 2^7
 constexpr float kTreeLift = 8.f;            // fp16 weights are held 2^8 times as large: a row's largest lies in [2^7, 2^15]
 
-// A partial state: O in blocks of 32 columns [D / 32][256][32], as it lies in shared memory on its way (the 16-byte
-// chunks of a row exchanged by the row's lowest bits), then (m, m of l, l) [256] float4.
+// A partial state: O, then (m, m of l, l) [256] float4. O is [256][D] for 16-bit pages; for 8 bits it lies as it does in
+// shared memory on its way, [D / 32][256][32] with the 16-byte chunks of a row exchanged by the row's lowest bits.
 __host__ __device__ constexpr int tree_slot_floats(int D) { return kTreeUnitRows * D + kTreeUnitRows * 4; }
+template <int D, bool EIGHT>
 __device__ __forceinline__ int tree_slot_at(int row, int column) {
-  return (column / 32 * kTreeUnitRows + row) * 32 + (((column / 4 % 8) ^ (row & 7)) << 2);
+  if constexpr (EIGHT) return (column / 32 * kTreeUnitRows + row) * 32 + (((column / 4 % 8) ^ (row & 7)) << 2);
+  return row * D + column;
 }
 // Where the CTAs of one unit meet, by the CTA that begins it. All zero before the first call; the last to arrive
 // zeroes the first and the third and raises the second.
@@ -614,7 +616,7 @@ __device__ __forceinline__ unsigned load_acquire(const unsigned* at) {
 // Rows [r0, r1) of a unit from its parts, by the 256 softmax threads: the parts' weights of each row into shared memory
 // (a thread for each row), then four columns a thread over the parts. The first CTA's part is its second state, the
 // others' their first.
-template <typename T, int D>
+template <typename T, int D, bool EIGHT>
 __device__ __forceinline__ void tree_join_rows(const TreeParams& p, const float* partials, const TreePending& x, int r0,
                                                int r1, float* weights) {
   const int rows = r1 - r0, parts = x.parts;
@@ -646,13 +648,13 @@ __device__ __forceinline__ void tree_join_rows(const TreeParams& p, const float*
     float4 acc[kRows];
 #pragma unroll
     for (int k = 0; k < kRows; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll(EIGHT ? 4 : 2)
     for (int i = 0; i < parts; ++i) {
       const float* const from = slot(i);
       float4 o[kRows];
 #pragma unroll
       for (int k = 0; k < kRows; ++k)
-        o[k] = __ldcg(reinterpret_cast<const float4*>(from + tree_slot_at(r0 + min(first + k * kStep, rows - 1), 4 * col)));
+        o[k] = __ldcg(reinterpret_cast<const float4*>(from + tree_slot_at<D, EIGHT>(r0 + min(first + k * kStep, rows - 1), 4 * col)));
 #pragma unroll
       for (int k = 0; k < kRows; ++k) {
         const float w = weights[i * rows + min(first + k * kStep, rows - 1)];
@@ -1355,9 +1357,11 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
       uint8_t* const exchange = smem + Shape::kExchange + (grp * kTreeTile) * 128;  // rows of this group
       const int c0 = two ? 0 : grp * (D / 2), c1 = two ? D : c0 + D / 2;
       const uint32_t o0 = two ? o_at : tmem + lanes + Shape::kO;
-      // A warp's own rows of a partial state leave by a bulk copy: stores of the threads, and the wait for them at the
-      // arrival, took 15 000 cycles for 256 rows of 128; what an SM can write takes 5 900.
-      const bool copied = !whole && (two || copies == 1);
+      // 8 bits: a warp's own rows of a partial state leave by a bulk copy. (256 rows of 128 by the threads' stores, and
+      // the wait for them at the arrival, took 15 000 cycles; what an SM can write takes 5 900. With copies, and four
+      // parts of a join on their way: 98 -> 94 us, 4 x 16384 of 64/8 heads, 32 drafts. 16-bit pages gained 1 us of 47
+      // where rows are many and lost 0.4 to 2 us where they are few.)
+      const bool copied = EIGHT && !whole && (two || copies == 1);
 #pragma unroll 1
       for (int at = c0; at < c1; at += 32) {
         if (copied && lane == 0) bulk_wait_read();
@@ -1389,7 +1393,7 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
           if (first < seg.count) {
             fence_proxy_async_shared();
             __syncwarp();
-            if (lane == 0) bulk_store(slot + tree_slot_at(first, at), exchange + (row - lane) * 128, 32 * 128);
+            if (lane == 0) bulk_store(slot + tree_slot_at<D, EIGHT>(first, at), exchange + (row - lane) * 128, 32 * 128);
           }
           continue;
         }
@@ -1407,7 +1411,7 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
             *reinterpret_cast<uint2*>(p.out + (to + at + 4 * ch) * 2) =
                 make_uint2(pack2<S::kBf16>(sum.x * f, sum.y * f), pack2<S::kBf16>(sum.z * f, sum.w * f));
           } else {
-            *reinterpret_cast<float4*>(slot + tree_slot_at(ur, at + 4 * ch)) = sum;
+            *reinterpret_cast<float4*>(slot + tree_slot_at<D, EIGHT>(ur, at + 4 * ch)) = sum;
           }
         };
         auto place = [&](int r) { return *reinterpret_cast<const float4*>(exchange + r * 128 + ((ch ^ (r & 7)) << 4)); };
@@ -1472,7 +1476,7 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
       named_barrier_sync<1, 256>();
       if (!c->ready) continue;
       if (alone) {
-        tree_join_rows<T, D>(p, partials, x, 0, x.rows, reinterpret_cast<float*>(smem + Shape::kExchange));
+        tree_join_rows<T, D, EIGHT>(p, partials, x, 0, x.rows, reinterpret_cast<float*>(smem + Shape::kExchange));
         continue;
       }
       const int share = max(16, ((x.rows + x.parts - 1) / x.parts + 7) & ~7), shares = (x.rows + share - 1) / share;
@@ -1483,7 +1487,7 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
         named_barrier_sync<1, 256>();
         if (ticket >= shares) break;
         // (weights: at most max(16 parts, rows + 8 parts) + rows floats)
-        tree_join_rows<T, D>(p, partials, x, ticket * share, min(x.rows, (ticket + 1) * share),
+        tree_join_rows<T, D, EIGHT>(p, partials, x, ticket * share, min(x.rows, (ticket + 1) * share),
                              reinterpret_cast<float*>(smem + Shape::kExchange));
       }
     }
