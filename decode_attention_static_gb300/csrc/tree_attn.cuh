@@ -35,7 +35,7 @@
 // softmax -> products, with the other group's in between: 3000 cycles for a tile of
 // 128 rows and 256 query rows (2048 of them the products'; 16 ragged up to 8191,
 // trees of 64, 32/8 heads: 85 us), 3800 with 8 bits (32 ragged up to 16384, trees of
-// 32, 64/8 heads: 346 us). Before the first tile there are 10 000 cycles (lengths,
+// 32, 64/8 heads: 340 us). Before the first tile there are 10 000 cycles (lengths,
 // share, page numbers, query and first K rows), behind the last one 10 000 to 25 000
 // (partial states, arrival, join): all of a small call (1 x 1024, a tree of 8, 16/16
 // heads: 14.7 us).
@@ -102,7 +102,8 @@ struct TreeShape {
   static constexpr int kRaw = EIGHT ? (D == 128 ? 4 : 6) : 0;
   // whole warpgroups (setmaxnreg); registers of a thread: at launch, of the softmax groups, of the others
   static constexpr int kThreads = EIGHT ? 512 : 384;
-  static constexpr int kRegsSoftmax = EIGHT ? 184 : 224, kRegsOther = EIGHT ? 72 : 56;
+  // (8 bits with 184 and 72: 347 us where these take 340, 32 sequences ragged up to 16384)
+  static constexpr int kRegsSoftmax = EIGHT ? 192 : 224, kRegsOther = EIGHT ? 64 : 56;
   static constexpr int kConverters = kThreads - 384;  // threads
   static constexpr int kQ = 0, kRing = 2 * kTileBytes, kRawRing = kRing + kSlots * kTileBytes;
   static constexpr int kControl = kRawRing + kRaw * kRawBytes;
@@ -140,7 +141,7 @@ struct TreeControl {
   int bad_page[8];
 };
 static_assert(sizeof(TreeControl) <= 2048 && offsetof(TreeControl, scales) % 16 == 0, "control area");
-static_assert(128 * (2 * 224 + 56) <= 384 * 168 && 128 * (2 * 184 + 2 * 72) <= 512 * 128, "registers of the launch");
+static_assert(128 * (2 * 224 + 56) <= 384 * 168 && 128 * (2 * 192 + 2 * 64) <= 512 * 128, "registers of the launch");
 
 // Tokens and rows of a sequence; kt tiles for each of mps units a KV head.
 struct TreeSeq {
