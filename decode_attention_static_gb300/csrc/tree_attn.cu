@@ -13,7 +13,8 @@ namespace da {
 namespace {
 
 constexpr int kMaxCtas = 256;
-constexpr int kMeetBytes = kMaxCtas * (int)sizeof(TreeMeet);
+constexpr int kMeetBytes = kCounterBytes + kMaxCtas * (int)sizeof(TreeMeet);
+static_assert(kMaxCtas <= kMaxCounterGroups && kMeetBytes % 16 == 0, "layout of the workspace");
 
 int tree_ctas(int sms) { return std::min(sms, kMaxCtas); }
 
@@ -33,11 +34,12 @@ cudaError_t launch_tree(const TreeParams& p, int dtype, int head_dim, bool e4m3,
         !encode_rows_map(&l.v_map, p.v, dtype, rows, head_dim, box))
       return cudaErrorInvalidValue;
   }
-  TreeMeet* const meets = static_cast<TreeMeet*>(p.workspace);
-  float* const partials = reinterpret_cast<float*>(static_cast<uint8_t*>(p.workspace) + kMeetBytes);
+  uint8_t* const at = static_cast<uint8_t*>(p.workspace);
+  const TreeSpace space = {reinterpret_cast<unsigned*>(at), reinterpret_cast<TreeMeet*>(at + kCounterBytes),
+                           reinterpret_cast<float*>(at + kMeetBytes)};
   const int ctas = tree_ctas(sms);
-  return dtype == DA_F16 ? launch_tree_f16(l, head_dim, e4m3, ctas, meets, partials, stream)
-                         : launch_tree_bf16(l, head_dim, e4m3, ctas, meets, partials, stream);
+  return dtype == DA_F16 ? launch_tree_f16(l, head_dim, e4m3, ctas, space, stream)
+                         : launch_tree_bf16(l, head_dim, e4m3, ctas, space, stream);
 }
 
 }  // namespace da

@@ -69,10 +69,12 @@ __device__ __forceinline__ int tree_slot_at(int row, int column) {
   if constexpr (EIGHT) return (column / 32 * kTreeUnitRows + row) * 32 + (((column / 4 % 8) ^ (row & 7)) << 2);
   return row * D + column;
 }
-// Where the CTAs of one unit meet, by the CTA that begins it. All zero before the first call; the last to arrive
-// zeroes the first and the third and raises the second.
-struct alignas(16) TreeMeet {
-  unsigned arrived, generation, ticket, unused;
+// Where the CTAs of one unit meet, by the CTA that begins it: a counter of arrivals in the workspace's first 4 KiB, where
+// every attention operator has counters that are zero between calls, and these words behind it, whose values between
+// calls do not matter (partial states of another operator may lie there). The last to arrive zeroes the counter and
+// the ticket and then raises the generation.
+struct alignas(8) TreeMeet {
+  unsigned generation, ticket;
 };
 // A unit that this CTA has a part of.
 struct TreePending {
@@ -87,9 +89,16 @@ struct alignas(64) TreeLaunch {
   TreeParams p;
 };
 
-cudaError_t launch_tree_f16(const TreeLaunch& l, int head_dim, bool e4m3, int ctas, TreeMeet* meets, float* partials,
+// The parts of a workspace.
+struct TreeSpace {
+  unsigned* arrived;
+  TreeMeet* meets;
+  float* partials;
+};
+
+cudaError_t launch_tree_f16(const TreeLaunch& l, int head_dim, bool e4m3, int ctas, const TreeSpace& space,
                             cudaStream_t stream);
-cudaError_t launch_tree_bf16(const TreeLaunch& l, int head_dim, bool e4m3, int ctas, TreeMeet* meets, float* partials,
+cudaError_t launch_tree_bf16(const TreeLaunch& l, int head_dim, bool e4m3, int ctas, const TreeSpace& space,
                              cudaStream_t stream);
 
 template <int D, bool EIGHT>
@@ -700,7 +709,7 @@ __device__ __forceinline__ void tree_join_rows(const TreeParams& p, const float*
 
 template <typename T, int D, bool EIGHT>
 __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
-    tree_kernel(const __grid_constant__ TreeLaunch launch, TreeMeet* meets, float* partials) {
+    tree_kernel(const __grid_constant__ TreeLaunch launch, unsigned* arrived, TreeMeet* meets, float* partials) {
   using Shape = TreeShape<D, EIGHT>;
   using S = Storage<T>;
   constexpr bool kBf16 = S::kBf16 && !EIGHT;  // type of the products
@@ -1466,11 +1475,11 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
       if (!whole && threadIdx.x == 0) {
         // this CTA's part of the unit is written: arrive where its CTAs meet
         TreeMeet* const meet = meets + part.c0;
-        const unsigned before = arrive_acq_rel(&meet->arrived);
+        const unsigned before = arrive_acq_rel(arrived + part.c0);
         part.last = before + 1 == (unsigned)part.parts;
         if (before >= (unsigned)part.parts && p.err_flag) atomicOr(p.err_flag, kErrWorkspace);
         if (part.last) {
-          meet->arrived = 0;
+          arrived[part.c0] = 0;
           meet->ticket = 0;
           store_release(&meet->generation, part.generation + 1);
         }

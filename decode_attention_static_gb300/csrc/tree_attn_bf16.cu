@@ -3,9 +3,9 @@
 
 namespace da {
 
-cudaError_t launch_tree_bf16(const TreeLaunch& l, int head_dim, bool e4m3, int ctas, TreeMeet* meets, float* partials,
+cudaError_t launch_tree_bf16(const TreeLaunch& l, int head_dim, bool e4m3, int ctas, const TreeSpace& space,
                             cudaStream_t stream) {
-  return launch_tree_as<__nv_bfloat16>(l, head_dim, e4m3, ctas, meets, partials, stream);
+  return launch_tree_as<__nv_bfloat16>(l, head_dim, e4m3, ctas, space, stream);
 }
 
 }  // namespace da

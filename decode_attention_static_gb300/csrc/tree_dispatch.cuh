@@ -8,8 +8,7 @@
 namespace da {
 
 template <typename T, int D, bool EIGHT>
-cudaError_t launch_tree_instance(const TreeLaunch& l, int ctas, TreeMeet* meets, float* partials,
-                                 cudaStream_t stream) {
+cudaError_t launch_tree_instance(const TreeLaunch& l, int ctas, const TreeSpace& space, cudaStream_t stream) {
   using Shape = TreeShape<D, EIGHT>;
   auto* fn = tree_kernel<T, D, EIGHT>;
   static std::atomic<bool> ready[64];  // per device: the shared-memory opt-in is applied
@@ -32,17 +31,17 @@ cudaError_t launch_tree_instance(const TreeLaunch& l, int ctas, TreeMeet* meets,
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fn, l, meets, partials);
+  return cudaLaunchKernelEx(&cfg, fn, l, space.arrived, space.meets, space.partials);
 }
 
 template <typename T>
-cudaError_t launch_tree_as(const TreeLaunch& l, int head_dim, bool e4m3, int ctas, TreeMeet* meets, float* partials,
+cudaError_t launch_tree_as(const TreeLaunch& l, int head_dim, bool e4m3, int ctas, const TreeSpace& space,
                            cudaStream_t stream) {
   if (head_dim == 128)
-    return e4m3 ? launch_tree_instance<T, 128, true>(l, ctas, meets, partials, stream)
-                : launch_tree_instance<T, 128, false>(l, ctas, meets, partials, stream);
-  return e4m3 ? launch_tree_instance<T, 64, true>(l, ctas, meets, partials, stream)
-              : launch_tree_instance<T, 64, false>(l, ctas, meets, partials, stream);
+    return e4m3 ? launch_tree_instance<T, 128, true>(l, ctas, space, stream)
+                : launch_tree_instance<T, 128, false>(l, ctas, space, stream);
+  return e4m3 ? launch_tree_instance<T, 64, true>(l, ctas, space, stream)
+              : launch_tree_instance<T, 64, false>(l, ctas, space, stream);
 }
 
 }  // namespace da

@@ -551,7 +551,9 @@ DA_API int kvcache_append_paged_q8_axes(void* k_pages, void* v_pages, float* k_s
 /* Bytes of scratch of one call of decode_attn_tree_fwd or
  * decode_attn_tree_q8_fwd on the current device; it depends on the heads alone.
  * Zero-fill it once before its first use; every call that completes leaves it
- * ready for the next. Calls that share it must not overlap on the GPU.
+ * ready for the next, of any operator of this library whose workspace it is large
+ * enough for (its counters lie in the first 4 KiB, as decode_attn_fwd's, and are zero
+ * between calls), and the other way round. Calls that share it must not overlap on the GPU.
  * Returns (size_t)-1 for invalid sizes or a failed device query. */
 DA_API size_t decode_attn_tree_workspace_size(int n_head, int n_kv_head, int head_dim);
 
