@@ -584,7 +584,9 @@ DA_API size_t decode_attn_tree_workspace_size(int n_head, int n_kv_head, int hea
  * tokens is skipped and sets DA_DEVERR_TOKENS; a page id outside the pool
  * among the first ceil(kv_len / page_size) of a sequence gives NaN for its
  * tokens and DA_DEVERR_PAGE; a wait that hits its time limit gives NaN for some
- * units of tokens and DA_DEVERR_TIMEOUT (zero the workspace then). An infinite
+ * units of tokens and DA_DEVERR_TIMEOUT; a workspace whose counters were not zero gives NaN
+ * for the tokens that several CTAs share and DA_DEVERR_WORKSPACE, or joins their parts
+ * early (as in decode_attn_workspace_size; zero the workspace after either). An infinite
  * element of V in a row that a token sees makes that element of its output infinite
  * or NaN. kv_len times the largest |V| stays below 2^110, or sums may
  * overflow. Equal calls give equal bits. Lengths, table, tokens and masks must

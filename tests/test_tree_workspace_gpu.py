@@ -62,3 +62,28 @@ def test_one_workspace_for_every_attention_operator(eight):
                 assert not ws[:COUNTERS].any(), f"a tree call left counters ({i})"
                 assert torch.equal(R.bits(call(ws)), R.bits(own[name])), f"{name} behind tree {i}"
                 assert not ws[:COUNTERS].any(), f"{name} left counters"
+
+
+@BOTH
+@pytest.mark.parametrize("lens,news", [([9000], [64]), ([5000], [3])], ids=["many rows", "few rows"])
+def test_workspace_never_zero_filled(lens, news, eight):
+    """Counters that are not zero: rows of units in parts become NaN with the error bit, none keeps what was in `out`;
+    zero-filled again the buffer serves."""
+    case = Case(lens, news, 8, 2, 128, "bf16", 64, eight, seed=3).cuda()
+    clean = case.check()
+    ws = torch.full((da.decode_attn_tree_workspace_size(8, 2, 128),), 1, dtype=torch.uint8, device="cuda")
+    for _ in range(2):
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out = torch.full_like(case.q, 7.0)
+        case.call(out=out, err_flag=err, workspace=ws)
+        assert int(err.item()) == da.DA_DEVERR_WORKSPACE and out.isnan().all()
+    da.workspace_init(ws)
+    assert torch.equal(R.bits(case.check(workspace=ws)), R.bits(clean))
+
+
+@BOTH
+def test_units_of_one_cta_need_no_counters(eight):
+    """Where no unit is divided the workspace's contents do not matter."""
+    case = Case([100, 30, 60], [5, 9, 60], 8, 2, 64, "f16", 16, eight, seed=3).cuda()
+    ws = torch.full((da.decode_attn_tree_workspace_size(8, 2, 64),), 1, dtype=torch.uint8, device="cuda")
+    case.check(workspace=ws)
