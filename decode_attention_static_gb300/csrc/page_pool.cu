@@ -291,6 +291,7 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const PoolParams p, int 
   __shared__ ScanArea area;
   struct Fork {
     int parent, child, rows, rank;  // rows -1: skipped
+    int last;                       // the parent's part-filled page (-1: none inside the pool)
   };
   __shared__ Fork forks[kThreads];
   const int cta = ctas > 1 ? (int)cluster_rank() : 0;
@@ -315,7 +316,7 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const PoolParams p, int 
   int taken = 0;
   for (int first = 0; first < p.n; first += kThreads) {
     const int mine = first + threadIdx.x;
-    Fork f = {0, 0, -1, 0};
+    Fork f = {0, 0, -1, 0, -1};
     if (mine < p.n) {
       f.parent = p.a[mine];
       f.child = p.b[mine];
@@ -330,7 +331,16 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const PoolParams p, int 
         }
       }
     }
-    int need = f.rows > 0 && (f.rows & (size - 1)) ? 1 : 0, all, none;
+    int need = 0, all, none;
+    if (f.rows > 0 && (f.rows & (size - 1))) {
+      // (no page is taken for rows that cannot be copied: the child must not hold a page of somebody else's)
+      f.last = p.table[(int64_t)f.parent * p.max_pages + (f.rows >> p.page_shift)];
+      need = f.last >= 0 && f.last < p.num_pages;
+      if (!need) {
+        f.last = -1;
+        errors |= kErrPage;
+      }
+    }
     f.rank = taken + scan_threads(need, 0, area, &all, &none);
     taken += all;
     if (need && f.rank >= free0) {
@@ -361,21 +371,18 @@ __global__ void __launch_bounds__(kThreads) fork_kernel(const PoolParams p, int 
       if (at0 == 0) {
         int src = -1, dst = -1, rows = 0;
         if (k.rows > 0 && rest) {
-          src = from[full];
-          dst = list[free0 - 1 - k.rank];
-          rows = rest;
-          if (dst < 0 || dst >= p.num_pages) {
-            errors |= kErrPool;
-            dst = -1;
-          } else {
-            atomicAdd(counts + dst, 1);
+          if (k.last >= 0) {
+            dst = list[free0 - 1 - k.rank];
+            if (dst < 0 || dst >= p.num_pages) {
+              errors |= kErrPool;
+              dst = -1;
+            } else {
+              atomicAdd(counts + dst, 1);
+              src = k.last;
+              rows = rest;
+            }
           }
           to[full] = dst;
-          if (src < 0 || src >= p.num_pages) errors |= kErrPage;
-          if (src < 0 || src >= p.num_pages || dst < 0) {
-            src = dst = -1;
-            rows = 0;
-          }
         }
         const int at = first + my_fork;
         p.copies[at] = src;

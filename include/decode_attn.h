@@ -665,8 +665,9 @@ DA_API int kvcache_resize_paged(int32_t* page_table, const int32_t* held_len, co
  * child lie outside [0, B), when its child is the child or the parent of
  * another fork, or its parent is a child (DA_DEVERR_SEQUENCE), when the parent's length is outside [0,
  * max_pages * page_size] (DA_DEVERR_KV_LEN), or when it needs a page and none is
- * left (DA_DEVERR_FULL). A table entry outside the pool is shared without a count, or
- * not copied (the child's entry becomes -1), and sets DA_DEVERR_PAGE.
+ * left (DA_DEVERR_FULL). A table entry outside the pool is shared without a count, or,
+ * for a partly filled page, not copied: no page is taken, the child's entry becomes -1
+ * and copies are -1, -1, 0. It sets DA_DEVERR_PAGE.
  *   parent, child int32 [forks]; copies int32 [3, forks]
  */
 DA_API int kvcache_fork_paged(int32_t* page_table, int32_t* kv_len, const int32_t* parent, const int32_t* child,

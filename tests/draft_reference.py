@@ -215,8 +215,8 @@ def fork(table, kv_len, parent, child, pool, size):
         if not good[i]:
             continue
         full, rest = divmod(kv_len[p], size)
-        new = None
-        if rest:
+        new, there = -1, rest > 0 and 0 <= table[p][full] < pool.n
+        if there:
             new = pool.take()
             if new < 0:
                 continue
@@ -229,7 +229,7 @@ def fork(table, kv_len, parent, child, pool, size):
                 pool.errors.add("page")
         if rest:
             table[c][full] = new
-            if 0 <= table[p][full] < pool.n:
+            if there:
                 copies[0][i], copies[1][i], copies[2][i] = table[p][full], new, rest
             else:
                 pool.errors.add("page")
