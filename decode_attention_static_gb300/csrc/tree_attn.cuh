@@ -460,7 +460,8 @@ __device__ __forceinline__ int weight_column(int k) {
 // taken against a running maximum; where a score passes it by 2^7 (or is the row's first) it is raised to the next
 // whole number, and the output, the sum and earlier weights of the tile are rescaled (by powers of two: exact). a: factor
 // of a score (positive); seen: bits of the columns, looked at where `masked`. 8 bits: scales holds the factor that K's scale is and log2 |V's scale|
-// of each 16 rows, sign (in lanes 0 to 7) the sign of V's scale or zero; PLAIN: all of K's are positive, and so are V's
+// of each 16 rows (-inf where it is zero: such rows count for l alone, and raise no reference but its own), sign (in lanes 0 to
+// 7) the sign of V's scale or zero; PLAIN: all of K's are positive, and so are V's
 // (a branch for every 16 columns took 4000 cycles an item). Straight code for the columns held in registers: as a loop
 // over 32 at a time, 128 took 4000 cycles instead of 1700.
 template <bool BF16, int D, bool EIGHT, int COLS, int PIECES, bool PLAIN>
@@ -570,6 +571,11 @@ __device__ __forceinline__ void softmax_columns(TreeState& st, uint32_t s_at, ui
       }
     }
     const float ref = st.m == -INFINITY ? 0.f : st.m - kLift, lref = st.ml == -INFINITY ? 0.f : st.ml;
+    if constexpr (EIGHT && !PLAIN) {
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g)
+        if (vk[g] == -INFINITY) vk[g] = ref - lref;  // (no scale: weights of l as they are)
+    }
     float total = 0.f;
 #pragma unroll
     for (int h = 0; h < kHold; h += 32) {
@@ -667,7 +673,8 @@ __device__ __forceinline__ void tree_join_rows(const TreeParams& p, const float*
       weights[i * rows + r] = fast_exp2(s.x - m0);
       l += s.z * fast_exp2(s.y - ml0);
     }
-    weights[parts * rows + r] = l == 0.f ? 0.f : fast_exp2(m0 - ml0) / l;
+    // (no reference: nothing but rows whose V has a scale of zero)
+    weights[parts * rows + r] = l == 0.f ? 0.f : (m == -INFINITY ? 0.f : fast_exp2(m0 - ml0)) / l;
   }
   named_barrier_sync<1, 256>();
   // four rows of a thread at once, so that as many loads of each part are on their way
@@ -1258,7 +1265,7 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
           sign = v_next == 0.f ? 0.f : v_next < 0.f ? -1.f : 1.f;
           plain = __all_sync(0xffffffffu, lane >= 8 || (k_next > 0.f && sign == 1.f));
           __syncwarp();
-          if (lane < 8) c->scales[warp][lane] = make_float2(k_next, v_next == 0.f ? 0.f : log2f(fabsf(v_next)));
+          if (lane < 8) c->scales[warp][lane] = make_float2(k_next, log2f(fabsf(v_next)));
           __syncwarp();
           scales_of(id_next);
           id_next = page_of(u + 4);
