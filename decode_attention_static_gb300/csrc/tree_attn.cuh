@@ -78,9 +78,9 @@ struct alignas(8) TreeMeet {
 };
 // A unit that this CTA has a part of.
 struct TreePending {
-  int c0, parts;           // its first CTA, and how many take part
+  int c0, parts;           // its first CTA, and how many take part (0: the counter was not zero before the call)
   unsigned generation;     // of its meeting place before this CTA arrived
-  int last;                // this CTA arrived last (1); the counter was not zero before the call (-1)
+  int last;                // this CTA arrived last
   int rows, token0, g;
 };
 
@@ -651,7 +651,7 @@ __device__ __forceinline__ unsigned load_acquire(const unsigned* at) {
 
 // Rows [r0, r1) of a unit from its parts, by the 256 softmax threads: the parts' weights of each row into shared memory
 // (a thread for each row), then four columns a thread over the parts. The first CTA's part is its second state, the
-// others' their first.
+// others' their first. No parts: NaN.
 template <typename T, int D, bool EIGHT>
 __device__ __forceinline__ void tree_join_rows(const TreeParams& p, const float* partials, const TreePending& x, int r0,
                                                int r1, float* weights) {
@@ -659,7 +659,7 @@ __device__ __forceinline__ void tree_join_rows(const TreeParams& p, const float*
   auto slot = [&](int i) { return partials + ((int64_t)(x.c0 + i) * 2 + (i == 0 ? 1 : 0)) * tree_slot_floats(D); };
   for (int r = threadIdx.x; r < rows; r += 256) {
     auto state = [&](int i) { return __ldcg(reinterpret_cast<const float4*>(slot(i) + kTreeUnitRows * D) + r0 + r); };
-    float m = -INFINITY, ml = -INFINITY, l = 0.f;
+    float m = -INFINITY, ml = -INFINITY, l = parts > 0 ? 0.f : NAN;
 #pragma unroll 4
     for (int i = 0; i < parts; ++i) {
       const float4 s = state(i);
@@ -711,18 +711,6 @@ __device__ __forceinline__ void tree_join_rows(const TreeParams& p, const float*
           make_uint2(pack2<Storage<T>::kBf16>(acc[k].x * inv, acc[k].y * inv),
                      pack2<Storage<T>::kBf16>(acc[k].z * inv, acc[k].w * inv));
     }
-  }
-}
-
-// All rows of a unit become NaN, by the 256 softmax threads.
-template <typename T, int D>
-__device__ __forceinline__ void tree_nan_rows(const TreeParams& p, const TreePending& x) {
-  const int shift = __ffs(p.group) - 1;
-  const uint32_t n = (uint32_t)Storage<T>::kNaN * 0x10001u;
-  for (int i = threadIdx.x; i < x.rows * (D / 8); i += 256) {
-    const int row = i / (D / 8);
-    const int64_t at = ((int64_t)(x.token0 + (row >> shift)) * p.n_head + x.g * p.group + (row & (p.group - 1))) * D;
-    reinterpret_cast<uint4*>(p.out + at * 2)[i % (D / 8)] = make_uint4(n, n, n, n);
   }
 }
 
@@ -1495,12 +1483,17 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
         // this CTA's part of the unit is written: arrive where its CTAs meet
         TreeMeet* const meet = meets + part.c0;
         const unsigned before = arrive_acq_rel(arrived + part.c0);
-        part.last = before >= (unsigned)part.parts ? -1 : before + 1 == (unsigned)part.parts;
-        if (part.last < 0 && p.err_flag) atomicOr(p.err_flag, kErrWorkspace);
-        if (part.last > 0) {
+        part.last = before + 1 == (unsigned)part.parts;
+        if (part.last) {
           arrived[part.c0] = 0;
           meet->ticket = 0;
           store_release(&meet->generation, part.generation + 1);
+        } else if (before >= (unsigned)part.parts) {
+          // nobody can tell when the unit's parts are written: its rows become NaN (the counter stays as it is, so that
+          // every later call on it says so too)
+          if (p.err_flag) atomicOr(p.err_flag, kErrWorkspace);
+          part.parts = 0;
+          part.last = 1;
         }
         c->pending[c->pendings++] = part;
       }
@@ -1511,19 +1504,13 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
     const int pendings = c->pendings;
     for (int i = 0; i < pendings; ++i) {
       const TreePending x = c->pending[i];
-      if (x.last < 0) {
-        // nobody can tell when the unit's parts are written (and the counter stays as it is, so that every later call
-        // on it says so too)
-        tree_nan_rows<T, D>(p, x);
-        continue;
-      }
       TreeMeet* const meet = meets + x.c0;
-      const bool alone = x.rows <= kTreeAloneRows;  // few rows: the last to arrive joins them, nobody waits
+      const bool alone = x.rows <= kTreeAloneRows || x.parts == 0;  // few rows: the last to arrive joins them, nobody waits
       named_barrier_sync<1, 256>();
       if (threadIdx.x == 0) {
         // The last to arrive joins the unit. The others wait for it a while, to help: it does without them, so that no
         // CTA depends on another one being there.
-        bool ready = x.last > 0;
+        bool ready = x.last;
         const unsigned long long t0 = global_ns();
         while (!alone && !ready && global_ns() - t0 < kTreeHelpNs) ready = load_acquire(&meet->generation) != x.generation;
         c->ready = ready;
