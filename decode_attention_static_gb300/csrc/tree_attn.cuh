@@ -21,9 +21,10 @@
 // one group's exponentials run under the other's products.
 //
 // Mathematics, for a query row: w_j = 2^(s_j - m), s_j = log2(e) scale <q, K_j> for
-// the rows j it sees; out = sum w_j V_j / sum w_j; the reference m is raised to the
-// next whole number when a score passes it by 7, so that what was summed before is
-// rescaled exactly. Scores, sums and outputs are held in fp32, weights are rounded
+// the rows j it sees; out = sum w_j V_j / sum w_j; the reference m is the maximum of
+// the first tile in which the row sees something (so the weight of a row's only key, or of
+// a sink, is 1, which no rounding changes) and is raised by a whole number when a score
+// passes it by 7, so that what was summed before is rescaled exactly. Scores, sums and outputs are held in fp32, weights are rounded
 // to the products' type (bf16 in two pieces, 16 bits, where one query tile leaves
 // time for it; fp16, with 8-bit pages, lifted by 2^8 against its smallest numbers).
 // With 8 bits a score is multiplied by K's scale, log2 |V's scale| is added to the
@@ -59,7 +60,7 @@ constexpr int kTreeJoinTiles = 8;           // what the ends of a share inside u
 constexpr int kTreeUnitTiles = 6;           // ... what beginning and ending a unit takes
 constexpr int kTreeAloneRows = 32;          // a unit of few rows is joined by the last CTA alone (1 x 1024: 16.5 -> 15.3 us)
 constexpr float kTreeLazy = 7.f;            // a running maximum is raised when a score passes it by 2^7
-constexpr float kTreeLift = 8.f;            // fp16 weights are held 2^8 times as large: a row's largest lies in [2^7, 2^15]
+constexpr float kTreeLift = 8.f;            // fp16 weights are held 2^8 times as large: a row's largest lies in (2^7, 2^15]
 
 // A partial state: O, then (m, m of l, l) [256] float4. O is [256][D] for 16-bit pages; for 8 bits it lies as it does in
 // shared memory on its way, [D / 32][256][32] with the 16-byte chunks of a row exchanged by the row's lowest bits.
@@ -457,7 +458,7 @@ __device__ __forceinline__ int weight_column(int k) {
 }
 
 // COLS columns of scores, from column `col` on, to weights in tensor memory, their sum to the state. The weights are
-// taken against a running maximum; where a score passes it by 2^7 (or is the row's first) it is raised to the next
+// taken against a running maximum: that of the row's first columns, and where a score passes it by 2^7 it is raised by a
 // whole number, and the output, the sum and earlier weights of the tile are rescaled (by powers of two: exact). a: factor
 // of a score (positive); seen: bits of the columns, looked at where `masked`. 8 bits: scales holds the factor that K's scale is and log2 |V's scale|
 // of each 16 rows (-inf where it is zero: such rows count for l alone, and raise no reference but its own), sign (in lanes 0 to
@@ -528,9 +529,10 @@ __device__ __forceinline__ void softmax_columns(TreeState& st, uint32_t s_at, ui
     const bool up = m_tile > st.m + kTreeLazy || (st.m == -INFINITY && m_tile > -INFINITY);
     const bool up_l = EIGHT && (ml_tile > st.ml + kTreeLazy || (st.ml == -INFINITY && ml_tile > -INFINITY));
     if (__any_sync(0xffffffffu, up || up_l)) {
-      const float m_new = up ? ceilf(m_tile) : st.m;
-      const float factor = !up ? 1.f : st.m == -INFINITY ? 0.f : fast_exp2(st.m - m_new);
-      st.m = m_new;
+      const bool none = st.m == -INFINITY;
+      const float step = up && !none ? ceilf(m_tile - st.m) : 0.f;
+      const float factor = up && none ? 0.f : fast_exp2(-step);
+      st.m = up && none ? m_tile : st.m + step;
       if constexpr (EIGHT) {
         if (up_l) {
           const float ml_new = ceilf(ml_tile);
