@@ -210,6 +210,9 @@ int tree_attention(const void* q, const void* k_pages, const void* v_pages, cons
   if (current_device_sms(&sms) != cudaSuccess) return DA_ERR_CUDA;
   if (!workspace || workspace_bytes < tree_workspace_bytes(sms, n_head / n_kv_head, head_dim)) return DA_ERR_WORKSPACE;
   if (!aligned(workspace, 16)) return DA_ERR_ALIGN;
+  const uintptr_t q0 = reinterpret_cast<uintptr_t>(q), out0 = reinterpret_cast<uintptr_t>(out);
+  const uint64_t bytes = (uint64_t)tokens * n_head * head_dim * 2;
+  if (out0 < q0 + bytes && q0 < out0 + bytes) return DA_ERR_SHAPE;  // nor any part of it
   TreeParams p = {};
   p.q = static_cast<const uint8_t*>(q);
   p.k = static_cast<const uint8_t*>(k_pages);

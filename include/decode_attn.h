@@ -590,7 +590,7 @@ DA_API size_t decode_attn_tree_workspace_size(int n_head, int n_kv_head, int hea
  * element of V in a row that a token sees makes that element of its output infinite
  * or NaN. kv_len times the largest |V| stays below 2^110, or sums may
  * overflow. Equal calls give equal bits. Lengths, table, tokens and masks must
- * not change while the call runs, and out must not be q (DA_ERR_SHAPE).
+ * not change while the call runs, and out must not overlap q (DA_ERR_SHAPE).
  * The pool has at most 2^31 - 1 rows of all KV heads, and B * n_kv_head * (n_head /
  * n_kv_head) times the 128-row tiles of a longest sequence, and 8 more, stay below
  * 2^31 (DA_ERR_SHAPE).
