@@ -12,7 +12,10 @@
 // pages of 12 layers (96 beams, 8 heads of 128, pages of 64), with the resize and the
 // fork before them, 37 us, of which the bytes need 29.6; the accepted rows of 8 sequences in one
 // layer 3.4 us (launch and three dependent loads), of 64 sequences in 36 layers of
-// 8 bits 19.6 us, floor 5.8: rows of 128 bytes, each by itself in 2.4 GB.
+// 8 bits 50 us (66 with nothing in L2), of which 7.7 would move the 6410 blocks whose
+// scale grows: a thread rounds its column of a block's other rows one after the other, each load
+// behind the store before it. Where no scale grows 19.4 us, floor 5.8: rows of 128 bytes, each
+// by itself in 2.4 GB.
 #include <stdint.h>
 
 #include "common.cuh"

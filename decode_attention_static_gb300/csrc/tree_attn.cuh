@@ -36,7 +36,7 @@
 // softmax -> products, with the other group's in between: 3000 cycles for a tile of
 // 128 rows and 256 query rows (2048 of them the products'; 16 ragged up to 8191,
 // trees of 64, 32/8 heads: 85 us), 3800 with 8 bits (32 ragged up to 16384, trees of
-// 32, 64/8 heads: 340 us). Before the first tile there are 10 000 cycles (lengths,
+// 32, 64/8 heads: 343 us). Before the first tile there are 10 000 cycles (lengths,
 // share, page numbers, query and first K rows), behind the last one 10 000 to 25 000
 // (partial states, arrival, join): all of a small call (1 x 1024, a tree of 8, 16/16
 // heads: 14.7 us).
@@ -124,7 +124,11 @@ struct TreeShape {
   static constexpr int kStates = D == 128 ? kQ + kExchangeBytes : kControl + 2048;
   static constexpr int kSmem = 1024 + kControl + 2048 + (D == 128 ? 0 : kStateBytes);
   // bf16 weights of units with one query tile are held in two pieces (16 bits): the products have time for it, and
-  // the columns behind the weights are free where they lie over the scores
+  // the columns behind the weights are free where they lie over the scores. With two query tiles the second piece
+  // would cost 16 ragged up to 8191 and trees of 64 86 -> 101 us (relative error 0.0023 -> 0.0017, that of rounding the
+  // output to bf16), with 8 bits 32 ragged up to 16384 342 -> 419 us; fp16 weights of one query tile 34.6 -> 36.0 us (4 x 8192,
+  // 5 drafts), 39.6 -> 42.2 (32 drafts; 0.00024 -> 0.00021). A sum of the weights as they are held instead of before their
+  // rounding: 86 -> 94 us.
   static constexpr bool kTwoPieces = D == 128 && !EIGHT;
   // tensor memory columns: scores of the groups, outputs, weights (in place of the scores where D is 128, whose two
   // products have one shape and therefore run in order)
@@ -1165,7 +1169,8 @@ __global__ void __launch_bounds__(TreeShape<D, EIGHT>::kThreads, 1)
           copy_commit();
           copy_wait<0>();
           if (EIGHT && S::kBf16) {
-            // To fp16 with the row's largest element in [2^14, 2^15), exact above 2^-39 of it: a thread its own row.
+            // To fp16 with the row's largest element in [2^14, 2^15): the eight bits of an element of 2^-17 and more
+            // are exact (2^-31 of 2^14), smaller ones err by 2^-25 (2^-39 of it). A thread its own row.
             __syncwarp();
             uint32_t top = 0;
             auto at = [&](int i) { return reinterpret_cast<uint4*>(to + chunk_at<D>(row, i)); };

@@ -545,7 +545,8 @@ DA_API int kvcache_append_paged_q8_axes(void* k_pages, void* v_pages, float* k_s
                     int B, int tokens, int n_head, int n_kv_head, int head_dim, int num_pages, int page_size,
                     int max_pages, int dtype, int32_t* err_flag, void* stream);
 
-/* Most tokens of one sequence in a call of decode_attn_tree_fwd. */
+/* Most tokens of one sequence in a call of decode_attn_tree_fwd. (More new tokens behind a prefix take a call
+ * for each 256 of them, in order, each of which reads the prefix again.) */
 #define DA_TREE_MAX_TOKENS 256
 
 /* Bytes of scratch of one call of decode_attn_tree_fwd or
@@ -573,7 +574,8 @@ DA_API size_t decode_attn_tree_workspace_size(int n_head, int n_kv_head, int hea
  *   out[t, h, :] = softmax_j(scale <q[t, h], K_j>) V_j over the rows seen
  * Products of the storage type, sums, maxima and exponentials in fp32; a
  * weight is rounded to the storage type, relative to its row's running
- * maximum, before it reaches V (bf16, head_dim 128, sequences of at most 128 query
+ * maximum (that of the first 128 rows, raised by whole powers of two: the weight of a
+ * token's only row, or of a sink among them, is 1 and not rounded), before it reaches V (bf16, head_dim 128, sequences of at most 128 query
  * heads times tokens for each KV head: to 16 bits), and the output is rounded once. A token that sees
  * nothing gets a row of zeros. Rows that a token does not see do not reach
  * it, whatever they hold (NaN and infinities among them). Rows of q and out
@@ -603,9 +605,11 @@ DA_API int decode_attn_tree_fwd(const void* q, const void* k_pages, const void* 
 
 /* decode_attn_tree_fwd over pages of e4m3 with their scales (finite), as
  * decode_attn_paged_q8_fwd. dtype is that of q and out. The products are of fp16:
- * a bf16 query keeps what lies above 2^-39 of its head's largest element, a weight,
- * with the scale of its V row, 11 bits above 2^-21 of its row's largest. Scales of V that
- * a token sees lie within 2^100 of one another. */
+ * of a bf16 query, with 2^e the power of two at or below its head's largest element,
+ * elements of 2^(e - 31) and more are exact, smaller ones are rounded to a multiple of
+ * 2^(e - 38) (off by 2^(e - 39) at most); a weight, with the scale of its V row, keeps 11
+ * bits above 2^-21 of its row's largest. Scales of V that a token sees are zero or lie
+ * within 2^100 of one another. */
 DA_API int decode_attn_tree_q8_fwd(const void* q, const void* k_pages, const void* v_pages, const float* k_scale,
                     const float* v_scale, const int32_t* page_table, const int32_t* kv_len,
                     const int32_t* token_start, const int64_t* tree_mask, int mask_words, int B, int tokens,
@@ -662,8 +666,9 @@ DA_API int kvcache_resize_paged(int32_t* page_table, const int32_t* held_len, co
  * is nothing). kv_len[child[i]] becomes n; further entries of the child's table
  * row are left as they were. A child holds no pages before (release them with
  * kvcache_resize_paged). A fork is skipped, with copies -1, -1, 0, when parent or
- * child lie outside [0, B), when its child is the child or the parent of
- * another fork, or its parent is a child (DA_DEVERR_SEQUENCE), when the parent's length is outside [0,
+ * child lie outside [0, B), when its child is another fork's child too, or its parent is
+ * the child of any fork of the call (DA_DEVERR_SEQUENCE; a fork whose child another one names
+ * as its parent is carried out, that other one is skipped), when the parent's length is outside [0,
  * max_pages * page_size] (DA_DEVERR_KV_LEN), or when it needs a page and none is
  * left (DA_DEVERR_FULL). A table entry outside the pool is shared without a count, or,
  * for a partly filled page, not copied: no page is taken, the child's entry becomes -1

@@ -106,3 +106,28 @@ def test_two_pieces_of_rows_that_cancel(m):
     slack = ((p[..., 1] + p[..., 2]) * weight + 8 * 2.0 ** -23 * p[..., 1]).view(B * m, H, 1).expand(-1, -1, D)
     out = attend(q.view(B * m, H, D), k, v, m, [0] * (B * m), False, 1.0)
     R.assert_rows(out, ref, slack, "rows that cancel")
+
+
+@pytest.mark.parametrize("exponent", [8, 15, 24, 31])
+@pytest.mark.parametrize("m,H", [(1, 2), (16, 16)])
+def test_small_elements_of_a_bf16_query(m, H, exponent):
+    """bf16 queries over 8-bit pages: elements 2^-31 times the largest one still count with all of their bits. The largest
+    element meets keys of zero in the two rows that take the weight, and their scores, around 1, come from the smallest
+    element alone, under a scale that lifts it. Products and scores are exact; a weight is off by 2^-11 and the base-2 exponential."""
+    B, D, n = 4, 64, 32
+    gen = torch.Generator().manual_seed(m + exponent)
+    small = (1 + torch.randint(0, 128, (B * m, H), generator=gen) / 128) * 2.0 ** -exponent
+    q = torch.zeros(B * m, H, D)
+    q[..., 0], q[..., 9] = 1.0, small
+    k, v = torch.zeros(B, n, 2, D), values((B, n, 2, D), "bf16", True, gen)
+    k[..., 0] = -1.0
+    k[:, :2, :, 0] = 0.0
+    k[:, 0, :, 9], k[:, 1, :, 9] = 0.5, -0.75
+    out = attend(q.to(torch.bfloat16), k, v, m, [0] * (B * m), True, 2.0 ** exponent)
+    score = small.double() * 2.0 ** exponent
+    x = torch.stack([0.5 * score, -0.75 * score], dim=-1)  # [B m, H, 2]
+    p = torch.softmax(x, -1)
+    vv = v[:, :2].double().permute(0, 2, 1, 3).repeat_interleave(m, 0).repeat_interleave(H // 2, 1)  # [B m, H, 2, D]
+    ref = torch.einsum("thr,thrd->thd", p, vv)
+    mass = torch.einsum("thr,thrd->thd", p, vv.abs())
+    R.assert_rows(out, ref, (2.0 ** -11 + 2.0 ** -19) * mass, f"2^-{exponent}")
