@@ -533,7 +533,9 @@ __device__ __forceinline__ void softmax_columns(TreeState& st, uint32_t s_at, ui
     const bool up = m_tile > st.m + kTreeLazy || (st.m == -INFINITY && m_tile > -INFINITY);
     const bool up_l = EIGHT && (ml_tile > st.ml + kTreeLazy || (st.ml == -INFINITY && ml_tile > -INFINITY));
     if (__any_sync(0xffffffffu, up || up_l)) {
-      const bool none = st.m == -INFINITY;
+      // (what was summed before counts for nothing, 2^-256, where the maximum rises by more: taken anew, as a sum with a
+      // reference so far away would be rounded to a step of many powers of two)
+      const bool none = st.m == -INFINITY || m_tile - st.m > 256.f;
       const float step = up && !none ? ceilf(m_tile - st.m) : 0.f;
       const float factor = up && none ? 0.f : fast_exp2(-step);
       st.m = up && none ? m_tile : st.m + step;

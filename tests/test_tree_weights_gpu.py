@@ -131,3 +131,31 @@ def test_small_elements_of_a_bf16_query(m, H, exponent):
     ref = torch.einsum("thr,thrd->thd", p, vv)
     mass = torch.einsum("thr,thrd->thd", p, vv.abs())
     R.assert_rows(out, ref, (2.0 ** -11 + 2.0 ** -19) * mass, f"2^-{exponent}")
+
+
+@FORMS
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("m,G", [(2, 4), (16, 8), (64, 4)])
+def test_scores_that_rise_from_far_below(m, G, D, dtype, eight):
+    """The first 256 rows' scores are -2^28 and less, the others' 80 and less: the sum is of the others, whatever the first
+    rows' reference was. Their two largest scores are alike and lie 8 above the next ones, all exact before the factor
+    log2 e: a weight is off by its rounding, 2^-8 or 2^-11, and by 2^-22 of a score and 2^-20; the first rows' weights
+    are zero."""
+    B, n = 160, 512  # (more units than CTAs: a CTA goes through whole ones)
+    gen = torch.Generator().manual_seed(m)
+    k, v = torch.zeros(B, n, 1, D), values((B, n, 1, D), dtype, eight, gen)
+    k[:, :256, 0, 0] = -2.0
+    step = torch.randint(0, 9, (B, 256), generator=gen)
+    step[:, 100], step[:, 200] = 10, 10
+    k[:, 256:, 0, 1] = step.float()
+    k[:, n - m:, 0, 1] = 0.0  # (drafts, which nobody sees)
+    q = torch.zeros(B * m, G, D)
+    q[..., 0], q[..., 1] = 1.0, 2.0 ** -24
+    out = attend(q.to(TYPES[dtype]), k, v, m, [0] * (B * m), eight, 2.0 ** 27)
+    x = 8.0 * k[:, 256:n - m, 0, 1].double()
+    p = torch.softmax(x, -1)
+    vv = v[:, 256:n - m, 0].double()
+    ref = torch.einsum("bn,bnd->bd", p, vv)[:, None, None].expand(B, m, G, D).reshape(B * m, G, D)
+    mass = torch.einsum("bn,bnd->bd", p, vv.abs())[:, None, None].expand(B, m, G, D).reshape(B * m, G, D)
+    weight = 2.0 ** -8 if dtype == "bf16" and not eight else 2.0 ** -11
+    R.assert_rows(out, ref, (weight + 2.1 * (2.0 ** -22 * 80 * 2 + 2.0 ** -20) + 256 * 2.0 ** -23) * mass, "rising scores")
