@@ -590,8 +590,9 @@ DA_API size_t decode_attn_tree_workspace_size(int n_head, int n_kv_head, int hea
  * for the tokens that several CTAs share and DA_DEVERR_WORKSPACE, or joins their parts
  * early (as in decode_attn_workspace_size; zero the workspace after either). An infinite
  * element of V in a row that a token sees makes that element of its output infinite
- * or NaN. kv_len times the largest |V| stays below 2^110, or sums may
- * overflow. Equal calls give equal bits. Lengths, table, tokens and masks must
+ * or NaN. Scores, |scale <q, K_j>| of the rows seen, stay below 2^22 (32 bits leave half a power
+ * of two open there, and a weight's type holds 2^16), and kv_len times the largest |V|
+ * below 2^110, or a token's output may become NaN. Equal calls give equal bits. Lengths, table, tokens and masks must
  * not change while the call runs, and out must not overlap q (DA_ERR_SHAPE).
  * The pool has at most 2^31 - 1 rows of all KV heads, and B * n_kv_head * (n_head /
  * n_kv_head) times the 128-row tiles of a longest sequence, and 8 more, stay below

@@ -159,3 +159,30 @@ def test_scores_that_rise_from_far_below(m, G, D, dtype, eight):
     mass = torch.einsum("bn,bnd->bd", p, vv.abs())[:, None, None].expand(B, m, G, D).reshape(B * m, G, D)
     weight = 2.0 ** -8 if dtype == "bf16" and not eight else 2.0 ** -11
     R.assert_rows(out, ref, (weight + 2.1 * (2.0 ** -22 * 80 * 2 + 2.0 ** -20) + 256 * 2.0 ** -23) * mass, "rising scores")
+
+
+@FORMS
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("m,G", [(3, 4), (16, 8), (64, 4)])
+def test_the_largest_scores(m, G, D, dtype, eight):
+    """Scores up to 2^21.9: the row of the largest one has all of the weight, 1 but for the rounding of a weight (half a
+    step) and of its sum. Looked at are tokens' heads whose largest score is ahead of the others by more than what
+    the sum of D products and the roundings of the score leave open, and 20."""
+    B, n = 2, 640
+    gen = torch.Generator().manual_seed(m + D)
+    k, v = values((B, n, 1, D), dtype, eight, gen), values((B, n, 1, D), dtype, eight, gen)
+    q = R.randn((B * m, G, D), TYPES[dtype], gen)
+    qk = torch.einsum("bmgd,bnd->bmgn", q.double().view(B, m, G, D), k[:, :n - m, 0].double())
+    size = torch.einsum("bmgd,bnd->bmgn", q.double().abs().view(B, m, G, D), k[:, :n - m, 0].double().abs()).amax(-1)
+    scale = 2.0 ** 21.9 / qk.abs().max().item()
+    out = attend(q, k, v, m, [0] * (B * m), eight, scale)
+    two = (qk * scale).topk(2, dim=-1)
+    ahead = two.values[..., 0] - two.values[..., 1]
+    sure = ahead > 2 * scale * ((D + 8) * 2.0 ** -23 * size) + 2 * 2.0 ** -22 * 2.0 ** 22 + 20
+    assert sure.double().mean() > 0.5
+    top = two.indices[..., 0]
+    ref = torch.stack([v[b, :, 0].double()[top[b]] for b in range(B)])  # [B, m, G, D]
+    weight = 2.0 ** -8 if dtype == "bf16" and not eight else 2.0 ** -11
+    got = out.view(B, m, G, D)
+    assert torch.isfinite(got).all()
+    R.assert_rows(got[sure], ref[sure], (weight + 2.0 ** -20) * ref[sure].abs(), "largest scores")
