@@ -66,3 +66,18 @@ def test_zero_scales_first():
     """A sequence whose first tiles have scales of zero alone, the later ones not, over several CTAs."""
     case = with_v_scales([6000, 700], [40, 5], 8, 128, lambda j: 0.0 if j < 30 else 2.0 ** -12)
     case.cuda().check()
+
+
+@pytest.mark.parametrize("eight", [False, True], ids=["16bit", "e4m3"])
+@pytest.mark.parametrize("exponent", [-96, 96])
+@pytest.mark.parametrize("lens,news", [([300, 47], [20, 7]), ([3000], [64])])
+def test_values_and_scales_far_from_one(lens, news, exponent, eight):
+    """V of 2^96 and 2^-96 and their like (bf16 pages), or under scales of that size: kv_len times |V| below 2^110."""
+    case = Case(lens, news, 8, 2, 128, "bf16", 32, eight, seed=7)
+    if eight:
+        case.vs *= 2.0 ** exponent
+    else:
+        case.v = (case.v.float() * 2.0 ** exponent).to(torch.bfloat16)
+    case.ref *= 2.0 ** exponent
+    case.slack *= 2.0 ** exponent
+    case.cuda().check(f"2^{exponent}")
